@@ -264,6 +264,107 @@ int moe_linear_w8a16(int32_t T, int32_t K, int32_t N, int32_t groups, const uint
                      const float* scale, void* out, int32_t out_is_fp32, void* workspace, size_t workspace_bytes,
                      void* stream);
 
+/* ---- MXFP4 tensors and their products
+ *
+ * The storage format of the routed experts (page "deepseek-v4-mxfp4-int8
+ * config.json", quantization_config, experts_w4a16) outside the layer: made
+ * from a tensor, read back, and multiplied with. A tensor of `rows` rows of K
+ * values (K % 32 == 0) is codes [rows][K/2] u8 (E2M1, element 2i in the low
+ * nibble of byte i) and scales [rows][K/32] u8 (E8M0), the layouts of
+ * w13_codes / w13_scales and w2_codes / w2_scales, so that weights encoded
+ * here go straight into moe_expert_ffn and moe_forward. A scale byte 255
+ * stands for NaN: such a group reads as NaN and so does every product with it
+ * (moe_mxfp4_quantize writes it only for a group that holds an Inf or NaN). */
+
+/* Element types of the conversions. */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F16 = 2 };
+
+/* x [rows][K] (row r at x + r ldx, in elements) -> codes, scales:
+ *   per 32 values with largest magnitude m: X = max(floor(log2 m) - 2, -127),
+ *   scale byte X + 127, code = the E2M1 value nearest to v / 2^X, ties to the
+ *   even code, magnitudes above 6 to 6; the sign of zeros is kept. A group
+ *   with an Inf or NaN: scale byte 255, codes 0.
+ * dtype: MOE_DTYPE_BF16, _F32 or _F16. ldx >= K and rows 16-byte aligned
+ * (x and ldx times the element size multiples of 16). 0 <= rows, 32 <= K <=
+ * 65536, rows K <= 2^36. */
+int moe_mxfp4_quantize(int64_t rows, int32_t K, int32_t dtype, const void* x, int64_t ldx, uint8_t* codes,
+                       uint8_t* scales, void* stream);
+
+/* codes, scales -> out [rows][K] contiguous, exact. dtype: MOE_DTYPE_BF16 or
+ * _F32 (binary16 does not hold every value: MOE_EUNSUPPORTED). */
+int moe_mxfp4_dequantize(int64_t rows, int32_t K, const uint8_t* codes, const uint8_t* scales, int32_t dtype,
+                         void* out, void* stream);
+
+/* What the activations of moe_linear_mxfp4 enter the product as. */
+enum {
+  MOE_ACT_BF16 = 0,  /* as they are ("w4a16") */
+  MOE_ACT_MXFP4 = 1  /* rounded to MXFP4 along K first, as moe_mxfp4_quantize does (4-bit x 4-bit) */
+};
+
+/* y = x W^T with W [N][K] in MXFP4:
+ *   x [T][K] bf16; out [T][N] bf16 (out_is_fp32 = 0) or f32, rounded once
+ *   from the fp32 sum.
+ *   T <= 64: one launch that streams the weights, no workspace (workspace
+ *   may be NULL). T > 64: the weights are expanded to bf16 in the workspace
+ *   (act bf16) or the activations encoded there (act mxfp4), then one matrix
+ *   product, whose K is split over blocks where the tiles would not fill the
+ *   chip (the partial sums are added in order: deterministic).
+ *   workspace: moe_linear_mxfp4_workspace_size(T, K, N, act) bytes, 256-byte
+ *   aligned, any contents; calls sharing one must be ordered on one stream.
+ * Supported: K a multiple of 32 up to 65536, 1 <= N <= 65536, 0 <= T <=
+ * 65536 (else MOE_EUNSUPPORTED, and the size is 0). */
+size_t moe_linear_mxfp4_workspace_size(int32_t T, int32_t K, int32_t N, int32_t act);
+int moe_linear_mxfp4(int32_t T, int32_t K, int32_t N, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
+                     int32_t act, void* out, int32_t out_is_fp32, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* The input gradient of the same product through frozen weights:
+ *   dx [T][K] = dy [T][N] W, dy bf16, dx bf16 or f32.
+ * Sizes, workspace and errors as for moe_linear_mxfp4; every T uses the
+ * workspace. */
+size_t moe_linear_mxfp4_dx_workspace_size(int32_t T, int32_t K, int32_t N);
+int moe_linear_mxfp4_dx(int32_t T, int32_t K, int32_t N, const uint16_t* dy, const uint8_t* codes,
+                        const uint8_t* scales, void* dx, int32_t out_is_fp32, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* ---- The gated feed-forward block with bf16 weights, and its gradients
+ *
+ * The layer's expert (clamped SwiGLU; page "DeepSeek-V4-Flash-0731", section
+ * "Checked in its code", row "SwiGLU feed-forward") as a dense block that can
+ * be trained:
+ *   g = x W1^T, u = x W3^T, h = silu(min(g, L)) * clamp(u, -L, L), y = h W2^T
+ *   x   [T][H] bf16;  w13 [2I][H] bf16, rows [0,I) W1 (gate), [I,2I) W3 (up);
+ *   w2  [H][I] bf16;  out [T][H] bf16 (out_is_fp32 = 0) or f32
+ *   limit  L > 0 (INFINITY: no clamp)
+ *   gu_saved [T][2I] bf16, h_saved [T][I] bf16: both given, they are written
+ *   for moe_gated_ffn_backward; both NULL otherwise.
+ * h, g and u are rounded to bf16 (h enters the second product as bf16); g and
+ * u are rounded without crossing L or -L, so the backward pass finds the
+ * clamp's masks of the unrounded values. NaN inputs give NaN outputs.
+ * Two launches (both projections, activation and product in the first; more
+ * where K is split, as for moe_linear_mxfp4).
+ *   workspace: moe_gated_ffn_workspace_size(T, H, I) bytes, 256-byte aligned,
+ *   any contents; calls sharing one must be ordered on one stream.
+ * Supported: H and I multiples of 8 up to 16384, 0 <= T <= 65536. */
+size_t moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
+int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* x, const uint16_t* w13,
+                  const uint16_t* w2, uint16_t* gu_saved, uint16_t* h_saved, void* out, int32_t out_is_fp32,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of the block for the output gradient dy [T][H] bf16, from the
+ * forward's inputs and saved tensors:
+ *   dx [T][H] bf16; dw13 [2I][H] and dw2 [H][I] bf16 (dw_is_fp32 = 0) or f32.
+ * Each of dx, dw13, dw2 may be NULL: it is not computed. No gradient passes
+ * a clamp that acted (g > L, |u| > L). The gradients of g and u are rounded
+ * to bf16 as operands of the products; sums are fp32. With T = 0 the weight
+ * gradients are zeros.
+ *   workspace: moe_gated_ffn_backward_workspace_size(T, H, I) bytes, as above. */
+size_t moe_gated_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I);
+int moe_gated_ffn_backward(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* dy, const uint16_t* x,
+                           const uint16_t* w13, const uint16_t* w2, const uint16_t* gu_saved,
+                           const uint16_t* h_saved, uint16_t* dx, void* dw13, void* dw2, int32_t dw_is_fp32,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* One MoE layer's parameters for moe_forward_stack (device pointers, layouts
  * as for moe_forward). tid2eid != NULL makes it a hash layer (V rows); then
  * bias and logit_offset are ignored. */

@@ -8,6 +8,10 @@ not built, or a call fails, an exception is raised.
 Entry points (same names as the C ABI): ``route``, ``hash_route``,
 ``permute``, ``expert_ffn``, ``forward``; plus ``workspace_size``,
 ``Workspace`` and ``DeviceLayer`` (device copies of one layer's parameters).
+Around the layer: ``quantize_mxfp4`` / ``dequantize_mxfp4`` (its weight
+format), ``linear_mxfp4`` / ``linear_mxfp4_dx`` (plain products with MXFP4
+weights) and ``gated_ffn`` / ``gated_ffn_backward`` (the expert's block with
+bf16 weights, and its gradients).
 """
 from __future__ import annotations
 
@@ -60,7 +64,7 @@ def config_of(wl) -> MoeConfig:
 
 
 _lib = None
-_VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_VP, _I32, _I64, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _CFGP = ctypes.POINTER(MoeConfig)
 
 _SIGNATURES = {
@@ -82,6 +86,17 @@ _SIGNATURES = {
     "moe_noalloc_max_bytes": ([], _SZ),
     "moe_linear_workspace_size": ([_I32, _I32, _I32, _I32], _SZ),
     "moe_linear_w8a16": ([_I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
+    "moe_mxfp4_quantize": ([_I64, _I32, _I32, _VP, _I64, _VP, _VP, _VP], ctypes.c_int),
+    "moe_mxfp4_dequantize": ([_I64, _I32, _VP, _VP, _I32, _VP, _VP], ctypes.c_int),
+    "moe_linear_mxfp4_workspace_size": ([_I32, _I32, _I32, _I32], _SZ),
+    "moe_linear_mxfp4": ([_I32, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
+    "moe_linear_mxfp4_dx_workspace_size": ([_I32, _I32, _I32], _SZ),
+    "moe_linear_mxfp4_dx": ([_I32, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
+    "moe_gated_ffn_workspace_size": ([_I32, _I32, _I32], _SZ),
+    "moe_gated_ffn": ([_I32, _I32, _I32, _F32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
+    "moe_gated_ffn_backward_workspace_size": ([_I32, _I32, _I32], _SZ),
+    "moe_gated_ffn_backward": ([_I32, _I32, _I32, _F32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ,
+                                _VP], ctypes.c_int),
     "moe_forward_stack": ([_CFGP, _I32, _VP, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
     "moe_forward_noalloc": ([_CFGP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP,
                              _VP, _VP, _VP, _I32, _VP, _VP, _VP], ctypes.c_int),
@@ -519,3 +534,195 @@ def linear_w8a16(x, q, scale, groups=1, out_fp32=False, out=None, ws=None):
     _check(lib().moe_linear_w8a16(T, K, N, groups, _ptr(x), _ptr(q), _ptr(scale), _ptr(out), int(out_fp32),
                                   _ptr(ws), ws.numel(), _stream(dev)), "moe_linear_w8a16")
     return out
+
+
+# ------------------------------------------------------------------ MXFP4 tensors and products, the gated block
+#
+# These calls take their scratch from torch's allocator per call (or from
+# ``ws``, a uint8 tensor of at least the size the C ABI names), so calls on
+# different streams and captured graphs never share one by accident. They run
+# on the device of their tensors, whatever the current device is.
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+_ACTS = {"bf16": 0, "mxfp4": 1}
+
+
+def _same_device(*named):
+    dev = named[0][1].device
+    for name, t in named[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    return dev
+
+
+def _call(dev, name, *args):
+    """Calls a library function with ``dev`` current, its current stream appended."""
+    fn = getattr(lib(), name)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)), name)
+
+
+def _scratch(need, dev, ws, what):
+    if need == 0:
+        raise MoEError(MOE_EUNSUPPORTED, what)
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(ws, torch.uint8, None, "ws")
+    return ws
+
+
+def _result(out, shape, dtype, dev, name="out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return _need(out, dtype, shape, name)
+
+
+def _mxfp4_weight(codes, scales):
+    """N and K of an MXFP4 matrix [N][K]."""
+    _need(codes, torch.uint8, None, "codes")
+    _need(scales, torch.uint8, None, "scales")
+    if codes.dim() != 2 or codes.shape[1] % 16:
+        raise ValueError("codes: shape [N, K/2] with K a multiple of 32 expected")
+    N, K = codes.shape[0], codes.shape[1] * 2
+    if tuple(scales.shape) != (N, K // 32):
+        raise ValueError(f"scales: shape {tuple(scales.shape)}, expected {(N, K // 32)}")
+    return N, K
+
+
+def quantize_mxfp4(x, out=None):
+    """x [..., K] (bf16, fp32 or fp16; K a multiple of 32) -> (codes uint8
+    [..., K/2], scales uint8 [..., K/32]), the layer's MXFP4 layout
+    (moe_mxfp4_quantize). x is contiguous, or 2-D with unit column stride and
+    16-byte aligned rows."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x: torch.Tensor expected")
+    if x.device.type != "cuda":
+        raise ValueError("x: must be a device (cuda/hip) tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"x: dtype {x.dtype}, expected bfloat16, float32 or float16")
+    if x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % 32:
+        raise ValueError("x: last dimension must be a positive multiple of 32")
+    K = x.shape[-1]
+    rows = x.numel() // K
+    ldx = K
+    if not x.is_contiguous():
+        if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < K:
+            raise ValueError("x: contiguous, or 2-D with unit column stride, expected")
+        ldx = x.stride(0)
+    lead = tuple(x.shape[:-1])
+    c, s = out if out is not None else (None, None)
+    codes = _result(c, lead + (K // 2,), torch.uint8, x.device, "codes")
+    scales = _result(s, lead + (K // 32,), torch.uint8, x.device, "scales")
+    dev = _same_device(("x", x), ("codes", codes), ("scales", scales))
+    _call(dev, "moe_mxfp4_quantize", rows, K, _DTYPES[x.dtype], _ptr(x), ldx, _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None):
+    """(codes [..., K/2], scales [..., K/32]) -> [..., K] in bf16 or fp32, exact (moe_mxfp4_dequantize)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype {dtype}, expected bfloat16 or float32")
+    _need(codes, torch.uint8, None, "codes")
+    _need(scales, torch.uint8, None, "scales")
+    if codes.dim() < 1 or codes.shape[-1] == 0 or codes.shape[-1] % 16:
+        raise ValueError("codes: last dimension must be a positive multiple of 16")
+    K = codes.shape[-1] * 2
+    lead = tuple(codes.shape[:-1])
+    _need(scales, torch.uint8, lead + (K // 32,), "scales")
+    out = _result(out, lead + (K,), dtype, codes.device)
+    dev = _same_device(("codes", codes), ("scales", scales), ("out", out))
+    _call(dev, "moe_mxfp4_dequantize", codes.numel() * 2 // K, K, _ptr(codes), _ptr(scales), _DTYPES[dtype], _ptr(out))
+    return out
+
+
+def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None):
+    """y = x W^T (moe_linear_mxfp4): x [T][K] bf16, W [N][K] as codes
+    [N][K/2] and scales [N][K/32] -> [T][N] (bf16 or fp32). act: "bf16", or
+    "mxfp4" to round x to MXFP4 first."""
+    if act not in _ACTS:
+        raise ValueError(f"act {act!r}, expected one of {sorted(_ACTS)}")
+    N, K = _mxfp4_weight(codes, scales)
+    _need(x, torch.bfloat16, None, "x")
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (T, {K})")
+    T = x.shape[0]
+    out = _result(out, (T, N), torch.float32 if out_fp32 else torch.bfloat16, x.device)
+    dev = _same_device(("x", x), ("codes", codes), ("scales", scales), ("out", out), ("ws", ws))
+    need = lib().moe_linear_mxfp4_workspace_size(T, K, N, _ACTS[act])
+    if need > 256 or ws is not None:
+        ws = _scratch(need, dev, ws, "moe_linear_mxfp4")
+    _call(dev, "moe_linear_mxfp4", T, K, N, _ptr(x), _ptr(codes), _ptr(scales), _ACTS[act], _ptr(out), int(out_fp32),
+          _ptr(ws), 0 if ws is None else ws.numel())
+    return out
+
+
+def linear_mxfp4_dx(dy, codes, scales, out_fp32=False, out=None, ws=None):
+    """dx = dy W, the input gradient of ``linear_mxfp4`` through frozen
+    weights (moe_linear_mxfp4_dx): dy [T][N] bf16 -> [T][K] (bf16 or fp32)."""
+    N, K = _mxfp4_weight(codes, scales)
+    _need(dy, torch.bfloat16, None, "dy")
+    if dy.dim() != 2 or dy.shape[1] != N:
+        raise ValueError(f"dy: shape {tuple(dy.shape)}, expected (T, {N})")
+    T = dy.shape[0]
+    out = _result(out, (T, K), torch.float32 if out_fp32 else torch.bfloat16, dy.device)
+    dev = _same_device(("dy", dy), ("codes", codes), ("scales", scales), ("out", out), ("ws", ws))
+    ws = _scratch(lib().moe_linear_mxfp4_dx_workspace_size(T, K, N), dev, ws, "moe_linear_mxfp4_dx")
+    _call(dev, "moe_linear_mxfp4_dx", T, K, N, _ptr(dy), _ptr(codes), _ptr(scales), _ptr(out), int(out_fp32), _ptr(ws),
+          ws.numel())
+    return out
+
+
+def _ffn_shapes(x, w13, w2):
+    _need(x, torch.bfloat16, None, "x")
+    if x.dim() != 2:
+        raise ValueError("x: shape [T, H] expected")
+    T, H = x.shape
+    _need(w2, torch.bfloat16, None, "w2")
+    if w2.dim() != 2 or w2.shape[0] != H:
+        raise ValueError(f"w2: shape {tuple(w2.shape)}, expected ({H}, I)")
+    I = w2.shape[1]
+    _need(w13, torch.bfloat16, (2 * I, H), "w13")
+    return T, H, I
+
+
+def gated_ffn(x, w13, w2, limit=10.0, save=False, out_fp32=False, out=None, ws=None):
+    """The expert's block with bf16 weights (moe_gated_ffn): x [T][H], w13
+    [2I][H] (gate rows, then up rows), w2 [H][I] -> y [T][H] (bf16 or fp32).
+    save=True returns (y, saved), ``saved`` being what ``gated_ffn_backward``
+    takes: (g and u [T][2I], h [T][I]), bf16."""
+    T, H, I = _ffn_shapes(x, w13, w2)
+    out = _result(out, (T, H), torch.float32 if out_fp32 else torch.bfloat16, x.device)
+    dev = _same_device(("x", x), ("w13", w13), ("w2", w2), ("out", out), ("ws", ws))
+    saved = None
+    if save:
+        saved = (torch.empty(T, 2 * I, dtype=torch.bfloat16, device=dev),
+                 torch.empty(T, I, dtype=torch.bfloat16, device=dev))
+    ws = _scratch(lib().moe_gated_ffn_workspace_size(T, H, I), dev, ws, "moe_gated_ffn")
+    gu, h = saved if save else (None, None)
+    _call(dev, "moe_gated_ffn", T, H, I, float(limit), _ptr(x), _ptr(w13), _ptr(w2), _ptr(gu), _ptr(h), _ptr(out),
+          int(out_fp32), _ptr(ws), ws.numel())
+    return (out, saved) if save else out
+
+
+def gated_ffn_backward(dy, x, w13, w2, saved, limit=10.0, need=(True, True, True), dw_fp32=False, ws=None):
+    """Gradients of ``gated_ffn`` (moe_gated_ffn_backward) for dy [T][H] bf16:
+    (dx [T][H] bf16, dw13 [2I][H], dw2 [H][I]; the weights' in bf16, or fp32
+    if dw_fp32). ``saved`` and ``limit``: the forward call's. ``need``: which
+    of the three to compute (None in the others' places)."""
+    T, H, I = _ffn_shapes(x, w13, w2)
+    _need(dy, torch.bfloat16, (T, H), "dy")
+    gu, h = saved
+    _need(gu, torch.bfloat16, (T, 2 * I), "saved[0]")
+    _need(h, torch.bfloat16, (T, I), "saved[1]")
+    dev = _same_device(("dy", dy), ("x", x), ("w13", w13), ("w2", w2), ("saved[0]", gu), ("saved[1]", h), ("ws", ws))
+    wt = torch.float32 if dw_fp32 else torch.bfloat16
+    dx = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if need[0] else None
+    dw13 = torch.empty(2 * I, H, dtype=wt, device=dev) if need[1] else None
+    dw2 = torch.empty(H, I, dtype=wt, device=dev) if need[2] else None
+    ws = _scratch(lib().moe_gated_ffn_backward_workspace_size(T, H, I), dev, ws, "moe_gated_ffn_backward")
+    _call(dev, "moe_gated_ffn_backward", T, H, I, float(limit), _ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(gu),
+          _ptr(h), _ptr(dx), _ptr(dw13), _ptr(dw2), int(dw_fp32), _ptr(ws), ws.numel())
+    return dx, dw13, dw2

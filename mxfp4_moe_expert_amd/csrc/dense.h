@@ -1,0 +1,445 @@
+// Dense matrix products of the trainable gated block and of the plain MXFP4
+// projections on gfx950's matrix cores: one kernel template,
+//   C[m][n] = sum_k X(m, k) W(n, k),
+// with each operand stored either along k ([row][k], "K-contiguous") or
+// across it ([k][row], "transposed"), in bf16 or (both K-contiguous) MXFP4.
+//
+// Tile BM x BN, one block of WGM x WGN waves. K runs in stages of 128 bytes
+// per row (64 bf16 or 256 E2M1 values), NBUF stages in LDS:
+//   - Operands go from global memory straight to LDS (16 bytes per lane, the
+//     64 lanes of a wave filling 1 KB), NBUF - 1 stages ahead; a stage costs
+//     one barrier. The loads are raw buffer loads whose out-of-range lanes
+//     (rows, columns or k past the end) write zeros, so no tail needs code
+//     in the K loop.
+//   - The 16-byte pieces of a K-contiguous row are stored rotated (piece c of
+//     row i at position c ^ (i / 2) % 8), so the 16 rows of an MFMA operand
+//     lie in different banks. A transposed operand keeps its k rows; its
+//     32-byte units are stored at unit ^ f(k), and the LDS transposing read
+//     (16 lanes x 4 elements) hands each lane 4 consecutive k of its row.
+//   - MFMA 16x16x32 (bf16) or 16x16x128 with E8M0 scales (MXFP4), W as the A
+//     operand: lane (r, g) ends with 4 consecutive n of one m, one 8-byte
+//     bf16 store.
+#pragma once
+
+#include "device.h"
+#include "internal.h"
+
+namespace moe {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((ext_vector_type(4))) short s16x4_t;
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+
+constexpr uint32_t kLaneOff = 0x80000000u;  // a lane offset past every buffer: reads zero
+constexpr int kStageB = 128;                // K bytes per row and stage
+
+// 16 (or 4) bytes per lane from buffer offset voff to LDS byte m0 + lane * 16 (4).
+// No output registers: the data is waited for with dense_wait before a barrier.
+// (m0 is a reserved register: the compiler sets it right before each use of its own.)
+__device__ __forceinline__ void load_lds16(u32x4_t rsrc, uint32_t voff, uint32_t lds_at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)lds_at)), "v"(voff), "s"(rsrc)
+               : "memory");
+}
+__device__ __forceinline__ void load_lds4(u32x4_t rsrc, uint32_t voff, uint32_t lds_at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)lds_at)), "v"(voff), "s"(rsrc)
+               : "memory");
+}
+
+// At most N of the wave's vector loads outstanding, and its LDS reads done.
+template <int N>
+__device__ __forceinline__ void dense_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+}
+
+__device__ __forceinline__ u32x4_t buffer_of(const void* p) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  return (u32x4_t){(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)), 0x7fffffffu,
+                   0x00027000u};
+}
+
+// Staging of one operand tile of ROWS rows (W waves). Rows past `rows` and k
+// past `kb` (bytes along k, K-contiguous) or `kn` (k rows, transposed) read
+// as zeros.
+template <bool TR, int ROWS, int W>
+struct Stager {
+  static constexpr int NI = ROWS * kStageB / 1024 / W;  // 1 KB loads per wave and stage
+  static constexpr int PPR = TR ? ROWS / 8 : 8;         // 16-byte pieces per stored row
+  uint32_t voff[NI];
+
+  static __device__ __forceinline__ int slot(int i, int wave, int lane) { return (i * W + wave) * 64 + lane; }
+  // the k position (16-byte piece of the row's 128 bytes, or k row) of slot s, and its piece
+  static __device__ __forceinline__ int piece(int s) {
+    const int row = s / PPR, pos = s % PPR;
+    if constexpr (TR) {
+      const int f = ((row & 3) | (((row >> 3) & 1) << 2)) & (ROWS / 16 - 1);
+      return ((((pos >> 1) ^ f) << 1) | (pos & 1));
+    } else {
+      return pos ^ ((row >> 1) & 7);
+    }
+  }
+
+  // row_of(i): the stored row of tile row i (K-contiguous), or -1 for none
+  template <class F>
+  __device__ __forceinline__ void init_kc(int wave, int lane, uint32_t ld, F row_of) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int s = slot(i, wave, lane);
+      const int row = row_of(s / PPR);
+      voff[i] = row < 0 ? kLaneOff : (uint32_t)row * ld + (uint32_t)piece(s) * 16;
+    }
+  }
+  __device__ __forceinline__ void init_tr(int wave, int lane, uint32_t ld, int cols) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int s = slot(i, wave, lane);
+      voff[i] = piece(s) * 8 < cols ? (uint32_t)(s / PPR) * ld + (uint32_t)piece(s) * 16 : kLaneOff;
+    }
+  }
+  // kleft: bytes (K-contiguous) or k rows (transposed) from the stage's start to the end of k
+  __device__ __forceinline__ void load(u32x4_t rsrc, uint32_t lds_at, int wave, int lane, int kleft) const {
+    constexpr int FULL = TR ? 64 : kStageB;
+    if (kleft >= FULL) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) load_lds16(rsrc, voff[i], lds_at + (uint32_t)((i * W + wave) * 1024));
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int s = slot(i, wave, lane);
+        const int at = TR ? s / PPR : piece(s) * 16;
+        load_lds16(rsrc, at < kleft ? voff[i] : kLaneOff, lds_at + (uint32_t)((i * W + wave) * 1024));
+      }
+    }
+  }
+};
+
+// Reading MFMA operands of 16 tile rows from a staged tile.
+template <bool TR, int ROWS, int NB>
+struct Reader {
+  // K-contiguous: offsets of the lane's piece for the two k-steps; transposed: one per row block
+  uint32_t off[TR ? NB : 2];
+  __device__ __forceinline__ void init(int row0, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    if constexpr (TR) {
+      const int j = r >> 2, q = r & 3, f = (j | ((g & 1) << 2)) & (ROWS / 16 - 1);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        off[b] = (uint32_t)((8 * g + j) * (ROWS * 2) + (((row0 >> 4) + b) ^ f) * 32 + q * 8);
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+        off[kk] = (uint32_t)((row0 + r) * kStageB + (((kk * 4 + g) ^ (r >> 1)) * 16));
+    }
+  }
+  __device__ __forceinline__ u32x4_t read(const lds_u8* tile, int b, int kk) const {
+    if constexpr (TR) {
+      const lds_u8* p = tile + off[b] + kk * 32 * (ROWS * 2);
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * (ROWS * 2)));
+      const uint2 a = __builtin_bit_cast(uint2, lo), c = __builtin_bit_cast(uint2, hi);
+      return (u32x4_t){a.x, a.y, c.x, c.y};
+    } else {
+      return *(const lds_u32x4*)(tile + off[kk] + b * (16 * kStageB));
+    }
+  }
+};
+
+__device__ __forceinline__ f32x4_t mfma_bf16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
+  return mfma_16x16x32(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c);
+}
+template <int KK>
+__device__ __forceinline__ f32x4_t mfma_mx4(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c, uint32_t sa,
+                                            uint32_t sb) {
+  const i32x8_t a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8_t b8 = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, KK, (int)sa, KK, (int)sb);
+}
+
+__device__ __forceinline__ uint2 pack4_bf16(const f32x4_t& v) {
+  return make_uint2((uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16),
+                    (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16));
+}
+
+// Four consecutive outputs out[at .. at+3], of which `live` (1..4) exist;
+// wide: at is a multiple of 4 elements and all four exist.
+__device__ __forceinline__ void store4(void* out, bool fp32, size_t at, const f32x4_t& v, int live, bool wide) {
+  if (fp32) {
+    float* o = static_cast<float*>(out) + at;
+    if (wide) {
+      *reinterpret_cast<f32x4_t*>(o) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < live) o[i] = v[i];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(out) + at;
+    if (wide) {
+      *reinterpret_cast<uint2*>(o) = pack4_bf16(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < live) o[i] = f32_to_bf16(v[i]);
+    }
+  }
+}
+
+// h = silu(min(g, L)) * clamp(u, -L, L); NaN operands give NaN.
+__device__ __forceinline__ float ffn_act(float g, float u, float L) {
+  const float gc = g > L ? L : g;
+  const float uc = u > L ? L : (u < -L ? -L : u);
+  return silu(gc) * uc;
+}
+
+// v rounded to bf16 for the backward pass without crossing the border L: a
+// value on one side of it (v > L or v <= L) stays there, so that the backward
+// finds the clamp's mask of the unrounded value. Only a value within one
+// rounding of L moves, by less than one step instead of half of one; values
+// past L count as L whatever is stored.
+__device__ __forceinline__ uint16_t save_side(float v, float L) {
+  uint16_t b = f32_to_bf16(v);
+  const float w = bf16_to_f32(b);
+  if (v > L && !(w > L)) b = (uint16_t)(L >= 0.0f ? b + 1 : b - 1);
+  if (v <= L && w > L) b = (uint16_t)(L >= 0.0f ? b - 1 : b + 1);
+  return b;
+}
+__device__ __forceinline__ uint16_t save_gate(float g, float L) { return save_side(g, L); }
+// both borders, by symmetry; L > 0
+__device__ __forceinline__ uint16_t save_up(float u, float L) {
+  const uint16_t s = __float_as_uint(u) >> 31 ? 0x8000u : 0u;
+  return (uint16_t)(save_side(fabsf(u), L) | s);
+}
+
+// Gradients of the gated product at the saved (g, u) for dh.
+__device__ __forceinline__ void ffn_act_grad(float g, float u, float dh, float L, float& dg, float& du) {
+  const float gc = g > L ? L : g;
+  const float uc = u > L ? L : (u < -L ? -L : u);
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gc * 1.4426950408889634f));
+  dg = g > L ? 0.0f : dh * uc * (s * (1.0f + gc * (1.0f - s)));
+  du = (u > L || u < -L) ? 0.0f : dh * gc * s;
+}
+
+enum DenseEpi {
+  kEpiStore = 0,    // out [M][N] bf16 or fp32
+  kEpiGate = 1,     // gate / up rows interleaved: h [M][I] bf16 (and gu [M][2I])
+  kEpiGrad = 2,     // dh -> dgu [M][2I] from gu
+  kEpiPartial = 3,  // fp32 partial sums [slice][M][N] (of a split K)
+};
+
+// Logical tile of a block: XCD x (block % 8) walks a contiguous run of the
+// tiles, ordered in bands of 8 row tiles, so that the tiles an XCD's blocks
+// run at once share operand rows in its L2.
+__device__ __forceinline__ void dense_tile(int bid, int tm, int tn, int& im, int& in) {
+  const int n = tm * tn, per = n >> 3, extra = n & 7, x = bid & 7;
+  const int t = x * per + min(x, extra) + (bid >> 3);
+  constexpr int BAND = 8;
+  const int band = t / (BAND * tn), left = tm - band * BAND;
+  const int h = left < BAND ? left : BAND;
+  const int o = t - band * BAND * tn;
+  im = band * BAND + o % h;
+  in = o / h;
+}
+
+// FP4: both operands MXFP4 K-contiguous, with packed scales (see mxfp4.hip).
+template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NBUF, bool FP4, int EPI>
+__global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
+  constexpr int W = WGM * WGN;
+  constexpr int MB = BM / WGM / 16, NB = BN / WGN / 16;  // 16-row blocks per wave
+  constexpr int XB = BM * kStageB, WB = BN * kStageB;    // bytes per stage
+  constexpr int SXB = FP4 ? BM * 8 : 0, SWB = FP4 ? BN * 8 : 0;
+  constexpr int SI = (SXB + SWB + 256 * W - 1) / (256 * W);  // scale loads per wave and stage (the last may be idle)
+  constexpr int STAGE = XB + WB + SI * 256 * W;
+  static_assert(!FP4 || (!XT && !WT), "MXFP4 operands are K-contiguous");
+  using SX = Stager<XT, BM, W>;
+  using SW = Stager<WT, BN, W>;
+  constexpr int LPS = SX::NI + SW::NI + SI;
+  static_assert(SX::NI * 1024 * W == XB && SW::NI * 1024 * W == WB, "tiles split evenly over the waves");
+  extern __shared__ __align__(16) unsigned char smem[];  // NBUF stages: X tile, W tile, scales
+  lds_u8* const lds = (lds_u8*)smem;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int im, in;
+  dense_tile(blockIdx.x, a.tm, a.tn, im, in);
+  const int m0 = im * BM, n0 = in * (EPI == kEpiGate ? BN / 2 : BN);
+  const int Kb = a.K * 2 / (FP4 ? 4 : 1);  // bytes along k (K-contiguous operands)
+  const int st0 = blockIdx.y * a.slice_stages;
+  const int nst = min(a.slice_stages, a.stages - st0);
+
+  SX sx;
+  SW sw;
+  const char* xbase = static_cast<const char*>(a.x);
+  const char* wbase = static_cast<const char*>(a.w);
+  if constexpr (XT) {
+    sx.init_tr(wave, lane, a.x_ld, a.M - m0);
+    xbase += (size_t)m0 * 2;
+  } else {
+    sx.init_kc(wave, lane, a.x_ld, [&](int i) { return m0 + i < a.M ? i : -1; });
+    xbase += (size_t)m0 * a.x_ld;
+  }
+  if constexpr (WT) {
+    sw.init_tr(wave, lane, a.w_ld, a.N - n0);
+    wbase += (size_t)n0 * 2;
+  } else if constexpr (EPI == kEpiGate) {
+    // tile rows: 16 gate rows, then the matching 16 up rows, and so on
+    sw.init_kc(wave, lane, a.w_ld, [&](int i) {
+      const int c = n0 + (i >> 5) * 16 + (i & 15);
+      return c < a.I ? ((i >> 4) & 1) * a.I + c : -1;
+    });
+  } else {
+    sw.init_kc(wave, lane, a.w_ld, [&](int i) { return n0 + i < a.N ? i : -1; });
+    wbase += (size_t)n0 * a.w_ld;
+  }
+  const size_t xstep = XT ? (size_t)64 * a.x_ld : kStageB, wstep = WT ? (size_t)64 * a.w_ld : kStageB;
+  const int kx = XT ? a.K : Kb, kw = WT ? a.K : Kb;
+  constexpr int xk = XT ? 64 : kStageB, wk = WT ? 64 : kStageB;
+
+  auto load_stage = [&](int i, int buf) {  // stage st0 + i
+    const int st = st0 + i;
+    const bool live = i < nst;
+    const uint32_t at = lds0 + (uint32_t)buf * STAGE;
+    const size_t sg = live ? (size_t)st : 0;
+    sx.load(buffer_of(xbase + sg * xstep), at, wave, lane, live ? kx - st * xk : 0);
+    sw.load(buffer_of(wbase + sg * wstep), at + XB, wave, lane, live ? kw - st * wk : 0);
+    if constexpr (FP4) {
+      // packed scales: [stage][16-row block][lane] u16; the tile's blocks of a stage are contiguous
+      const u32x4_t rx = buffer_of(a.x_scales + (sg * a.x_blocks + (size_t)im * (BM / 16)) * 64);
+      const u32x4_t rw = buffer_of(a.w_scales + (sg * a.w_blocks + (size_t)in * (BN / 16)) * 64);
+      const uint32_t endx = (uint32_t)(a.x_blocks - im * (BM / 16)) * 128;
+      const uint32_t endw = min((uint32_t)(a.w_blocks - in * (BN / 16)) * 128, (uint32_t)SWB);
+#pragma unroll
+      for (int j = 0; j < SI; ++j) {
+        const uint32_t o = (uint32_t)(j * W + wave) * 256;  // byte of the stage's scale area
+        const bool isw = o >= SXB;
+        const uint32_t off = (isw ? o - SXB : o) + (uint32_t)lane * 4;
+        load_lds4(isw ? rw : rx, live && off < (isw ? endw : endx) ? off : kLaneOff, at + XB + WB + o);
+      }
+    }
+  };
+
+  const int wm = wave / WGN, wn = wave % WGN;
+  Reader<XT, BM, MB> rx;
+  Reader<WT, BN, NB> rw;
+  rx.init(wm * MB * 16, lane);
+  rw.init(wn * NB * 16, lane);
+
+  f32x4_t acc[NB][MB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int c = 0; c < MB; ++c) acc[b][c] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int i = 0; i < NBUF - 1; ++i) load_stage(i, i);
+  int buf = 0;
+  for (int i = 0; i < nst; ++i) {
+    dense_wait<(NBUF - 2) * LPS>();  // stage i has landed (this wave's part) ...
+    __builtin_amdgcn_s_barrier();    // ... and every wave's; the buffer of stage i - 1 is free
+    asm volatile("" ::: "memory");
+    load_stage(i + NBUF - 1, buf == 0 ? NBUF - 1 : buf - 1);
+    const lds_u8* xt = lds + buf * STAGE;
+    const lds_u8* wt = xt + XB;
+    uint32_t sxv[MB], swv[NB];
+    if constexpr (FP4) {
+      const lds_u8* sc = xt + XB + WB;
+#pragma unroll
+      for (int c = 0; c < MB; ++c) sxv[c] = *(const lds_u16*)(sc + ((wm * MB + c) * 64 + lane) * 2);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) swv[b] = *(const lds_u16*)(sc + SXB + ((wn * NB + b) * 64 + lane) * 2);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      u32x4_t xf[MB], wf[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) wf[b] = rw.read(wt, b, kk);
+#pragma unroll
+      for (int c = 0; c < MB; ++c) xf[c] = rx.read(xt, c, kk);
+#pragma unroll
+      for (int c = 0; c < MB; ++c)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if constexpr (FP4) {
+            if (kk == 0) acc[b][c] = mfma_mx4<0>(wf[b], xf[c], acc[b][c], swv[b], sxv[c]);
+            else acc[b][c] = mfma_mx4<1>(wf[b], xf[c], acc[b][c], swv[b], sxv[c]);
+          } else {
+            acc[b][c] = mfma_bf16(wf[b], xf[c], acc[b][c]);
+          }
+        }
+    }
+    buf = buf + 1 == NBUF ? 0 : buf + 1;
+  }
+  dense_wait<0>();  // nothing may still write this block's LDS when it ends
+
+  // lane (r, g): acc[b][c][i] = C[m = .. + 16 c + r][n = .. + 16 b + 4 g + i]
+  const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int c = 0; c < MB; ++c) {
+    const int m = m0 + (wm * MB + c) * 16 + r;
+    if (m >= a.M) continue;
+    if constexpr (EPI == kEpiGate) {
+#pragma unroll
+      for (int b = 0; b < NB; b += 2) {
+        const int n = n0 + (wn * NB + b) * 8 + 4 * g;  // h column
+        if (n >= a.I) continue;                        // I % 8 == 0: four columns exist or none
+        f32x4_t h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = ffn_act(acc[b][c][i], acc[b + 1][c][i], a.limit);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (size_t)m * a.I + n) = pack4_bf16(h);
+        if (a.gu_out) {
+          uint16_t* o = a.gu_out + (size_t)m * 2 * a.I + n;
+          uint16_t sg[4], su[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sg[i] = save_gate(acc[b][c][i], a.limit);
+            su[i] = save_up(acc[b + 1][c][i], a.limit);
+          }
+          *reinterpret_cast<uint2*>(o) =
+              make_uint2(sg[0] | ((uint32_t)sg[1] << 16), sg[2] | ((uint32_t)sg[3] << 16));
+          *reinterpret_cast<uint2*>(o + a.I) =
+              make_uint2(su[0] | ((uint32_t)su[1] << 16), su[2] | ((uint32_t)su[3] << 16));
+        }
+      }
+    } else if constexpr (EPI == kEpiGrad) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int n = n0 + (wn * NB + b) * 16 + 4 * g;
+        if (n >= a.N) continue;
+        const uint16_t* s = a.gu_in + (size_t)m * 2 * a.I + n;
+        const uint2 gv = *reinterpret_cast<const uint2*>(s), uv = *reinterpret_cast<const uint2*>(s + a.I);
+        f32x4_t dg, du;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t gw = i < 2 ? gv.x : gv.y, uw = i < 2 ? uv.x : uv.y;
+          float p, q;
+          ffn_act_grad(bf16_to_f32((uint16_t)(gw >> (16 * (i & 1)))), bf16_to_f32((uint16_t)(uw >> (16 * (i & 1)))),
+                       acc[b][c][i], a.limit, p, q);
+          dg[i] = p;
+          du[i] = q;
+        }
+        uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I + n;
+        *reinterpret_cast<uint2*>(o) = pack4_bf16(dg);
+        *reinterpret_cast<uint2*>(o + a.I) = pack4_bf16(du);
+      }
+    } else {
+      void* out = a.out;
+      if constexpr (EPI == kEpiPartial) out = a.part + (size_t)blockIdx.y * a.M * a.N;
+      const bool fp32 = EPI == kEpiPartial || a.out_is_fp32;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int n = n0 + (wn * NB + b) * 16 + 4 * g;
+        if (n >= a.N) continue;
+        store4(out, fp32, (size_t)m * a.N + n, acc[b][c], a.N - n, (a.N & 3) == 0);
+      }
+    }
+  }
+}
+
+}  // namespace moe

@@ -1,0 +1,183 @@
+// Launching the dense products of dense.h: tile configurations, the split of
+// K for products with few tiles, and its reduction.
+#include "dense.h"
+
+namespace moe {
+
+namespace {
+
+struct TileCfg {
+  int bm, bn, waves, nbuf;
+};
+// 0: large products; 1: fewer tiles than CUs at 256 x 256; 2: few rows
+constexpr TileCfg kTiles[] = {{256, 256, 8, 2}, {128, 128, 4, 4}, {64, 128, 4, 5}};
+constexpr int kNumTiles = 3;
+
+constexpr size_t tile_lds(const TileCfg& t, bool fp4) {
+  const size_t sc = fp4 ? (((size_t)(t.bm + t.bn) * 8 + 256 * t.waves - 1) / (256 * t.waves)) * 256 * t.waves : 0;
+  return t.nbuf * ((size_t)(t.bm + t.bn) * kStageB + sc);
+}
+
+// Sums the slices of a split K in order, then the epilogue of the product.
+// Thread: four consecutive columns of one row.
+template <int EPI>
+__global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
+  const int cols = EPI == kEpiGate ? a.I : a.N;
+  const int per = (cols + 3) / 4;
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(id / per), n = (int)(id - (long long)m * per) * 4;
+  if (m >= a.M) return;
+  const size_t plane = (size_t)a.M * a.N;
+  const bool wide = (a.N & 3) == 0;
+  auto sum = [&](int col) {
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    const float* p = a.part + (size_t)m * a.N + col;
+    for (int s = 0; s < slices; ++s, p += plane) {
+      if (wide) {
+        v += *reinterpret_cast<const f32x4_t*>(p);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col + i < a.N) v[i] += p[i];
+      }
+    }
+    return v;
+  };
+  if constexpr (EPI == kEpiGate) {
+    const f32x4_t g = sum(n), u = sum(a.I + n);
+    f32x4_t h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = ffn_act(g[i], u[i], a.limit);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (size_t)m * a.I + n) = pack4_bf16(h);
+    if (a.gu_out) {
+      uint16_t* o = a.gu_out + (size_t)m * 2 * a.I + n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[i] = save_gate(g[i], a.limit);
+        o[a.I + i] = save_up(u[i], a.limit);
+      }
+    }
+  } else if constexpr (EPI == kEpiGrad) {
+    const f32x4_t dh = sum(n);
+    const uint16_t* s = a.gu_in + (size_t)m * 2 * a.I + n;
+    f32x4_t dg, du;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float p, q;
+      ffn_act_grad(bf16_to_f32(s[i]), bf16_to_f32(s[a.I + i]), dh[i], a.limit, p, q);
+      dg[i] = p;
+      du[i] = q;
+    }
+    uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I + n;
+    *reinterpret_cast<uint2*>(o) = pack4_bf16(dg);
+    *reinterpret_cast<uint2*>(o + a.I) = pack4_bf16(du);
+  } else {
+    store4(a.out, a.out_is_fp32, (size_t)m * a.N + n, sum(n), a.N - n, wide);
+  }
+}
+
+template <class K>
+hipError_t run(K kern, const TileCfg& t, bool fp4, int slices, const DenseArgs& a, hipStream_t st) {
+  const size_t lds = tile_lds(t, fp4);
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  kern<<<dim3((unsigned)(a.tm * a.tn), (unsigned)slices), t.waves * 64, lds, st>>>(a);
+  return hipGetLastError();
+}
+
+template <bool XT, bool WT, bool FP4, int EPI>
+hipError_t run_tile(int tile, int slices, const DenseArgs& a, hipStream_t st) {
+  if (tile == 0) return run(&k_dense<XT, WT, 256, 256, 2, 4, 2, FP4, EPI>, kTiles[0], FP4, slices, a, st);
+  if (tile == 1) return run(&k_dense<XT, WT, 128, 128, 2, 2, 4, FP4, EPI>, kTiles[1], FP4, slices, a, st);
+  return run(&k_dense<XT, WT, 64, 128, 2, 2, 5, FP4, EPI>, kTiles[2], FP4, slices, a, st);
+}
+
+template <int EPI>
+hipError_t run_bf16(DenseLayout layout, int tile, int slices, const DenseArgs& a, hipStream_t st) {
+  if constexpr (EPI == kEpiGate) {
+    return layout == kDenseNT ? run_tile<false, false, false, EPI>(tile, slices, a, st) : hipErrorInvalidValue;
+  } else if constexpr (EPI == kEpiGrad) {
+    return layout == kDenseNN ? run_tile<false, true, false, EPI>(tile, slices, a, st) : hipErrorInvalidValue;
+  } else {
+    if (layout == kDenseNT) return run_tile<false, false, false, EPI>(tile, slices, a, st);
+    if (layout == kDenseNN) return run_tile<false, true, false, EPI>(tile, slices, a, st);
+    return run_tile<true, true, false, EPI>(tile, slices, a, st);
+  }
+}
+
+inline int stages_of(DenseKind kind, int K) { return kind == kDenseFp4 ? mxfp4_stages(K) : (K + 63) / 64; }
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+// The plan with the least estimated time: rounds of blocks over 256 CUs times
+// the stages each runs, plus the partial sums' traffic for a split.
+DensePlan dense_plan(DenseKind kind, DenseLayout layout, int epi, int M, int N, int K) {
+  (void)layout;
+  (void)epi;
+  const int nst = stages_of(kind, K);
+  // microseconds per stage of a block that has a CU to itself, and per block
+  constexpr double stage_us[kNumTiles] = {1.05, 0.40, 0.30}, start_us = 3.0;
+  DensePlan best = {0, 1};
+  double best_us = 1e30;
+  for (int t = 0; t < kNumTiles; ++t) {
+    const long long tiles = (long long)ceil_div(M, kTiles[t].bm) * ceil_div(N, kTiles[t].bn);
+    for (int s = 1; s <= 16 && s * 4 <= nst + 3; s *= 2) {
+      const int per = ceil_div(nst, s), slices = ceil_div(nst, per);
+      const double rounds = (double)((tiles * slices + 255) / 256);
+      double us = rounds * (per * stage_us[t] + start_us);
+      if (slices > 1) us += 4.0 + 2.0 * slices * M * (double)N * 4 / 4e6;
+      if (us < best_us) {
+        best_us = us;
+        best = {t, slices};
+      }
+    }
+  }
+  return best;
+}
+
+size_t dense_part_bytes(const DensePlan& p, int M, int N) {
+  return p.slices > 1 ? (size_t)p.slices * M * N * sizeof(float) : 0;
+}
+
+hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const DensePlan& p, DenseArgs a, hipStream_t st) {
+  if (a.M <= 0 || a.N <= 0 || a.K <= 0 || p.tile < 0 || p.tile >= kNumTiles || p.slices < 1 ||
+      (p.slices > 1 && !a.part))
+    return hipErrorInvalidValue;
+  const TileCfg& t = kTiles[p.tile];
+  a.stages = stages_of(kind, a.K);
+  a.slice_stages = ceil_div(a.stages, p.slices);
+  if (ceil_div(a.stages, a.slice_stages) != p.slices) return hipErrorInvalidValue;
+  const bool split = p.slices > 1;
+  a.tm = ceil_div(a.M, t.bm);
+  // the gate epilogue pairs gate and up rows in a tile; its split product is a plain [M][2I]
+  const bool gate = epi == kEpiGate && !split;
+  a.tn = gate ? ceil_div(a.I, t.bn / 2) : ceil_div(a.N, t.bn);
+  if ((long long)a.tm * a.tn > 0x3fffff) return hipErrorInvalidValue;
+  hipError_t e;
+  const int first = split ? (int)kEpiPartial : epi;
+  if (kind == kDenseFp4) {
+    if (layout != kDenseNT || epi != kEpiStore) return hipErrorInvalidValue;
+    e = split ? run_tile<false, false, true, kEpiPartial>(p.tile, p.slices, a, st)
+              : run_tile<false, false, true, kEpiStore>(p.tile, p.slices, a, st);
+  } else if (first == kEpiGate) {
+    e = run_bf16<kEpiGate>(layout, p.tile, p.slices, a, st);
+  } else if (first == kEpiGrad) {
+    e = run_bf16<kEpiGrad>(layout, p.tile, p.slices, a, st);
+  } else if (first == kEpiPartial) {
+    e = run_bf16<kEpiPartial>(layout, p.tile, p.slices, a, st);
+  } else {
+    e = run_bf16<kEpiStore>(layout, p.tile, p.slices, a, st);
+  }
+  if (e != hipSuccess || !split) return e;
+  const int cols = epi == kEpiGate ? a.I : a.N;
+  const long long threads = (long long)a.M * ((cols + 3) / 4);
+  const unsigned nb = (unsigned)((threads + 255) / 256);
+  if (epi == kEpiGate) k_dense_reduce<kEpiGate><<<nb, 256, 0, st>>>(a, p.slices);
+  else if (epi == kEpiGrad) k_dense_reduce<kEpiGrad><<<nb, 256, 0, st>>>(a, p.slices);
+  else k_dense_reduce<kEpiStore><<<nb, 256, 0, st>>>(a, p.slices);
+  return hipGetLastError();
+}
+
+}  // namespace moe

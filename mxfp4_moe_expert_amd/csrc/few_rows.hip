@@ -1,0 +1,192 @@
+// Products of at most 64 rows with a weight matrix that is streamed once:
+// MXFP4 weights (moe_linear_mxfp4) and bf16 weights (the gated block).
+//
+// A block owns 16 weight rows (gate: 8 gate rows and the matching 8 up rows)
+// and its NW waves split K, wave w taking k-steps w, w + NW, ...: a block
+// reads NW consecutive pieces of each row at a time, all its loads in flight
+// at once for the usual K, and needs neither LDS staging (no wave shares
+// activations with another) nor a second launch: the waves' fp32 sums meet
+// in LDS and are added in wave order, so results do not depend on timing.
+//   MXFP4: a k-step is 128 values; lane (r, g) reads 16 bytes, exactly group
+//     g of row r. Activations in bf16: the codes are converted to bf16 (exact)
+//     for four MFMA 16x16x32. Activations rounded to MXFP4: lane (t, g) holds
+//     exactly one group of token t, encodes it, and the codes of both sides
+//     go to one scaled MFMA 16x16x128.
+//   bf16: a k-step is 64 values; lane (r, g) reads 32 bytes of row r.
+// Bound by the weight bytes; at one token by launch and load latency.
+#include "dense.h"
+
+namespace moe {
+
+// x [32 values of one group, as 4 x 8 bf16] -> E2M1 codes and exponent byte,
+// all in one lane (the encoding of mxfp4.hip).
+__device__ __forceinline__ u32x4_t lane_encode(const u32x4_t (&x)[4], uint32_t& byte) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max((x[i][j] << 16) & 0x7fff0000u, x[i][j] & 0x7fff0000u));
+  const uint32_t field = m >> 23;
+  const bool bad = field == 255u;
+  const uint32_t e = field > 2u ? field - 2u : 0u;
+  byte = bad ? 255u : e;
+  const float sc = e8m0_scale_operand(e);
+  u32x4_t c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t d = 0;
+    d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, __uint_as_float(x[i][0] << 16),
+                                                 __uint_as_float(x[i][0] & 0xffff0000u), sc, 0);
+    d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, __uint_as_float(x[i][1] << 16),
+                                                 __uint_as_float(x[i][1] & 0xffff0000u), sc, 1);
+    d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, __uint_as_float(x[i][2] << 16),
+                                                 __uint_as_float(x[i][2] & 0xffff0000u), sc, 2);
+    d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, __uint_as_float(x[i][3] << 16),
+                                                 __uint_as_float(x[i][3] & 0xffff0000u), sc, 3);
+    c[i] = bad ? 0u : d;
+  }
+  return c;
+}
+
+enum RowsFmt { kRowsBf16 = 0, kRowsMx = 1, kRowsMxA4 = 2 };
+
+template <int FMT, bool GATE, int CT, int NW>
+__global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
+  constexpr int STEP = FMT == kRowsBf16 ? 64 : 128;  // k values per step
+  constexpr int XV = STEP / 32;                    // 16-byte activation pieces per lane, token block and step
+  constexpr int WV = FMT == kRowsBf16 ? 2 : 1;       // 16-byte weight pieces per lane and step
+  constexpr int U = CT == 1 ? 4 : CT == 2 ? 2 : 1; // steps whose loads are in flight together
+  __shared__ __align__(16) float red[NW][CT * 256];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * (GATE ? 8 : 16);
+  int row;  // the lane's weight row (past the end: the last row again, never stored)
+  if constexpr (GATE) row = (r < 8 ? 0 : a.N) + n0 + (r & 7);  // N % 8 == 0
+  else row = min(n0 + r, a.N - 1);
+  const int S = (a.K + STEP - 1) / STEP;
+  const int kl = g * (STEP / 4);  // the lane's first k of a step
+  const uint8_t* wrow;
+  const uint8_t* srow = nullptr;
+  if constexpr (FMT == kRowsBf16) {
+    wrow = reinterpret_cast<const uint8_t*>(a.w + (size_t)row * a.K + kl);
+  } else {
+    wrow = a.codes + (size_t)row * (a.K / 2) + kl / 2;
+    srow = a.scales + (size_t)row * (a.K / 32) + g;
+  }
+  const uint16_t* xrow[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) xrow[c] = a.x + (size_t)min(16 * c + r, a.T - 1) * a.K + kl;
+
+  f32x4_t acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) acc[c] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
+
+  for (int s0 = wave; s0 < S; s0 += NW * U) {
+    u32x4_t w[U][WV], x[U][CT][XV];
+    uint32_t sc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u * NW, k = s * STEP + kl;
+#pragma unroll
+      for (int v = 0; v < WV; ++v) {
+        // a piece past K is zeros on both sides (K % 8 == 0; MXFP4: K % 32 == 0)
+        const bool in = k + v * 8 < a.K;
+        w[u][v] = in ? *reinterpret_cast<const u32x4_t*>(wrow + (size_t)s * (FMT == kRowsBf16 ? 128 : 64) + v * 16) : zero;
+      }
+      if constexpr (FMT != kRowsBf16) sc[u] = k < a.K ? srow[s * 4] : 0u;
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int v = 0; v < XV; ++v) {
+          const bool in = k + v * 8 < a.K;
+          x[u][c][v] = in ? *reinterpret_cast<const u32x4_t*>(xrow[c] + (size_t)s * STEP + v * 8) : zero;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (FMT == kRowsBf16) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int c = 0; c < CT; ++c) acc[c] = mfma_bf16(w[u][v], x[u][c][v], acc[c]);
+      } else if constexpr (FMT == kRowsMx) {
+        const float sv = e8m0_scale_operand(sc[u]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const u32x4_t wf = __builtin_bit_cast(u32x4_t, fp4x8_to_bf16x8(w[u][0][v], sv));
+#pragma unroll
+          for (int c = 0; c < CT; ++c) acc[c] = mfma_bf16(wf, x[u][c][v], acc[c]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          uint32_t sx;
+          const u32x4_t xc = lane_encode(x[u][c], sx);
+          acc[c] = mfma_mx4<0>(w[u][0], xc, acc[c], sc[u], sx);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c) *reinterpret_cast<f32x4_t*>(&red[wave][(c * 64 + lane) * 4]) = acc[c];
+  __syncthreads();
+  // value j: row 4 (lane / 16) + j % 4, token 16 c + lane % 16, where (c, lane) = j / 4
+  for (int j = tid; j < CT * 256; j += NW * 64) {
+    const int l = (j >> 2) & 63, t = (j >> 8) * 16 + (l & 15), n = 4 * (l >> 4) + (j & 3);
+    if (t >= a.T) continue;
+    if constexpr (GATE) {
+      if (n >= 8) continue;
+      float gv = 0.0f, uv = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        gv += red[w][j];
+        uv += red[w][j + 128];  // row n + 8
+      }
+      static_cast<uint16_t*>(a.out)[(size_t)t * a.N + n0 + n] = f32_to_bf16(ffn_act(gv, uv, a.limit));
+      if (a.gu_out) {
+        uint16_t* o = a.gu_out + (size_t)t * 2 * a.N + n0 + n;
+        o[0] = save_gate(gv, a.limit);
+        o[a.N] = save_up(uv, a.limit);
+      }
+    } else {
+      if (n0 + n >= a.N) continue;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v += red[w][j];
+      const size_t at = (size_t)t * a.N + n0 + n;
+      if (a.out_is_fp32) static_cast<float*>(a.out)[at] = v;
+      else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
+    }
+  }
+}
+
+// Waves per block: enough that the blocks of 16 rows give each of the 256 CUs
+// about 16 waves, and no more than there are k-steps.
+template <int FMT, bool GATE, int CT>
+static hipError_t go_waves(const FewRowsArgs& a, hipStream_t st) {
+  const int blocks = GATE ? a.N / 8 : (a.N + 15) / 16;
+  if (blocks <= 320) k_few_rows<FMT, GATE, CT, 16><<<blocks, 16 * 64, 0, st>>>(a);
+  else if (blocks <= 640) k_few_rows<FMT, GATE, CT, 8><<<blocks, 8 * 64, 0, st>>>(a);
+  else k_few_rows<FMT, GATE, CT, 4><<<blocks, 4 * 64, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int FMT, bool GATE>
+static hipError_t go_tokens(const FewRowsArgs& a, hipStream_t st) {
+  if (a.T <= 16) return go_waves<FMT, GATE, 1>(a, st);
+  if (a.T <= 32) return go_waves<FMT, GATE, 2>(a, st);
+  return go_waves<FMT, GATE, 4>(a, st);
+}
+
+hipError_t launch_few_rows_mxfp4(const FewRowsArgs& a, hipStream_t st) {
+  if (a.T <= 0 || a.T > kSmallT || a.N <= 0 || a.K <= 0 || a.K % 32) return hipErrorInvalidValue;
+  return a.act_mxfp4 ? go_tokens<kRowsMxA4, false>(a, st) : go_tokens<kRowsMx, false>(a, st);
+}
+
+hipError_t launch_few_rows_bf16(const FewRowsArgs& a, bool gate, hipStream_t st) {
+  if (a.T <= 0 || a.T > kSmallT || a.N <= 0 || a.K <= 0 || a.K % 8 || (gate && a.N % 8)) return hipErrorInvalidValue;
+  return gate ? go_tokens<kRowsBf16, true>(a, st) : go_tokens<kRowsBf16, false>(a, st);
+}
+
+}  // namespace moe

@@ -378,4 +378,72 @@ constexpr uint32_t kFlagTokenId = 1u, kFlagTableEntry = 2u, kFlagExpertId = 4u, 
                    kFlagPermutation = 16u;
 uint32_t* device_flags();
 
+// ---- dense products (dense.h, dense.hip, few_rows.hip): plain MXFP4 linears and the gated block
+
+struct DenseArgs {
+  const void* x;             // the row operand: [M][K], or [K][M] transposed
+  const void* w;             // the column operand: [N][K] ([2I][K] for the gate epilogue), or [K][N]
+  uint32_t x_ld, w_ld;       // bytes between stored rows
+  int M, N, K;               // K in values
+  int stages, slice_stages;  // K stages (128 bytes of a K-contiguous row each), stages per slice of a split K
+  int tm, tn;                // tiles along M and N
+  const uint16_t* x_scales;  // packed E8M0 bytes (MXFP4 operands), see mxfp4_pack_at
+  const uint16_t* w_scales;
+  int x_blocks, w_blocks;    // their 16-row blocks
+  void* out;                 // [M][N]; gate: h [M][I] bf16; grad: dgu [M][2I] bf16
+  int out_is_fp32;
+  int I;
+  float limit;
+  uint16_t* gu_out;          // gate: the rounded pre-activations [M][2I], or null
+  const uint16_t* gu_in;     // grad: the same
+  float* part;               // split K: fp32 partial sums [slices][M][N] (gate: N = 2I)
+};
+
+enum DenseKind { kDenseBf16 = 0, kDenseFp4 = 1 };
+enum DenseLayout { kDenseNT = 0, kDenseNN = 1, kDenseTN = 2 };  // X, W along k; W transposed; both transposed
+
+// How a product is cut: the tile configuration and the slices of K.
+struct DensePlan {
+  int tile;    // index of the tile configuration
+  int slices;  // 1: no split
+};
+DensePlan dense_plan(DenseKind kind, DenseLayout layout, int epi, int M, int N, int K);
+size_t dense_part_bytes(const DensePlan& p, int M, int N);  // partial sums of a split plan (0 if not split)
+// Fills stages, slices and tiles of `a` for the plan and launches it, with the
+// reduction of a split. a.part: dense_part_bytes(plan, M, N) bytes.
+hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const DensePlan& p, DenseArgs a, hipStream_t st);
+
+// MXFP4 encoding and decoding (mxfp4.hip)
+constexpr int kMxGroup = 32;
+enum { kDtBf16 = 0, kDtF32 = 1, kDtF16 = 2 };
+hipError_t launch_mxfp4_quantize(long long rows, int K, int dtype, const void* x, long long ldx, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t st);
+hipError_t launch_mxfp4_dequantize(long long rows, int K, const uint8_t* codes, const uint8_t* scales, int dtype,
+                                   void* out, hipStream_t st);
+inline int mxfp4_stages(int K) { return (K + 255) / 256; }
+inline int mxfp4_blocks(int rows) { return (rows + 15) / 16; }
+inline size_t mxfp4_pack_bytes(int rows, int K) { return (size_t)mxfp4_stages(K) * mxfp4_blocks(rows) * 128; }
+// x [T][K] bf16 -> codes [T][K/2] and packed scales; w scales [N][K/32] -> packed scales
+hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, uint16_t* xpack, int N,
+                             const uint8_t* wscales, uint16_t* wpack, hipStream_t st);
+// W codes -> bf16 [N][K]; dy [T][N] -> rows padded to ld values with zeros (dy may be null)
+hipError_t launch_mxfp4_expand(int N, int K, const uint8_t* codes, const uint8_t* scales, uint16_t* w, int T,
+                               const uint16_t* dy, uint16_t* dyp, int ld, hipStream_t st);
+
+// Up to kSmallT rows: K split over the waves of a block (few_rows.hip)
+struct FewRowsArgs {
+  int T, N, K;
+  const uint16_t* x;       // [T][K] bf16
+  const uint8_t* codes;    // MXFP4 weights [N][K/2], scales [N][K/32]
+  const uint8_t* scales;
+  const uint16_t* w;       // bf16 weights [N][K] (gate: [2I][K], N = I)
+  int act_mxfp4;           // round x to MXFP4 first
+  void* out;               // [T][N]
+  int out_is_fp32;
+  float limit;             // gate
+  uint16_t* gu_out;        // gate: [T][2N] or null
+};
+hipError_t launch_few_rows_mxfp4(const FewRowsArgs& a, hipStream_t st);
+hipError_t launch_few_rows_bf16(const FewRowsArgs& a, bool gate, hipStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,276 @@
+// MXFP4 encoding and decoding on gfx950 (page "deepseek-v4-mxfp4-int8
+// config.json", quantization_config, experts_w4a16; OCP Microscaling Formats
+// v1.0): per 32 consecutive values along K with largest magnitude m,
+//   X = max(floor(log2 m) - 2, -127), exponent byte X + 127,
+//   code = E2M1 value nearest to v / 2^X, ties to the even code, at most 6.
+// floor(log2 m) is the exponent field of m as fp32 (a subnormal m has field 0
+// and ends at X = -127 like every m below 2^-125), and v / 2^X is exact inside
+// the hardware's scaled conversion, so no rounding happens but the one to
+// E2M1. A group with an Inf or NaN gets the byte 255 (NaN), and reads back as
+// NaN; its codes are 0.
+//
+// Memory-bound in both directions. Four lanes share a group, eight values
+// each, so a wave reads 1 KB (bf16) or 2 KB (fp32) of consecutive values per
+// step and writes 256 consecutive code bytes; the group's maximum is two lane
+// exchanges within a quad.
+#include "device.h"
+#include "internal.h"
+
+namespace moe {
+
+typedef __attribute__((ext_vector_type(8))) float f32x8_t;
+
+template <int DT>
+__device__ __forceinline__ f32x8_t load8(const void* p, size_t at) {
+  f32x8_t v;
+  if constexpr (DT == kDtF32) {
+    const f32x4_t* s = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + at);
+    const f32x4_t a = s[0], b = s[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  } else {
+    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == kDtBf16) {
+        v[2 * i] = __uint_as_float(a[i] << 16);
+        v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+      } else {
+        v[2 * i] = f16_bits_to_f32(a[i] & 0xffffu);
+        v[2 * i + 1] = f16_bits_to_f32(a[i] >> 16);
+      }
+    }
+  }
+  return v;
+}
+
+// The quad's four lanes hold one group, eight values each -> the lane's codes
+// (one dword) and the group's exponent byte.
+__device__ __forceinline__ uint32_t quad_encode(const f32x8_t& v, uint32_t& byte) {
+  // magnitudes compare as integers, Inf and NaN above every finite value
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));  // quad_perm [1,0,3,2]
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));  // quad_perm [2,3,0,1]
+  const uint32_t field = m >> 23;
+  const bool bad = field == 255u;
+  const uint32_t e = field > 2u ? field - 2u : 0u;
+  byte = bad ? 255u : e;
+  const float sc = e8m0_scale_operand(e);
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], sc, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], sc, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], sc, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], sc, 3);
+  return bad ? 0u : c;
+}
+
+// Units of 8 values; a thread takes kQuantUnits of them, 256 apart, and has
+// all their loads in flight together.
+constexpr int kQuantUnits = 4;
+constexpr long long kMaxBlocks = 0xffffff;  // of 256 threads: a grid holds fewer than 2^32 threads
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_mxfp4_quantize(const void* x, long long units, int upr, long long ldx,
+                                                        uint32_t* codes, uint8_t* scales) {
+  const long long u0 = (long long)blockIdx.x * (256 * kQuantUnits) + threadIdx.x;
+  f32x8_t v[kQuantUnits];
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const long long u = u0 + i * 256;
+    if (u >= units) continue;  // units % 4 == 0: a quad is live or not as one
+    size_t at = (size_t)u * 8;
+    if (ldx != (long long)upr * 8) {
+      const long long row = u / upr;
+      at = (size_t)row * ldx + (size_t)(u - row * upr) * 8;
+    }
+    v[i] = load8<DT>(x, at);
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const long long u = u0 + i * 256;
+    if (u >= units) continue;
+    uint32_t byte;
+    codes[u] = quad_encode(v[i], byte);
+    if ((u & 3) == 0) scales[u >> 2] = (uint8_t)byte;
+  }
+}
+
+hipError_t launch_mxfp4_quantize(long long rows, int K, int dtype, const void* x, long long ldx, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t st) {
+  const int upr = K / 8;
+  const long long units = rows * upr;
+  if (K % kMxGroup || ldx < K) return hipErrorInvalidValue;
+  if (units <= 0) return hipSuccess;
+  const long long nb = (units + 256 * kQuantUnits - 1) / (256 * kQuantUnits);
+  if (nb > kMaxBlocks) return hipErrorInvalidValue;
+  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+  if (dtype == kDtBf16) k_mxfp4_quantize<kDtBf16><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, c, scales);
+  else if (dtype == kDtF32) k_mxfp4_quantize<kDtF32><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, c, scales);
+  else if (dtype == kDtF16) k_mxfp4_quantize<kDtF16><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, c, scales);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+// Decoding: a unit is 8 codes (one dword) and its group's byte. Byte 255
+// makes the hardware conversion return NaN.
+template <int DT>
+__device__ __forceinline__ void decode_unit(uint32_t c, uint32_t byte, void* out, size_t at) {
+  const float sc = e8m0_scale_operand(byte);
+  const bf16x8_t v = fp4x8_to_bf16x8(c, sc);
+  if constexpr (DT == kDtBf16) {
+    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + at) = __builtin_bit_cast(u32x4_t, v);
+  } else {
+    const u32x4_t b = __builtin_bit_cast(u32x4_t, v);
+    f32x4_t lo, hi;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lo[2 * i] = __uint_as_float(b[i] << 16);
+      lo[2 * i + 1] = __uint_as_float(b[i] & 0xffff0000u);
+      hi[2 * i] = __uint_as_float(b[2 + i] << 16);
+      hi[2 * i + 1] = __uint_as_float(b[2 + i] & 0xffff0000u);
+    }
+    f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + at);
+    o[0] = lo;
+    o[1] = hi;
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales,
+                                                          long long units, void* out) {
+  const long long u0 = (long long)blockIdx.x * (256 * kQuantUnits) + threadIdx.x;
+  uint32_t c[kQuantUnits], b[kQuantUnits];
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const long long u = min(u0 + i * 256, units - 1);
+    c[i] = codes[u];
+    b[i] = scales[u >> 2];
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const long long u = u0 + i * 256;
+    if (u < units) decode_unit<DT>(c[i], b[i], out, (size_t)u * 8);
+  }
+}
+
+hipError_t launch_mxfp4_dequantize(long long rows, int K, const uint8_t* codes, const uint8_t* scales, int dtype,
+                                   void* out, hipStream_t st) {
+  const long long units = rows * (K / 8);
+  if (K % kMxGroup) return hipErrorInvalidValue;
+  if (units <= 0) return hipSuccess;
+  const long long nb = (units + 256 * kQuantUnits - 1) / (256 * kQuantUnits);
+  if (nb > kMaxBlocks) return hipErrorInvalidValue;
+  const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
+  if (dtype == kDtBf16) k_mxfp4_dequantize<kDtBf16><<<(unsigned)nb, 256, 0, st>>>(c, scales, units, out);
+  else if (dtype == kDtF32) k_mxfp4_dequantize<kDtF32><<<(unsigned)nb, 256, 0, st>>>(c, scales, units, out);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+// ---- operands of the 4-bit x 4-bit product
+//
+// Packed scales: the product's MFMA k-step kk (128 values) of stage s (256
+// values) takes, in lane (r, g), the exponent byte of row 16 b + r, group
+// 8 s + 4 kk + g. Packed as u16 [s][b][16 g + r], byte kk: a stage's scales of
+// consecutive row blocks are contiguous and lane-ordered. Groups past K get
+// the byte 0 (their codes are zeros, and 2^-127 keeps the products zero).
+__device__ __forceinline__ size_t mxfp4_pack_at(int row, int group, int blocks) {
+  return (((size_t)(group >> 3) * blocks + (row >> 4)) * 64 + (group & 3) * 16 + (row & 15)) * 2 + ((group >> 2) & 1);
+}
+
+// Blocks [0, xblocks): x [T][K] bf16 to codes and packed scales, a unit of 8
+// values per thread, with the unit index running over whole stages of 256 (so
+// that the groups past K of the last stage are written too). Blocks from
+// xblocks on: the weights' exponent bytes to the packed order.
+__global__ __launch_bounds__(256) void k_mxfp4_prep(int T, int K, const uint16_t* x, uint32_t* xcodes, uint8_t* xpack,
+                                                    unsigned xblocks, int N, const uint8_t* wscales, uint8_t* wpack) {
+  const int stages = (K + 255) / 256;
+  if (blockIdx.x < xblocks) {
+    const int ups = stages * 32;  // units per row, padded
+    const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int row = (int)(u / ups), i = (int)(u - (long long)row * ups);
+    if (row >= T) return;  // ups % 4 == 0: whole quads leave
+    uint32_t byte = 0;
+    if (i * 8 < K) {  // K % 32 == 0: a quad is in or out as one
+      const f32x8_t v = load8<kDtBf16>(x, (size_t)row * K + (size_t)i * 8);
+      xcodes[(size_t)row * (K / 8) + i] = quad_encode(v, byte);
+    }
+    if ((i & 3) == 0) xpack[mxfp4_pack_at(row, i >> 2, (T + 15) / 16)] = (uint8_t)byte;
+  } else {
+    // a thread packs one (row, stage): 8 bytes
+    const long long u = (long long)(blockIdx.x - xblocks) * 256 + threadIdx.x;
+    const int row = (int)(u / stages), s = (int)(u - (long long)row * stages);
+    if (row >= N) return;
+    const int G = K / kMxGroup;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int g0 = 8 * s + q, g1 = g0 + 4;
+      const uint32_t b0 = g0 < G ? wscales[(size_t)row * G + g0] : 0u, b1 = g1 < G ? wscales[(size_t)row * G + g1] : 0u;
+      *reinterpret_cast<uint16_t*>(wpack + mxfp4_pack_at(row, g0, (N + 15) / 16)) = (uint16_t)(b0 | (b1 << 8));
+    }
+  }
+}
+
+hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, uint16_t* xpack, int N,
+                             const uint8_t* wscales, uint16_t* wpack, hipStream_t st) {
+  if (K % kMxGroup || T <= 0 || N <= 0) return hipErrorInvalidValue;
+  const long long stages = mxfp4_stages(K);
+  const long long xb = ((long long)T * stages * 32 + 255) / 256, wb = ((long long)N * stages + 255) / 256;
+  if (xb + wb > kMaxBlocks) return hipErrorInvalidValue;
+  k_mxfp4_prep<<<(unsigned)(xb + wb), 256, 0, st>>>(T, K, x, reinterpret_cast<uint32_t*>(xcodes),
+                                                    reinterpret_cast<uint8_t*>(xpack), (unsigned)xb, N, wscales,
+                                                    reinterpret_cast<uint8_t*>(wpack));
+  return hipGetLastError();
+}
+
+// Weights to bf16 [N][K] for the bf16 product of many rows, and (blocks from
+// wblocks on) dy [T][N] to rows of ld values, zero-padded, where N is not a
+// multiple of 8 (the product reads 16-byte pieces of each row).
+__global__ __launch_bounds__(256) void k_mxfp4_expand(const uint32_t* codes, const uint8_t* scales, long long units,
+                                                      uint16_t* w, unsigned wblocks, int T, int N, const uint16_t* dy,
+                                                      uint16_t* dyp, int ld) {
+  if (blockIdx.x < wblocks) {
+    const long long u0 = (long long)blockIdx.x * (256 * kQuantUnits) + threadIdx.x;
+    uint32_t c[kQuantUnits], b[kQuantUnits];
+#pragma unroll
+    for (int i = 0; i < kQuantUnits; ++i) {
+      const long long u = min(u0 + i * 256, units - 1);
+      c[i] = codes[u];
+      b[i] = scales[u >> 2];
+    }
+#pragma unroll
+    for (int i = 0; i < kQuantUnits; ++i) {
+      const long long u = u0 + i * 256;
+      if (u < units) decode_unit<kDtBf16>(c[i], b[i], w, (size_t)u * 8);
+    }
+  } else {
+    const long long i = (long long)(blockIdx.x - wblocks) * 256 + threadIdx.x;  // 8 values of a padded row
+    const long long row = i / (ld / 8);
+    const int col = (int)(i - row * (ld / 8)) * 8;
+    if (row >= T) return;
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = col + j < N ? dy[row * N + col + j] : 0u;
+    *reinterpret_cast<u32x4_t*>(dyp + i * 8) =
+        (u32x4_t){v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
+  }
+}
+
+hipError_t launch_mxfp4_expand(int N, int K, const uint8_t* codes, const uint8_t* scales, uint16_t* w, int T,
+                               const uint16_t* dy, uint16_t* dyp, int ld, hipStream_t st) {
+  if (K % kMxGroup || N <= 0) return hipErrorInvalidValue;
+  const long long units = (long long)N * (K / 8);
+  const long long wb = (units + 256 * kQuantUnits - 1) / (256 * kQuantUnits);
+  const long long db = dy ? ((long long)T * (ld / 8) + 255) / 256 : 0;
+  if (ld % 8 || wb + db > kMaxBlocks) return hipErrorInvalidValue;
+  k_mxfp4_expand<<<(unsigned)(wb + db), 256, 0, st>>>(reinterpret_cast<const uint32_t*>(codes), scales, units, w,
+                                                      (unsigned)wb, T, N, dy, dyp, ld);
+  return hipGetLastError();
+}
+
+}  // namespace moe
