@@ -219,8 +219,8 @@ int moe_linear_mxfp4(int32_t T, int32_t K, int32_t N, const uint16_t* x, const u
   float* part = at<float>(workspace, L.part);
   if (act == MOE_ACT_MXFP4) {
     uint8_t* xc = at<uint8_t>(workspace, L.codes);
-    uint16_t* xp = at<uint16_t>(workspace, L.xpack);
-    uint16_t* wp = at<uint16_t>(workspace, L.wpack);
+    uint32_t* xp = at<uint32_t>(workspace, L.xpack);
+    uint32_t* wp = at<uint32_t>(workspace, L.wpack);
     const hipError_t e = launch_mxfp4_prep(T, K, x, xc, xp, N, scales, wp, st);
     if (e != hipSuccess) return status(e);
     DenseArgs a = dense_args(xc, (size_t)K / 4, codes, (size_t)K / 4, T, N, K, out, out_is_fp32, part);

@@ -4,22 +4,32 @@
 // with each operand stored either along k ([row][k], "K-contiguous") or
 // across it ([k][row], "transposed"), in bf16 or (both K-contiguous) MXFP4.
 //
-// Tile BM x BN, one block of WGM x WGN waves. K runs in stages of 128 bytes
-// per row (64 bf16 or 256 E2M1 values), NBUF stages in LDS:
+// Tile BM x BN, one block of WGM x WGN waves. K runs in stages of two MFMA
+// k-steps (128 bytes per row: 64 bf16 or 256 E2M1 values); LDS holds NX stages
+// of the X tile and NW of the W tile:
 //   - Operands go from global memory straight to LDS (16 bytes per lane, the
-//     64 lanes of a wave filling 1 KB), NBUF - 1 stages ahead; a stage costs
-//     one barrier. The loads are raw buffer loads whose out-of-range lanes
-//     (rows, columns or k past the end) write zeros, so no tail needs code
-//     in the K loop.
-//   - The 16-byte pieces of a K-contiguous row are stored rotated (piece c of
-//     row i at position c ^ (i / 2) % 8), so the 16 rows of an MFMA operand
-//     lie in different banks. A transposed operand keeps its k rows; its
-//     32-byte units are stored at unit ^ f(k), and the LDS transposing read
-//     (16 lanes x 4 elements) hands each lane 4 consecutive k of its row.
+//     64 lanes of a wave filling 1 KB), whole 128-byte lines at a time (half
+//     lines cost as much L2 bandwidth as whole ones). The loads are raw
+//     buffer loads whose out-of-range lanes (rows, columns or k past the end)
+//     write zeros, so no tail needs code in the K loop.
+//   - The MFMAs of a k-step run on operands already in registers, with the
+//     LDS reads of the next k-step's operands and a share of a later stage's
+//     loads spread between them: a burst of either stalls the waves (the
+//     loads of a CU share one 64 B/clock path), and MFMAs behind a stalled
+//     instruction do not issue. X is loaded in the first k-step and W in the
+//     second; one barrier per stage, between them.
+//   - The eight 16-byte pieces of a K-contiguous row i are stored at piece ^
+//     (i / 2) % 8, so the 16 rows of an MFMA operand lie in different banks
+//     (no conflicts counted in any product). A transposed operand keeps its
+//     k rows; its 32-byte units are stored at unit ^ f(k), and the LDS
+//     transposing read (16 lanes x 4 elements) hands each lane 4 consecutive
+//     k of its row.
 //   - MFMA 16x16x32 (bf16) or 16x16x128 with E8M0 scales (MXFP4), W as the A
 //     operand: lane (r, g) ends with 4 consecutive n of one m, one 8-byte
 //     bf16 store.
 #pragma once
+
+#include <type_traits>
 
 #include "device.h"
 #include "internal.h"
@@ -31,12 +41,13 @@ typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
-typedef __attribute__((address_space(3))) uint16_t lds_u16;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
 
 constexpr uint32_t kLaneOff = 0x80000000u;  // a lane offset past every buffer: reads zero
 constexpr int kStageB = 128;                // K bytes per row and stage
+constexpr int kStageK = 64;                 // k rows of a transposed operand per stage
 
-// 16 (or 4) bytes per lane from buffer offset voff to LDS byte m0 + lane * 16 (4).
+// 16 bytes per lane from buffer offset voff to LDS byte m0 + lane * 16.
 // No output registers: the data is waited for with dense_wait before a barrier.
 // (m0 is a reserved register: the compiler sets it right before each use of its own.)
 __device__ __forceinline__ void load_lds16(u32x4_t rsrc, uint32_t voff, uint32_t lds_at) {
@@ -45,13 +56,6 @@ __device__ __forceinline__ void load_lds16(u32x4_t rsrc, uint32_t voff, uint32_t
                : "s"(__builtin_amdgcn_readfirstlane((int)lds_at)), "v"(voff), "s"(rsrc)
                : "memory");
 }
-__device__ __forceinline__ void load_lds4(u32x4_t rsrc, uint32_t voff, uint32_t lds_at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :
-               : "s"(__builtin_amdgcn_readfirstlane((int)lds_at)), "v"(voff), "s"(rsrc)
-               : "memory");
-}
-
 // At most N of the wave's vector loads outstanding, and its LDS reads done.
 template <int N>
 __device__ __forceinline__ void dense_wait() {
@@ -72,10 +76,11 @@ template <bool TR, int ROWS, int W>
 struct Stager {
   static constexpr int NI = ROWS * kStageB / 1024 / W;  // 1 KB loads per wave and stage
   static constexpr int PPR = TR ? ROWS / 8 : 8;         // 16-byte pieces per stored row
+  static_assert(W % 4 == 0 && (W * 64) % PPR == 0, "loads of a wave share their k offsets");
   uint32_t voff[NI];
 
   static __device__ __forceinline__ int slot(int i, int wave, int lane) { return (i * W + wave) * 64 + lane; }
-  // the k position (16-byte piece of the row's 128 bytes, or k row) of slot s, and its piece
+  // the 16-byte piece that slot s holds of its stored row (row of the tile, or k row)
   static __device__ __forceinline__ int piece(int s) {
     const int row = s / PPR, pos = s % PPR;
     if constexpr (TR) {
@@ -103,20 +108,15 @@ struct Stager {
       voff[i] = piece(s) * 8 < cols ? (uint32_t)(s / PPR) * ld + (uint32_t)piece(s) * 16 : kLaneOff;
     }
   }
-  // kleft: bytes (K-contiguous) or k rows (transposed) from the stage's start to the end of k
-  __device__ __forceinline__ void load(u32x4_t rsrc, uint32_t lds_at, int wave, int lane, int kleft) const {
-    constexpr int FULL = TR ? 64 : kStageB;
-    if (kleft >= FULL) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) load_lds16(rsrc, voff[i], lds_at + (uint32_t)((i * W + wave) * 1024));
-    } else {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int s = slot(i, wave, lane);
-        const int at = TR ? s / PPR : piece(s) * 16;
-        load_lds16(rsrc, at < kleft ? voff[i] : kLaneOff, lds_at + (uint32_t)((i * W + wave) * 1024));
-      }
-    }
+  // Load i of a stage. kleft: bytes (K-contiguous) or k rows (transposed) from the stage's start to the end of k;
+  // lanes past it read zeros. `at` is the lane's first k of load 0: the others differ by a constant.
+  __device__ __forceinline__ void load(int i, u32x4_t rsrc, uint32_t lds_at, int wave, int at, int kleft) const {
+    const int step = TR ? W * 64 / PPR : 0;  // K-contiguous: the piece is the same in every load (W % 4 == 0)
+    load_lds16(rsrc, at < kleft - i * step ? voff[i] : kLaneOff, lds_at + (uint32_t)((i * W + wave) * 1024));
+  }
+  static __device__ __forceinline__ int first_k(int wave, int lane) {
+    const int s = slot(0, wave, lane);
+    return TR ? s / PPR : piece(s) * 16;
   }
 };
 
@@ -248,20 +248,26 @@ __device__ __forceinline__ void dense_tile(int bid, int tm, int tn, int& im, int
 }
 
 // FP4: both operands MXFP4 K-contiguous, with packed scales (see mxfp4.hip).
-template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NBUF, bool FP4, int EPI>
+template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, bool FP4, int EPI>
 __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
   constexpr int W = WGM * WGN;
   constexpr int MB = BM / WGM / 16, NB = BN / WGN / 16;  // 16-row blocks per wave
   constexpr int XB = BM * kStageB, WB = BN * kStageB;    // bytes per stage
-  constexpr int SXB = FP4 ? BM * 8 : 0, SWB = FP4 ? BN * 8 : 0;
-  constexpr int SI = (SXB + SWB + 256 * W - 1) / (256 * W);  // scale loads per wave and stage (the last may be idle)
-  constexpr int STAGE = XB + WB + SI * 256 * W;
+  constexpr int SXB = FP4 ? BM * 16 : 0, SWB = FP4 ? BN * 16 : 0;  // scales of two stages
+  constexpr int SI = (SXB + SWB + 1024 * W - 1) / (1024 * W);      // their loads per wave
+  constexpr uint32_t WBASE = NX * XB, SCALES = WBASE + NW * WB, SCB = SI * 1024 * W;  // LDS: X, W, scales
+  // scales are loaded SD pairs of stages ahead, so that the waits below cover them, into NS sets
+  constexpr int SD = NW <= 2 ? 1 : (NW + 1) / 2 - (NW & 1), NS = SD + 1;
+  static_assert(2 * SD - 1 >= NW - 2, "a stage's scales land with it");
   static_assert(!FP4 || (!XT && !WT), "MXFP4 operands are K-contiguous");
+  static_assert(NW >= 2 && (NX == NW || NX == NW + 1), "the waits below assume it");
+  // X is loaded in the first k-step; with two stages of both, a load there would be waited for in the same stage, and
+  // both operands are loaded in the second
+  constexpr bool XK0 = NX > NW || NW > 2;
   using SX = Stager<XT, BM, W>;
   using SW = Stager<WT, BN, W>;
-  constexpr int LPS = SX::NI + SW::NI + SI;
   static_assert(SX::NI * 1024 * W == XB && SW::NI * 1024 * W == WB, "tiles split evenly over the waves");
-  extern __shared__ __align__(16) unsigned char smem[];  // NBUF stages: X tile, W tile, scales
+  extern __shared__ __align__(16) unsigned char smem[];
   lds_u8* const lds = (lds_u8*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
@@ -298,30 +304,42 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
     sw.init_kc(wave, lane, a.w_ld, [&](int i) { return n0 + i < a.N ? i : -1; });
     wbase += (size_t)n0 * a.w_ld;
   }
-  const size_t xstep = XT ? (size_t)64 * a.x_ld : kStageB, wstep = WT ? (size_t)64 * a.w_ld : kStageB;
+  const size_t xstep = XT ? (size_t)kStageK * a.x_ld : kStageB, wstep = WT ? (size_t)kStageK * a.w_ld : kStageB;
   const int kx = XT ? a.K : Kb, kw = WT ? a.K : Kb;
-  constexpr int xk = XT ? 64 : kStageB, wk = WT ? 64 : kStageB;
+  constexpr int xk = XT ? kStageK : kStageB, wk = WT ? kStageK : kStageB;
 
-  auto load_stage = [&](int i, int buf) {  // stage st0 + i
-    const int st = st0 + i;
+  const int xat = SX::first_k(wave, lane), wat = SW::first_k(wave, lane);
+
+  // The loads of stage st0 + i of one operand into its buffer buf, one at a time (op 0 .. NI - 1); past the slice: zeros
+  struct Source {
+    u32x4_t rsrc;
+    int kleft;
+    uint32_t at;
+  };
+  auto x_source = [&](int i, int buf) {
+    const int st = i < nst ? st0 + i : 0;
+    return Source{buffer_of(xbase + (size_t)st * xstep), i < nst ? kx - st * xk : 0, lds0 + (uint32_t)buf * XB};
+  };
+  auto w_source = [&](int i, int buf) {
+    const int st = i < nst ? st0 + i : 0;
+    return Source{buffer_of(wbase + (size_t)st * wstep), i < nst ? kw - st * wk : 0,
+                  lds0 + WBASE + (uint32_t)buf * WB};
+  };
+  auto load_scales = [&](int i) {  // of stages i and i + 1, i even
+    // packed: [two stages][16-row block][lane] u32; the tile's blocks are contiguous
     const bool live = i < nst;
-    const uint32_t at = lds0 + (uint32_t)buf * STAGE;
-    const size_t sg = live ? (size_t)st : 0;
-    sx.load(buffer_of(xbase + sg * xstep), at, wave, lane, live ? kx - st * xk : 0);
-    sw.load(buffer_of(wbase + sg * wstep), at + XB, wave, lane, live ? kw - st * wk : 0);
-    if constexpr (FP4) {
-      // packed scales: [stage][16-row block][lane] u16; the tile's blocks of a stage are contiguous
-      const u32x4_t rx = buffer_of(a.x_scales + (sg * a.x_blocks + (size_t)im * (BM / 16)) * 64);
-      const u32x4_t rw = buffer_of(a.w_scales + (sg * a.w_blocks + (size_t)in * (BN / 16)) * 64);
-      const uint32_t endx = (uint32_t)(a.x_blocks - im * (BM / 16)) * 128;
-      const uint32_t endw = min((uint32_t)(a.w_blocks - in * (BN / 16)) * 128, (uint32_t)SWB);
+    const size_t pr = live ? (size_t)((st0 + i) >> 1) : 0;
+    const u32x4_t rx = buffer_of(a.x_scales + (pr * a.x_blocks + (size_t)im * (BM / 16)) * 64);
+    const u32x4_t rw = buffer_of(a.w_scales + (pr * a.w_blocks + (size_t)in * (BN / 16)) * 64);
+    const uint32_t endx = (uint32_t)(a.x_blocks - im * (BM / 16)) * 256;
+    const uint32_t endw = min((uint32_t)(a.w_blocks - in * (BN / 16)) * 256, (uint32_t)SWB);
 #pragma unroll
-      for (int j = 0; j < SI; ++j) {
-        const uint32_t o = (uint32_t)(j * W + wave) * 256;  // byte of the stage's scale area
-        const bool isw = o >= SXB;
-        const uint32_t off = (isw ? o - SXB : o) + (uint32_t)lane * 4;
-        load_lds4(isw ? rw : rx, live && off < (isw ? endw : endx) ? off : kLaneOff, at + XB + WB + o);
-      }
+    for (int j = 0; j < SI; ++j) {
+      const uint32_t o = (uint32_t)(j * W + wave) * 1024;  // byte of the set
+      const bool isw = o >= SXB;
+      const uint32_t off = (isw ? o - SXB : o) + (uint32_t)lane * 16;
+      load_lds16(isw ? rw : rx, live && off < (isw ? endw : endx) ? off : kLaneOff,
+                 lds0 + SCALES + (uint32_t)((i >> 1) % NS) * SCB + o);
     }
   };
 
@@ -337,44 +355,106 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
 #pragma unroll
     for (int c = 0; c < MB; ++c) acc[b][c] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 
+  // Registers: the W operands of this k-step and the next; of the X operands the first half once (xr[c] is read again,
+  // for the next k-step, after its last MFMA of this one) and the second half twice, so that every read of a k-step is
+  // issued by the middle of the one before.
+  constexpr int XR = MB / 2;
+  u32x4_t xr[XR], xd[2][MB - XR], wf[2][NB];
+  uint32_t sxv[MB], swv[NB];  // MXFP4: the lane's scale bytes of two stages, one per k-step
+  auto read_scales = [&](int i) {
+    const lds_u8* sc = lds + SCALES + (uint32_t)((i >> 1) % NS) * SCB;
 #pragma unroll
-  for (int i = 0; i < NBUF - 1; ++i) load_stage(i, i);
-  int buf = 0;
-  for (int i = 0; i < nst; ++i) {
-    dense_wait<(NBUF - 2) * LPS>();  // stage i has landed (this wave's part) ...
-    __builtin_amdgcn_s_barrier();    // ... and every wave's; the buffer of stage i - 1 is free
+    for (int c = 0; c < MB; ++c) sxv[c] = *(const lds_u32*)(sc + ((wm * MB + c) * 64 + lane) * 4);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) swv[b] = *(const lds_u32*)(sc + SXB + ((wn * NB + b) * 64 + lane) * 4);
+  };
+  // The MFMAs of k-step kk (parity q of its stage), reading the next k-step's operands from the tiles xt and wt and
+  // issuing the loads load(0) .. load(nload - 1). The order is pinned, or the compiler gathers the memory operations.
+  auto step = [&](auto kk, auto q, const lds_u8* xt, const lds_u8* wt, auto nload, auto&& load) {
+    constexpr int NM = MB * NB, NR = NB + MB - XR;
+    int loads = 0, reads = 0;
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const int c = m / NB, b = m % NB;
+      const u32x4_t& x = c < XR ? xr[c < XR ? c : 0] : xd[kk][c < XR ? 0 : c - XR];
+      if constexpr (FP4) acc[b][c] = mfma_mx4<kk + 2 * q>(wf[kk][b], x, acc[b][c], swv[b], sxv[c]);
+      else acc[b][c] = mfma_bf16(wf[kk][b], x, acc[b][c]);
+      __builtin_amdgcn_sched_barrier(0);
+      while (loads < nload && loads * NM <= m * nload) load(loads++);
+      while (reads < NR && reads * NM <= m * 2 * NR) {
+        if (reads < NB) wf[1 - kk][reads] = rw.read(wt, reads, 1 - kk);
+        else xd[1 - kk][reads - NB] = rx.read(xt, reads - NB + XR, 1 - kk);
+        ++reads;
+      }
+      if (b == NB - 1 && c < XR) xr[c < XR ? c : 0] = rx.read(xt, c, 1 - kk);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using K0 = std::integral_constant<int, 0>;
+  using K1 = std::integral_constant<int, 1>;
+
+  // Loads in order X(0) W(0) X(1) W(1) ..., as the loop continues it
+  if constexpr (FP4) {
+#pragma unroll
+    for (int d = 0; d < SD; ++d) load_scales(2 * d);
+  }
+#pragma unroll
+  for (int i = 0; i < (NX > NW ? NX : NW); ++i) {
+    if (i < (XK0 ? NX - 1 : NX)) {
+      const Source s = x_source(i, i);
+#pragma unroll
+      for (int op = 0; op < SX::NI; ++op) sx.load(op, s.rsrc, s.at, wave, xat, s.kleft);
+    }
+    if (i < NW) {
+      const Source s = w_source(i, i);
+#pragma unroll
+      for (int op = 0; op < SW::NI; ++op) sw.load(op, s.rsrc, s.at, wave, wat, s.kleft);
+    }
+  }
+  dense_wait<(XK0 ? NX - 2 : NX - 1) * SX::NI + (NW - 1) * SW::NI>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int b = 0; b < NB; ++b) wf[0][b] = rw.read(lds + WBASE, b, 0);
+#pragma unroll
+  for (int c = 0; c < MB; ++c) (c < XR ? xr[c] : xd[0][c - XR]) = rx.read(lds, c, 0);
+  int bx = 0, bw = 0;  // buffers of stage i
+  auto stage = [&](int i, auto q) {
+    if constexpr (FP4 && q == 0) read_scales(i);
+    const int nx = bx + 1 == NX ? 0 : bx + 1, nw = bw + 1 == NW ? 0 : bw + 1;
+    if constexpr (XK0) {
+      const Source s = x_source(i - 1 + NX, bx == 0 ? NX - 1 : bx - 1);  // where stage i - 1 was
+      step(K0{}, q, lds + bx * XB, lds + WBASE + bw * WB, std::integral_constant<int, SX::NI>{},
+           [&](int op) { sx.load(op, s.rsrc, s.at, wave, xat, s.kleft); });
+    } else {
+      step(K0{}, q, lds + bx * XB, lds + WBASE + bw * WB, K0{}, [](int) {});
+    }
+    // stage i + 1 has landed (this wave's part) and this wave has read stage i, then every wave
+    dense_wait<(NW - 2) * (SX::NI + SW::NI) + (NX > NW ? SX::NI : 0)>();
+    __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    load_stage(i + NBUF - 1, buf == 0 ? NBUF - 1 : buf - 1);
-    const lds_u8* xt = lds + buf * STAGE;
-    const lds_u8* wt = xt + XB;
-    uint32_t sxv[MB], swv[NB];
-    if constexpr (FP4) {
-      const lds_u8* sc = xt + XB + WB;
-#pragma unroll
-      for (int c = 0; c < MB; ++c) sxv[c] = *(const lds_u16*)(sc + ((wm * MB + c) * 64 + lane) * 2);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) swv[b] = *(const lds_u16*)(sc + SXB + ((wn * NB + b) * 64 + lane) * 2);
+    if constexpr (FP4 && q == 0) load_scales(i + 2 * SD);
+    const Source s = w_source(i + NW, bw);
+    if constexpr (XK0) {
+      step(K1{}, q, lds + nx * XB, lds + WBASE + nw * WB, std::integral_constant<int, SW::NI>{},
+           [&](int op) { sw.load(op, s.rsrc, s.at, wave, wat, s.kleft); });
+    } else {
+      const Source t = x_source(i + NX, bx);
+      step(K1{}, q, lds + nx * XB, lds + WBASE + nw * WB, std::integral_constant<int, SX::NI + SW::NI>{}, [&](int op) {
+        if (op < SX::NI) sx.load(op, t.rsrc, t.at, wave, xat, t.kleft);
+        else sw.load(op - SX::NI, s.rsrc, s.at, wave, wat, s.kleft);
+      });
     }
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4_t xf[MB], wf[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) wf[b] = rw.read(wt, b, kk);
-#pragma unroll
-      for (int c = 0; c < MB; ++c) xf[c] = rx.read(xt, c, kk);
-#pragma unroll
-      for (int c = 0; c < MB; ++c)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          if constexpr (FP4) {
-            if (kk == 0) acc[b][c] = mfma_mx4<0>(wf[b], xf[c], acc[b][c], swv[b], sxv[c]);
-            else acc[b][c] = mfma_mx4<1>(wf[b], xf[c], acc[b][c], swv[b], sxv[c]);
-          } else {
-            acc[b][c] = mfma_bf16(wf[b], xf[c], acc[b][c]);
-          }
-        }
+    bx = nx;
+    bw = nw;
+  };
+  if constexpr (FP4) {
+    for (int i = 0; i < nst; i += 2) {
+      stage(i, K0{});
+      if (i + 1 < nst) stage(i + 1, K1{});
     }
-    buf = buf + 1 == NBUF ? 0 : buf + 1;
+  } else {
+    for (int i = 0; i < nst; ++i) stage(i, K0{});
   }
   dense_wait<0>();  // nothing may still write this block's LDS when it ends
 

@@ -7,15 +7,18 @@ namespace moe {
 namespace {
 
 struct TileCfg {
-  int bm, bn, waves, nbuf;
+  int bm, bn, waves, nx, nw;  // nx, nw: stages of X and W in LDS
 };
-// 0: large products; 1: fewer tiles than CUs at 256 x 256; 2: few rows
-constexpr TileCfg kTiles[] = {{256, 256, 8, 2}, {128, 128, 4, 4}, {64, 128, 4, 5}};
+// 0: large products (MXFP4: two stages of X, the scales take the third's place); 1: fewer tiles than CUs at
+// 256 x 256; 2: few rows
+constexpr TileCfg kTiles[] = {{256, 256, 8, 3, 2}, {128, 128, 4, 4, 4}, {64, 128, 4, 5, 5}};
+constexpr TileCfg kTilesFp4[] = {{256, 256, 8, 2, 2}, {128, 128, 4, 4, 4}, {64, 128, 4, 4, 4}};
 constexpr int kNumTiles = 3;
 
 constexpr size_t tile_lds(const TileCfg& t, bool fp4) {
-  const size_t sc = fp4 ? (((size_t)(t.bm + t.bn) * 8 + 256 * t.waves - 1) / (256 * t.waves)) * 256 * t.waves : 0;
-  return t.nbuf * ((size_t)(t.bm + t.bn) * kStageB + sc);
+  const size_t sc = fp4 ? (((size_t)(t.bm + t.bn) * 16 + 1024 * t.waves - 1) / (1024 * t.waves)) * 1024 * t.waves : 0;
+  const int sets = t.nw <= 2 ? 2 : (t.nw + 1) / 2 - (t.nw & 1) + 1;
+  return ((size_t)t.nx * t.bm + (size_t)t.nw * t.bn) * kStageB + sets * sc;
 }
 
 // Sums the slices of a split K in order, then the epilogue of the product.
@@ -88,9 +91,10 @@ hipError_t run(K kern, const TileCfg& t, bool fp4, int slices, const DenseArgs& 
 
 template <bool XT, bool WT, bool FP4, int EPI>
 hipError_t run_tile(int tile, int slices, const DenseArgs& a, hipStream_t st) {
-  if (tile == 0) return run(&k_dense<XT, WT, 256, 256, 2, 4, 2, FP4, EPI>, kTiles[0], FP4, slices, a, st);
-  if (tile == 1) return run(&k_dense<XT, WT, 128, 128, 2, 2, 4, FP4, EPI>, kTiles[1], FP4, slices, a, st);
-  return run(&k_dense<XT, WT, 64, 128, 2, 2, 5, FP4, EPI>, kTiles[2], FP4, slices, a, st);
+  constexpr const TileCfg* t = FP4 ? kTilesFp4 : kTiles;
+  if (tile == 0) return run(&k_dense<XT, WT, 256, 256, 2, 4, t[0].nx, t[0].nw, FP4, EPI>, t[0], FP4, slices, a, st);
+  if (tile == 1) return run(&k_dense<XT, WT, 128, 128, 2, 2, t[1].nx, t[1].nw, FP4, EPI>, t[1], FP4, slices, a, st);
+  return run(&k_dense<XT, WT, 64, 128, 2, 2, t[2].nx, t[2].nw, FP4, EPI>, t[2], FP4, slices, a, st);
 }
 
 template <int EPI>
@@ -106,8 +110,13 @@ hipError_t run_bf16(DenseLayout layout, int tile, int slices, const DenseArgs& a
   }
 }
 
-inline int stages_of(DenseKind kind, int K) { return kind == kDenseFp4 ? mxfp4_stages(K) : (K + 63) / 64; }
+inline int stages_of(DenseKind kind, int K) { return kind == kDenseFp4 ? (K + 255) / 256 : (K + 63) / 64; }
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// stages per slice; MXFP4 slices are whole pairs of stages (their scales are packed so)
+inline int slice_stages(DenseKind kind, int nst, int slices) {
+  const int per = ceil_div(nst, slices);
+  return kind == kDenseFp4 && slices > 1 ? (per + 1) & ~1 : per;
+}
 
 }  // namespace
 
@@ -124,7 +133,7 @@ DensePlan dense_plan(DenseKind kind, DenseLayout layout, int epi, int M, int N, 
   for (int t = 0; t < kNumTiles; ++t) {
     const long long tiles = (long long)ceil_div(M, kTiles[t].bm) * ceil_div(N, kTiles[t].bn);
     for (int s = 1; s <= 16 && s * 4 <= nst + 3; s *= 2) {
-      const int per = ceil_div(nst, s), slices = ceil_div(nst, per);
+      const int per = slice_stages(kind, nst, s), slices = ceil_div(nst, per);
       const double rounds = (double)((tiles * slices + 255) / 256);
       double us = rounds * (per * stage_us[t] + start_us);
       if (slices > 1) us += 4.0 + 2.0 * slices * M * (double)N * 4 / 4e6;
@@ -147,7 +156,7 @@ hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const Dense
     return hipErrorInvalidValue;
   const TileCfg& t = kTiles[p.tile];
   a.stages = stages_of(kind, a.K);
-  a.slice_stages = ceil_div(a.stages, p.slices);
+  a.slice_stages = slice_stages(kind, a.stages, p.slices);
   if (ceil_div(a.stages, a.slice_stages) != p.slices) return hipErrorInvalidValue;
   const bool split = p.slices > 1;
   a.tm = ceil_div(a.M, t.bm);

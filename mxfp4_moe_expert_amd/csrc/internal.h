@@ -387,8 +387,8 @@ struct DenseArgs {
   int M, N, K;               // K in values
   int stages, slice_stages;  // K stages (128 bytes of a K-contiguous row each), stages per slice of a split K
   int tm, tn;                // tiles along M and N
-  const uint16_t* x_scales;  // packed E8M0 bytes (MXFP4 operands), see mxfp4_pack_at
-  const uint16_t* w_scales;
+  const uint32_t* x_scales;  // packed E8M0 bytes (MXFP4 operands), see mxfp4_pack_at
+  const uint32_t* w_scales;
   int x_blocks, w_blocks;    // their 16-row blocks
   void* out;                 // [M][N]; gate: h [M][I] bf16; grad: dgu [M][2I] bf16
   int out_is_fp32;
@@ -420,12 +420,12 @@ hipError_t launch_mxfp4_quantize(long long rows, int K, int dtype, const void* x
                                  uint8_t* scales, hipStream_t st);
 hipError_t launch_mxfp4_dequantize(long long rows, int K, const uint8_t* codes, const uint8_t* scales, int dtype,
                                    void* out, hipStream_t st);
-inline int mxfp4_stages(int K) { return (K + 255) / 256; }
+constexpr int mxfp4_pairs(int K) { return (K + 511) / 512; }  // of product stages (256 values each)
 inline int mxfp4_blocks(int rows) { return (rows + 15) / 16; }
-inline size_t mxfp4_pack_bytes(int rows, int K) { return (size_t)mxfp4_stages(K) * mxfp4_blocks(rows) * 128; }
+inline size_t mxfp4_pack_bytes(int rows, int K) { return (size_t)mxfp4_pairs(K) * mxfp4_blocks(rows) * 256; }
 // x [T][K] bf16 -> codes [T][K/2] and packed scales; w scales [N][K/32] -> packed scales
-hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, uint16_t* xpack, int N,
-                             const uint8_t* wscales, uint16_t* wpack, hipStream_t st);
+hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, uint32_t* xpack, int N,
+                             const uint8_t* wscales, uint32_t* wpack, hipStream_t st);
 // W codes -> bf16 [N][K]; dy [T][N] -> rows padded to ld values with zeros (dy may be null)
 hipError_t launch_mxfp4_expand(int N, int K, const uint8_t* codes, const uint8_t* scales, uint16_t* w, int T,
                                const uint16_t* dy, uint16_t* dyp, int ld, hipStream_t st);

@@ -174,27 +174,27 @@ hipError_t launch_mxfp4_dequantize(long long rows, int K, const uint8_t* codes, 
 
 // ---- operands of the 4-bit x 4-bit product
 //
-// Packed scales: the product's MFMA k-step kk (128 values) of stage s (256
-// values) takes, in lane (r, g), the exponent byte of row 16 b + r, group
-// 8 s + 4 kk + g. Packed as u16 [s][b][16 g + r], byte kk: a stage's scales of
+// Packed scales: the product's k-step j (128 values) of two stages p (512 values) takes, in lane (r, g), the exponent byte of row 16 b + r, group
+// 16 p + 4 j + g. Packed as u32 [p][b][16 g + r], byte j: the scales of
 // consecutive row blocks are contiguous and lane-ordered. Groups past K get
 // the byte 0 (their codes are zeros, and 2^-127 keeps the products zero).
 __device__ __forceinline__ size_t mxfp4_pack_at(int row, int group, int blocks) {
-  return (((size_t)(group >> 3) * blocks + (row >> 4)) * 64 + (group & 3) * 16 + (row & 15)) * 2 + ((group >> 2) & 1);
+  return (((size_t)(group >> 4) * blocks + (row >> 4)) * 64 + (group & 3) * 16 + (row & 15)) * 4 + ((group >> 2) & 3);
 }
 
 // Blocks [0, xblocks): x [T][K] bf16 to codes and packed scales, a unit of 8
-// values per thread, with the unit index running over whole stages of 256 (so
-// that the groups past K of the last stage are written too). Blocks from
-// xblocks on: the weights' exponent bytes to the packed order.
+// values per thread, with the unit index running over whole pairs of
+// stages (so that the groups past K are written too). Blocks from
+// xblocks on: the weights' exponent bytes to the packed order, a thread per
+// dword (row, p, g).
 __global__ __launch_bounds__(256) void k_mxfp4_prep(int T, int K, const uint16_t* x, uint32_t* xcodes, uint8_t* xpack,
                                                     unsigned xblocks, int N, const uint8_t* wscales, uint8_t* wpack) {
-  const int stages = (K + 255) / 256;
+  const int pairs = mxfp4_pairs(K);
   if (blockIdx.x < xblocks) {
-    const int ups = stages * 32;  // units per row, padded
+    const int ups = pairs * 64;  // units per row, padded
     const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
     const int row = (int)(u / ups), i = (int)(u - (long long)row * ups);
-    if (row >= T) return;  // ups % 4 == 0: whole quads leave
+    if (row >= T) return;  // ups % 4 == 0: whole pairs leave
     uint32_t byte = 0;
     if (i * 8 < K) {  // K % 32 == 0: a quad is in or out as one
       const f32x8_t v = load8<kDtBf16>(x, (size_t)row * K + (size_t)i * 8);
@@ -202,25 +202,23 @@ __global__ __launch_bounds__(256) void k_mxfp4_prep(int T, int K, const uint16_t
     }
     if ((i & 3) == 0) xpack[mxfp4_pack_at(row, i >> 2, (T + 15) / 16)] = (uint8_t)byte;
   } else {
-    // a thread packs one (row, stage): 8 bytes
     const long long u = (long long)(blockIdx.x - xblocks) * 256 + threadIdx.x;
-    const int row = (int)(u / stages), s = (int)(u - (long long)row * stages);
+    const int row = (int)(u / (pairs * 4)), q = (int)(u - (long long)row * (pairs * 4));
     if (row >= N) return;
-    const int G = K / kMxGroup;
+    const int G = K / kMxGroup, g0 = (q >> 2) * 16 + (q & 3);
+    uint32_t d = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int g0 = 8 * s + q, g1 = g0 + 4;
-      const uint32_t b0 = g0 < G ? wscales[(size_t)row * G + g0] : 0u, b1 = g1 < G ? wscales[(size_t)row * G + g1] : 0u;
-      *reinterpret_cast<uint16_t*>(wpack + mxfp4_pack_at(row, g0, (N + 15) / 16)) = (uint16_t)(b0 | (b1 << 8));
-    }
+    for (int j = 0; j < 4; ++j)
+      if (g0 + 4 * j < G) d |= (uint32_t)wscales[(size_t)row * G + g0 + 4 * j] << (8 * j);
+    *reinterpret_cast<uint32_t*>(wpack + mxfp4_pack_at(row, g0, (N + 15) / 16)) = d;
   }
 }
 
-hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, uint16_t* xpack, int N,
-                             const uint8_t* wscales, uint16_t* wpack, hipStream_t st) {
+hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, uint32_t* xpack, int N,
+                             const uint8_t* wscales, uint32_t* wpack, hipStream_t st) {
   if (K % kMxGroup || T <= 0 || N <= 0) return hipErrorInvalidValue;
-  const long long stages = mxfp4_stages(K);
-  const long long xb = ((long long)T * stages * 32 + 255) / 256, wb = ((long long)N * stages + 255) / 256;
+  const long long pairs = mxfp4_pairs(K);
+  const long long xb = ((long long)T * pairs * 64 + 255) / 256, wb = ((long long)N * pairs * 4 + 255) / 256;
   if (xb + wb > kMaxBlocks) return hipErrorInvalidValue;
   k_mxfp4_prep<<<(unsigned)(xb + wb), 256, 0, st>>>(T, K, x, reinterpret_cast<uint32_t*>(xcodes),
                                                     reinterpret_cast<uint8_t*>(xpack), (unsigned)xb, N, wscales,
