@@ -543,53 +543,60 @@ def linear_w8a16(x, q, scale, groups=1, out_fp32=False, out=None, ws=None):
 # different streams and captured graphs never share one by accident. They run
 # on the device of their tensors, whatever the current device is.
 
+# Small calls last a few microseconds, so the argument checks here are the
+# short forms; a check that fails is repeated by ``_need``, which words it.
+
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 _ACTS = {"bf16": 0, "mxfp4": 1}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _same_device(*named):
-    dev = named[0][1].device
-    for name, t in named[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, expected {dev}")
-    return dev
+def _arg(t, dtype, shape, index, name):
+    """t's pointer, t being a contiguous ``dtype`` tensor of ``shape`` on device ``index``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
 
 
-def _call(dev, name, *args):
-    """Calls a library function with ``dev`` current, its current stream appended."""
+def _matrix(t, dtype, name):
+    """Rows, columns and device index of a 2-D tensor whose own checks follow."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
+        _need(t, dtype, None, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name}: two dimensions expected")
+    return t.shape[0], t.shape[1], t.get_device()
+
+
+def _call(index, name, *args):
+    """Calls a library function with device ``index`` current, its current stream appended."""
     fn = getattr(lib(), name)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev)), name)
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)), name)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != MOE_OK:
+        raise MoEError(status, name)
 
 
-def _scratch(need, dev, ws, what):
+def _scratch(need, like, ws, what):
+    """Pointer and size of the workspace, and its tensor (to be kept until the call is queued)."""
     if need == 0:
         raise MoEError(MOE_EUNSUPPORTED, what)
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    _need(ws, torch.uint8, None, "ws")
-    return ws
+        ws = like.new_empty((need,), dtype=torch.uint8)
+        return ws.data_ptr(), need, ws
+    return _arg(ws, torch.uint8, ws.shape, like.get_device(), "ws"), ws.numel(), ws
 
 
-def _result(out, shape, dtype, dev, name="out"):
+def _result(out, shape, dtype, like, name="out"):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    return _need(out, dtype, shape, name)
-
-
-def _mxfp4_weight(codes, scales):
-    """N and K of an MXFP4 matrix [N][K]."""
-    _need(codes, torch.uint8, None, "codes")
-    _need(scales, torch.uint8, None, "scales")
-    if codes.dim() != 2 or codes.shape[1] % 16:
-        raise ValueError("codes: shape [N, K/2] with K a multiple of 32 expected")
-    N, K = codes.shape[0], codes.shape[1] * 2
-    if tuple(scales.shape) != (N, K // 32):
-        raise ValueError(f"scales: shape {tuple(scales.shape)}, expected {(N, K // 32)}")
-    return N, K
+        return like.new_empty(shape, dtype=dtype)
+    _arg(out, dtype, shape, like.get_device(), name)
+    return out
 
 
 def quantize_mxfp4(x, out=None):
@@ -599,93 +606,95 @@ def quantize_mxfp4(x, out=None):
     16-byte aligned rows."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x: torch.Tensor expected")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("x: must be a device (cuda/hip) tensor")
-    if x.dtype not in _DTYPES:
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
         raise TypeError(f"x: dtype {x.dtype}, expected bfloat16, float32 or float16")
-    if x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % 32:
+    shape = x.shape
+    K = shape[-1] if len(shape) else 0
+    if K == 0 or K % 32:
         raise ValueError("x: last dimension must be a positive multiple of 32")
-    K = x.shape[-1]
-    rows = x.numel() // K
     ldx = K
     if not x.is_contiguous():
         if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < K:
             raise ValueError("x: contiguous, or 2-D with unit column stride, expected")
         ldx = x.stride(0)
-    lead = tuple(x.shape[:-1])
+    lead = tuple(shape[:-1])
     c, s = out if out is not None else (None, None)
-    codes = _result(c, lead + (K // 2,), torch.uint8, x.device, "codes")
-    scales = _result(s, lead + (K // 32,), torch.uint8, x.device, "scales")
-    dev = _same_device(("x", x), ("codes", codes), ("scales", scales))
-    _call(dev, "moe_mxfp4_quantize", rows, K, _DTYPES[x.dtype], _ptr(x), ldx, _ptr(codes), _ptr(scales))
+    codes = _result(c, lead + (K // 2,), torch.uint8, x, "codes")
+    scales = _result(s, lead + (K // 32,), torch.uint8, x, "scales")
+    _call(x.get_device(), "moe_mxfp4_quantize", x.numel() // K, K, dt, x.data_ptr(), ldx, codes.data_ptr(),
+          scales.data_ptr())
     return codes, scales
 
 
 def dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None):
     """(codes [..., K/2], scales [..., K/32]) -> [..., K] in bf16 or fp32, exact (moe_mxfp4_dequantize)."""
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"dtype {dtype}, expected bfloat16 or float32")
-    _need(codes, torch.uint8, None, "codes")
-    _need(scales, torch.uint8, None, "scales")
-    if codes.dim() < 1 or codes.shape[-1] == 0 or codes.shape[-1] % 16:
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        _need(codes, torch.uint8, None, "codes")
+    shape, index = codes.shape, codes.get_device()
+    K = shape[-1] * 2 if len(shape) else 0
+    if K == 0 or K % 32:
         raise ValueError("codes: last dimension must be a positive multiple of 16")
-    K = codes.shape[-1] * 2
-    lead = tuple(codes.shape[:-1])
-    _need(scales, torch.uint8, lead + (K // 32,), "scales")
-    out = _result(out, lead + (K,), dtype, codes.device)
-    dev = _same_device(("codes", codes), ("scales", scales), ("out", out))
-    _call(dev, "moe_mxfp4_dequantize", codes.numel() * 2 // K, K, _ptr(codes), _ptr(scales), _DTYPES[dtype], _ptr(out))
+    lead = tuple(shape[:-1])
+    pc = _arg(codes, torch.uint8, shape, index, "codes")
+    ps = _arg(scales, torch.uint8, lead + (K // 32,), index, "scales")
+    out = _result(out, lead + (K,), dtype, codes)
+    _call(index, "moe_mxfp4_dequantize", codes.numel() * 2 // K, K, pc, ps, _DTYPES[dtype], out.data_ptr())
     return out
+
+
+def _mxfp4_weight(codes, scales, index):
+    """N, K and the pointers of an MXFP4 matrix [N][K]."""
+    N, half, _ = _matrix(codes, torch.uint8, "codes")
+    if half == 0 or half % 16:
+        raise ValueError("codes: shape [N, K/2] with K a positive multiple of 32 expected")
+    return (N, half * 2, _arg(codes, torch.uint8, (N, half), index, "codes"),
+            _arg(scales, torch.uint8, (N, half // 16), index, "scales"))
 
 
 def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None):
     """y = x W^T (moe_linear_mxfp4): x [T][K] bf16, W [N][K] as codes
     [N][K/2] and scales [N][K/32] -> [T][N] (bf16 or fp32). act: "bf16", or
     "mxfp4" to round x to MXFP4 first."""
-    if act not in _ACTS:
+    mode = _ACTS.get(act)
+    if mode is None:
         raise ValueError(f"act {act!r}, expected one of {sorted(_ACTS)}")
-    N, K = _mxfp4_weight(codes, scales)
-    _need(x, torch.bfloat16, None, "x")
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected (T, {K})")
-    T = x.shape[0]
-    out = _result(out, (T, N), torch.float32 if out_fp32 else torch.bfloat16, x.device)
-    dev = _same_device(("x", x), ("codes", codes), ("scales", scales), ("out", out), ("ws", ws))
-    need = lib().moe_linear_mxfp4_workspace_size(T, K, N, _ACTS[act])
-    if need > 256 or ws is not None:
-        ws = _scratch(need, dev, ws, "moe_linear_mxfp4")
-    _call(dev, "moe_linear_mxfp4", T, K, N, _ptr(x), _ptr(codes), _ptr(scales), _ACTS[act], _ptr(out), int(out_fp32),
-          _ptr(ws), 0 if ws is None else ws.numel())
+    T, _, index = _matrix(x, torch.bfloat16, "x")
+    N, K, pc, ps = _mxfp4_weight(codes, scales, index)
+    px = _arg(x, torch.bfloat16, (T, K), index, "x")
+    out = _result(out, (T, N), torch.float32 if out_fp32 else torch.bfloat16, x)
+    need = lib().moe_linear_mxfp4_workspace_size(T, K, N, mode)
+    pw = nw = None
+    if need > 256 or ws is not None or need == 0:
+        pw, nw, ws = _scratch(need, x, ws, "moe_linear_mxfp4")
+    _call(index, "moe_linear_mxfp4", T, K, N, px, pc, ps, mode, out.data_ptr(), 1 if out_fp32 else 0, pw, nw or 0)
     return out
 
 
 def linear_mxfp4_dx(dy, codes, scales, out_fp32=False, out=None, ws=None):
     """dx = dy W, the input gradient of ``linear_mxfp4`` through frozen
     weights (moe_linear_mxfp4_dx): dy [T][N] bf16 -> [T][K] (bf16 or fp32)."""
-    N, K = _mxfp4_weight(codes, scales)
-    _need(dy, torch.bfloat16, None, "dy")
-    if dy.dim() != 2 or dy.shape[1] != N:
-        raise ValueError(f"dy: shape {tuple(dy.shape)}, expected (T, {N})")
-    T = dy.shape[0]
-    out = _result(out, (T, K), torch.float32 if out_fp32 else torch.bfloat16, dy.device)
-    dev = _same_device(("dy", dy), ("codes", codes), ("scales", scales), ("out", out), ("ws", ws))
-    ws = _scratch(lib().moe_linear_mxfp4_dx_workspace_size(T, K, N), dev, ws, "moe_linear_mxfp4_dx")
-    _call(dev, "moe_linear_mxfp4_dx", T, K, N, _ptr(dy), _ptr(codes), _ptr(scales), _ptr(out), int(out_fp32), _ptr(ws),
-          ws.numel())
+    T, _, index = _matrix(dy, torch.bfloat16, "dy")
+    N, K, pc, ps = _mxfp4_weight(codes, scales, index)
+    py = _arg(dy, torch.bfloat16, (T, N), index, "dy")
+    out = _result(out, (T, K), torch.float32 if out_fp32 else torch.bfloat16, dy)
+    pw, nw, ws = _scratch(lib().moe_linear_mxfp4_dx_workspace_size(T, K, N), dy, ws, "moe_linear_mxfp4_dx")
+    _call(index, "moe_linear_mxfp4_dx", T, K, N, py, pc, ps, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
     return out
 
 
-def _ffn_shapes(x, w13, w2):
-    _need(x, torch.bfloat16, None, "x")
-    if x.dim() != 2:
-        raise ValueError("x: shape [T, H] expected")
-    T, H = x.shape
-    _need(w2, torch.bfloat16, None, "w2")
-    if w2.dim() != 2 or w2.shape[0] != H:
+def _ffn_args(x, w13, w2):
+    """T, H, I, the device index and the pointers of the block's inputs."""
+    T, H, index = _matrix(x, torch.bfloat16, "x")
+    h2, I, _ = _matrix(w2, torch.bfloat16, "w2")
+    if h2 != H:
         raise ValueError(f"w2: shape {tuple(w2.shape)}, expected ({H}, I)")
-    I = w2.shape[1]
-    _need(w13, torch.bfloat16, (2 * I, H), "w13")
-    return T, H, I
+    return (T, H, I, index, _arg(x, torch.bfloat16, (T, H), index, "x"),
+            _arg(w13, torch.bfloat16, (2 * I, H), index, "w13"), _arg(w2, torch.bfloat16, (H, I), index, "w2"))
 
 
 def gated_ffn(x, w13, w2, limit=10.0, save=False, out_fp32=False, out=None, ws=None):
@@ -693,17 +702,12 @@ def gated_ffn(x, w13, w2, limit=10.0, save=False, out_fp32=False, out=None, ws=N
     [2I][H] (gate rows, then up rows), w2 [H][I] -> y [T][H] (bf16 or fp32).
     save=True returns (y, saved), ``saved`` being what ``gated_ffn_backward``
     takes: (g and u [T][2I], h [T][I]), bf16."""
-    T, H, I = _ffn_shapes(x, w13, w2)
-    out = _result(out, (T, H), torch.float32 if out_fp32 else torch.bfloat16, x.device)
-    dev = _same_device(("x", x), ("w13", w13), ("w2", w2), ("out", out), ("ws", ws))
-    saved = None
-    if save:
-        saved = (torch.empty(T, 2 * I, dtype=torch.bfloat16, device=dev),
-                 torch.empty(T, I, dtype=torch.bfloat16, device=dev))
-    ws = _scratch(lib().moe_gated_ffn_workspace_size(T, H, I), dev, ws, "moe_gated_ffn")
-    gu, h = saved if save else (None, None)
-    _call(dev, "moe_gated_ffn", T, H, I, float(limit), _ptr(x), _ptr(w13), _ptr(w2), _ptr(gu), _ptr(h), _ptr(out),
-          int(out_fp32), _ptr(ws), ws.numel())
+    T, H, I, index, px, p13, p2 = _ffn_args(x, w13, w2)
+    out = _result(out, (T, H), torch.float32 if out_fp32 else torch.bfloat16, x)
+    saved = (x.new_empty((T, 2 * I)), x.new_empty((T, I))) if save else None
+    pg, ph = (saved[0].data_ptr(), saved[1].data_ptr()) if save else (None, None)
+    pw, nw, ws = _scratch(lib().moe_gated_ffn_workspace_size(T, H, I), x, ws, "moe_gated_ffn")
+    _call(index, "moe_gated_ffn", T, H, I, limit, px, p13, p2, pg, ph, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
     return (out, saved) if save else out
 
 
@@ -712,17 +716,16 @@ def gated_ffn_backward(dy, x, w13, w2, saved, limit=10.0, need=(True, True, True
     (dx [T][H] bf16, dw13 [2I][H], dw2 [H][I]; the weights' in bf16, or fp32
     if dw_fp32). ``saved`` and ``limit``: the forward call's. ``need``: which
     of the three to compute (None in the others' places)."""
-    T, H, I = _ffn_shapes(x, w13, w2)
-    _need(dy, torch.bfloat16, (T, H), "dy")
-    gu, h = saved
-    _need(gu, torch.bfloat16, (T, 2 * I), "saved[0]")
-    _need(h, torch.bfloat16, (T, I), "saved[1]")
-    dev = _same_device(("dy", dy), ("x", x), ("w13", w13), ("w2", w2), ("saved[0]", gu), ("saved[1]", h), ("ws", ws))
+    T, H, I, index, px, p13, p2 = _ffn_args(x, w13, w2)
+    pd = _arg(dy, torch.bfloat16, (T, H), index, "dy")
+    pg = _arg(saved[0], torch.bfloat16, (T, 2 * I), index, "saved[0]")
+    ph = _arg(saved[1], torch.bfloat16, (T, I), index, "saved[1]")
     wt = torch.float32 if dw_fp32 else torch.bfloat16
-    dx = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if need[0] else None
-    dw13 = torch.empty(2 * I, H, dtype=wt, device=dev) if need[1] else None
-    dw2 = torch.empty(H, I, dtype=wt, device=dev) if need[2] else None
-    ws = _scratch(lib().moe_gated_ffn_backward_workspace_size(T, H, I), dev, ws, "moe_gated_ffn_backward")
-    _call(dev, "moe_gated_ffn_backward", T, H, I, float(limit), _ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(gu),
-          _ptr(h), _ptr(dx), _ptr(dw13), _ptr(dw2), int(dw_fp32), _ptr(ws), ws.numel())
+    dx = x.new_empty((T, H)) if need[0] else None
+    dw13 = x.new_empty((2 * I, H), dtype=wt) if need[1] else None
+    dw2 = x.new_empty((H, I), dtype=wt) if need[2] else None
+    pw, nw, ws = _scratch(lib().moe_gated_ffn_backward_workspace_size(T, H, I), x, ws, "moe_gated_ffn_backward")
+    _call(index, "moe_gated_ffn_backward", T, H, I, limit, pd, px, p13, p2, pg, ph,
+          None if dx is None else dx.data_ptr(), None if dw13 is None else dw13.data_ptr(),
+          None if dw2 is None else dw2.data_ptr(), 1 if dw_fp32 else 0, pw, nw)
     return dx, dw13, dw2

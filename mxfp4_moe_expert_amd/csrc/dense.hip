@@ -9,11 +9,11 @@ namespace {
 struct TileCfg {
   int bm, bn, waves, nx, nw;  // nx, nw: stages of X and W in LDS
 };
-// 0: large products (MXFP4: two stages of X, the scales take the third's place); 1: fewer tiles than CUs at
-// 256 x 256; 2: few rows
-constexpr TileCfg kTiles[] = {{256, 256, 8, 3, 2}, {128, 128, 4, 4, 4}, {64, 128, 4, 5, 5}};
-constexpr TileCfg kTilesFp4[] = {{256, 256, 8, 2, 2}, {128, 128, 4, 4, 4}, {64, 128, 4, 4, 4}};
-constexpr int kNumTiles = 3;
+// Two LDS rings fill the 160 KB of a CU (64 x 128: half of it, two blocks per CU). MXFP4: the scales take the place of
+// a stage of X in the largest tile.
+constexpr TileCfg kTiles[] = {{256, 256, 8, 3, 2}, {256, 128, 8, 3, 3}, {128, 128, 8, 4, 4}, {64, 128, 8, 3, 3}};
+constexpr TileCfg kTilesFp4[] = {{256, 256, 8, 2, 2}, {256, 128, 8, 3, 3}, {128, 128, 8, 4, 4}, {64, 128, 8, 3, 2}};
+constexpr int kNumTiles = 4;
 
 constexpr size_t tile_lds(const TileCfg& t, bool fp4) {
   const size_t sc = fp4 ? (((size_t)(t.bm + t.bn) * 16 + 1024 * t.waves - 1) / (1024 * t.waves)) * 1024 * t.waves : 0;
@@ -93,8 +93,9 @@ template <bool XT, bool WT, bool FP4, int EPI>
 hipError_t run_tile(int tile, int slices, const DenseArgs& a, hipStream_t st) {
   constexpr const TileCfg* t = FP4 ? kTilesFp4 : kTiles;
   if (tile == 0) return run(&k_dense<XT, WT, 256, 256, 2, 4, t[0].nx, t[0].nw, FP4, EPI>, t[0], FP4, slices, a, st);
-  if (tile == 1) return run(&k_dense<XT, WT, 128, 128, 2, 2, t[1].nx, t[1].nw, FP4, EPI>, t[1], FP4, slices, a, st);
-  return run(&k_dense<XT, WT, 64, 128, 2, 2, t[2].nx, t[2].nw, FP4, EPI>, t[2], FP4, slices, a, st);
+  if (tile == 1) return run(&k_dense<XT, WT, 256, 128, 2, 4, t[1].nx, t[1].nw, FP4, EPI>, t[1], FP4, slices, a, st);
+  if (tile == 2) return run(&k_dense<XT, WT, 128, 128, 2, 4, t[2].nx, t[2].nw, FP4, EPI>, t[2], FP4, slices, a, st);
+  return run(&k_dense<XT, WT, 64, 128, 2, 4, t[3].nx, t[3].nw, FP4, EPI>, t[3], FP4, slices, a, st);
 }
 
 template <int EPI>
@@ -120,23 +121,27 @@ inline int slice_stages(DenseKind kind, int nst, int slices) {
 
 }  // namespace
 
-// The plan with the least estimated time: rounds of blocks over 256 CUs times
-// the stages each runs, plus the partial sums' traffic for a split.
+// The plan with the least estimated time: rounds of blocks over the 256 CUs times the stages each runs, plus the
+// partial sums' traffic (written and read at about 4 TB/s) and launch for a split. Per stage a block is bound by its
+// share of the L2 -> LDS path, then by the matrix cores: measured on 4096 x 4096 weights at 300, 1000, 2048 and 8192
+// rows as 1.45, 0.88, 0.57 and 0.39 us for the four tiles on a full chip (64 x 128 with two blocks on every CU: 0.65
+// for both).
 DensePlan dense_plan(DenseKind kind, DenseLayout layout, int epi, int M, int N, int K) {
   (void)layout;
   (void)epi;
   const int nst = stages_of(kind, K);
-  // microseconds per stage of a block that has a CU to itself, and per block
-  constexpr double stage_us[kNumTiles] = {1.05, 0.40, 0.30}, start_us = 3.0;
+  constexpr double stage_us[kNumTiles] = {1.45, 0.88, 0.57, 0.39}, pair_us = 0.65, start_us = 3.0;
   DensePlan best = {0, 1};
   double best_us = 1e30;
   for (int t = 0; t < kNumTiles; ++t) {
     const long long tiles = (long long)ceil_div(M, kTiles[t].bm) * ceil_div(N, kTiles[t].bn);
     for (int s = 1; s <= 16 && s * 4 <= nst + 3; s *= 2) {
       const int per = slice_stages(kind, nst, s), slices = ceil_div(nst, per);
-      const double rounds = (double)((tiles * slices + 255) / 256);
-      double us = rounds * (per * stage_us[t] + start_us);
-      if (slices > 1) us += 4.0 + 2.0 * slices * M * (double)N * 4 / 4e6;
+      const long long blocks = tiles * slices;
+      double us;
+      if (t == 3 && blocks > 256) us = (double)((blocks + 511) / 512) * (per * pair_us + start_us);
+      else us = (double)((blocks + 255) / 256) * (per * stage_us[t] + start_us);
+      if (slices > 1) us += 3.0 + 2.0 * slices * M * (double)N * 4 / 4e6;
       if (us < best_us) {
         best_us = us;
         best = {t, slices};
