@@ -304,13 +304,14 @@ enum {
 /* y = x W^T with W [N][K] in MXFP4:
  *   x [T][K] bf16; out [T][N] bf16 (out_is_fp32 = 0) or f32, rounded once
  *   from the fp32 sum.
- *   T <= 64: one launch that streams the weights, no workspace (workspace
- *   may be NULL). T > 64: the weights are expanded to bf16 in the workspace
- *   (act bf16) or the activations encoded there (act mxfp4), then one matrix
- *   product, whose K is split over blocks where the tiles would not fill the
- *   chip (the partial sums are added in order: deterministic).
+ *   Few rows: one launch that streams the weights. More: a matrix product that
+ *   reads the codes, or (many rows) one on the weights expanded to bf16 in
+ *   the workspace; act mxfp4: one on the activations encoded there. K is
+ *   split over blocks where the tiles would not fill the chip (the partial
+ *   sums are added in order: deterministic).
  *   workspace: moe_linear_mxfp4_workspace_size(T, K, N, act) bytes, 256-byte
  *   aligned, any contents; calls sharing one must be ordered on one stream.
+ *   A size of 256 means that none is used: workspace may then be NULL.
  * Supported: K a multiple of 32 up to 65536, 1 <= N <= 65536, 0 <= T <=
  * 65536 (else MOE_EUNSUPPORTED, and the size is 0). */
 size_t moe_linear_mxfp4_workspace_size(int32_t T, int32_t K, int32_t N, int32_t act);

@@ -14,6 +14,14 @@ using namespace moe;
 
 constexpr int kMaxRows = 65536;   // T
 constexpr int kMaxLinear = 65536; // K and N of a linear
+#ifndef FEWROWS
+#define FEWROWS 64
+#endif
+#ifndef FFNROWS
+#define FFNROWS 64
+#endif
+constexpr int kFewRows = FEWROWS;
+constexpr int kFfnRows = FFNROWS;
 constexpr int kMaxFfn = 16384;    // H and I of the gated block: 2 I H values stay below 2^30
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -39,9 +47,12 @@ bool linear_ok(int T, int K, int N) {
 
 // ---- workspace layouts
 
+constexpr size_t kNoWorkspace = 256;  // the stated size where none is used (0 stands for unsupported)
+
 struct LinearLayout {
   DensePlan plan;
-  size_t w;                     // act bf16: W as bf16 [N][K]
+  bool codes_direct;            // act bf16: the product reads W's codes (dense_w4.hip)
+  size_t w;                     // act bf16 otherwise: W as bf16 [N][K]
   size_t codes, xpack, wpack;   // act mxfp4: activation codes, packed scales of both sides
   size_t part, total;
 };
@@ -55,18 +66,27 @@ LinearLayout linear_layout(int T, int K, int N, int act) {
     o = align256(o + bytes);
     return p;
   };
-  if (T > kSmallT) {
-    L.plan = dense_plan(act == MOE_ACT_MXFP4 ? kDenseFp4 : kDenseBf16, kDenseNT, 0, T, N, K);
+  if (T > kFewRows) {
+    double us;
+    L.plan = dense_plan(act == MOE_ACT_MXFP4 ? kDenseFp4 : kDenseBf16, T, N, K, &us);
+    if (act == MOE_ACT_BF16) {
+      // expanding W: a launch, and 17/32 of a byte read and 2 written per weight
+      const double expand_us = 3.0 + (double)N * K * (17.0 / 32 + 2) / 4.5e6;
+      double direct_us;
+      const DensePlan direct = dense_w4_plan(T, N, K, &direct_us);
+      L.codes_direct = direct.tile >= 0 && direct_us < us + expand_us;
+      if (L.codes_direct) L.plan = direct;
+    }
     if (act == MOE_ACT_MXFP4) {
       L.codes = take((size_t)T * K / 2);
       L.xpack = take(mxfp4_pack_bytes(T, K));
       L.wpack = take(mxfp4_pack_bytes(N, K));
-    } else {
+    } else if (!L.codes_direct) {
       L.w = take((size_t)N * K * 2);
     }
     L.part = take(dense_part_bytes(L.plan, T, N));
   }
-  L.total = o < 256 ? 256 : o;
+  L.total = o == 0 ? kNoWorkspace : o < 512 ? 512 : o;
   return L;
 }
 
@@ -86,7 +106,7 @@ DxLayout dx_layout(int T, int K, int N) {
     return p;
   };
   L.ldy = (N + 7) & ~7;
-  L.plan = dense_plan(kDenseBf16, kDenseNN, 0, T > 0 ? T : 1, K, N);
+  L.plan = dense_plan(kDenseBf16, T > 0 ? T : 1, K, N);
   L.w = take((size_t)N * K * 2);
   L.dyp = take(L.ldy != N ? (size_t)T * L.ldy * 2 : 0);
   L.part = take(dense_part_bytes(L.plan, T, K));
@@ -111,9 +131,9 @@ FfnLayout ffn_layout(int T, int H, int I) {
   L.h = 0;
   size_t o = align256((size_t)T * I * 2);
   L.part = o;
-  if (T > kSmallT) {
-    L.up = dense_plan(kDenseBf16, kDenseNT, kGate, T, 2 * I, H);
-    L.down = dense_plan(kDenseBf16, kDenseNT, kStore, T, H, I);
+  if (T > kFfnRows) {
+    L.up = dense_plan(kDenseBf16, T, 2 * I, H);
+    L.down = dense_plan(kDenseBf16, T, H, I);
     o = align256(o + max_of(dense_part_bytes(L.up, T, 2 * I), dense_part_bytes(L.down, T, H)));
   }
   L.total = o < 256 ? 256 : o;
@@ -129,10 +149,10 @@ FfnGradLayout ffn_grad_layout(int T, int H, int I) {
   FfnGradLayout L;
   memset(&L, 0, sizeof(L));
   const int t = T > 0 ? T : 1;
-  L.dh = dense_plan(kDenseBf16, kDenseNN, kGrad, t, I, H);
-  L.dx = dense_plan(kDenseBf16, kDenseNN, kStore, t, H, 2 * I);
-  L.dw13 = dense_plan(kDenseBf16, kDenseTN, kStore, 2 * I, H, t);
-  L.dw2 = dense_plan(kDenseBf16, kDenseTN, kStore, H, I, t);
+  L.dh = dense_plan(kDenseBf16, t, I, H);
+  L.dx = dense_plan(kDenseBf16, t, H, 2 * I);
+  L.dw13 = dense_plan(kDenseBf16, 2 * I, H, t);
+  L.dw2 = dense_plan(kDenseBf16, H, I, t);
   L.dgu = 0;
   L.part = align256((size_t)T * 2 * I * 2);
   size_t p = max_of(dense_part_bytes(L.dh, t, I), dense_part_bytes(L.dx, t, H));
@@ -199,7 +219,7 @@ int moe_linear_mxfp4(int32_t T, int32_t K, int32_t N, const uint16_t* x, const u
   if (!x || !codes || !scales || !out) return MOE_EINVAL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(out)) return MOE_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (T <= kSmallT) {
+  if (T <= kFewRows) {
     FewRowsArgs a;
     memset(&a, 0, sizeof(a));
     a.T = T;
@@ -214,8 +234,10 @@ int moe_linear_mxfp4(int32_t T, int32_t K, int32_t N, const uint16_t* x, const u
     return status(launch_few_rows_mxfp4(a, st));
   }
   const LinearLayout L = linear_layout(T, K, N, act);
-  const int rc = check_ws(workspace, workspace_bytes, L.total);
-  if (rc) return rc;
+  if (L.total != kNoWorkspace) {
+    const int rc = check_ws(workspace, workspace_bytes, L.total);
+    if (rc) return rc;
+  }
   float* part = at<float>(workspace, L.part);
   if (act == MOE_ACT_MXFP4) {
     uint8_t* xc = at<uint8_t>(workspace, L.codes);
@@ -230,6 +252,9 @@ int moe_linear_mxfp4(int32_t T, int32_t K, int32_t N, const uint16_t* x, const u
     a.w_blocks = mxfp4_blocks(N);
     return status(launch_dense(kDenseFp4, kDenseNT, kStore, L.plan, a, st));
   }
+  if (L.codes_direct)
+    return status(launch_dense_w4(L.plan, dense_args(x, K, codes, (size_t)K / 4, T, N, K, out, out_is_fp32, part),
+                                  scales, st));
   uint16_t* w = at<uint16_t>(workspace, L.w);
   const hipError_t e = launch_mxfp4_expand(N, K, codes, scales, w, 0, nullptr, nullptr, 8, st);
   if (e != hipSuccess) return status(e);
@@ -282,7 +307,7 @@ int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* 
   if (rc) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint16_t* h = h_saved ? h_saved : at<uint16_t>(workspace, L.h);
-  if (T <= kSmallT) {
+  if (T <= kFfnRows) {
     FewRowsArgs a;
     memset(&a, 0, sizeof(a));
     a.T = T;

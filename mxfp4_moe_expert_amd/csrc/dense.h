@@ -226,12 +226,35 @@ __device__ __forceinline__ void ffn_act_grad(float g, float u, float dh, float L
   du = (u > L || u < -L) ? 0.0f : dh * gc * s;
 }
 
+// The wave's accumulators to out [M][N]: lane (r, g) holds acc[b][c][i] = C[m0 + 16 c + r][n0 + 16 b + 4 g + i].
+template <int MB, int NB>
+__device__ __forceinline__ void store_tile(const f32x4_t (&acc)[NB][MB], void* out, bool fp32, int M, int N, int m0,
+                                           int n0, int lane) {
+  const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int c = 0; c < MB; ++c) {
+    const int m = m0 + c * 16 + r;
+    if (m >= M) continue;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int n = n0 + b * 16 + 4 * g;
+      if (n >= N) continue;
+      store4(out, fp32, (size_t)m * N + n, acc[b][c], N - n, (N & 3) == 0);
+    }
+  }
+}
+
 enum DenseEpi {
   kEpiStore = 0,    // out [M][N] bf16 or fp32
   kEpiGate = 1,     // gate / up rows interleaved: h [M][I] bf16 (and gu [M][2I])
   kEpiGrad = 2,     // dh -> dgu [M][2I] from gu
   kEpiPartial = 3,  // fp32 partial sums [slice][M][N] (of a split K)
 };
+
+// Of n operations spread evenly over nm places: how many are done by place m (at m < 0: none).
+__device__ constexpr int spread(int m, int nm, int n) {
+  return m < 0 ? 0 : (m * n / nm + 1 < n ? m * n / nm + 1 : n);
+}
 
 // Logical tile of a block: XCD x (block % 8) walks a contiguous run of the
 // tiles, ordered in bands of 8 row tiles, so that the tiles an XCD's blocks
@@ -372,7 +395,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
   // issuing the loads load(0) .. load(nload - 1). The order is pinned, or the compiler gathers the memory operations.
   auto step = [&](auto kk, auto q, const lds_u8* xt, const lds_u8* wt, auto nload, auto&& load) {
     constexpr int NM = MB * NB, NR = NB + MB - XR;
-    int loads = 0, reads = 0;
+    static_assert(nload <= NM, "one load per MFMA at most");
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       const int c = m / NB, b = m % NB;
@@ -380,11 +403,12 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
       if constexpr (FP4) acc[b][c] = mfma_mx4<kk + 2 * q>(wf[kk][b], x, acc[b][c], swv[b], sxv[c]);
       else acc[b][c] = mfma_bf16(wf[kk][b], x, acc[b][c]);
       __builtin_amdgcn_sched_barrier(0);
-      while (loads < nload && loads * NM <= m * nload) load(loads++);
-      while (reads < NR && reads * NM <= m * 2 * NR) {
-        if (reads < NB) wf[1 - kk][reads] = rw.read(wt, reads, 1 - kk);
-        else xd[1 - kk][reads - NB] = rx.read(xt, reads - NB + XR, 1 - kk);
-        ++reads;
+#pragma unroll
+      for (int i = spread(m - 1, NM, nload); i < spread(m, NM, nload); ++i) load(i);
+#pragma unroll
+      for (int i = spread(2 * m - 2, NM, NR); i < spread(2 * m, NM, NR); ++i) {
+        if (i < NB) wf[1 - kk][i] = rw.read(wt, i, 1 - kk);
+        else xd[1 - kk][i - NB] = rx.read(xt, i - NB + XR, 1 - kk);
       }
       if (b == NB - 1 && c < XR) xr[c < XR ? c : 0] = rx.read(xt, c, 1 - kk);
       __builtin_amdgcn_sched_barrier(0);
@@ -458,6 +482,12 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
   }
   dense_wait<0>();  // nothing may still write this block's LDS when it ends
 
+  if constexpr (EPI == kEpiStore || EPI == kEpiPartial) {
+    void* out = EPI == kEpiPartial ? static_cast<void*>(a.part + (size_t)blockIdx.y * a.M * a.N) : a.out;
+    store_tile<MB, NB>(acc, out, EPI == kEpiPartial || a.out_is_fp32, a.M, a.N, m0 + wm * MB * 16, n0 + wn * NB * 16,
+                       lane);
+    return;
+  }
   // lane (r, g): acc[b][c][i] = C[m = .. + 16 c + r][n = .. + 16 b + 4 g + i]
   const int r = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -507,16 +537,6 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
         uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I + n;
         *reinterpret_cast<uint2*>(o) = pack4_bf16(dg);
         *reinterpret_cast<uint2*>(o + a.I) = pack4_bf16(du);
-      }
-    } else {
-      void* out = a.out;
-      if constexpr (EPI == kEpiPartial) out = a.part + (size_t)blockIdx.y * a.M * a.N;
-      const bool fp32 = EPI == kEpiPartial || a.out_is_fp32;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int n = n0 + (wn * NB + b) * 16 + 4 * g;
-        if (n >= a.N) continue;
-        store4(out, fp32, (size_t)m * a.N + n, acc[b][c], a.N - n, (a.N & 3) == 0);
       }
     }
   }

@@ -126,9 +126,7 @@ inline int slice_stages(DenseKind kind, int nst, int slices) {
 // share of the L2 -> LDS path, then by the matrix cores: measured on 4096 x 4096 weights at 300, 1000, 2048 and 8192
 // rows as 1.45, 0.88, 0.57 and 0.39 us for the four tiles on a full chip (64 x 128 with two blocks on every CU: 0.65
 // for both).
-DensePlan dense_plan(DenseKind kind, DenseLayout layout, int epi, int M, int N, int K) {
-  (void)layout;
-  (void)epi;
+DensePlan dense_plan(DenseKind kind, int M, int N, int K, double* us_out) {
   const int nst = stages_of(kind, K);
   constexpr double stage_us[kNumTiles] = {1.45, 0.88, 0.57, 0.39}, pair_us = 0.65, start_us = 3.0;
   DensePlan best = {0, 1};
@@ -148,6 +146,7 @@ DensePlan dense_plan(DenseKind kind, DenseLayout layout, int epi, int M, int N, 
       }
     }
   }
+  if (us_out) *us_out = best_us;
   return best;
 }
 
@@ -184,13 +183,16 @@ hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const Dense
   } else {
     e = run_bf16<kEpiStore>(layout, p.tile, p.slices, a, st);
   }
-  if (e != hipSuccess || !split) return e;
+  return e != hipSuccess || !split ? e : launch_dense_reduce(epi, a, p.slices, st);
+}
+
+hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st) {
   const int cols = epi == kEpiGate ? a.I : a.N;
   const long long threads = (long long)a.M * ((cols + 3) / 4);
   const unsigned nb = (unsigned)((threads + 255) / 256);
-  if (epi == kEpiGate) k_dense_reduce<kEpiGate><<<nb, 256, 0, st>>>(a, p.slices);
-  else if (epi == kEpiGrad) k_dense_reduce<kEpiGrad><<<nb, 256, 0, st>>>(a, p.slices);
-  else k_dense_reduce<kEpiStore><<<nb, 256, 0, st>>>(a, p.slices);
+  if (epi == kEpiGate) k_dense_reduce<kEpiGate><<<nb, 256, 0, st>>>(a, slices);
+  else if (epi == kEpiGrad) k_dense_reduce<kEpiGrad><<<nb, 256, 0, st>>>(a, slices);
+  else k_dense_reduce<kEpiStore><<<nb, 256, 0, st>>>(a, slices);
   return hipGetLastError();
 }
 

@@ -407,11 +407,18 @@ struct DensePlan {
   int tile;    // index of the tile configuration
   int slices;  // 1: no split
 };
-DensePlan dense_plan(DenseKind kind, DenseLayout layout, int epi, int M, int N, int K);
+DensePlan dense_plan(DenseKind kind, int M, int N, int K, double* us_out = nullptr);  // and its estimated time
 size_t dense_part_bytes(const DensePlan& p, int M, int N);  // partial sums of a split plan (0 if not split)
 // Fills stages, slices and tiles of `a` for the plan and launches it, with the
 // reduction of a split. a.part: dense_part_bytes(plan, M, N) bytes.
 hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const DensePlan& p, DenseArgs a, hipStream_t st);
+
+hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st);  // of a split's partials
+
+// The product with W read as MXFP4 codes (dense_w4.hip): the plan and its estimated microseconds (tile -1: K too long
+// for its LDS), and its launch on x bf16 (a.x, a.x_ld), codes (a.w, a.w_ld) and exponent bytes.
+DensePlan dense_w4_plan(int M, int N, int K, double* us_out);
+hipError_t launch_dense_w4(const DensePlan& p, DenseArgs a, const uint8_t* scales, hipStream_t st);
 
 // MXFP4 encoding and decoding (mxfp4.hip)
 constexpr int kMxGroup = 32;

@@ -132,7 +132,7 @@ def test_quantize_refusals_on_device():
     with pytest.raises(ValueError):
         mx.linear_mxfp4(x[:, :32].to(torch.bfloat16).contiguous(), c, s)
     with pytest.raises(mx.MoEError):
-        mx.linear_mxfp4(torch.zeros(100, 64, dtype=torch.bfloat16, device=DEV), c, s,
+        mx.linear_mxfp4(torch.zeros(100, 64, dtype=torch.bfloat16, device=DEV), c, s, act="mxfp4",
                         ws=torch.empty(256, dtype=torch.uint8, device=DEV))
 
 

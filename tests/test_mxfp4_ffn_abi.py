@@ -47,8 +47,8 @@ def test_linear_refusals():
     for T, K, N, act in ((-1, 64, 16, 0), (65537, 64, 16, 0), (8, 48, 16, 0), (8, 65568, 16, 0), (8, 64, 0, 0),
                          (8, 64, 65537, 0), (8, 64, 16, 2)):
         assert size(T, K, N, act) == 0, (T, K, N, act)
-    assert 0 < size(64, 4096, 4096, 0) <= 256                       # streamed: nothing to keep
-    assert size(65, 4096, 4096, 0) >= 4096 * 4096 * 2               # the weights in bf16
+    assert 0 < size(1, 4096, 4096, 0) <= 256                        # streamed: nothing to keep
+    assert size(8192, 4096, 4096, 0) >= 4096 * 4096 * 2             # the weights in bf16
     assert 65 * 4096 // 2 < size(65, 4096, 4096, 1) < 4096 * 4096 * 2
     assert f(8, 64, 16, P, P, P, 2, P, 0, None, 0, None) == EUNSUP
     assert f(8, 48, 16, P, P, P, 0, P, 0, None, 0, None) == EUNSUP
@@ -58,10 +58,10 @@ def test_linear_refusals():
             args = [8, 64, 16, P, P, P, 0, P, 0, None, 0, None]
             args[i] = v
             assert f(*args) == EINVAL, (i, v)
-    need = size(100, 64, 16, 0)
-    assert f(100, 64, 16, P, P, P, 0, P, 0, None, need, None) == EINVAL
-    assert f(100, 64, 16, P, P, P, 0, P, 0, P + 16, need, None) == EINVAL
-    assert f(100, 64, 16, P, P, P, 0, P, 0, P, need - 1, None) == EWS
+    need = size(100, 64, 16, 1)
+    assert f(100, 64, 16, P, P, P, 1, P, 0, None, need, None) == EINVAL
+    assert f(100, 64, 16, P, P, P, 1, P, 0, P + 16, need, None) == EINVAL
+    assert f(100, 64, 16, P, P, P, 1, P, 0, P, need - 1, None) == EWS
     assert f(0, 64, 16, None, None, None, 0, None, 0, None, 0, None) == OK
 
 
