@@ -14,14 +14,6 @@ using namespace moe;
 
 constexpr int kMaxRows = 65536;   // T
 constexpr int kMaxLinear = 65536; // K and N of a linear
-#ifndef FEWROWS
-#define FEWROWS 64
-#endif
-#ifndef FFNROWS
-#define FFNROWS 64
-#endif
-constexpr int kFewRows = FEWROWS;
-constexpr int kFfnRows = FFNROWS;
 constexpr int kMaxFfn = 16384;    // H and I of the gated block: 2 I H values stay below 2^30
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -45,6 +37,22 @@ bool linear_ok(int T, int K, int N) {
          N <= kMaxLinear;
 }
 
+// Rows up to which a product runs in the streaming pass (few_rows.hip) rather than as a tile product. Every block of
+// the pass reads all activations, T K values, through its CU's share of the L2, while the tile product splits K over
+// blocks at the price of a second launch: at 4096 x 4096 (MXFP4, bf16 activations) 11.1 against 12.4 us at 32 rows and
+// 15.8 against 13.8 at 48; at K = 8192 the two meet at 16 rows (15.2 us at 17), at K = 2048 at 64 (10.2 against 11.0).
+// Activations that the pass encodes to MXFP4 itself cost it a little more (9.5 against 10.4 us at 17 rows of 4096,
+// 11.9 against 11.2 at 32).
+bool linear_few(int T, int K, int act) {
+  if (act == MOE_ACT_MXFP4) return T <= 32 && (long long)T * K <= 98304;
+  return T <= kSmallT && (long long)T * K <= 131072;
+}
+// The gated block: the same bytes over both products, by rounds of 256 blocks (of 8 gate rows; of 16). Measured to meet
+// at 42 rows of 4096 x 2048 (hidden x intermediate), 32 of 1024 x 4096, and past 64 of 2048 x 1024.
+bool ffn_few(int T, int H, int I) {
+  return T <= kSmallT && (long long)T * ((long long)H * ((I + 2047) / 2048) + (long long)I * ((H + 4095) / 4096)) <= 220000;
+}
+
 // ---- workspace layouts
 
 constexpr size_t kNoWorkspace = 256;  // the stated size where none is used (0 stands for unsupported)
@@ -66,7 +74,7 @@ LinearLayout linear_layout(int T, int K, int N, int act) {
     o = align256(o + bytes);
     return p;
   };
-  if (T > kFewRows) {
+  if (T > 0 && !linear_few(T, K, act)) {
     double us;
     L.plan = dense_plan(act == MOE_ACT_MXFP4 ? kDenseFp4 : kDenseBf16, T, N, K, &us);
     if (act == MOE_ACT_BF16) {
@@ -131,7 +139,7 @@ FfnLayout ffn_layout(int T, int H, int I) {
   L.h = 0;
   size_t o = align256((size_t)T * I * 2);
   L.part = o;
-  if (T > kFfnRows) {
+  if (T > 0 && !ffn_few(T, H, I)) {
     L.up = dense_plan(kDenseBf16, T, 2 * I, H);
     L.down = dense_plan(kDenseBf16, T, H, I);
     o = align256(o + max_of(dense_part_bytes(L.up, T, 2 * I), dense_part_bytes(L.down, T, H)));
@@ -219,7 +227,7 @@ int moe_linear_mxfp4(int32_t T, int32_t K, int32_t N, const uint16_t* x, const u
   if (!x || !codes || !scales || !out) return MOE_EINVAL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(out)) return MOE_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (T <= kFewRows) {
+  if (linear_few(T, K, act)) {
     FewRowsArgs a;
     memset(&a, 0, sizeof(a));
     a.T = T;
@@ -307,7 +315,7 @@ int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* 
   if (rc) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint16_t* h = h_saved ? h_saved : at<uint16_t>(workspace, L.h);
-  if (T <= kFfnRows) {
+  if (ffn_few(T, H, I)) {
     FewRowsArgs a;
     memset(&a, 0, sizeof(a));
     a.T = T;

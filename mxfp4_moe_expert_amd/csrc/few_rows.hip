@@ -176,7 +176,8 @@ template <int FMT, bool GATE>
 static hipError_t go_tokens(const FewRowsArgs& a, hipStream_t st) {
   if (a.T <= 16) return go_waves<FMT, GATE, 1>(a, st);
   if (a.T <= 32) return go_waves<FMT, GATE, 2>(a, st);
-  return go_waves<FMT, GATE, 4>(a, st);
+  if constexpr (FMT == kRowsMxA4) return hipErrorInvalidValue;  // the caller takes the tile product there
+  else return go_waves<FMT, GATE, 4>(a, st);
 }
 
 hipError_t launch_few_rows_mxfp4(const FewRowsArgs& a, hipStream_t st) {
