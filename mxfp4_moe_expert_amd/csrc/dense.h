@@ -29,6 +29,7 @@
 //     bf16 store.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "device.h"
@@ -163,8 +164,25 @@ __device__ __forceinline__ f32x4_t mfma_mx4(const u32x4_t& a, const u32x4_t& b, 
 }
 
 __device__ __forceinline__ uint2 pack4_bf16(const f32x4_t& v) {
-  return make_uint2((uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16),
-                    (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16));
+  return make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+}
+
+// Lane row g of a wave holds columns 4 g .. 4 g + 3 (8 bytes) of two 16-column blocks -> columns 8 g .. 8 g + 7 of the 32
+// (16 bytes), so that a store covers 64 consecutive bytes of each of 16 rows. unjoin is its inverse.
+__device__ __forceinline__ u32x4_t join_blocks(const uint2& p, const uint2& q) {
+  const auto a = __builtin_amdgcn_permlane32_swap(p.x, q.x, false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(p.y, q.y, false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(b[0], b[1], false, false);
+  return (u32x4_t){c[0], d[0], c[1], d[1]};
+}
+__device__ __forceinline__ void unjoin_blocks(const u32x4_t& v, uint2& p, uint2& q) {
+  const auto c = __builtin_amdgcn_permlane16_swap(v[0], v[2], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(v[1], v[3], false, false);
+  const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[1], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(d[0], d[1], false, false);
+  p = make_uint2(a[0], b[0]);
+  q = make_uint2(a[1], b[1]);
 }
 
 // Four consecutive outputs out[at .. at+3], of which `live` (1..4) exist;
@@ -203,18 +221,24 @@ __device__ __forceinline__ float ffn_act(float g, float u, float L) {
 // finds the clamp's mask of the unrounded value. Only a value within one
 // rounding of L moves, by less than one step instead of half of one; values
 // past L count as L whatever is stored.
-__device__ __forceinline__ uint16_t save_side(float v, float L) {
-  uint16_t b = f32_to_bf16(v);
-  const float w = bf16_to_f32(b);
-  if (v > L && !(w > L)) b = (uint16_t)(L >= 0.0f ? b + 1 : b - 1);
-  if (v <= L && w > L) b = (uint16_t)(L >= 0.0f ? b - 1 : b + 1);
-  return b;
+__device__ __forceinline__ uint32_t fix_side(uint32_t b, float v, float L) {  // b: v's bf16 bits
+  const float w = __uint_as_float(b << 16);
+  const uint32_t out = L >= 0.0f ? 1u : ~0u;  // one step away from zero, for L's sign
+  if (v > L && !(w > L)) b += out;
+  if (v <= L && w > L) b -= out;
+  return b & 0xffffu;
 }
-__device__ __forceinline__ uint16_t save_gate(float g, float L) { return save_side(g, L); }
+__device__ __forceinline__ uint2 save_gate4(const f32x4_t& g, float L) {
+  const uint2 p = pack4_bf16(g);
+  return make_uint2(fix_side(p.x & 0xffffu, g[0], L) | (fix_side(p.x >> 16, g[1], L) << 16),
+                    fix_side(p.y & 0xffffu, g[2], L) | (fix_side(p.y >> 16, g[3], L) << 16));
+}
 // both borders, by symmetry; L > 0
-__device__ __forceinline__ uint16_t save_up(float u, float L) {
-  const uint16_t s = __float_as_uint(u) >> 31 ? 0x8000u : 0u;
-  return (uint16_t)(save_side(fabsf(u), L) | s);
+__device__ __forceinline__ uint2 save_up4(const f32x4_t& u, float L) {
+  const uint2 p = pack4_bf16(u);
+  auto one = [&](uint32_t b, float v) { return fix_side(b & 0x7fffu, fabsf(v), L) | (b & 0x8000u); };
+  return make_uint2(one(p.x & 0xffffu, u[0]) | (one(p.x >> 16, u[1]) << 16),
+                    one(p.y & 0xffffu, u[2]) | (one(p.y >> 16, u[3]) << 16));
 }
 
 // Gradients of the gated product at the saved (g, u) for dh.
@@ -231,15 +255,25 @@ template <int MB, int NB>
 __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[NB][MB], void* out, bool fp32, int M, int N, int m0,
                                            int n0, int lane) {
   const int r = lane & 15, g = lane >> 4;
+  const bool joined = !fp32 && (N & 7) == 0;  // 16-byte pieces of bf16 rows exist whole or not at all
 #pragma unroll
   for (int c = 0; c < MB; ++c) {
     const int m = m0 + c * 16 + r;
-    if (m >= M) continue;
+    if (joined) {
+      uint16_t* row = static_cast<uint16_t*>(out) + (size_t)m * N;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int n = n0 + b * 16 + 4 * g;
-      if (n >= N) continue;
-      store4(out, fp32, (size_t)m * N + n, acc[b][c], N - n, (N & 3) == 0);
+      for (int b = 0; b < NB; b += 2) {
+        const int n = n0 + b * 16 + 8 * g;
+        const u32x4_t v = join_blocks(pack4_bf16(acc[b][c]), pack4_bf16(acc[b + 1][c]));
+        if (m < M && n < N) *reinterpret_cast<u32x4_t*>(row + n) = v;
+      }
+    } else if (m < M) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int n = n0 + b * 16 + 4 * g;
+        if (n >= N) continue;
+        store4(out, fp32, (size_t)m * N + n, acc[b][c], N - n, (N & 3) == 0);
+      }
     }
   }
 }
@@ -270,101 +304,215 @@ __device__ __forceinline__ void dense_tile(int bid, int tm, int tn, int& im, int
   in = o / h;
 }
 
-// FP4: both operands MXFP4 K-contiguous, with packed scales (see mxfp4.hip).
-template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, bool FP4, int EPI>
-__global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
-  constexpr int W = WGM * WGN;
-  constexpr int MB = BM / WGM / 16, NB = BN / WGN / 16;  // 16-row blocks per wave
-  constexpr int XB = BM * kStageB, WB = BN * kStageB;    // bytes per stage
-  constexpr int SXB = FP4 ? BM * 16 : 0, SWB = FP4 ? BN * 16 : 0;  // scales of two stages
-  constexpr int SI = (SXB + SWB + 1024 * W - 1) / (1024 * W);      // their loads per wave
-  constexpr uint32_t WBASE = NX * XB, SCALES = WBASE + NW * WB, SCB = SI * 1024 * W;  // LDS: X, W, scales
-  // scales are loaded SD pairs of stages ahead, so that the waits below cover them, into NS sets
-  constexpr int SD = NW <= 2 ? 1 : (NW + 1) / 2 - (NW & 1), NS = SD + 1;
-  static_assert(2 * SD - 1 >= NW - 2, "a stage's scales land with it");
-  static_assert(!FP4 || (!XT && !WT), "MXFP4 operands are K-contiguous");
-  static_assert(NW >= 2 && (NX == NW || NX == NW + 1), "the waits below assume it");
-  // X is loaded in the first k-step; with two stages of both, a load there would be waited for in the same stage, and
-  // both operands are loaded in the second
-  constexpr bool XK0 = NX > NW || NW > 2;
+// The LDS rings of a tile and the loads that fill them: NX stages of X, NW of W, then (MXFP4) NS sets of the packed
+// scales of two stages (see mxfp4.hip). Past the slice's stages a load writes zeros, so that every stage has its loads
+// and the waits can count them.
+template <bool XT, bool WT, int BM, int BN, int W, int NX, int NW, bool FP4, int NS, bool GATE>
+struct TileLoads {
+  static constexpr int XB = BM * kStageB, WB = BN * kStageB;              // bytes per stage
+  static constexpr int SXB = FP4 ? BM * 16 : 0, SWB = FP4 ? BN * 16 : 0;  // scales of two stages
+  static constexpr uint32_t WBASE = NX * XB, SCALES = WBASE + NW * WB, SCB = SXB + SWB;
   using SX = Stager<XT, BM, W>;
   using SW = Stager<WT, BN, W>;
-  static_assert(SX::NI * 1024 * W == XB && SW::NI * 1024 * W == WB, "tiles split evenly over the waves");
-  extern __shared__ __align__(16) unsigned char smem[];
-  lds_u8* const lds = (lds_u8*)smem;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int im, in;
-  dense_tile(blockIdx.x, a.tm, a.tn, im, in);
-  const int m0 = im * BM, n0 = in * (EPI == kEpiGate ? BN / 2 : BN);
-  const int Kb = a.K * 2 / (FP4 ? 4 : 1);  // bytes along k (K-contiguous operands)
-  const int st0 = blockIdx.y * a.slice_stages;
-  const int nst = min(a.slice_stages, a.stages - st0);
+  static constexpr int LX = SX::NI, LW = SW::NI;  // loads per wave and stage
+  static_assert(LX * 1024 * W == XB && LW * 1024 * W == WB, "tiles split evenly over the waves");
+  static_assert(!FP4 || (!XT && !WT), "MXFP4 operands are K-contiguous");
+  // Where the next stage of one operand comes from and goes to. Past the slice kleft is 0 or less: every lane is out of
+  // range and nothing is read.
+  struct Feed {
+    const char* src;
+    int kleft;    // bytes (K-contiguous) or k rows (transposed) from the stage's start to the slice's end
+    uint32_t at;  // ring place, LDS bytes
+  };
 
   SX sx;
   SW sw;
-  const char* xbase = static_cast<const char*>(a.x);
-  const char* wbase = static_cast<const char*>(a.w);
-  if constexpr (XT) {
-    sx.init_tr(wave, lane, a.x_ld, a.M - m0);
-    xbase += (size_t)m0 * 2;
-  } else {
-    sx.init_kc(wave, lane, a.x_ld, [&](int i) { return m0 + i < a.M ? i : -1; });
-    xbase += (size_t)m0 * a.x_ld;
-  }
-  if constexpr (WT) {
-    sw.init_tr(wave, lane, a.w_ld, a.N - n0);
-    wbase += (size_t)n0 * 2;
-  } else if constexpr (EPI == kEpiGate) {
-    // tile rows: 16 gate rows, then the matching 16 up rows, and so on
-    sw.init_kc(wave, lane, a.w_ld, [&](int i) {
-      const int c = n0 + (i >> 5) * 16 + (i & 15);
-      return c < a.I ? ((i >> 4) & 1) * a.I + c : -1;
-    });
-  } else {
-    sw.init_kc(wave, lane, a.w_ld, [&](int i) { return n0 + i < a.N ? i : -1; });
-    wbase += (size_t)n0 * a.w_ld;
-  }
-  const size_t xstep = XT ? (size_t)kStageK * a.x_ld : kStageB, wstep = WT ? (size_t)kStageK * a.w_ld : kStageB;
-  const int kx = XT ? a.K : Kb, kw = WT ? a.K : Kb;
-  constexpr int xk = XT ? kStageK : kStageB, wk = WT ? kStageK : kStageB;
+  Feed fx, fw;
+  size_t xstep, wstep;
+  int xat, wat;
+  uint32_t lds0;
+  int wave, lane, st0, nst, im, in;
 
-  const int xat = SX::first_k(wave, lane), wat = SW::first_k(wave, lane);
-
-  // The loads of stage st0 + i of one operand into its buffer buf, one at a time (op 0 .. NI - 1); past the slice: zeros
-  struct Source {
-    u32x4_t rsrc;
-    int kleft;
-    uint32_t at;
-  };
-  auto x_source = [&](int i, int buf) {
-    const int st = i < nst ? st0 + i : 0;
-    return Source{buffer_of(xbase + (size_t)st * xstep), i < nst ? kx - st * xk : 0, lds0 + (uint32_t)buf * XB};
-  };
-  auto w_source = [&](int i, int buf) {
-    const int st = i < nst ? st0 + i : 0;
-    return Source{buffer_of(wbase + (size_t)st * wstep), i < nst ? kw - st * wk : 0,
-                  lds0 + WBASE + (uint32_t)buf * WB};
-  };
-  auto load_scales = [&](int i) {  // of stages i and i + 1, i even
-    // packed: [two stages][16-row block][lane] u32; the tile's blocks are contiguous
+  __device__ __forceinline__ void init(const DenseArgs& a, uint32_t lds, int wave_, int lane_, int im_, int in_) {
+    lds0 = lds;
+    wave = wave_;
+    lane = lane_;
+    im = im_;
+    in = in_;
+    st0 = blockIdx.y * a.slice_stages;
+    nst = min(a.slice_stages, a.stages - st0);
+    const int m0 = im * BM, n0 = in * (GATE ? BN / 2 : BN);
+    const int kb = a.K * 2 / (FP4 ? 4 : 1);  // bytes along k (K-contiguous operands)
+    const char *xbase = static_cast<const char*>(a.x), *wbase = static_cast<const char*>(a.w);
+    if constexpr (XT) {
+      sx.init_tr(wave, lane, a.x_ld, a.M - m0);
+      xbase += (size_t)m0 * 2;
+    } else {
+      sx.init_kc(wave, lane, a.x_ld, [&](int i) { return m0 + i < a.M ? i : -1; });
+      xbase += (size_t)m0 * a.x_ld;
+    }
+    if constexpr (WT) {
+      sw.init_tr(wave, lane, a.w_ld, a.N - n0);
+      wbase += (size_t)n0 * 2;
+    } else if constexpr (GATE) {
+      // tile rows: 16 gate rows, then the matching 16 up rows, and so on
+      sw.init_kc(wave, lane, a.w_ld, [&](int i) {
+        const int c = n0 + (i >> 5) * 16 + (i & 15);
+        return c < a.I ? ((i >> 4) & 1) * a.I + c : -1;
+      });
+    } else {
+      sw.init_kc(wave, lane, a.w_ld, [&](int i) { return n0 + i < a.N ? i : -1; });
+      wbase += (size_t)n0 * a.w_ld;
+    }
+    xstep = XT ? (size_t)kStageK * a.x_ld : kStageB;
+    wstep = WT ? (size_t)kStageK * a.w_ld : kStageB;
+    xat = SX::first_k(wave, lane);
+    wat = SW::first_k(wave, lane);
+    constexpr int xk = XT ? kStageK : kStageB, wk = WT ? kStageK : kStageB;
+    const int end = st0 + nst;  // K up to the slice's end
+    fx = {xbase + (size_t)st0 * xstep, min(XT ? a.K : kb, end * xk) - st0 * xk, lds0};
+    fw = {wbase + (size_t)st0 * wstep, min(WT ? a.K : kb, end * wk) - st0 * wk, lds0 + WBASE};
+  }
+  // The loads 0 .. LX - 1 (LW - 1) of the next stage, then the step to the one after it
+  __device__ __forceinline__ void load_x(int op) const { sx.load(op, buffer_of(fx.src), fx.at, wave, xat, fx.kleft); }
+  __device__ __forceinline__ void load_w(int op) const { sw.load(op, buffer_of(fw.src), fw.at, wave, wat, fw.kleft); }
+  __device__ __forceinline__ void next_x() {
+    fx.src += xstep;
+    fx.kleft -= XT ? kStageK : kStageB;
+    fx.at = fx.at == lds0 + (NX - 1) * XB ? lds0 : fx.at + XB;
+  }
+  __device__ __forceinline__ void next_w() {
+    fw.src += wstep;
+    fw.kleft -= WT ? kStageK : kStageB;
+    fw.at = fw.at == lds0 + WBASE + (NW - 1) * WB ? lds0 + WBASE : fw.at + WB;
+  }
+  // The scales of stages i and i + 1, i even: [two stages][16-row block][lane] u32, the tile's blocks contiguous
+  __device__ __forceinline__ void load_scales(const DenseArgs& a, int i) const {
     const bool live = i < nst;
     const size_t pr = live ? (size_t)((st0 + i) >> 1) : 0;
     const u32x4_t rx = buffer_of(a.x_scales + (pr * a.x_blocks + (size_t)im * (BM / 16)) * 64);
     const u32x4_t rw = buffer_of(a.w_scales + (pr * a.w_blocks + (size_t)in * (BN / 16)) * 64);
     const uint32_t endx = (uint32_t)(a.x_blocks - im * (BM / 16)) * 256;
-    const uint32_t endw = min((uint32_t)(a.w_blocks - in * (BN / 16)) * 256, (uint32_t)SWB);
-#pragma unroll
-    for (int j = 0; j < SI; ++j) {
-      const uint32_t o = (uint32_t)(j * W + wave) * 1024;  // byte of the set
+    const uint32_t endw = (uint32_t)(a.w_blocks - in * (BN / 16)) * 256;
+    for (uint32_t o = (uint32_t)wave * 1024; o < SCB; o += W * 1024) {  // byte of the set
       const bool isw = o >= SXB;
       const uint32_t off = (isw ? o - SXB : o) + (uint32_t)lane * 16;
       load_lds16(isw ? rw : rx, live && off < (isw ? endw : endx) ? off : kLaneOff,
                  lds0 + SCALES + (uint32_t)((i >> 1) % NS) * SCB + o);
     }
+  }
+};
+
+// What a wave does with its sums: lane (r, g) holds acc[b][c][i] = C[m0 + 16 c + r][n0 + 16 b + 4 g + i] (gate: blocks b
+// alternate between gate and up, n0 is the first h column).
+template <int EPI, int MB, int NB>
+__device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t (&acc)[NB][MB], int m0, int n0,
+                                               int lane) {
+  if constexpr (EPI == kEpiStore || EPI == kEpiPartial) {
+    void* out = EPI == kEpiPartial ? static_cast<void*>(a.part + (size_t)blockIdx.y * a.M * a.N) : a.out;
+    store_tile<MB, NB>(acc, out, EPI == kEpiPartial || a.out_is_fp32, a.M, a.N, m0, n0, lane);
+    return;
+  }
+  // N and I are multiples of 8: 16-byte pieces exist whole or not at all
+  const int r = lane & 15, g = lane >> 4;
+  auto put = [&](uint16_t* p, const u32x4_t& v, bool live) {
+    if (live) *reinterpret_cast<u32x4_t*>(p) = v;
   };
+#pragma unroll
+  for (int c = 0; c < MB; ++c) {
+    const int m = m0 + c * 16 + r;
+    if constexpr (EPI == kEpiGate) {
+      uint16_t* hrow = static_cast<uint16_t*>(a.out) + (size_t)m * a.I;
+      uint16_t* grow = a.gu_out + (size_t)m * 2 * a.I;
+      auto act = [&](int b) {
+        f32x4_t h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = ffn_act(acc[b][c][i], acc[b + 1][c][i], a.limit);
+        return pack4_bf16(h);
+      };
+      if constexpr (NB % 4 == 0) {
+#pragma unroll
+        for (int b = 0; b < NB; b += 4) {
+          const int n = n0 + b * 8 + 8 * g;  // h column
+          const bool live = m < a.M && n < a.I;
+          put(hrow + n, join_blocks(act(b), act(b + 2)), live);
+          if (a.gu_out) {
+            put(grow + n, join_blocks(save_gate4(acc[b][c], a.limit), save_gate4(acc[b + 2][c], a.limit)), live);
+            put(grow + a.I + n, join_blocks(save_up4(acc[b + 1][c], a.limit), save_up4(acc[b + 3][c], a.limit)), live);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < NB; b += 2) {
+          const int n = n0 + b * 8 + 4 * g;
+          if (m >= a.M || n >= a.I) continue;
+          *reinterpret_cast<uint2*>(hrow + n) = act(b);
+          if (a.gu_out) {
+            *reinterpret_cast<uint2*>(grow + n) = save_gate4(acc[b][c], a.limit);
+            *reinterpret_cast<uint2*>(grow + a.I + n) = save_up4(acc[b + 1][c], a.limit);
+          }
+        }
+      }
+    } else {
+      const uint16_t* s = a.gu_in + (size_t)m * 2 * a.I;
+      uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I;
+#pragma unroll
+      for (int b = 0; b < NB; b += 2) {
+        const int n = n0 + b * 16 + 8 * g;
+        const bool live = m < a.M && n < a.N;
+        const u32x4_t zero = {0u, 0u, 0u, 0u};
+        const u32x4_t gj = live ? *reinterpret_cast<const u32x4_t*>(s + n) : zero;
+        const u32x4_t uj = live ? *reinterpret_cast<const u32x4_t*>(s + a.I + n) : zero;
+        uint2 gv[2], uv[2], dgv[2], duv[2];
+        unjoin_blocks(gj, gv[0], gv[1]);
+        unjoin_blocks(uj, uv[0], uv[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          f32x4_t dg, du;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t gw = i < 2 ? gv[j].x : gv[j].y, uw = i < 2 ? uv[j].x : uv[j].y;
+            float p, q;
+            ffn_act_grad(bf16_to_f32((uint16_t)(gw >> (16 * (i & 1)))), bf16_to_f32((uint16_t)(uw >> (16 * (i & 1)))),
+                         acc[b + j][c][i], a.limit, p, q);
+            dg[i] = p;
+            du[i] = q;
+          }
+          dgv[j] = pack4_bf16(dg);
+          duv[j] = pack4_bf16(du);
+        }
+        put(o + n, join_blocks(dgv[0], dgv[1]), live);
+        put(o + a.I + n, join_blocks(duv[0], duv[1]), live);
+      }
+    }
+  }
+}
+
+// The tile product. FP4: both operands MXFP4 K-contiguous, with packed scales.
+template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, bool FP4, int EPI>
+__global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
+  constexpr int W = WGM * WGN;
+  constexpr int MB = BM / WGM / 16, NB = BN / WGN / 16;  // 16-row blocks per wave
+  // scales are loaded SD pairs of stages ahead, so that the waits below cover them
+  constexpr int SD = NW <= 2 ? 1 : (NW + 1) / 2 - (NW & 1);
+  using L = TileLoads<XT, WT, BM, BN, W, NX, NW, FP4, SD + 1, EPI == kEpiGate>;
+  constexpr int XB = L::XB, WB = L::WB, LX = L::LX, LW = L::LW;
+  constexpr uint32_t WBASE = L::WBASE;
+  static_assert(2 * SD - 1 >= NW - 2, "a stage's scales land with it");
+  static_assert(NW >= 2 && (NX == NW || NX == NW + 1), "the waits below assume it");
+  // X is loaded in the first k-step; with two stages of both, a load there would be waited for in the same stage, and
+  // both operands are loaded in the second
+  constexpr bool XK0 = NX > NW || NW > 2;
+  extern __shared__ __align__(16) unsigned char smem[];
+  lds_u8* const lds = (lds_u8*)smem;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int im, in;
+  dense_tile(blockIdx.x, a.tm, a.tn, im, in);
+  L t;
+  t.init(a, (uint32_t)(uintptr_t)lds, wave, lane, im, in);
+  const int nst = t.nst;
 
   const int wm = wave / WGN, wn = wave % WGN;
   Reader<XT, BM, MB> rx;
@@ -385,17 +533,19 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
   u32x4_t xr[XR], xd[2][MB - XR], wf[2][NB];
   uint32_t sxv[MB], swv[NB];  // MXFP4: the lane's scale bytes of two stages, one per k-step
   auto read_scales = [&](int i) {
-    const lds_u8* sc = lds + SCALES + (uint32_t)((i >> 1) % NS) * SCB;
+    const lds_u8* sc = lds + L::SCALES + (uint32_t)((i >> 1) % (SD + 1)) * L::SCB;
 #pragma unroll
     for (int c = 0; c < MB; ++c) sxv[c] = *(const lds_u32*)(sc + ((wm * MB + c) * 64 + lane) * 4);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) swv[b] = *(const lds_u32*)(sc + SXB + ((wn * NB + b) * 64 + lane) * 4);
+    for (int b = 0; b < NB; ++b) swv[b] = *(const lds_u32*)(sc + L::SXB + ((wn * NB + b) * 64 + lane) * 4);
   };
   // The MFMAs of k-step kk (parity q of its stage), reading the next k-step's operands from the tiles xt and wt and
   // issuing the loads load(0) .. load(nload - 1). The order is pinned, or the compiler gathers the memory operations.
-  auto step = [&](auto kk, auto q, const lds_u8* xt, const lds_u8* wt, auto nload, auto&& load) {
+  auto step = [&](auto kk, auto q, const lds_u8* xt, const lds_u8* wt, auto nload, auto&& load, auto&& next) {
     constexpr int NM = MB * NB, NR = NB + MB - XR;
-    static_assert(nload <= NM, "one load per MFMA at most");
+    // the loads' places; then the sources move on, in the shadow of the last MFMAs
+    constexpr int NP = XK0 ? NM * 3 / 4 : NM - 2;
+    static_assert(nload <= NP, "one load per MFMA at most");
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       const int c = m / NB, b = m % NB;
@@ -404,7 +554,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
       else acc[b][c] = mfma_bf16(wf[kk][b], x, acc[b][c]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = spread(m - 1, NM, nload); i < spread(m, NM, nload); ++i) load(i);
+      for (int i = spread(m - 1, NP, nload); i < spread(m, NP, nload); ++i) load(i);
+      if (m == NP) next();
 #pragma unroll
       for (int i = spread(2 * m - 2, NM, NR); i < spread(2 * m, NM, NR); ++i) {
         if (i < NB) wf[1 - kk][i] = rw.read(wt, i, 1 - kk);
@@ -420,22 +571,22 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
   // Loads in order X(0) W(0) X(1) W(1) ..., as the loop continues it
   if constexpr (FP4) {
 #pragma unroll
-    for (int d = 0; d < SD; ++d) load_scales(2 * d);
+    for (int d = 0; d < SD; ++d) t.load_scales(a, 2 * d);
   }
 #pragma unroll
   for (int i = 0; i < (NX > NW ? NX : NW); ++i) {
     if (i < (XK0 ? NX - 1 : NX)) {
-      const Source s = x_source(i, i);
 #pragma unroll
-      for (int op = 0; op < SX::NI; ++op) sx.load(op, s.rsrc, s.at, wave, xat, s.kleft);
+      for (int op = 0; op < LX; ++op) t.load_x(op);
+      t.next_x();
     }
     if (i < NW) {
-      const Source s = w_source(i, i);
 #pragma unroll
-      for (int op = 0; op < SW::NI; ++op) sw.load(op, s.rsrc, s.at, wave, wat, s.kleft);
+      for (int op = 0; op < LW; ++op) t.load_w(op);
+      t.next_w();
     }
   }
-  dense_wait<(XK0 ? NX - 2 : NX - 1) * SX::NI + (NW - 1) * SW::NI>();
+  dense_wait<(XK0 ? NX - 2 : NX - 1) * LX + (NW - 1) * LW>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 #pragma unroll
@@ -446,28 +597,30 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
   auto stage = [&](int i, auto q) {
     if constexpr (FP4 && q == 0) read_scales(i);
     const int nx = bx + 1 == NX ? 0 : bx + 1, nw = bw + 1 == NW ? 0 : bw + 1;
-    if constexpr (XK0) {
-      const Source s = x_source(i - 1 + NX, bx == 0 ? NX - 1 : bx - 1);  // where stage i - 1 was
-      step(K0{}, q, lds + bx * XB, lds + WBASE + bw * WB, std::integral_constant<int, SX::NI>{},
-           [&](int op) { sx.load(op, s.rsrc, s.at, wave, xat, s.kleft); });
+    if constexpr (XK0) {  // X of stage i - 1 + NX, where stage i - 1 was
+      step(K0{}, q, lds + bx * XB, lds + WBASE + bw * WB, std::integral_constant<int, LX>{},
+           [&](int op) { t.load_x(op); }, [&]() { t.next_x(); });
     } else {
-      step(K0{}, q, lds + bx * XB, lds + WBASE + bw * WB, K0{}, [](int) {});
+      step(K0{}, q, lds + bx * XB, lds + WBASE + bw * WB, K0{}, [](int) {}, []() {});
     }
     // stage i + 1 has landed (this wave's part) and this wave has read stage i, then every wave
-    dense_wait<(NW - 2) * (SX::NI + SW::NI) + (NX > NW ? SX::NI : 0)>();
+    dense_wait<(NW - 2) * (LX + LW) + (NX > NW ? LX : 0)>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if constexpr (FP4 && q == 0) load_scales(i + 2 * SD);
-    const Source s = w_source(i + NW, bw);
+    if constexpr (FP4 && q == 0) t.load_scales(a, i + 2 * SD);
     if constexpr (XK0) {
-      step(K1{}, q, lds + nx * XB, lds + WBASE + nw * WB, std::integral_constant<int, SW::NI>{},
-           [&](int op) { sw.load(op, s.rsrc, s.at, wave, wat, s.kleft); });
+      step(K1{}, q, lds + nx * XB, lds + WBASE + nw * WB, std::integral_constant<int, LW>{},
+           [&](int op) { t.load_w(op); }, [&]() { t.next_w(); });
     } else {
-      const Source t = x_source(i + NX, bx);
-      step(K1{}, q, lds + nx * XB, lds + WBASE + nw * WB, std::integral_constant<int, SX::NI + SW::NI>{}, [&](int op) {
-        if (op < SX::NI) sx.load(op, t.rsrc, t.at, wave, xat, t.kleft);
-        else sw.load(op - SX::NI, s.rsrc, s.at, wave, wat, s.kleft);
-      });
+      step(K1{}, q, lds + nx * XB, lds + WBASE + nw * WB, std::integral_constant<int, LX + LW>{},
+           [&](int op) {
+             if (op < LX) t.load_x(op);
+             else t.load_w(op - LX);
+           },
+           [&]() {
+             t.next_x();
+             t.next_w();
+           });
     }
     bx = nx;
     bw = nw;
@@ -481,65 +634,23 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
     for (int i = 0; i < nst; ++i) stage(i, K0{});
   }
   dense_wait<0>();  // nothing may still write this block's LDS when it ends
+  dense_epilogue<EPI, MB, NB>(a, acc, im * BM + wm * MB * 16,
+                              EPI == kEpiGate ? in * (BN / 2) + wn * NB * 8 : in * BN + wn * NB * 16, lane);
+}
 
-  if constexpr (EPI == kEpiStore || EPI == kEpiPartial) {
-    void* out = EPI == kEpiPartial ? static_cast<void*>(a.part + (size_t)blockIdx.y * a.M * a.N) : a.out;
-    store_tile<MB, NB>(acc, out, EPI == kEpiPartial || a.out_is_fp32, a.M, a.N, m0 + wm * MB * 16, n0 + wn * NB * 16,
-                       lane);
-    return;
-  }
-  // lane (r, g): acc[b][c][i] = C[m = .. + 16 c + r][n = .. + 16 b + 4 g + i]
-  const int r = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int c = 0; c < MB; ++c) {
-    const int m = m0 + (wm * MB + c) * 16 + r;
-    if (m >= a.M) continue;
-    if constexpr (EPI == kEpiGate) {
-#pragma unroll
-      for (int b = 0; b < NB; b += 2) {
-        const int n = n0 + (wn * NB + b) * 8 + 4 * g;  // h column
-        if (n >= a.I) continue;                        // I % 8 == 0: four columns exist or none
-        f32x4_t h;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = ffn_act(acc[b][c][i], acc[b + 1][c][i], a.limit);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (size_t)m * a.I + n) = pack4_bf16(h);
-        if (a.gu_out) {
-          uint16_t* o = a.gu_out + (size_t)m * 2 * a.I + n;
-          uint16_t sg[4], su[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sg[i] = save_gate(acc[b][c][i], a.limit);
-            su[i] = save_up(acc[b + 1][c][i], a.limit);
-          }
-          *reinterpret_cast<uint2*>(o) =
-              make_uint2(sg[0] | ((uint32_t)sg[1] << 16), sg[2] | ((uint32_t)sg[3] << 16));
-          *reinterpret_cast<uint2*>(o + a.I) =
-              make_uint2(su[0] | ((uint32_t)su[1] << 16), su[2] | ((uint32_t)su[3] << 16));
-        }
-      }
-    } else if constexpr (EPI == kEpiGrad) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int n = n0 + (wn * NB + b) * 16 + 4 * g;
-        if (n >= a.N) continue;
-        const uint16_t* s = a.gu_in + (size_t)m * 2 * a.I + n;
-        const uint2 gv = *reinterpret_cast<const uint2*>(s), uv = *reinterpret_cast<const uint2*>(s + a.I);
-        f32x4_t dg, du;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t gw = i < 2 ? gv.x : gv.y, uw = i < 2 ? uv.x : uv.y;
-          float p, q;
-          ffn_act_grad(bf16_to_f32((uint16_t)(gw >> (16 * (i & 1)))), bf16_to_f32((uint16_t)(uw >> (16 * (i & 1)))),
-                       acc[b][c][i], a.limit, p, q);
-          dg[i] = p;
-          du[i] = q;
-        }
-        uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I + n;
-        *reinterpret_cast<uint2*>(o) = pack4_bf16(dg);
-        *reinterpret_cast<uint2*>(o + a.I) = pack4_bf16(du);
-      }
-    }
-  }
+// Allows KERNEL `bytes` of dynamic LDS on the current device, asking the runtime once per device and kernel (the call
+// is not needed again, and costs a small product part of its time).
+template <auto KERNEL>
+inline hipError_t allow_lds(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace moe

@@ -7,18 +7,18 @@ namespace moe {
 namespace {
 
 struct TileCfg {
-  int bm, bn, waves, nx, nw;  // nx, nw: stages of X and W in LDS
+  int bm, bn, nx, nw;  // nx, nw: stages of X and W in LDS
+  int scale_sets;      // MXFP4: sets of scales of two stages
 };
-// Two LDS rings fill the 160 KB of a CU (64 x 128: half of it, two blocks per CU). MXFP4: the scales take the place of
-// a stage of X in the largest tile.
-constexpr TileCfg kTiles[] = {{256, 256, 8, 3, 2}, {256, 128, 8, 3, 3}, {128, 128, 8, 4, 4}, {64, 128, 8, 3, 3}};
-constexpr TileCfg kTilesFp4[] = {{256, 256, 8, 2, 2}, {256, 128, 8, 3, 3}, {128, 128, 8, 4, 4}, {64, 128, 8, 3, 2}};
+// The rings fill the 160 KB of a CU (64 x 128: half of it, two blocks per CU). MXFP4: the scales take the place of a
+// stage of X in the largest tile.
+constexpr TileCfg kTiles[] = {{256, 256, 3, 2, 2}, {256, 128, 3, 3, 2}, {128, 128, 4, 4, 3}, {64, 128, 3, 3, 2}};
+constexpr TileCfg kTilesFp4[] = {{256, 256, 2, 2, 2}, {256, 128, 3, 3, 2}, {128, 128, 4, 4, 3}, {64, 128, 3, 3, 2}};
 constexpr int kNumTiles = 4;
+constexpr int kTileThreads = 512;
 
 constexpr size_t tile_lds(const TileCfg& t, bool fp4) {
-  const size_t sc = fp4 ? (((size_t)(t.bm + t.bn) * 16 + 1024 * t.waves - 1) / (1024 * t.waves)) * 1024 * t.waves : 0;
-  const int sets = t.nw <= 2 ? 2 : (t.nw + 1) / 2 - (t.nw & 1) + 1;
-  return ((size_t)t.nx * t.bm + (size_t)t.nw * t.bn) * kStageB + sets * sc;
+  return ((size_t)t.nx * t.bm + (size_t)t.nw * t.bn) * kStageB + (fp4 ? (size_t)t.scale_sets * (t.bm + t.bn) * 16 : 0);
 }
 
 // Sums the slices of a split K in order, then the epilogue of the product.
@@ -54,11 +54,8 @@ __global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (size_t)m * a.I + n) = pack4_bf16(h);
     if (a.gu_out) {
       uint16_t* o = a.gu_out + (size_t)m * 2 * a.I + n;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[i] = save_gate(g[i], a.limit);
-        o[a.I + i] = save_up(u[i], a.limit);
-      }
+      *reinterpret_cast<uint2*>(o) = save_gate4(g, a.limit);
+      *reinterpret_cast<uint2*>(o + a.I) = save_up4(u, a.limit);
     }
   } else if constexpr (EPI == kEpiGrad) {
     const f32x4_t dh = sum(n);
@@ -79,23 +76,22 @@ __global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
   }
 }
 
-template <class K>
-hipError_t run(K kern, const TileCfg& t, bool fp4, int slices, const DenseArgs& a, hipStream_t st) {
+template <auto KERNEL>
+hipError_t run(const TileCfg& t, bool fp4, int slices, const DenseArgs& a, hipStream_t st) {
   const size_t lds = tile_lds(t, fp4);
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  const hipError_t e = allow_lds<KERNEL>((int)lds);
   if (e != hipSuccess) return e;
-  kern<<<dim3((unsigned)(a.tm * a.tn), (unsigned)slices), t.waves * 64, lds, st>>>(a);
+  KERNEL<<<dim3((unsigned)(a.tm * a.tn), (unsigned)slices), kTileThreads, lds, st>>>(a);
   return hipGetLastError();
 }
 
 template <bool XT, bool WT, bool FP4, int EPI>
 hipError_t run_tile(int tile, int slices, const DenseArgs& a, hipStream_t st) {
   constexpr const TileCfg* t = FP4 ? kTilesFp4 : kTiles;
-  if (tile == 0) return run(&k_dense<XT, WT, 256, 256, 2, 4, t[0].nx, t[0].nw, FP4, EPI>, t[0], FP4, slices, a, st);
-  if (tile == 1) return run(&k_dense<XT, WT, 256, 128, 2, 4, t[1].nx, t[1].nw, FP4, EPI>, t[1], FP4, slices, a, st);
-  if (tile == 2) return run(&k_dense<XT, WT, 128, 128, 2, 4, t[2].nx, t[2].nw, FP4, EPI>, t[2], FP4, slices, a, st);
-  return run(&k_dense<XT, WT, 64, 128, 2, 4, t[3].nx, t[3].nw, FP4, EPI>, t[3], FP4, slices, a, st);
+  if (tile == 0) return run<&k_dense<XT, WT, 256, 256, 2, 4, t[0].nx, t[0].nw, FP4, EPI>>(t[0], FP4, slices, a, st);
+  if (tile == 1) return run<&k_dense<XT, WT, 256, 128, 2, 4, t[1].nx, t[1].nw, FP4, EPI>>(t[1], FP4, slices, a, st);
+  if (tile == 2) return run<&k_dense<XT, WT, 128, 128, 2, 4, t[2].nx, t[2].nw, FP4, EPI>>(t[2], FP4, slices, a, st);
+  return run<&k_dense<XT, WT, 64, 128, 2, 4, t[3].nx, t[3].nw, FP4, EPI>>(t[3], FP4, slices, a, st);
 }
 
 template <int EPI>
