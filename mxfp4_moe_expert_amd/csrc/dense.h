@@ -255,14 +255,15 @@ template <int MB, int NB>
 __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[NB][MB], void* out, bool fp32, int M, int N, int m0,
                                            int n0, int lane) {
   const int r = lane & 15, g = lane >> 4;
-  const bool joined = !fp32 && (N & 7) == 0;  // 16-byte pieces of bf16 rows exist whole or not at all
+  // 16-byte pieces of bf16 rows exist whole or not at all
+  const bool joined = NB % 2 == 0 && !fp32 && (N & 7) == 0;
 #pragma unroll
   for (int c = 0; c < MB; ++c) {
     const int m = m0 + c * 16 + r;
     if (joined) {
       uint16_t* row = static_cast<uint16_t*>(out) + (size_t)m * N;
 #pragma unroll
-      for (int b = 0; b < NB; b += 2) {
+      for (int b = 0; b + 1 < NB; b += 2) {
         const int n = n0 + b * 16 + 8 * g;
         const u32x4_t v = join_blocks(pack4_bf16(acc[b][c]), pack4_bf16(acc[b + 1][c]));
         if (m < M && n < N) *reinterpret_cast<u32x4_t*>(row + n) = v;

@@ -3,9 +3,12 @@
 // as it is stored. W's tile holds the 16 bytes of codes that a row has per
 // group of 32 values, eight groups (128-byte lines) per ring stage; lane
 // (r, g) of a k-step reads the 4 bytes of its 8 values and converts them to
-// bf16 (exact) right before the MFMAs, four conversions per operand against
-// MB MFMAs. The tile's exponent bytes are copied to LDS once, before the K
-// loop (a byte per row and k-step is then one LDS read).
+// bf16 (exact) under the previous k-step's last MFMAs. Conversions and MFMAs
+// share the SIMD's issue, so at 64 rows every wave takes all of them and
+// converts its own 16 columns only (0.375 against 0.40 us a stage with two
+// waves per column block; the bf16 product: 0.30). The tile's exponent bytes
+// are copied to LDS once, before the K loop (a byte per row and k-step is then
+// one LDS read).
 #include "dense.h"
 
 namespace moe {
@@ -42,19 +45,18 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense_w4(DenseArgs a, const u
   SW sw;
   sx.init_kc(wave, lane, a.x_ld, [&](int i) { return m0 + i < a.M ? i : -1; });
   sw.init_kc(wave, lane, a.w_ld, [&](int i) { return n0 + i < a.N ? i : -1; });
-  const char* xbase = static_cast<const char*>(a.x) + (size_t)m0 * a.x_ld;
   const char* wbase = static_cast<const char*>(a.w) + (size_t)n0 * a.w_ld;
   const int xat = SX::first_k(wave, lane), wat = SW::first_k(wave, lane);
 
-  struct Source {
-    u32x4_t rsrc;
-    int kleft;
-    uint32_t at;
-  };
-  auto x_source = [&](int i, int buf) {
-    const int st = i < nst ? st0 + i : 0;
-    return Source{buffer_of(xbase + (size_t)st * kStageB), i < nst ? 2 * a.K - st * kStageB : 0,
-                  lds0 + (uint32_t)buf * XB};
+  // the next X stage to load: from, bytes of k left in the slice (0 or less: nothing is read), ring place
+  const char* xsrc = static_cast<const char*>(a.x) + (size_t)m0 * a.x_ld + (size_t)st0 * kStageB;
+  int xleft = min(2 * a.K, (st0 + nst) * kStageB) - st0 * kStageB;
+  uint32_t xat_lds = lds0;
+  auto load_x = [&](int op) { sx.load(op, buffer_of(xsrc), xat_lds, wave, xat, xleft); };
+  auto next_x = [&]() {
+    xsrc += kStageB;
+    xleft -= kStageB;
+    xat_lds = xat_lds == lds0 + (NX - 1) * XB ? lds0 : xat_lds + XB;
   };
   auto load_w = [&](int j) {  // ring stage j: X stages 4 j .. 4 j + 3 of the slice
     const bool live = j * kWStage < nst;
@@ -81,9 +83,9 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense_w4(DenseArgs a, const u
   load_w(0);
 #pragma unroll
   for (int i = 0; i < NX - 1; ++i) {
-    const Source s = x_source(i, i);
 #pragma unroll
-    for (int op = 0; op < SX::NI; ++op) sx.load(op, s.rsrc, s.at, wave, xat, s.kleft);
+    for (int op = 0; op < SX::NI; ++op) load_x(op);
+    next_x();
   }
   {
     // exponent bytes of the slice; groups past K as 0 (their codes are zeros). scld is a multiple of 4.
@@ -106,38 +108,41 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense_w4(DenseArgs a, const u
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 
-  u32x4_t xf[2][MB];
-  uint32_t wq[2][NB], ws[2][NB];
-  auto read_w = [&](int b, int j, int t, int kk) {
-    wq[kk][b] = read_codes(lds + WBASE + (j & 1) * WB, wrow + b * (16 * kStageB), wkey, t & 7);
-    ws[kk][b] = srow[b * 16 * scld + j * 8 + (t & 7)];
+  u32x4_t xf[2][MB], wf[2][NB];
+  uint32_t wq[NB], ws[NB];  // the next k-step's codes and exponent bytes
+  auto read_w = [&](int b, int t) {
+    wq[b] = read_codes(lds + WBASE + ((t >> 3) & 1) * WB, wrow + b * (16 * kStageB), wkey, t & 7);
+    ws[b] = srow[b * 16 * scld + t];
+  };
+  auto convert = [&](int b) {
+    return __builtin_bit_cast(u32x4_t, fp4x8_to_bf16x8(wq[b], e8m0_scale_operand(ws[b])));
   };
 #pragma unroll
-  for (int b = 0; b < NB; ++b) read_w(b, 0, 0, 0);
+  for (int b = 0; b < NB; ++b) read_w(b, 0);
 #pragma unroll
   for (int c = 0; c < MB; ++c) xf[0][c] = rx.read(lds, c, 0);
-
-  // The MFMAs of k-step kk, reading k-step t (of the slice) into the other register set: X from tile xt
-  auto step = [&](auto kk, const lds_u8* xt, int t, auto nload, auto&& load) {
-    constexpr int NM = MB * NB, NR = NB + MB;
-    u32x4_t wf[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const bf16x8_t v = fp4x8_to_bf16x8(wq[kk][b], e8m0_scale_operand(ws[kk][b]));
-      wf[b] = __builtin_bit_cast(u32x4_t, v);
-    }
+  for (int b = 0; b < NB; ++b) wf[0][b] = convert(b);
+
+  // The MFMAs of k-step kk; between them the loads, the reads of k-step t (of the slice) into the other register set
+  // (X from tile xt), and late enough for those to have arrived the conversions of its W operands.
+  auto step = [&](auto kk, const lds_u8* xt, int t, auto nload) {
+    constexpr int NM = MB * NB, NR = NB + MB, CV = NM - NB;
+    static_assert(nload <= CV, "the loads end before the conversions begin");
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       const int c = m / NB, b = m % NB;
-      acc[b][c] = mfma_bf16(wf[b], xf[kk][c], acc[b][c]);
+      acc[b][c] = mfma_bf16(wf[kk][b], xf[kk][c], acc[b][c]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = spread(m - 1, NM, nload); i < spread(m, NM, nload); ++i) load(i);
+      for (int i = spread(m - 1, CV, nload); i < spread(m, CV, nload); ++i) load_x(i);
 #pragma unroll
       for (int i = spread(2 * m - 2, NM, NR); i < spread(2 * m, NM, NR); ++i) {
-        if (i < NB) read_w(i, t >> 3, t, 1 - kk);
+        if (i < NB) read_w(i, t);
         else xf[1 - kk][i - NB] = rx.read(xt, i - NB, 1 - kk);
       }
+      if (nload > 0 && m == CV) next_x();
+      if (m >= CV) wf[1 - kk][m - CV] = convert(m - CV);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -146,16 +151,15 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense_w4(DenseArgs a, const u
   int bx = 0;
   for (int i = 0; i < nst; ++i) {
     const int nx = bx + 1 == NX ? 0 : bx + 1;
-    const Source s = x_source(i - 1 + NX, bx == 0 ? NX - 1 : bx - 1);  // where stage i - 1 was
-    step(K0{}, lds + bx * XB, 2 * i + 1, std::integral_constant<int, SX::NI>{},
-         [&](int op) { sx.load(op, s.rsrc, s.at, wave, xat, s.kleft); });
+    // X of stage i - 1 + NX is loaded where stage i - 1 was
+    step(K0{}, lds + bx * XB, 2 * i + 1, std::integral_constant<int, SX::NI>{});
     // X of stage i + 1 has landed (W of its ring stage was loaded before it) and this wave has read stage i, then
     // every wave
     dense_wait<(NX - 2) * SX::NI>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if (i % kWStage == 0) load_w(i / kWStage + 1);  // over ring stage i / 4 - 1, which every wave has read
-    step(K1{}, lds + nx * XB, 2 * i + 2, K0{}, [](int) {});
+    step(K1{}, lds + nx * XB, 2 * i + 2, K0{});
     bx = nx;
   }
   dense_wait<0>();  // nothing may still write this block's LDS when it ends
@@ -193,7 +197,7 @@ hipError_t go(int tile, int slices, const DenseArgs& a, const uint8_t* scales, s
                                                                                     w4_scld(a.slice_stages));
     return hipGetLastError();
   };
-  if (tile == 0) return run(&k_dense_w4<64, 128, 2, 4, kW4[0].nx, EPI>);
+  if (tile == 0) return run(&k_dense_w4<64, 128, 1, 8, kW4[0].nx, EPI>);
   if (tile == 1) return run(&k_dense_w4<128, 128, 2, 4, kW4[1].nx, EPI>);
   return run(&k_dense_w4<256, 128, 2, 4, kW4[2].nx, EPI>);
 }
@@ -202,7 +206,8 @@ hipError_t go(int tile, int slices, const DenseArgs& a, const uint8_t* scales, s
 
 DensePlan dense_w4_plan(int M, int N, int K, double* us_out) {
   const int nst = (K + 63) / 64;
-  constexpr double stage_us[kNumW4] = {0.36, 0.52, 0.85}, start_us = 4.0;
+  // full-chip stage times at 4096 x 4096 weights, 1000 rows of 128 x 128 tiles and 2048 of 256 x 128
+  constexpr double stage_us[kNumW4] = {0.38, 0.53, 0.83}, start_us = 4.0;
   DensePlan best = {-1, 0};
   double best_us = 1e30;
   for (int t = 0; t < kNumW4; ++t) {

@@ -9,10 +9,9 @@
 // E2M1. A group with an Inf or NaN gets the byte 255 (NaN), and reads back as
 // NaN; its codes are 0.
 //
-// Memory-bound in both directions. Four lanes share a group, eight values
-// each, so a wave reads 1 KB (bf16) or 2 KB (fp32) of consecutive values per
-// step and writes 256 consecutive code bytes; the group's maximum is two lane
-// exchanges within a quad.
+// Memory-bound in both directions. A lane takes 16 bytes per load (8 values of
+// 16 bits or 4 of 32), consecutive lanes consecutive bytes, so 4 or 8 lanes
+// share a group and its maximum is two or three lane exchanges.
 #include "device.h"
 #include "internal.h"
 
@@ -20,101 +19,119 @@ namespace moe {
 
 typedef __attribute__((ext_vector_type(8))) float f32x8_t;
 
+// Eight 16-bit values as fp32.
 template <int DT>
-__device__ __forceinline__ f32x8_t load8(const void* p, size_t at) {
+__device__ __forceinline__ f32x8_t widen8(const u32x4_t& a) {
   f32x8_t v;
-  if constexpr (DT == kDtF32) {
-    const f32x4_t* s = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + at);
-    const f32x4_t a = s[0], b = s[1];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
-    }
-  } else {
-    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == kDtBf16) {
-        v[2 * i] = __uint_as_float(a[i] << 16);
-        v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-      } else {
-        v[2 * i] = f16_bits_to_f32(a[i] & 0xffffu);
-        v[2 * i + 1] = f16_bits_to_f32(a[i] >> 16);
-      }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == kDtBf16) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    } else {
+      v[2 * i] = f16_bits_to_f32(a[i] & 0xffffu);
+      v[2 * i + 1] = f16_bits_to_f32(a[i] >> 16);
     }
   }
   return v;
 }
 
+// Largest magnitude of a lane's values as bits: magnitudes compare as integers, Inf and NaN above every finite value.
+template <class V, int N>
+__device__ __forceinline__ uint32_t top_bits(const V& v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return m;
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_max(uint32_t m) {
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+  return lane_max<0x4E>(lane_max<0xB1>(m));  // quad_perm [1,0,3,2], then [2,3,0,1]
+}
+// The exponent byte of a group with largest magnitude m (bits): 255 if it is not finite. scale: for the conversion.
+__device__ __forceinline__ uint32_t group_byte(uint32_t m, float& scale) {
+  const uint32_t field = m >> 23, e = field > 2u ? field - 2u : 0u;
+  scale = e8m0_scale_operand(e);
+  return field == 255u ? 255u : e;
+}
+
 // The quad's four lanes hold one group, eight values each -> the lane's codes
 // (one dword) and the group's exponent byte.
 __device__ __forceinline__ uint32_t quad_encode(const f32x8_t& v, uint32_t& byte) {
-  // magnitudes compare as integers, Inf and NaN above every finite value
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));  // quad_perm [1,0,3,2]
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));  // quad_perm [2,3,0,1]
-  const uint32_t field = m >> 23;
-  const bool bad = field == 255u;
-  const uint32_t e = field > 2u ? field - 2u : 0u;
-  byte = bad ? 255u : e;
-  const float sc = e8m0_scale_operand(e);
+  float sc;
+  byte = group_byte(quad_max(top_bits<f32x8_t, 8>(v)), sc);
   uint32_t c = 0;
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], sc, 0);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], sc, 1);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], sc, 2);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], sc, 3);
-  return bad ? 0u : c;
+  return byte == 255u ? 0u : c;
+}
+// Eight lanes hold one group, four values each -> the lane's codes (16 bits) and the exponent byte.
+__device__ __forceinline__ uint32_t oct_encode(const f32x4_t& v, uint32_t& byte) {
+  float sc;
+  byte = group_byte(lane_max<0x141>(quad_max(top_bits<f32x4_t, 4>(v))), sc);  // row_half_mirror: the other quad of 8
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], sc, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], sc, 1);
+  return byte == 255u ? 0u : c;
 }
 
-// Units of 8 values; a thread takes kQuantUnits of them, 256 apart, and has
-// all their loads in flight together.
-constexpr int kQuantUnits = 4;
+// Units of 16 bytes of x; a thread takes kQuantUnits of them, 256 apart, and
+// has all their loads in flight together.
+constexpr int kQuantUnits = 8;
 constexpr long long kMaxBlocks = 0xffffff;  // of 256 threads: a grid holds fewer than 2^32 threads
 
 template <int DT>
 __global__ __launch_bounds__(256) void k_mxfp4_quantize(const void* x, long long units, int upr, long long ldx,
-                                                        uint32_t* codes, uint8_t* scales) {
+                                                        uint8_t* codes, uint8_t* scales) {
+  constexpr int V = DT == kDtF32 ? 4 : 8, LPG = kMxGroup / V;  // values per unit, lanes per group
   const long long u0 = (long long)blockIdx.x * (256 * kQuantUnits) + threadIdx.x;
-  f32x8_t v[kQuantUnits];
+  u32x4_t v[kQuantUnits];
 #pragma unroll
   for (int i = 0; i < kQuantUnits; ++i) {
-    const long long u = u0 + i * 256;
-    if (u >= units) continue;  // units % 4 == 0: a quad is live or not as one
-    size_t at = (size_t)u * 8;
-    if (ldx != (long long)upr * 8) {
+    const long long u = min(u0 + i * 256, units - 1);
+    size_t at = (size_t)u * V;
+    if (ldx != (long long)upr * V) {
       const long long row = u / upr;
-      at = (size_t)row * ldx + (size_t)(u - row * upr) * 8;
+      at = (size_t)row * ldx + (size_t)(u - row * upr) * V;
     }
-    v[i] = load8<DT>(x, at);
+    v[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(x) + at * (16 / V));
   }
 #pragma unroll
   for (int i = 0; i < kQuantUnits; ++i) {
     const long long u = u0 + i * 256;
-    if (u >= units) continue;
+    if (u >= units) continue;  // units are whole groups: a group's lanes are live or not as one
     uint32_t byte;
-    codes[u] = quad_encode(v[i], byte);
-    if ((u & 3) == 0) scales[u >> 2] = (uint8_t)byte;
+    if constexpr (DT == kDtF32) {
+      const uint32_t c = oct_encode(__builtin_bit_cast(f32x4_t, v[i]), byte);
+      reinterpret_cast<uint16_t*>(codes)[u] = (uint16_t)c;
+    } else {
+      reinterpret_cast<uint32_t*>(codes)[u] = quad_encode(widen8<DT>(v[i]), byte);
+    }
+    if ((u & (LPG - 1)) == 0) scales[u / LPG] = (uint8_t)byte;
   }
 }
 
 hipError_t launch_mxfp4_quantize(long long rows, int K, int dtype, const void* x, long long ldx, uint8_t* codes,
                                  uint8_t* scales, hipStream_t st) {
-  const int upr = K / 8;
+  const int upr = K / (dtype == kDtF32 ? 4 : 8);
   const long long units = rows * upr;
   if (K % kMxGroup || ldx < K) return hipErrorInvalidValue;
   if (units <= 0) return hipSuccess;
   const long long nb = (units + 256 * kQuantUnits - 1) / (256 * kQuantUnits);
   if (nb > kMaxBlocks) return hipErrorInvalidValue;
-  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-  if (dtype == kDtBf16) k_mxfp4_quantize<kDtBf16><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, c, scales);
-  else if (dtype == kDtF32) k_mxfp4_quantize<kDtF32><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, c, scales);
-  else if (dtype == kDtF16) k_mxfp4_quantize<kDtF16><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, c, scales);
+  if (dtype == kDtBf16) k_mxfp4_quantize<kDtBf16><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, codes, scales);
+  else if (dtype == kDtF32) k_mxfp4_quantize<kDtF32><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, codes, scales);
+  else if (dtype == kDtF16) k_mxfp4_quantize<kDtF16><<<(unsigned)nb, 256, 0, st>>>(x, units, upr, ldx, codes, scales);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
+
+constexpr int kDecodeUnits = 4;
 
 // Decoding: a unit is 8 codes (one dword) and its group's byte. Byte 255
 // makes the hardware conversion return NaN.
@@ -143,16 +160,16 @@ __device__ __forceinline__ void decode_unit(uint32_t c, uint32_t byte, void* out
 template <int DT>
 __global__ __launch_bounds__(256) void k_mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales,
                                                           long long units, void* out) {
-  const long long u0 = (long long)blockIdx.x * (256 * kQuantUnits) + threadIdx.x;
-  uint32_t c[kQuantUnits], b[kQuantUnits];
+  const long long u0 = (long long)blockIdx.x * (256 * kDecodeUnits) + threadIdx.x;
+  uint32_t c[kDecodeUnits], b[kDecodeUnits];
 #pragma unroll
-  for (int i = 0; i < kQuantUnits; ++i) {
+  for (int i = 0; i < kDecodeUnits; ++i) {
     const long long u = min(u0 + i * 256, units - 1);
     c[i] = codes[u];
     b[i] = scales[u >> 2];
   }
 #pragma unroll
-  for (int i = 0; i < kQuantUnits; ++i) {
+  for (int i = 0; i < kDecodeUnits; ++i) {
     const long long u = u0 + i * 256;
     if (u < units) decode_unit<DT>(c[i], b[i], out, (size_t)u * 8);
   }
@@ -163,7 +180,7 @@ hipError_t launch_mxfp4_dequantize(long long rows, int K, const uint8_t* codes, 
   const long long units = rows * (K / 8);
   if (K % kMxGroup) return hipErrorInvalidValue;
   if (units <= 0) return hipSuccess;
-  const long long nb = (units + 256 * kQuantUnits - 1) / (256 * kQuantUnits);
+  const long long nb = (units + 256 * kDecodeUnits - 1) / (256 * kDecodeUnits);
   if (nb > kMaxBlocks) return hipErrorInvalidValue;
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   if (dtype == kDtBf16) k_mxfp4_dequantize<kDtBf16><<<(unsigned)nb, 256, 0, st>>>(c, scales, units, out);
@@ -174,43 +191,55 @@ hipError_t launch_mxfp4_dequantize(long long rows, int K, const uint8_t* codes, 
 
 // ---- operands of the 4-bit x 4-bit product
 //
-// Packed scales: the product's k-step j (128 values) of two stages p (512 values) takes, in lane (r, g), the exponent byte of row 16 b + r, group
+// Packed scales: the product's k-step j (128 values) of two stages p (512
+// values) takes, in lane (r, g), the exponent byte of row 16 b + r, group
 // 16 p + 4 j + g. Packed as u32 [p][b][16 g + r], byte j: the scales of
 // consecutive row blocks are contiguous and lane-ordered. Groups past K get
 // the byte 0 (their codes are zeros, and 2^-127 keeps the products zero).
-__device__ __forceinline__ size_t mxfp4_pack_at(int row, int group, int blocks) {
-  return (((size_t)(group >> 4) * blocks + (row >> 4)) * 64 + (group & 3) * 16 + (row & 15)) * 4 + ((group >> 2) & 3);
-}
-
-// Blocks [0, xblocks): x [T][K] bf16 to codes and packed scales, a unit of 8
-// values per thread, with the unit index running over whole pairs of
-// stages (so that the groups past K are written too). Blocks from
-// xblocks on: the weights' exponent bytes to the packed order, a thread per
-// dword (row, p, g).
-__global__ __launch_bounds__(256) void k_mxfp4_prep(int T, int K, const uint16_t* x, uint32_t* xcodes, uint8_t* xpack,
-                                                    unsigned xblocks, int N, const uint8_t* wscales, uint8_t* wpack) {
+//
+// Blocks [0, xblocks): x [T][K] bf16 to codes and packed scales, a block per
+// 16 rows and 512 values, each wave a row at a time (1 KB per load): the
+// block's 256 scale bytes meet in LDS and are stored as one piece (stored byte
+// by byte, the rows' blocks on several XCDs shared their lines). Blocks from
+// xblocks on: the weights' exponent bytes to the packed order, a dword per
+// thread in its place's order.
+__global__ __launch_bounds__(256) void k_mxfp4_prep(int T, int K, const uint16_t* x, uint32_t* xcodes, uint32_t* xpack,
+                                                    unsigned xblocks, int N, const uint8_t* wscales, uint32_t* wpack) {
   const int pairs = mxfp4_pairs(K);
   if (blockIdx.x < xblocks) {
-    const int ups = pairs * 64;  // units per row, padded
-    const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int row = (int)(u / ups), i = (int)(u - (long long)row * ups);
-    if (row >= T) return;  // ups % 4 == 0: whole pairs leave
-    uint32_t byte = 0;
-    if (i * 8 < K) {  // K % 32 == 0: a quad is in or out as one
-      const f32x8_t v = load8<kDtBf16>(x, (size_t)row * K + (size_t)i * 8);
-      xcodes[(size_t)row * (K / 8) + i] = quad_encode(v, byte);
+    __shared__ __align__(16) uint8_t pack[256];
+    const int tb = (T + 15) / 16, p = (int)(blockIdx.x / tb), b = (int)(blockIdx.x - (unsigned)p * tb);
+    const int unit = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = p * 64 + unit;  // K % 32 == 0: a quad is in or out as one
+    u32x4_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 16 * b + 4 * j + wave;
+      v[j] = (u32x4_t){0u, 0u, 0u, 0u};
+      if (row < T && col * 8 < K) v[j] = *reinterpret_cast<const u32x4_t*>(x + (size_t)row * K + (size_t)col * 8);
     }
-    if ((i & 3) == 0) xpack[mxfp4_pack_at(row, i >> 2, (T + 15) / 16)] = (uint8_t)byte;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 4 * j + wave, row = 16 * b + r, group = unit >> 2;
+      uint32_t byte;
+      const uint32_t c = quad_encode(widen8<kDtBf16>(v[j]), byte);
+      if (row < T && col * 8 < K) xcodes[(size_t)row * (K / 8) + col] = c;
+      if ((unit & 3) == 0) pack[((group & 3) * 16 + r) * 4 + (group >> 2)] = col * 8 < K ? (uint8_t)byte : (uint8_t)0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) xpack[((size_t)p * tb + b) * 64 + threadIdx.x] = reinterpret_cast<const uint32_t*>(pack)[threadIdx.x];
   } else {
+    const int nb = (N + 15) / 16;
     const long long u = (long long)(blockIdx.x - xblocks) * 256 + threadIdx.x;
-    const int row = (int)(u / (pairs * 4)), q = (int)(u - (long long)row * (pairs * 4));
-    if (row >= N) return;
-    const int G = K / kMxGroup, g0 = (q >> 2) * 16 + (q & 3);
+    const long long blk = u >> 6;  // p * nb + b
+    const int p = (int)(blk / nb), row = (int)(blk - (long long)p * nb) * 16 + ((int)u & 15), g = ((int)u >> 4) & 3;
+    if (p >= pairs || row >= N) return;
+    const int G = K / kMxGroup, g0 = p * 16 + g;
     uint32_t d = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (g0 + 4 * j < G) d |= (uint32_t)wscales[(size_t)row * G + g0 + 4 * j] << (8 * j);
-    *reinterpret_cast<uint32_t*>(wpack + mxfp4_pack_at(row, g0, (N + 15) / 16)) = d;
+    wpack[u] = d;
   }
 }
 
@@ -218,11 +247,10 @@ hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, u
                              const uint8_t* wscales, uint32_t* wpack, hipStream_t st) {
   if (K % kMxGroup || T <= 0 || N <= 0) return hipErrorInvalidValue;
   const long long pairs = mxfp4_pairs(K);
-  const long long xb = ((long long)T * pairs * 64 + 255) / 256, wb = ((long long)N * pairs * 4 + 255) / 256;
+  const long long xb = pairs * mxfp4_blocks(T), wb = (pairs * mxfp4_blocks(N) * 64 + 255) / 256;
   if (xb + wb > kMaxBlocks) return hipErrorInvalidValue;
-  k_mxfp4_prep<<<(unsigned)(xb + wb), 256, 0, st>>>(T, K, x, reinterpret_cast<uint32_t*>(xcodes),
-                                                    reinterpret_cast<uint8_t*>(xpack), (unsigned)xb, N, wscales,
-                                                    reinterpret_cast<uint8_t*>(wpack));
+  k_mxfp4_prep<<<(unsigned)(xb + wb), 256, 0, st>>>(T, K, x, reinterpret_cast<uint32_t*>(xcodes), xpack, (unsigned)xb, N,
+                                                    wscales, wpack);
   return hipGetLastError();
 }
 
@@ -233,16 +261,16 @@ __global__ __launch_bounds__(256) void k_mxfp4_expand(const uint32_t* codes, con
                                                       uint16_t* w, unsigned wblocks, int T, int N, const uint16_t* dy,
                                                       uint16_t* dyp, int ld) {
   if (blockIdx.x < wblocks) {
-    const long long u0 = (long long)blockIdx.x * (256 * kQuantUnits) + threadIdx.x;
-    uint32_t c[kQuantUnits], b[kQuantUnits];
+    const long long u0 = (long long)blockIdx.x * (256 * kDecodeUnits) + threadIdx.x;
+    uint32_t c[kDecodeUnits], b[kDecodeUnits];
 #pragma unroll
-    for (int i = 0; i < kQuantUnits; ++i) {
+    for (int i = 0; i < kDecodeUnits; ++i) {
       const long long u = min(u0 + i * 256, units - 1);
       c[i] = codes[u];
       b[i] = scales[u >> 2];
     }
 #pragma unroll
-    for (int i = 0; i < kQuantUnits; ++i) {
+    for (int i = 0; i < kDecodeUnits; ++i) {
       const long long u = u0 + i * 256;
       if (u < units) decode_unit<kDtBf16>(c[i], b[i], w, (size_t)u * 8);
     }
@@ -263,7 +291,7 @@ hipError_t launch_mxfp4_expand(int N, int K, const uint8_t* codes, const uint8_t
                                const uint16_t* dy, uint16_t* dyp, int ld, hipStream_t st) {
   if (K % kMxGroup || N <= 0) return hipErrorInvalidValue;
   const long long units = (long long)N * (K / 8);
-  const long long wb = (units + 256 * kQuantUnits - 1) / (256 * kQuantUnits);
+  const long long wb = (units + 256 * kDecodeUnits - 1) / (256 * kDecodeUnits);
   const long long db = dy ? ((long long)T * (ld / 8) + 255) / 256 : 0;
   if (ld % 8 || wb + db > kMaxBlocks) return hipErrorInvalidValue;
   k_mxfp4_expand<<<(unsigned)(wb + db), 256, 0, st>>>(reinterpret_cast<const uint32_t*>(codes), scales, units, w,
