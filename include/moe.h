@@ -337,11 +337,10 @@ int moe_linear_mxfp4_dx(int32_t T, int32_t K, int32_t N, const uint16_t* dy, con
  *   x   [T][H] bf16;  w13 [2I][H] bf16, rows [0,I) W1 (gate), [I,2I) W3 (up);
  *   w2  [H][I] bf16;  out [T][H] bf16 (out_is_fp32 = 0) or f32
  *   limit  L > 0 (INFINITY: no clamp)
- *   gu_saved [T][2I] bf16, h_saved [T][I] bf16: both given, they are written
+ *   gu_saved [T][2I] f32 (g, then u), h_saved [T][I] bf16: both given, they are written
  *   for moe_gated_ffn_backward; both NULL otherwise.
- * h, g and u are rounded to bf16 (h enters the second product as bf16); g and
- * u are rounded without crossing L or -L, so the backward pass finds the
- * clamp's masks of the unrounded values. NaN inputs give NaN outputs.
+ * h is rounded to bf16 as an operand of the second product; g and u are kept in
+ * fp32. NaN inputs give NaN outputs.
  * Two launches (both projections, activation and product in the first; more
  * where K is split, as for moe_linear_mxfp4).
  *   workspace: moe_gated_ffn_workspace_size(T, H, I) bytes, 256-byte aligned,
@@ -349,7 +348,7 @@ int moe_linear_mxfp4_dx(int32_t T, int32_t K, int32_t N, const uint16_t* dy, con
  * Supported: H and I multiples of 8 up to 16384, 0 <= T <= 65536. */
 size_t moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
 int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* x, const uint16_t* w13,
-                  const uint16_t* w2, uint16_t* gu_saved, uint16_t* h_saved, void* out, int32_t out_is_fp32,
+                  const uint16_t* w2, float* gu_saved, uint16_t* h_saved, void* out, int32_t out_is_fp32,
                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of the block for the output gradient dy [T][H] bf16, from the
@@ -362,7 +361,7 @@ int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* 
  *   workspace: moe_gated_ffn_backward_workspace_size(T, H, I) bytes, as above. */
 size_t moe_gated_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I);
 int moe_gated_ffn_backward(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* dy, const uint16_t* x,
-                           const uint16_t* w13, const uint16_t* w2, const uint16_t* gu_saved,
+                           const uint16_t* w13, const uint16_t* w2, const float* gu_saved,
                            const uint16_t* h_saved, uint16_t* dx, void* dw13, void* dw2, int32_t dw_is_fp32,
                            void* workspace, size_t workspace_bytes, void* stream);
 

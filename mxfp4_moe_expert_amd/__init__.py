@@ -570,10 +570,13 @@ def _matrix(t, dtype, name):
     return t.shape[0], t.shape[1], t.get_device()
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(index, name, *args):
     """Calls a library function with device ``index`` current, its current stream appended."""
-    fn = getattr(lib(), name)
-    if index == torch.cuda.current_device():
+    fn = getattr(_lib or lib(), name)
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -648,12 +651,15 @@ def dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None):
 
 
 def _mxfp4_weight(codes, scales, index):
-    """N, K and the pointers of an MXFP4 matrix [N][K]."""
-    N, half, _ = _matrix(codes, torch.uint8, "codes")
-    if half == 0 or half % 16:
-        raise ValueError("codes: shape [N, K/2] with K a positive multiple of 32 expected")
-    return (N, half * 2, _arg(codes, torch.uint8, (N, half), index, "codes"),
-            _arg(scales, torch.uint8, (N, half // 16), index, "scales"))
+    """N, K and the pointers of an MXFP4 matrix [N][K] on device ``index``."""
+    if (isinstance(codes, torch.Tensor) and codes.dtype is torch.uint8 and codes.dim() == 2
+            and codes.get_device() == index and codes.is_contiguous()):
+        N, half = codes.shape
+        if half and half % 16 == 0:
+            return N, half * 2, codes.data_ptr(), _arg(scales, torch.uint8, (N, half // 16), index, "scales")
+    _matrix(codes, torch.uint8, "codes")
+    _arg(codes, torch.uint8, codes.shape, index, "codes")
+    raise ValueError("codes: shape [N, K/2] with K a positive multiple of 32 expected")
 
 
 def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None):
@@ -663,15 +669,20 @@ def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None
     mode = _ACTS.get(act)
     if mode is None:
         raise ValueError(f"act {act!r}, expected one of {sorted(_ACTS)}")
-    T, _, index = _matrix(x, torch.bfloat16, "x")
+    T, cols, index = _matrix(x, torch.bfloat16, "x")
     N, K, pc, ps = _mxfp4_weight(codes, scales, index)
-    px = _arg(x, torch.bfloat16, (T, K), index, "x")
-    out = _result(out, (T, N), torch.float32 if out_fp32 else torch.bfloat16, x)
-    need = lib().moe_linear_mxfp4_workspace_size(T, K, N, mode)
-    pw = nw = None
-    if need > 256 or ws is not None or need == 0:
-        pw, nw, ws = _scratch(need, x, ws, "moe_linear_mxfp4")
-    _call(index, "moe_linear_mxfp4", T, K, N, px, pc, ps, mode, out.data_ptr(), 1 if out_fp32 else 0, pw, nw or 0)
+    if cols != K or not x.is_contiguous():
+        _need(x, torch.bfloat16, (T, K), "x")
+    if out is None:
+        out = x.new_empty((T, N), dtype=torch.float32) if out_fp32 else x.new_empty((T, N))
+    else:
+        _arg(out, torch.float32 if out_fp32 else torch.bfloat16, (T, N), index, "out")
+    pw, nw = None, 0
+    if T > 1 or ws is not None:  # one row is always streamed, without a workspace
+        need = lib().moe_linear_mxfp4_workspace_size(T, K, N, mode)
+        if need != 256 or ws is not None:
+            pw, nw, ws = _scratch(need, x, ws, "moe_linear_mxfp4")
+    _call(index, "moe_linear_mxfp4", T, K, N, x.data_ptr(), pc, ps, mode, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
     return out
 
 
@@ -701,10 +712,10 @@ def gated_ffn(x, w13, w2, limit=10.0, save=False, out_fp32=False, out=None, ws=N
     """The expert's block with bf16 weights (moe_gated_ffn): x [T][H], w13
     [2I][H] (gate rows, then up rows), w2 [H][I] -> y [T][H] (bf16 or fp32).
     save=True returns (y, saved), ``saved`` being what ``gated_ffn_backward``
-    takes: (g and u [T][2I], h [T][I]), bf16."""
+    takes: (g and u [T][2I] fp32, h [T][I] bf16)."""
     T, H, I, index, px, p13, p2 = _ffn_args(x, w13, w2)
     out = _result(out, (T, H), torch.float32 if out_fp32 else torch.bfloat16, x)
-    saved = (x.new_empty((T, 2 * I)), x.new_empty((T, I))) if save else None
+    saved = (x.new_empty((T, 2 * I), dtype=torch.float32), x.new_empty((T, I))) if save else None
     pg, ph = (saved[0].data_ptr(), saved[1].data_ptr()) if save else (None, None)
     pw, nw, ws = _scratch(lib().moe_gated_ffn_workspace_size(T, H, I), x, ws, "moe_gated_ffn")
     _call(index, "moe_gated_ffn", T, H, I, limit, px, p13, p2, pg, ph, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
@@ -718,7 +729,7 @@ def gated_ffn_backward(dy, x, w13, w2, saved, limit=10.0, need=(True, True, True
     of the three to compute (None in the others' places)."""
     T, H, I, index, px, p13, p2 = _ffn_args(x, w13, w2)
     pd = _arg(dy, torch.bfloat16, (T, H), index, "dy")
-    pg = _arg(saved[0], torch.bfloat16, (T, 2 * I), index, "saved[0]")
+    pg = _arg(saved[0], torch.float32, (T, 2 * I), index, "saved[0]")
     ph = _arg(saved[1], torch.bfloat16, (T, I), index, "saved[1]")
     wt = torch.float32 if dw_fp32 else torch.bfloat16
     dx = x.new_empty((T, H)) if need[0] else None

@@ -301,7 +301,7 @@ size_t moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I) {
 }
 
 int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* x, const uint16_t* w13,
-                  const uint16_t* w2, uint16_t* gu_saved, uint16_t* h_saved, void* out, int32_t out_is_fp32,
+                  const uint16_t* w2, float* gu_saved, uint16_t* h_saved, void* out, int32_t out_is_fp32,
                   void* workspace, size_t workspace_bytes, void* stream) {
   if (T < 0 || H <= 0 || I <= 0 || !(limit > 0.0f)) return MOE_EINVAL;
   if (!ffn_ok(T, H, I)) return MOE_EUNSUPPORTED;
@@ -354,7 +354,7 @@ size_t moe_gated_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I) {
 }
 
 int moe_gated_ffn_backward(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* dy, const uint16_t* x,
-                           const uint16_t* w13, const uint16_t* w2, const uint16_t* gu_saved,
+                           const uint16_t* w13, const uint16_t* w2, const float* gu_saved,
                            const uint16_t* h_saved, uint16_t* dx, void* dw13, void* dw2, int32_t dw_is_fp32,
                            void* workspace, size_t workspace_bytes, void* stream) {
   if (T < 0 || H <= 0 || I <= 0 || !(limit > 0.0f)) return MOE_EINVAL;

@@ -168,7 +168,7 @@ __device__ __forceinline__ uint2 pack4_bf16(const f32x4_t& v) {
 }
 
 // Lane row g of a wave holds columns 4 g .. 4 g + 3 (8 bytes) of two 16-column blocks -> columns 8 g .. 8 g + 7 of the 32
-// (16 bytes), so that a store covers 64 consecutive bytes of each of 16 rows. unjoin is its inverse.
+// (16 bytes), so that a store covers 64 consecutive bytes of each of 16 rows.
 __device__ __forceinline__ u32x4_t join_blocks(const uint2& p, const uint2& q) {
   const auto a = __builtin_amdgcn_permlane32_swap(p.x, q.x, false, false);
   const auto b = __builtin_amdgcn_permlane32_swap(p.y, q.y, false, false);
@@ -176,15 +176,6 @@ __device__ __forceinline__ u32x4_t join_blocks(const uint2& p, const uint2& q) {
   const auto d = __builtin_amdgcn_permlane16_swap(b[0], b[1], false, false);
   return (u32x4_t){c[0], d[0], c[1], d[1]};
 }
-__device__ __forceinline__ void unjoin_blocks(const u32x4_t& v, uint2& p, uint2& q) {
-  const auto c = __builtin_amdgcn_permlane16_swap(v[0], v[2], false, false);
-  const auto d = __builtin_amdgcn_permlane16_swap(v[1], v[3], false, false);
-  const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[1], false, false);
-  const auto b = __builtin_amdgcn_permlane32_swap(d[0], d[1], false, false);
-  p = make_uint2(a[0], b[0]);
-  q = make_uint2(a[1], b[1]);
-}
-
 // Four consecutive outputs out[at .. at+3], of which `live` (1..4) exist;
 // wide: at is a multiple of 4 elements and all four exist.
 __device__ __forceinline__ void store4(void* out, bool fp32, size_t at, const f32x4_t& v, int live, bool wide) {
@@ -216,38 +207,20 @@ __device__ __forceinline__ float ffn_act(float g, float u, float L) {
   return silu(gc) * uc;
 }
 
-// v rounded to bf16 for the backward pass without crossing the border L: a
-// value on one side of it (v > L or v <= L) stays there, so that the backward
-// finds the clamp's mask of the unrounded value. Only a value within one
-// rounding of L moves, by less than one step instead of half of one; values
-// past L count as L whatever is stored.
-__device__ __forceinline__ uint32_t fix_side(uint32_t b, float v, float L) {  // b: v's bf16 bits
-  const float w = __uint_as_float(b << 16);
-  const uint32_t out = L >= 0.0f ? 1u : ~0u;  // one step away from zero, for L's sign
-  if (v > L && !(w > L)) b += out;
-  if (v <= L && w > L) b -= out;
-  return b & 0xffffu;
-}
-__device__ __forceinline__ uint2 save_gate4(const f32x4_t& g, float L) {
-  const uint2 p = pack4_bf16(g);
-  return make_uint2(fix_side(p.x & 0xffffu, g[0], L) | (fix_side(p.x >> 16, g[1], L) << 16),
-                    fix_side(p.y & 0xffffu, g[2], L) | (fix_side(p.y >> 16, g[3], L) << 16));
-}
-// both borders, by symmetry; L > 0
-__device__ __forceinline__ uint2 save_up4(const f32x4_t& u, float L) {
-  const uint2 p = pack4_bf16(u);
-  auto one = [&](uint32_t b, float v) { return fix_side(b & 0x7fffu, fabsf(v), L) | (b & 0x8000u); };
-  return make_uint2(one(p.x & 0xffffu, u[0]) | (one(p.x >> 16, u[1]) << 16),
-                    one(p.y & 0xffffu, u[2]) | (one(p.y >> 16, u[3]) << 16));
-}
-
-// Gradients of the gated product at the saved (g, u) for dh.
-__device__ __forceinline__ void ffn_act_grad(float g, float u, float dh, float L, float& dg, float& du) {
-  const float gc = g > L ? L : g;
-  const float uc = u > L ? L : (u < -L ? -L : u);
-  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gc * 1.4426950408889634f));
-  dg = g > L ? 0.0f : dh * uc * (s * (1.0f + gc * (1.0f - s)));
-  du = (u > L || u < -L) ? 0.0f : dh * gc * s;
+// Gradients of the gated product at the saved (g, u) for dh, four columns. g and u are saved in fp32: rounded to bf16
+// they would cost the gradients as much precision again as the rounding of dg and du (relative L2 error of dx 3.0e-3
+// against 2.4e-3), and a value next to the clamp could cross it.
+__device__ __forceinline__ void ffn_act_grad4(const f32x4_t& g4, const f32x4_t& u4, const f32x4_t& dh, float L,
+                                              f32x4_t& dg, f32x4_t& du) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float g = g4[i], u = u4[i];
+    const float gc = g > L ? L : g;
+    const float uc = u > L ? L : (u < -L ? -L : u);
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gc * 1.4426950408889634f));
+    dg[i] = g > L ? 0.0f : dh[i] * uc * (s * (1.0f + gc * (1.0f - s)));
+    du[i] = (u > L || u < -L) ? 0.0f : dh[i] * gc * s;
+  }
 }
 
 // The wave's accumulators to out [M][N]: lane (r, g) holds acc[b][c][i] = C[m0 + 16 c + r][n0 + 16 b + 4 g + i].
@@ -281,7 +254,7 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[NB][MB], void* o
 
 enum DenseEpi {
   kEpiStore = 0,    // out [M][N] bf16 or fp32
-  kEpiGate = 1,     // gate / up rows interleaved: h [M][I] bf16 (and gu [M][2I])
+  kEpiGate = 1,     // gate / up rows interleaved: h [M][I] bf16 (and gu [M][2I] fp32)
   kEpiGrad = 2,     // dh -> dgu [M][2I] from gu
   kEpiPartial = 3,  // fp32 partial sums [slice][M][N] (of a split K)
 };
@@ -424,7 +397,6 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t
     const int m = m0 + c * 16 + r;
     if constexpr (EPI == kEpiGate) {
       uint16_t* hrow = static_cast<uint16_t*>(a.out) + (size_t)m * a.I;
-      uint16_t* grow = a.gu_out + (size_t)m * 2 * a.I;
       auto act = [&](int b) {
         f32x4_t h;
 #pragma unroll
@@ -435,53 +407,45 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t
 #pragma unroll
         for (int b = 0; b < NB; b += 4) {
           const int n = n0 + b * 8 + 8 * g;  // h column
-          const bool live = m < a.M && n < a.I;
-          put(hrow + n, join_blocks(act(b), act(b + 2)), live);
-          if (a.gu_out) {
-            put(grow + n, join_blocks(save_gate4(acc[b][c], a.limit), save_gate4(acc[b + 2][c], a.limit)), live);
-            put(grow + a.I + n, join_blocks(save_up4(acc[b + 1][c], a.limit), save_up4(acc[b + 3][c], a.limit)), live);
-          }
+          put(hrow + n, join_blocks(act(b), act(b + 2)), m < a.M && n < a.I);
         }
       } else {
 #pragma unroll
         for (int b = 0; b < NB; b += 2) {
           const int n = n0 + b * 8 + 4 * g;
+          if (m < a.M && n < a.I) *reinterpret_cast<uint2*>(hrow + n) = act(b);
+        }
+      }
+      if (a.gu_out) {
+        float* grow = a.gu_out + (size_t)m * 2 * a.I;
+#pragma unroll
+        for (int b = 0; b < NB; b += 2) {
+          const int n = n0 + b * 8 + 4 * g;
           if (m >= a.M || n >= a.I) continue;
-          *reinterpret_cast<uint2*>(hrow + n) = act(b);
-          if (a.gu_out) {
-            *reinterpret_cast<uint2*>(grow + n) = save_gate4(acc[b][c], a.limit);
-            *reinterpret_cast<uint2*>(grow + a.I + n) = save_up4(acc[b + 1][c], a.limit);
-          }
+          *reinterpret_cast<f32x4_t*>(grow + n) = acc[b][c];
+          *reinterpret_cast<f32x4_t*>(grow + a.I + n) = acc[b + 1][c];
         }
       }
     } else {
-      const uint16_t* s = a.gu_in + (size_t)m * 2 * a.I;
+      const float* s = a.gu_in + (size_t)m * 2 * a.I;
       uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I;
 #pragma unroll
       for (int b = 0; b < NB; b += 2) {
-        const int n = n0 + b * 16 + 8 * g;
-        const bool live = m < a.M && n < a.N;
-        const u32x4_t zero = {0u, 0u, 0u, 0u};
-        const u32x4_t gj = live ? *reinterpret_cast<const u32x4_t*>(s + n) : zero;
-        const u32x4_t uj = live ? *reinterpret_cast<const u32x4_t*>(s + a.I + n) : zero;
-        uint2 gv[2], uv[2], dgv[2], duv[2];
-        unjoin_blocks(gj, gv[0], gv[1]);
-        unjoin_blocks(uj, uv[0], uv[1]);
+        uint2 dgv[2], duv[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          f32x4_t dg, du;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t gw = i < 2 ? gv[j].x : gv[j].y, uw = i < 2 ? uv[j].x : uv[j].y;
-            float p, q;
-            ffn_act_grad(bf16_to_f32((uint16_t)(gw >> (16 * (i & 1)))), bf16_to_f32((uint16_t)(uw >> (16 * (i & 1)))),
-                         acc[b + j][c][i], a.limit, p, q);
-            dg[i] = p;
-            du[i] = q;
+          const int n = n0 + (b + j) * 16 + 4 * g;
+          f32x4_t gv = {0.f, 0.f, 0.f, 0.f}, uv = gv, dg, du;
+          if (m < a.M && n < a.N) {
+            gv = *reinterpret_cast<const f32x4_t*>(s + n);
+            uv = *reinterpret_cast<const f32x4_t*>(s + a.I + n);
           }
+          ffn_act_grad4(gv, uv, acc[b + j][c], a.limit, dg, du);
           dgv[j] = pack4_bf16(dg);
           duv[j] = pack4_bf16(du);
         }
+        const int n = n0 + b * 16 + 8 * g;
+        const bool live = m < a.M && n < a.N;
         put(o + n, join_blocks(dgv[0], dgv[1]), live);
         put(o + a.I + n, join_blocks(duv[0], duv[1]), live);
       }

@@ -53,21 +53,15 @@ __global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
     for (int i = 0; i < 4; ++i) h[i] = ffn_act(g[i], u[i], a.limit);
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (size_t)m * a.I + n) = pack4_bf16(h);
     if (a.gu_out) {
-      uint16_t* o = a.gu_out + (size_t)m * 2 * a.I + n;
-      *reinterpret_cast<uint2*>(o) = save_gate4(g, a.limit);
-      *reinterpret_cast<uint2*>(o + a.I) = save_up4(u, a.limit);
+      float* o = a.gu_out + (size_t)m * 2 * a.I + n;
+      *reinterpret_cast<f32x4_t*>(o) = g;
+      *reinterpret_cast<f32x4_t*>(o + a.I) = u;
     }
   } else if constexpr (EPI == kEpiGrad) {
     const f32x4_t dh = sum(n);
-    const uint16_t* s = a.gu_in + (size_t)m * 2 * a.I + n;
+    const float* s = a.gu_in + (size_t)m * 2 * a.I + n;
     f32x4_t dg, du;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float p, q;
-      ffn_act_grad(bf16_to_f32(s[i]), bf16_to_f32(s[a.I + i]), dh[i], a.limit, p, q);
-      dg[i] = p;
-      du[i] = q;
-    }
+    ffn_act_grad4(*reinterpret_cast<const f32x4_t*>(s), *reinterpret_cast<const f32x4_t*>(s + a.I), dh, a.limit, dg, du);
     uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I + n;
     *reinterpret_cast<uint2*>(o) = pack4_bf16(dg);
     *reinterpret_cast<uint2*>(o + a.I) = pack4_bf16(du);

@@ -145,10 +145,9 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
       }
       static_cast<uint16_t*>(a.out)[(size_t)t * a.N + n0 + n] = f32_to_bf16(ffn_act(gv, uv, a.limit));
       if (a.gu_out) {
-        uint16_t* o = a.gu_out + (size_t)t * 2 * a.N + n0 + n;
-        const f32x4_t g4 = {gv, gv, gv, gv}, u4 = {uv, uv, uv, uv};
-        o[0] = (uint16_t)save_gate4(g4, a.limit).x;
-        o[a.N] = (uint16_t)save_up4(u4, a.limit).x;
+        float* o = a.gu_out + (size_t)t * 2 * a.N + n0 + n;
+        o[0] = gv;
+        o[a.N] = uv;
       }
     } else {
       if (n0 + n >= a.N) continue;

@@ -394,8 +394,8 @@ struct DenseArgs {
   int out_is_fp32;
   int I;
   float limit;
-  uint16_t* gu_out;          // gate: the rounded pre-activations [M][2I], or null
-  const uint16_t* gu_in;     // grad: the same
+  float* gu_out;             // gate: the pre-activations [M][2I] for the backward pass, or null
+  const float* gu_in;        // grad: the same
   float* part;               // split K: fp32 partial sums [slices][M][N] (gate: N = 2I)
 };
 
@@ -448,7 +448,7 @@ struct FewRowsArgs {
   void* out;               // [T][N]
   int out_is_fp32;
   float limit;             // gate
-  uint16_t* gu_out;        // gate: [T][2N] or null
+  float* gu_out;           // gate: [T][2N] or null
 };
 hipError_t launch_few_rows_mxfp4(const FewRowsArgs& a, hipStream_t st);
 hipError_t launch_few_rows_bf16(const FewRowsArgs& a, bool gate, hipStream_t st);

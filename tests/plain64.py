@@ -83,8 +83,7 @@ def ffn(x, w13, w2, L, dy=None):
     edh = sum_err(dy.abs() @ w2.abs(), H)
     d1 = s * (1 + gc * (1 - s))
     dg, du = dh * uc * d1, dh * silu
-    # saved g, u: half a bf16 step, a whole one next to a border
-    sg, su = eg + 2 * U16 * g.abs(), eu + 2 * U16 * u.abs()
+    sg, su = eg, eu  # g and u are saved in fp32
     edg = (uc * d1).abs() * edh + (dh * d1).abs() * su + 0.5 * (dh * uc).abs() * sg + (U16 + 4 * fast) * dg.abs()
     edu = silu.abs() * edh + 1.1 * dh.abs() * sg + (U16 + 4 * fast) * du.abs()
     # within the fp32 error of a border the mask may fall either way

@@ -31,9 +31,8 @@ def _ref(x, w13, w2, L, dy=None):
 
 
 # Relative L2 of the whole: independent roundings of at most a half step each, so no more than the sum of the half
-# steps on the way: y: h and the output; dw2: h and the output; dx, dw13: the saved g and u (a derivative moves by
-# up to about twice their relative change), dg / du, the output.
-L2_OUT, L2_GRAD = 2 * U16, 5 * U16
+# steps on the way: y and dw2: h and the output; dx and dw13: dg / du and the output.
+L2_OUT, L2_GRAD = 2 * U16, 2 * U16
 
 SHAPES = [  # T, H, I: the streaming pass (1 .. 64), then every tile size, splits and ragged edges
     (1, 8, 8), (1, 4096, 2048), (2, 264, 136), (16, 1024, 512), (17, 2048, 72), (33, 512, 1024), (64, 4096, 512),
@@ -52,7 +51,8 @@ def test_forward(T, H, I):
     assert torch.equal(y2.to(torch.bfloat16), y)
     g, u = x.double() @ w13[:I].double().t(), x.double() @ w13[I:].double().t()
     eg = plain64.sum_err(x.double().abs() @ w13.double().abs().t(), H)
-    check(gu, torch.cat((g, u), 1), eg + 2 * U16 * torch.cat((g, u), 1).abs(), "gu")
+    assert gu.dtype == torch.float32 and h.dtype == torch.bfloat16
+    check(gu, torch.cat((g, u), 1), eg, "gu")
     assert torch.equal(y, mx.gated_ffn(x, w13, w2))  # repeatable
 
 
@@ -99,8 +99,8 @@ def test_clamp_borders(T, limit):
 
 @pytest.mark.parametrize("T", [1, 100])
 def test_saved_values_at_the_border(T):
-    """g and u exactly at, just above and just below the limit: the stored value stays on its side, and only the one
-    past it stops the gradient (a value at the limit passes it)."""
+    """g and u exactly at, just above and just below the limit, by less than a bf16 step: only the one past it stops
+    the gradient (a value at the limit passes it)."""
     H, I, L = 8, 8, 10.0
     x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
     x[:, 0], x[:, 1] = 1.0, 1.0 / 64
@@ -157,9 +157,9 @@ def test_gradients_against_differences(T):
         curve = abs(float(exact[0] - exact[1]) / 2 - float((plain64.ffn(
             x.double(), w13.double(), w2.double(), 10.0, dy.double())["d" + name][0] * v.double()).sum()))
         ana = float((grad.double() * v.double()).sum())
-        # deviations: h's rounding in both outputs, and the gradient's own roundings (5 half steps of each element)
+        # deviations: h's rounding in both outputs, and the gradient's own roundings (2 half steps of each element)
         dh = (dy.double() @ w2.double()).abs()
-        dev = U16 * float((dh * (hv + 1)).norm()) + 5 * U16 * float((grad.double() * v.double()).norm())
+        dev = U16 * float((dh * (hv + 1)).norm()) + 2 * U16 * float((grad.double() * v.double()).norm())
         assert abs(num - ana) <= curve + 6 * dev, (name, num, ana, curve, dev)
     assert h["y"][0].shape == y.shape
 
@@ -219,7 +219,7 @@ def test_refusals_on_device():
     y, saved = mx.gated_ffn(x, w13, w2, save=True)
     with pytest.raises(ValueError):
         mx.gated_ffn_backward(dy[:2], x, w13, w2, saved)
-    with pytest.raises(ValueError):
+    with pytest.raises(TypeError):
         mx.gated_ffn_backward(dy, x, w13, w2, (saved[1], saved[0]))
 
 
