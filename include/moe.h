@@ -357,7 +357,8 @@ int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* 
  * Each of dx, dw13, dw2 may be NULL: it is not computed. No gradient passes
  * a clamp that acted (g > L, |u| > L). The gradients of g and u are rounded
  * to bf16 as operands of the products; sums are fp32. With T = 0 the weight
- * gradients are zeros.
+ * gradients are zeros. Two launches, one for dw2 and the gradients of g and u,
+ * one for dw13 and dx (more where K is split or a gradient is left out).
  *   workspace: moe_gated_ffn_backward_workspace_size(T, H, I) bytes, as above. */
 size_t moe_gated_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I);
 int moe_gated_ffn_backward(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* dy, const uint16_t* x,

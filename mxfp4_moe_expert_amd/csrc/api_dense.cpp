@@ -148,8 +148,13 @@ FfnLayout ffn_layout(int T, int H, int I) {
   return L;
 }
 
+// The plan of one product of a pair whose other gradient is not wanted: cut as in the pair (a split K would add in
+// another order), so a gradient's bits do not depend on which others are computed.
+DensePlan alone_a(const DensePairPlan& p) { return p.tile >= 0 ? DensePlan{p.tile, 1} : p.a; }
+DensePlan alone_b(const DensePairPlan& p) { return p.tile >= 0 ? DensePlan{p.tile, 1} : p.b; }
+
 struct FfnGradLayout {
-  DensePlan dh, dx, dw13, dw2;
+  DensePairPlan first, second;  // dw2 with dgu (from dh); dw13 with dx
   size_t dgu, part, total;
 };
 
@@ -157,14 +162,12 @@ FfnGradLayout ffn_grad_layout(int T, int H, int I) {
   FfnGradLayout L;
   memset(&L, 0, sizeof(L));
   const int t = T > 0 ? T : 1;
-  L.dh = dense_plan(kDenseBf16, t, I, H);
-  L.dx = dense_plan(kDenseBf16, t, H, 2 * I);
-  L.dw13 = dense_plan(kDenseBf16, 2 * I, H, t);
-  L.dw2 = dense_plan(kDenseBf16, H, I, t);
+  L.first = dense_pair_plan(H, I, t, t, I, H);
+  L.second = dense_pair_plan(2 * I, H, t, t, H, 2 * I);
   L.dgu = 0;
   L.part = align256((size_t)T * 2 * I * 2);
-  size_t p = max_of(dense_part_bytes(L.dh, t, I), dense_part_bytes(L.dx, t, H));
-  p = max_of(p, max_of(dense_part_bytes(L.dw13, 2 * I, H), dense_part_bytes(L.dw2, H, I)));
+  size_t p = max_of(dense_part_bytes(alone_a(L.first), H, I), dense_part_bytes(alone_b(L.first), t, I));
+  p = max_of(p, max_of(dense_part_bytes(alone_a(L.second), 2 * I, H), dense_part_bytes(alone_b(L.second), t, H)));
   L.total = L.part + align256(p);
   if (L.total < 256) L.total = 256;
   return L;
@@ -379,21 +382,21 @@ int moe_gated_ffn_backward(int32_t T, int32_t H, int32_t I, float limit, const u
   uint16_t* dgu = at<uint16_t>(workspace, L.dgu);
   float* part = at<float>(workspace, L.part);
   hipError_t e = hipSuccess;
-  if (dx || dw13) {
-    DenseArgs a = dense_args(dy, H, w2, I, T, I, H, dgu, 0, part);
-    a.I = I;
-    a.limit = limit;
-    a.gu_in = gu_saved;
-    e = launch_dense(kDenseBf16, kDenseNN, kGrad, L.dh, a, st);
-  }
-  if (e == hipSuccess && dx)
-    e = launch_dense(kDenseBf16, kDenseNN, kStore, L.dx, dense_args(dgu, 2 * I, w13, H, T, H, 2 * I, dx, 0, part), st);
-  if (e == hipSuccess && dw13)
-    e = launch_dense(kDenseBf16, kDenseTN, kStore, L.dw13,
-                     dense_args(dgu, 2 * I, x, H, 2 * I, H, T, dw13, dw_is_fp32, part), st);
-  if (e == hipSuccess && dw2)
-    e = launch_dense(kDenseBf16, kDenseTN, kStore, L.dw2, dense_args(dy, H, h_saved, I, H, I, T, dw2, dw_is_fp32, part),
-                     st);
+  const DenseArgs gw2 = dense_args(dy, H, h_saved, I, H, I, T, dw2, dw_is_fp32, part);
+  DenseArgs gdgu = dense_args(dy, H, w2, I, T, I, H, dgu, 0, part);
+  gdgu.I = I;
+  gdgu.limit = limit;
+  gdgu.gu_in = gu_saved;
+  const bool inner = dx || dw13;
+  if (dw2 && inner) e = launch_dense_pair(kGrad, L.first, gw2, gdgu, st);
+  else if (dw2) e = launch_dense(kDenseBf16, kDenseTN, kStore, alone_a(L.first), gw2, st);
+  else if (inner) e = launch_dense(kDenseBf16, kDenseNN, kGrad, alone_b(L.first), gdgu, st);
+  if (e != hipSuccess || !inner) return status(e);
+  const DenseArgs gw13 = dense_args(dgu, 2 * I, x, H, 2 * I, H, T, dw13, dw_is_fp32, part);
+  const DenseArgs gx = dense_args(dgu, 2 * I, w13, H, T, H, 2 * I, dx, 0, part);
+  if (dx && dw13) e = launch_dense_pair(kStore, L.second, gw13, gx, st);
+  else if (dw13) e = launch_dense(kDenseBf16, kDenseTN, kStore, alone_a(L.second), gw13, st);
+  else e = launch_dense(kDenseBf16, kDenseNN, kStore, alone_b(L.second), gx, st);
   return status(e);
 }
 

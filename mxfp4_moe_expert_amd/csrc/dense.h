@@ -453,9 +453,10 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t
   }
 }
 
-// The tile product. FP4: both operands MXFP4 K-contiguous, with packed scales.
+// One tile (block `bid` of the product's a.tm a.tn) of the product. FP4: both operands MXFP4 K-contiguous, with packed
+// scales.
 template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, bool FP4, int EPI>
-__global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
+__device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
   constexpr int W = WGM * WGN;
   constexpr int MB = BM / WGM / 16, NB = BN / WGN / 16;  // 16-row blocks per wave
   // scales are loaded SD pairs of stages ahead, so that the waits below cover them
@@ -474,7 +475,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int im, in;
-  dense_tile(blockIdx.x, a.tm, a.tn, im, in);
+  dense_tile(bid, a.tm, a.tn, im, in);
   L t;
   t.init(a, (uint32_t)(uintptr_t)lds, wave, lane, im, in);
   const int nst = t.nst;
@@ -601,6 +602,25 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
   dense_wait<0>();  // nothing may still write this block's LDS when it ends
   dense_epilogue<EPI, MB, NB>(a, acc, im * BM + wm * MB * 16,
                               EPI == kEpiGate ? in * (BN / 2) + wn * NB * 8 : in * BN + wn * NB * 16, lane);
+}
+
+template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, bool FP4, int EPI>
+__global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
+  dense_block<XT, WT, BM, BN, WGM, WGN, NX, NW, FP4, EPI>(a, blockIdx.x);
+}
+
+// Two independent products in one launch: the weight gradient `a` (both operands transposed) and a product `b` with W
+// transposed. One's blocks come first, the other's from block `second` on (a multiple of 8, so that blocks keep their
+// XCDs). Blocks start in order: the product with the longer K goes first, and the other's blocks fill up behind it.
+template <int BM, int BN, int WGM, int WGN, int NX, int NW, int EPI>
+__global__ __launch_bounds__(WGM* WGN * 64) void k_dense_pair(DenseArgs a, DenseArgs b, int second, int b_first) {
+  const int in_first = (int)blockIdx.x < second;
+  const int bid = in_first ? (int)blockIdx.x : (int)blockIdx.x - second;
+  if (in_first != b_first) {
+    if (bid < a.tm * a.tn) dense_block<true, true, BM, BN, WGM, WGN, NX, NW, false, kEpiStore>(a, bid);
+  } else {
+    if (bid < b.tm * b.tn) dense_block<false, true, BM, BN, WGM, WGN, NX, NW, false, EPI>(b, bid);
+  }
 }
 
 // Allows KERNEL `bytes` of dynamic LDS on the current device, asking the runtime once per device and kernel (the call

@@ -71,6 +71,11 @@ __global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
 }
 
 template <auto KERNEL>
+struct Kernel {
+  static constexpr auto value = KERNEL;
+};
+
+template <auto KERNEL>
 hipError_t run(const TileCfg& t, bool fp4, int slices, const DenseArgs& a, hipStream_t st) {
   const size_t lds = tile_lds(t, fp4);
   const hipError_t e = allow_lds<KERNEL>((int)lds);
@@ -111,14 +116,24 @@ inline int slice_stages(DenseKind kind, int nst, int slices) {
 
 }  // namespace
 
+// Microseconds per stage of a block, by tile, where few CUs are busy and on a full chip, and the rest of a block's time
+// (launch, first loads, epilogue). A block is bound by its share of the L2 -> LDS path, then by the matrix cores.
+// Measured on 4096 x 4096 weights at 33 to 4096 rows: of the cuts tried for each size, the rule takes the fastest or one
+// within a few percent of it.
+constexpr double kFewUs[kNumTiles] = {0.95, 0.47, 0.32, 0.26}, kFullUs[kNumTiles] = {1.45, 0.80, 0.47, 0.34};
+constexpr double kStartUs = 4.5;
+constexpr double kPairUs = 0.56;  // 64 x 128: a stage of both blocks of a CU
+inline double stage_us(int tile, double blocks) {
+  const double full = blocks < 256 ? blocks / 256 : 1.0;
+  if (tile == 3 && blocks > 256) return kFullUs[3] + (blocks > 512 ? 1.0 : (blocks - 256) / 256) * (kPairUs - kFullUs[3]);
+  return kFewUs[tile] + full * (kFullUs[tile] - kFewUs[tile]);
+}
+inline int places(int tile) { return tile == 3 ? 512 : 256; }  // blocks the chip holds
+
 // The plan with the least estimated time: rounds of blocks over the 256 CUs times the stages each runs, plus the
-// partial sums' traffic (written and read at about 4 TB/s) and launch for a split. Per stage a block is bound by its
-// share of the L2 -> LDS path, then by the matrix cores: measured on 4096 x 4096 weights at 300, 1000, 2048 and 8192
-// rows as 1.45, 0.88, 0.57 and 0.39 us for the four tiles on a full chip (64 x 128 with two blocks on every CU: 0.65
-// for both).
+// partial sums' traffic (written and read at about 4 TB/s) and launch for a split.
 DensePlan dense_plan(DenseKind kind, int M, int N, int K, double* us_out) {
   const int nst = stages_of(kind, K);
-  constexpr double stage_us[kNumTiles] = {1.45, 0.88, 0.57, 0.39}, pair_us = 0.65, start_us = 3.0;
   DensePlan best = {0, 1};
   double best_us = 1e30;
   for (int t = 0; t < kNumTiles; ++t) {
@@ -126,9 +141,7 @@ DensePlan dense_plan(DenseKind kind, int M, int N, int K, double* us_out) {
     for (int s = 1; s <= 16 && s * 4 <= nst + 3; s *= 2) {
       const int per = slice_stages(kind, nst, s), slices = ceil_div(nst, per);
       const long long blocks = tiles * slices;
-      double us;
-      if (t == 3 && blocks > 256) us = (double)((blocks + 511) / 512) * (per * pair_us + start_us);
-      else us = (double)((blocks + 255) / 256) * (per * stage_us[t] + start_us);
+      double us = (double)((blocks + places(t) - 1) / places(t)) * (per * stage_us(t, (double)blocks) + kStartUs);
       if (slices > 1) us += 3.0 + 2.0 * slices * M * (double)N * 4 / 4e6;
       if (us < best_us) {
         best_us = us;
@@ -174,6 +187,84 @@ hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const Dense
     e = run_bf16<kEpiStore>(layout, p.tile, p.slices, a, st);
   }
   return e != hipSuccess || !split ? e : launch_dense_reduce(epi, a, p.slices, st);
+}
+
+namespace {
+
+template <int EPI>
+hipError_t run_pair(int tile, const DenseArgs& a, const DenseArgs& b, hipStream_t st) {
+  const int na = a.tm * a.tn, nb = b.tm * b.tn;
+  const int b_first = b.stages > a.stages;
+  const int second = ((b_first ? nb : na) + 7) & ~7;
+  const unsigned grid = (unsigned)(second + (b_first ? na : nb));
+  auto go = [&](auto kern) -> hipError_t {
+    const size_t lds = tile_lds(kTiles[tile], false);
+    const hipError_t e = allow_lds<decltype(kern)::value>((int)lds);
+    if (e != hipSuccess) return e;
+    decltype(kern)::value<<<grid, kTileThreads, lds, st>>>(a, b, second, b_first);
+    return hipGetLastError();
+  };
+  constexpr const TileCfg* t = kTiles;
+  if (tile == 0) return go(Kernel<&k_dense_pair<256, 256, 2, 4, t[0].nx, t[0].nw, EPI>>{});
+  if (tile == 1) return go(Kernel<&k_dense_pair<256, 128, 2, 4, t[1].nx, t[1].nw, EPI>>{});
+  if (tile == 2) return go(Kernel<&k_dense_pair<128, 128, 2, 4, t[2].nx, t[2].nw, EPI>>{});
+  return go(Kernel<&k_dense_pair<64, 128, 2, 4, t[3].nx, t[3].nw, EPI>>{});
+}
+
+}  // namespace
+
+// When n1 blocks of time c1, then n2 of time c2 <= c1, started in order as places come free, have all ended.
+static double makespan(long long n1, double c1, long long n2, double c2, long long places) {
+  const long long q = n1 / places, r = n1 % places;  // places - r come free at q c1, r at (q + 1) c1
+  const double early = q * c1, late = r ? early + c1 : early;
+  // the end is a whole number of c2 after early or after late
+  auto first_end = [&](double from) {
+    for (double end = from;; end += c2) {
+      if (end < late) continue;
+      const long long a = (long long)((end - early) / c2 + 1e-6), b = (long long)((end - late) / c2 + 1e-6);
+      if (a * (places - r) + b * r >= n2) return end;
+    }
+  };
+  const double x = first_end(early), y = first_end(late);
+  return x < y ? x : y;
+}
+
+DensePairPlan dense_pair_plan(int Ma, int Na, int Ka, int Mb, int Nb, int Kb) {
+  DensePairPlan best;
+  double ua, ub;
+  best.a = dense_plan(kDenseBf16, Ma, Na, Ka, &ua);
+  best.b = dense_plan(kDenseBf16, Mb, Nb, Kb, &ub);
+  best.tile = -1;
+  double best_us = ua + ub;
+  const int sa = stages_of(kDenseBf16, Ka), sb = stages_of(kDenseBf16, Kb);
+  for (int t = kNumTiles - 1; t >= 0; --t) {  // a larger tile only where it is clearly faster: its blocks mix less well
+    const long long na = (long long)ceil_div(Ma, kTiles[t].bm) * ceil_div(Na, kTiles[t].bn);
+    const long long nb = (long long)ceil_div(Mb, kTiles[t].bm) * ceil_div(Nb, kTiles[t].bn);
+    const double c = stage_us(t, (double)(na + nb)), ca = sa * c + kStartUs, cb = sb * c + kStartUs;
+    const double us = sa > sb ? makespan(na, ca, nb, cb, places(t)) : makespan(nb, cb, na, ca, places(t));
+    if (us < (best.tile < 0 ? 1.0 : 0.92) * best_us) {
+      best_us = us;
+      best.tile = t;
+    }
+  }
+  return best;
+}
+
+hipError_t launch_dense_pair(int epi, const DensePairPlan& p, DenseArgs a, DenseArgs b, hipStream_t st) {
+  if (p.tile < 0) {
+    const hipError_t e = launch_dense(kDenseBf16, kDenseTN, kEpiStore, p.a, a, st);
+    return e != hipSuccess ? e : launch_dense(kDenseBf16, kDenseNN, epi, p.b, b, st);
+  }
+  if (p.tile >= kNumTiles || (epi != kEpiStore && epi != kEpiGrad)) return hipErrorInvalidValue;
+  const TileCfg& t = kTiles[p.tile];
+  for (DenseArgs* x : {&a, &b}) {
+    if (x->M <= 0 || x->N <= 0 || x->K <= 0) return hipErrorInvalidValue;
+    x->stages = x->slice_stages = stages_of(kDenseBf16, x->K);
+    x->tm = ceil_div(x->M, t.bm);
+    x->tn = ceil_div(x->N, t.bn);
+    if ((long long)x->tm * x->tn > 0x1fffff) return hipErrorInvalidValue;
+  }
+  return epi == kEpiGrad ? run_pair<kEpiGrad>(p.tile, a, b, st) : run_pair<kEpiStore>(p.tile, a, b, st);
 }
 
 hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st) {

@@ -413,6 +413,15 @@ size_t dense_part_bytes(const DensePlan& p, int M, int N);  // partial sums of a
 // reduction of a split. a.part: dense_part_bytes(plan, M, N) bytes.
 hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const DensePlan& p, DenseArgs a, hipStream_t st);
 
+// Two independent bf16 products, a: layout TN, stored; b: layout NN with epilogue epi. In one launch of a common tile
+// where that is estimated to be faster (tile >= 0), else one after the other.
+struct DensePairPlan {
+  DensePlan a, b;
+  int tile;
+};
+DensePairPlan dense_pair_plan(int Ma, int Na, int Ka, int Mb, int Nb, int Kb);
+hipError_t launch_dense_pair(int epi, const DensePairPlan& p, DenseArgs a, DenseArgs b, hipStream_t st);
+
 hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st);  // of a split's partials
 
 // The product with W read as MXFP4 codes (dense_w4.hip): the plan and its estimated microseconds (tile -1: K too long
