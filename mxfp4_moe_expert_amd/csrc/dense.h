@@ -638,4 +638,10 @@ inline hipError_t allow_lds(int bytes) {
   return e;
 }
 
+// A kernel as a value that a function can take.
+template <auto KERNEL>
+struct Kernel {
+  static constexpr auto value = KERNEL;
+};
+
 }  // namespace moe

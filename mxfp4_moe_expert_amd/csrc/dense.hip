@@ -71,11 +71,6 @@ __global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
 }
 
 template <auto KERNEL>
-struct Kernel {
-  static constexpr auto value = KERNEL;
-};
-
-template <auto KERNEL>
 hipError_t run(const TileCfg& t, bool fp4, int slices, const DenseArgs& a, hipStream_t st) {
   const size_t lds = tile_lds(t, fp4);
   const hipError_t e = allow_lds<KERNEL>((int)lds);

@@ -190,16 +190,15 @@ inline int w4_slice_stages(int nst, int slices) { return (ceil_div(nst, slices) 
 template <int EPI>
 hipError_t go(int tile, int slices, const DenseArgs& a, const uint8_t* scales, size_t lds, hipStream_t st) {
   auto run = [&](auto kern) -> hipError_t {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    const hipError_t e = allow_lds<decltype(kern)::value>(kLdsBlockMax);  // lds differs from call to call
     if (e != hipSuccess) return e;
-    kern<<<dim3((unsigned)(a.tm * a.tn), (unsigned)slices), kW4Threads, lds, st>>>(a, scales,
-                                                                                    w4_scld(a.slice_stages));
+    decltype(kern)::value<<<dim3((unsigned)(a.tm * a.tn), (unsigned)slices), kW4Threads, lds, st>>>(
+        a, scales, w4_scld(a.slice_stages));
     return hipGetLastError();
   };
-  if (tile == 0) return run(&k_dense_w4<64, 128, 1, 8, kW4[0].nx, EPI>);
-  if (tile == 1) return run(&k_dense_w4<128, 128, 2, 4, kW4[1].nx, EPI>);
-  return run(&k_dense_w4<256, 128, 2, 4, kW4[2].nx, EPI>);
+  if (tile == 0) return run(Kernel<&k_dense_w4<64, 128, 1, 8, kW4[0].nx, EPI>>{});
+  if (tile == 1) return run(Kernel<&k_dense_w4<128, 128, 2, 4, kW4[1].nx, EPI>>{});
+  return run(Kernel<&k_dense_w4<256, 128, 2, 4, kW4[2].nx, EPI>>{});
 }
 
 }  // namespace
