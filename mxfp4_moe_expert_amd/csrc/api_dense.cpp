@@ -76,7 +76,7 @@ LinearLayout linear_layout(int T, int K, int N, int act) {
   };
   if (T > 0 && !linear_few(T, K, act)) {
     double us;
-    L.plan = dense_plan(act == MOE_ACT_MXFP4 ? kDenseFp4 : kDenseBf16, T, N, K, &us);
+    L.plan = dense_plan(act == MOE_ACT_MXFP4 ? kDenseFp4 : kDenseBf16, kDenseNT, T, N, K, &us);
     if (act == MOE_ACT_BF16) {
       // expanding W: a launch, and 17/32 of a byte read and 2 written per weight
       const double expand_us = 3.0 + (double)N * K * (17.0 / 32 + 2) / 4.5e6;
@@ -114,7 +114,7 @@ DxLayout dx_layout(int T, int K, int N) {
     return p;
   };
   L.ldy = (N + 7) & ~7;
-  L.plan = dense_plan(kDenseBf16, T > 0 ? T : 1, K, N);
+  L.plan = dense_plan(kDenseBf16, kDenseNN, T > 0 ? T : 1, K, N);
   L.w = take((size_t)N * K * 2);
   L.dyp = take(L.ldy != N ? (size_t)T * L.ldy * 2 : 0);
   L.part = take(dense_part_bytes(L.plan, T, K));
@@ -140,8 +140,8 @@ FfnLayout ffn_layout(int T, int H, int I) {
   size_t o = align256((size_t)T * I * 2);
   L.part = o;
   if (T > 0 && !ffn_few(T, H, I)) {
-    L.up = dense_plan(kDenseBf16, T, 2 * I, H);
-    L.down = dense_plan(kDenseBf16, T, H, I);
+    L.up = dense_plan(kDenseBf16, kDenseNT, T, 2 * I, H);
+    L.down = dense_plan(kDenseBf16, kDenseNT, T, H, I);
     o = align256(o + max_of(dense_part_bytes(L.up, T, 2 * I), dense_part_bytes(L.down, T, H)));
   }
   L.total = o < 256 ? 256 : o;
@@ -162,8 +162,8 @@ FfnGradLayout ffn_grad_layout(int T, int H, int I) {
   FfnGradLayout L;
   memset(&L, 0, sizeof(L));
   const int t = T > 0 ? T : 1;
-  L.first = dense_pair_plan(H, I, t, t, I, H);
-  L.second = dense_pair_plan(2 * I, H, t, t, H, 2 * I);
+  L.first = dense_pair_plan(H, I, t, t, I, H, 2 * 4 + 2);  // g and u read, a second bf16 value written
+  L.second = dense_pair_plan(2 * I, H, t, t, H, 2 * I, 0);
   L.dgu = 0;
   L.part = align256((size_t)T * 2 * I * 2);
   size_t p = max_of(dense_part_bytes(alone_a(L.first), H, I), dense_part_bytes(alone_b(L.first), t, I));

@@ -200,26 +200,27 @@ __device__ __forceinline__ void store4(void* out, bool fp32, size_t at, const f3
   }
 }
 
-// h = silu(min(g, L)) * clamp(u, -L, L); NaN operands give NaN.
-__device__ __forceinline__ float ffn_act(float g, float u, float L) {
-  const float gc = g > L ? L : g;
-  const float uc = u > L ? L : (u < -L ? -L : u);
-  return silu(gc) * uc;
-}
+// min(v, L) and clamp(v, -L, L), one and two instructions; NaN stays NaN.
+__device__ __forceinline__ float at_most(float v, float L) { return __builtin_elementwise_minimum(v, L); }
+__device__ __forceinline__ float clamped(float v, float L) { return __builtin_elementwise_maximum(at_most(v, L), -L); }
 
-// Gradients of the gated product at the saved (g, u) for dh, four columns. g and u are saved in fp32: rounded to bf16
-// they would cost the gradients as much precision again as the rounding of dg and du (relative L2 error of dx 3.0e-3
-// against 2.4e-3), and a value next to the clamp could cross it.
+// h = silu(min(g, L)) * clamp(u, -L, L); NaN operands give NaN.
+__device__ __forceinline__ float ffn_act(float g, float u, float L) { return silu(at_most(g, L)) * clamped(u, L); }
+
+// Gradients of the gated product at the saved (g, u) for dh, four columns: with s = sigmoid(g) and t = silu(g) = g s,
+// du = dh t and dg = dh u (s + t (1 - s)). Few instructions count here: where all blocks of a launch end together, a
+// 256 x 256 tile's 128 exponentials and reciprocals per lane are bare (14 us of a launch; 17 with clamps by comparison).
+// g and u are saved in fp32: rounded to bf16 they would cost the gradients as much precision again as the rounding of
+// dg and du (relative L2 error of dx 3.0e-3 against 2.4e-3), and a value next to the clamp could cross it.
 __device__ __forceinline__ void ffn_act_grad4(const f32x4_t& g4, const f32x4_t& u4, const f32x4_t& dh, float L,
                                               f32x4_t& dg, f32x4_t& du) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float g = g4[i], u = u4[i];
-    const float gc = g > L ? L : g;
-    const float uc = u > L ? L : (u < -L ? -L : u);
+    const float gc = at_most(g4[i], L);
     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gc * 1.4426950408889634f));
-    dg[i] = g > L ? 0.0f : dh[i] * uc * (s * (1.0f + gc * (1.0f - s)));
-    du[i] = (u > L || u < -L) ? 0.0f : dh[i] * gc * s;
+    const float t = gc * s;
+    dg[i] = g4[i] > L ? 0.0f : dh[i] * clamped(u4[i], L) * __builtin_fmaf(-t, s, s + t);
+    du[i] = __builtin_fabsf(u4[i]) > L ? 0.0f : dh[i] * t;
   }
 }
 
@@ -392,10 +393,10 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t
   auto put = [&](uint16_t* p, const u32x4_t& v, bool live) {
     if (live) *reinterpret_cast<u32x4_t*>(p) = v;
   };
+  if constexpr (EPI == kEpiGate) {
 #pragma unroll
-  for (int c = 0; c < MB; ++c) {
-    const int m = m0 + c * 16 + r;
-    if constexpr (EPI == kEpiGate) {
+    for (int c = 0; c < MB; ++c) {
+      const int m = m0 + c * 16 + r;
       uint16_t* hrow = static_cast<uint16_t*>(a.out) + (size_t)m * a.I;
       auto act = [&](int b) {
         f32x4_t h;
@@ -426,21 +427,32 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t
           *reinterpret_cast<f32x4_t*>(grow + a.I + n) = acc[b + 1][c];
         }
       }
-    } else {
-      const float* s = a.gu_in + (size_t)m * 2 * a.I;
+    }
+  } else {
+    // g and u of the next 16 rows are fetched before this one's stores, which the compiler may not move loads across
+    f32x4_t gv[2][NB], uv[2][NB];
+    auto fetch = [&](int c) {  // past the edges: the last row, the first column (never stored)
+      const float* s = a.gu_in + (size_t)min(m0 + c * 16 + r, a.M - 1) * 2 * a.I;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int n = n0 + b * 16 + 4 * g, col = n < a.N ? n : 0;
+        gv[c & 1][b] = *reinterpret_cast<const f32x4_t*>(s + col);
+        uv[c & 1][b] = *reinterpret_cast<const f32x4_t*>(s + a.I + col);
+      }
+    };
+    fetch(0);
+#pragma unroll
+    for (int c = 0; c < MB; ++c) {
+      if (c + 1 < MB) fetch(c + 1);
+      const int m = m0 + c * 16 + r;
       uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I;
 #pragma unroll
       for (int b = 0; b < NB; b += 2) {
         uint2 dgv[2], duv[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int n = n0 + (b + j) * 16 + 4 * g;
-          f32x4_t gv = {0.f, 0.f, 0.f, 0.f}, uv = gv, dg, du;
-          if (m < a.M && n < a.N) {
-            gv = *reinterpret_cast<const f32x4_t*>(s + n);
-            uv = *reinterpret_cast<const f32x4_t*>(s + a.I + n);
-          }
-          ffn_act_grad4(gv, uv, acc[b + j][c], a.limit, dg, du);
+          f32x4_t dg, du;
+          ffn_act_grad4(gv[c & 1][b + j], uv[c & 1][b + j], acc[b + j][c], a.limit, dg, du);
           dgv[j] = pack4_bf16(dg);
           duv[j] = pack4_bf16(du);
         }

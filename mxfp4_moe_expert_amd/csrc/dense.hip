@@ -118,6 +118,7 @@ inline int slice_stages(DenseKind kind, int nst, int slices) {
 constexpr double kFewUs[kNumTiles] = {0.95, 0.47, 0.32, 0.26}, kFullUs[kNumTiles] = {1.45, 0.80, 0.47, 0.34};
 constexpr double kStartUs = 4.5;
 constexpr double kPairUs = 0.56;  // 64 x 128: a stage of both blocks of a CU
+constexpr double kTnCost = 1.12;  // a stage with both operands transposed (7 to 16 % by tile at 4096 x 4096 x 8192)
 inline double stage_us(int tile, double blocks) {
   const double full = blocks < 256 ? blocks / 256 : 1.0;
   if (tile == 3 && blocks > 256) return kFullUs[3] + (blocks > 512 ? 1.0 : (blocks - 256) / 256) * (kPairUs - kFullUs[3]);
@@ -127,7 +128,7 @@ inline int places(int tile) { return tile == 3 ? 512 : 256; }  // blocks the chi
 
 // The plan with the least estimated time: rounds of blocks over the 256 CUs times the stages each runs, plus the
 // partial sums' traffic (written and read at about 4 TB/s) and launch for a split.
-DensePlan dense_plan(DenseKind kind, int M, int N, int K, double* us_out) {
+DensePlan dense_plan(DenseKind kind, DenseLayout layout, int M, int N, int K, double* us_out) {
   const int nst = stages_of(kind, K);
   DensePlan best = {0, 1};
   double best_us = 1e30;
@@ -136,7 +137,8 @@ DensePlan dense_plan(DenseKind kind, int M, int N, int K, double* us_out) {
     for (int s = 1; s <= 16 && s * 4 <= nst + 3; s *= 2) {
       const int per = slice_stages(kind, nst, s), slices = ceil_div(nst, per);
       const long long blocks = tiles * slices;
-      double us = (double)((blocks + places(t) - 1) / places(t)) * (per * stage_us(t, (double)blocks) + kStartUs);
+      const double stage = stage_us(t, (double)blocks) * (layout == kDenseTN ? kTnCost : 1.0);
+      double us = (double)((blocks + places(t) - 1) / places(t)) * (per * stage + kStartUs);
       if (slices > 1) us += 3.0 + 2.0 * slices * M * (double)N * 4 / 4e6;
       if (us < best_us) {
         best_us = us;
@@ -224,20 +226,34 @@ static double makespan(long long n1, double c1, long long n2, double c2, long lo
   return x < y ? x : y;
 }
 
-DensePairPlan dense_pair_plan(int Ma, int Na, int Ka, int Mb, int Nb, int Kb) {
+// Blocks reach an epilogue that moves many bytes together, at the memory's rate, unless others run beside them: its
+// cost grows with b's share of the blocks at work. dw2 with the gradients of g and u, hidden 4096, intermediate 2048,
+// in one launch against two of the products' best tiles: 255 against 289 us at 8192 tokens, 117 / 138 at 4096, 72 / 83
+// at 2048, 30 / 37 at 512; dw13 with dx: 393 / 420, 199 / 204, 110 / 116 (at 6000 tokens 205 / 206: two launches).
+DensePairPlan dense_pair_plan(int Ma, int Na, int Ka, int Mb, int Nb, int Kb, int epi_bytes) {
   DensePairPlan best;
   double ua, ub;
-  best.a = dense_plan(kDenseBf16, Ma, Na, Ka, &ua);
-  best.b = dense_plan(kDenseBf16, Mb, Nb, Kb, &ub);
+  best.a = dense_plan(kDenseBf16, kDenseTN, Ma, Na, Ka, &ua);
+  best.b = dense_plan(kDenseBf16, kDenseNN, Mb, Nb, Kb, &ub);
   best.tile = -1;
-  double best_us = ua + ub;
+  constexpr double kBytesPerUs = 5.1e6, kEpiUs = 2.1e-4;
+  constexpr double kTwoLaunches = 1.07;  // measured over the sum of the estimates: 2 to 13 % more
+  // the epilogue of a block of tile t, with `blocks` of them at a time: its bytes, or its arithmetic
+  auto epi_us = [&](int t, double blocks) {
+    const double values = (double)kTiles[t].bm * kTiles[t].bn, bytes = blocks * epi_bytes * values / kBytesPerUs;
+    return !epi_bytes || bytes > kEpiUs * values ? bytes : kEpiUs * values;
+  };
+  double best_us = kTwoLaunches * (ua + ub) + epi_us(best.b.tile, (double)Mb * Nb / kTiles[best.b.tile].bm / kTiles[best.b.tile].bn);
   const int sa = stages_of(kDenseBf16, Ka), sb = stages_of(kDenseBf16, Kb);
-  for (int t = kNumTiles - 1; t >= 0; --t) {  // a larger tile only where it is clearly faster: its blocks mix less well
+  for (int t = kNumTiles - 1; t >= 0; --t) {
     const long long na = (long long)ceil_div(Ma, kTiles[t].bm) * ceil_div(Na, kTiles[t].bn);
     const long long nb = (long long)ceil_div(Mb, kTiles[t].bm) * ceil_div(Nb, kTiles[t].bn);
-    const double c = stage_us(t, (double)(na + nb)), ca = sa * c + kStartUs, cb = sb * c + kStartUs;
+    // blocks at work at a time, over the longer product's stages
+    const double n = ((double)na * sa + (double)nb * sb) / (sa > sb ? sa : sb), c = stage_us(t, n);
+    const double ca = sa * c * kTnCost + kStartUs;
+    const double cb = sb * c + kStartUs + epi_us(t, (n < places(t) ? n : places(t)) * nb / (double)(na + nb));
     const double us = sa > sb ? makespan(na, ca, nb, cb, places(t)) : makespan(nb, cb, na, ca, places(t));
-    if (us < (best.tile < 0 ? 1.0 : 0.92) * best_us) {
+    if (us < 0.97 * best_us) {  // near ties: separate, then the smaller tile, whose blocks mix better
       best_us = us;
       best.tile = t;
     }

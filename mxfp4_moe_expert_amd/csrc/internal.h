@@ -407,19 +407,20 @@ struct DensePlan {
   int tile;    // index of the tile configuration
   int slices;  // 1: no split
 };
-DensePlan dense_plan(DenseKind kind, int M, int N, int K, double* us_out = nullptr);  // and its estimated time
+DensePlan dense_plan(DenseKind kind, DenseLayout layout, int M, int N, int K, double* us_out = nullptr);  // and its time
 size_t dense_part_bytes(const DensePlan& p, int M, int N);  // partial sums of a split plan (0 if not split)
 // Fills stages, slices and tiles of `a` for the plan and launches it, with the
 // reduction of a split. a.part: dense_part_bytes(plan, M, N) bytes.
 hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const DensePlan& p, DenseArgs a, hipStream_t st);
 
 // Two independent bf16 products, a: layout TN, stored; b: layout NN with epilogue epi. In one launch of a common tile
-// where that is estimated to be faster (tile >= 0), else one after the other.
+// where that is estimated to be faster (tile >= 0), else one after the other. epi_bytes: what b's epilogue moves per
+// value of the product beyond a store of bf16.
 struct DensePairPlan {
   DensePlan a, b;
   int tile;
 };
-DensePairPlan dense_pair_plan(int Ma, int Na, int Ka, int Mb, int Nb, int Kb);
+DensePairPlan dense_pair_plan(int Ma, int Na, int Ka, int Mb, int Nb, int Kb, int epi_bytes);
 hipError_t launch_dense_pair(int epi, const DensePairPlan& p, DenseArgs a, DenseArgs b, hipStream_t st);
 
 hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st);  // of a split's partials
