@@ -130,16 +130,17 @@ constexpr int kStore = 0, kGate = 1, kGrad = 2;  // epilogues of dense.h
 
 struct FfnLayout {
   DensePlan up, down;
-  size_t h, part, total;
+  size_t h, part, total;  // h: [T][I] bf16; of few rows followed by what its rounding left, another [T][I]
 };
 
 FfnLayout ffn_layout(int T, int H, int I) {
   FfnLayout L;
   memset(&L, 0, sizeof(L));
   L.h = 0;
-  size_t o = align256((size_t)T * I * 2);
+  const bool few = ffn_few(T, H, I);
+  size_t o = align256((size_t)T * I * (few ? 4 : 2));
   L.part = o;
-  if (T > 0 && !ffn_few(T, H, I)) {
+  if (!few) {
     L.up = dense_plan(kDenseBf16, kDenseNT, T, 2 * I, H);
     L.down = dense_plan(kDenseBf16, kDenseNT, T, H, I);
     o = align256(o + max_of(dense_part_bytes(L.up, T, 2 * I), dense_part_bytes(L.down, T, H)));
@@ -319,6 +320,7 @@ int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* 
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint16_t* h = h_saved ? h_saved : at<uint16_t>(workspace, L.h);
   if (ffn_few(T, H, I)) {
+    uint16_t* h_lo = at<uint16_t>(workspace, L.h) + (size_t)T * I;
     FewRowsArgs a;
     memset(&a, 0, sizeof(a));
     a.T = T;
@@ -327,19 +329,21 @@ int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* 
     a.x = x;
     a.w = w13;
     a.out = h;
+    a.out_lo = h_lo;
     a.limit = limit;
     a.gu_out = gu_saved;
-    hipError_t e = launch_few_rows_bf16(a, true, st);
+    const hipError_t e = launch_few_rows_gate(a, st);
     if (e != hipSuccess) return status(e);
     memset(&a, 0, sizeof(a));
     a.T = T;
     a.N = H;
     a.K = I;
     a.x = h;
+    a.x_lo = h_lo;
     a.w = w2;
     a.out = out;
     a.out_is_fp32 = out_is_fp32 ? 1 : 0;
-    return status(launch_few_rows_bf16(a, false, st));
+    return status(launch_few_rows_two(a, st));
   }
   float* part = at<float>(workspace, L.part);
   DenseArgs a = dense_args(x, H, w13, H, T, 2 * I, H, h, 0, part);

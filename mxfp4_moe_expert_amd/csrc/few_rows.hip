@@ -12,7 +12,11 @@
 //     for four MFMA 16x16x32. Activations rounded to MXFP4: lane (t, g) holds
 //     exactly one group of token t, encodes it, and the codes of both sides
 //     go to one scaled MFMA 16x16x128.
-//   bf16: a k-step is 64 values; lane (r, g) reads 32 bytes of row r.
+//   bf16: a k-step is 64 values; lane (r, g) reads 32 bytes of row r. The gated
+//     block's h enters its second product as two bf16 values, the nearest and
+//     the nearest to what that leaves (16 bits together): the weights bound the
+//     pass, and h rounded to bf16 alone would cost the output as much again as
+//     its own rounding (relative L2 2.4e-3 against 1.7e-3).
 // Bound by the weight bytes; at one token by launch and load latency.
 #include "dense.h"
 
@@ -48,14 +52,22 @@ __device__ __forceinline__ u32x4_t lane_encode(const u32x4_t (&x)[4], uint32_t& 
   return c;
 }
 
-enum RowsFmt { kRowsBf16 = 0, kRowsMx = 1, kRowsMxA4 = 2 };
+enum RowsFmt {
+  kRowsGate = 0,   // bf16 weights and activations, gated
+  kRowsMx = 1,     // MXFP4 weights, bf16 activations
+  kRowsMxA4 = 2,   // MXFP4 weights, activations encoded to MXFP4
+  kRowsTwo = 3,    // bf16 weights, activations the sum of two bf16
+  kRowsPair = 4,   // the same for up to 8 tokens: the second parts are tokens 8 .. 15 of the MFMA, at no cost
+};
 
-template <int FMT, bool GATE, int CT, int NW>
+template <int FMT, int CT, int NW>
 __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
-  constexpr int STEP = FMT == kRowsBf16 ? 64 : 128;  // k values per step
-  constexpr int XV = STEP / 32;                    // 16-byte activation pieces per lane, token block and step
-  constexpr int WV = FMT == kRowsBf16 ? 2 : 1;       // 16-byte weight pieces per lane and step
-  constexpr int U = CT == 1 ? 4 : CT == 2 ? 2 : 1; // steps whose loads are in flight together
+  constexpr bool GATE = FMT == kRowsGate, BF = GATE || FMT == kRowsTwo || FMT == kRowsPair;
+  constexpr int STEP = BF ? 64 : 128;                  // k values per step
+  constexpr int PV = STEP / 32;                        // 16-byte activation pieces per lane, token block and step
+  constexpr int XV = FMT == kRowsTwo ? 2 * PV : PV;    // and those of the second part
+  constexpr int WV = BF ? 2 : 1;                       // 16-byte weight pieces per lane and step
+  constexpr int U = CT == 1 ? 4 : CT == 2 ? 2 : 1;     // steps whose loads are in flight together
   __shared__ __align__(16) float red[NW][CT * 256];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -67,19 +79,24 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
   const int kl = g * (STEP / 4);  // the lane's first k of a step
   const uint8_t* wrow;
   const uint8_t* srow = nullptr;
-  if constexpr (FMT == kRowsBf16) {
+  if constexpr (BF) {
     wrow = reinterpret_cast<const uint8_t*>(a.w + (size_t)row * a.K + kl);
   } else {
     wrow = a.codes + (size_t)row * (a.K / 2) + kl / 2;
     srow = a.scales + (size_t)row * (a.K / 32) + g;
   }
-  const uint16_t* xrow[CT];
+  const uint16_t *xrow[CT], *lorow[CT];
 #pragma unroll
-  for (int c = 0; c < CT; ++c) xrow[c] = a.x + (size_t)min(16 * c + r, a.T - 1) * a.K + kl;
+  for (int c = 0; c < CT; ++c) {
+    const int t = min(FMT == kRowsPair ? r & 7 : 16 * c + r, a.T - 1);
+    xrow[c] = (FMT == kRowsPair && r >= 8 ? a.x_lo : a.x) + (size_t)t * a.K + kl;
+    if constexpr (FMT == kRowsTwo) lorow[c] = a.x_lo + (size_t)t * a.K + kl;
+  }
 
-  f32x4_t acc[CT];
+  constexpr int LOW = FMT == kRowsTwo && CT == 1 ? 1 : 0;  // one block of tokens: the lo parts' sums apart, for two chains
+  f32x4_t acc[CT + LOW];
 #pragma unroll
-  for (int c = 0; c < CT; ++c) acc[c] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < CT + LOW; ++c) acc[c] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   const u32x4_t zero = {0u, 0u, 0u, 0u};
 
   for (int s0 = wave; s0 < S; s0 += NW * U) {
@@ -92,24 +109,28 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
       for (int v = 0; v < WV; ++v) {
         // a piece past K is zeros on both sides (K % 8 == 0; MXFP4: K % 32 == 0)
         const bool in = k + v * 8 < a.K;
-        w[u][v] = in ? *reinterpret_cast<const u32x4_t*>(wrow + (size_t)s * (FMT == kRowsBf16 ? 128 : 64) + v * 16) : zero;
+        w[u][v] = in ? *reinterpret_cast<const u32x4_t*>(wrow + (size_t)s * (BF ? 128 : 64) + v * 16) : zero;
       }
-      if constexpr (FMT != kRowsBf16) sc[u] = k < a.K ? srow[s * 4] : 0u;
+      if constexpr (!BF) sc[u] = k < a.K ? srow[s * 4] : 0u;
 #pragma unroll
       for (int c = 0; c < CT; ++c)
 #pragma unroll
         for (int v = 0; v < XV; ++v) {
-          const bool in = k + v * 8 < a.K;
-          x[u][c][v] = in ? *reinterpret_cast<const u32x4_t*>(xrow[c] + (size_t)s * STEP + v * 8) : zero;
+          const int at = v % PV * 8;
+          const uint16_t* from = (v < PV ? xrow[c] : lorow[c]) + (size_t)s * STEP + at;
+          x[u][c][v] = k + at < a.K ? *reinterpret_cast<const u32x4_t*>(from) : zero;
         }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if constexpr (FMT == kRowsBf16) {
+      if constexpr (BF) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
+        for (int v = 0; v < XV; ++v)
 #pragma unroll
-          for (int c = 0; c < CT; ++c) acc[c] = mfma_bf16(w[u][v], x[u][c][v], acc[c]);
+          for (int c = 0; c < CT; ++c) {
+            f32x4_t& to = acc[v < PV ? c : c + LOW];
+            to = mfma_bf16(w[u][v % PV], x[u][c][v], to);
+          }
       } else if constexpr (FMT == kRowsMx) {
         const float sv = e8m0_scale_operand(sc[u]);
 #pragma unroll
@@ -128,6 +149,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
       }
     }
   }
+  if constexpr (LOW) acc[0] += acc[1];
 #pragma unroll
   for (int c = 0; c < CT; ++c) *reinterpret_cast<f32x4_t*>(&red[wave][(c * 64 + lane) * 4]) = acc[c];
   __syncthreads();
@@ -143,7 +165,12 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
         gv += red[w][j];
         uv += red[w][j + 128];  // row n + 8
       }
-      static_cast<uint16_t*>(a.out)[(size_t)t * a.N + n0 + n] = f32_to_bf16(ffn_act(gv, uv, a.limit));
+      const size_t at = (size_t)t * a.N + n0 + n;
+      const float h = ffn_act(gv, uv, a.limit);
+      const uint16_t hi = f32_to_bf16(h);
+      const float top = __uint_as_float((uint32_t)hi << 16);
+      static_cast<uint16_t*>(a.out)[at] = hi;
+      a.out_lo[at] = f32_to_bf16(__builtin_fabsf(top) < __builtin_inff() ? h - top : 0.0f);  // none beside Inf or NaN
       if (a.gu_out) {
         float* o = a.gu_out + (size_t)t * 2 * a.N + n0 + n;
         o[0] = gv;
@@ -153,7 +180,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
       if (n0 + n >= a.N) continue;
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) v += red[w][j];
+      for (int w = 0; w < NW; ++w) v += FMT == kRowsPair ? red[w][j] + red[w][j + 32] : red[w][j];  // + token t + 8
       const size_t at = (size_t)t * a.N + n0 + n;
       if (a.out_is_fp32) static_cast<float*>(a.out)[at] = v;
       else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
@@ -163,31 +190,41 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
 
 // Waves per block: enough that the blocks of 16 rows give each of the 256 CUs
 // about 16 waves, and no more than there are k-steps.
-template <int FMT, bool GATE, int CT>
+template <int FMT, int CT>
 static hipError_t go_waves(const FewRowsArgs& a, hipStream_t st) {
-  const int blocks = GATE ? a.N / 8 : (a.N + 15) / 16;
-  if (blocks <= 320) k_few_rows<FMT, GATE, CT, 16><<<blocks, 16 * 64, 0, st>>>(a);
-  else if (blocks <= 640) k_few_rows<FMT, GATE, CT, 8><<<blocks, 8 * 64, 0, st>>>(a);
-  else k_few_rows<FMT, GATE, CT, 4><<<blocks, 4 * 64, 0, st>>>(a);
+  const int blocks = FMT == kRowsGate ? a.N / 8 : (a.N + 15) / 16;
+  if (blocks <= 320) k_few_rows<FMT, CT, 16><<<blocks, 16 * 64, 0, st>>>(a);
+  else if (blocks <= 640) k_few_rows<FMT, CT, 8><<<blocks, 8 * 64, 0, st>>>(a);
+  else k_few_rows<FMT, CT, 4><<<blocks, 4 * 64, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <int FMT, bool GATE>
+template <int FMT>
 static hipError_t go_tokens(const FewRowsArgs& a, hipStream_t st) {
-  if (a.T <= 16) return go_waves<FMT, GATE, 1>(a, st);
-  if (a.T <= 32) return go_waves<FMT, GATE, 2>(a, st);
+  if (a.T <= 16) return go_waves<FMT, 1>(a, st);
+  if (a.T <= 32) return go_waves<FMT, 2>(a, st);
   if constexpr (FMT == kRowsMxA4) return hipErrorInvalidValue;  // the caller takes the tile product there
-  else return go_waves<FMT, GATE, 4>(a, st);
+  else return go_waves<FMT, 4>(a, st);
+}
+
+static bool few_rows_ok(const FewRowsArgs& a, int step) {
+  return a.T > 0 && a.T <= kSmallT && a.N > 0 && a.K > 0 && a.K % step == 0;
 }
 
 hipError_t launch_few_rows_mxfp4(const FewRowsArgs& a, hipStream_t st) {
-  if (a.T <= 0 || a.T > kSmallT || a.N <= 0 || a.K <= 0 || a.K % 32) return hipErrorInvalidValue;
-  return a.act_mxfp4 ? go_tokens<kRowsMxA4, false>(a, st) : go_tokens<kRowsMx, false>(a, st);
+  if (!few_rows_ok(a, 32)) return hipErrorInvalidValue;
+  return a.act_mxfp4 ? go_tokens<kRowsMxA4>(a, st) : go_tokens<kRowsMx>(a, st);
 }
 
-hipError_t launch_few_rows_bf16(const FewRowsArgs& a, bool gate, hipStream_t st) {
-  if (a.T <= 0 || a.T > kSmallT || a.N <= 0 || a.K <= 0 || a.K % 8 || (gate && a.N % 8)) return hipErrorInvalidValue;
-  return gate ? go_tokens<kRowsBf16, true>(a, st) : go_tokens<kRowsBf16, false>(a, st);
+hipError_t launch_few_rows_gate(const FewRowsArgs& a, hipStream_t st) {
+  if (!few_rows_ok(a, 8) || a.N % 8 || !a.out_lo) return hipErrorInvalidValue;
+  return go_tokens<kRowsGate>(a, st);
+}
+
+hipError_t launch_few_rows_two(const FewRowsArgs& a, hipStream_t st) {
+  if (!few_rows_ok(a, 8) || !a.x_lo) return hipErrorInvalidValue;
+  if (a.T <= 8) return go_waves<kRowsPair, 1>(a, st);
+  return go_tokens<kRowsTwo>(a, st);
 }
 
 }  // namespace moe

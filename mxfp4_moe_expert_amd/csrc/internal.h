@@ -451,16 +451,19 @@ hipError_t launch_mxfp4_expand(int N, int K, const uint8_t* codes, const uint8_t
 struct FewRowsArgs {
   int T, N, K;
   const uint16_t* x;       // [T][K] bf16
+  const uint16_t* x_lo;    // [T][K] bf16 (bf16 weights, not gate): added to x
   const uint8_t* codes;    // MXFP4 weights [N][K/2], scales [N][K/32]
   const uint8_t* scales;
   const uint16_t* w;       // bf16 weights [N][K] (gate: [2I][K], N = I)
   int act_mxfp4;           // round x to MXFP4 first
-  void* out;               // [T][N]
+  void* out;               // [T][N] (gate: bf16)
   int out_is_fp32;
   float limit;             // gate
+  uint16_t* out_lo;        // gate: [T][N] bf16, what out's rounding left
   float* gu_out;           // gate: [T][2N] or null
 };
 hipError_t launch_few_rows_mxfp4(const FewRowsArgs& a, hipStream_t st);
-hipError_t launch_few_rows_bf16(const FewRowsArgs& a, bool gate, hipStream_t st);
+hipError_t launch_few_rows_gate(const FewRowsArgs& a, hipStream_t st);
+hipError_t launch_few_rows_two(const FewRowsArgs& a, hipStream_t st);
 
 }  // namespace moe

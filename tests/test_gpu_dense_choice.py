@@ -73,6 +73,37 @@ def test_ffn_streamed_or_tiled(T, H, I):
     check(mx.gated_ffn(x, w13, w2), *ref["y"], "y", l2=2 * U16)
 
 
+@pytest.mark.parametrize("T,H,I", [(1, 4096, 2048), (1, 256, 128), (7, 264, 136), (16, 1024, 512), (17, 2048, 72),
+                                   (33, 512, 1024), (64, 2048, 1024)])
+def test_ffn_streamed_keeps_sixteen_bits_of_h(T, H, I):
+    """Streamed rows: h = hi + lo, each rounded by at most a half step of bf16 of what is left, 2^-16 of h together;
+    with random signs the fp32 output is within that of its norm (beside 2^-20 of the activation, 1e-6 of the sums)."""
+    x, w13 = _bf16(T, T, H), _bf16(H, 2 * I, H, scale=1.3 / math.sqrt(H))
+    w2 = _bf16(I, H, I, scale=1 / math.sqrt(I))
+    y, bound = plain64.ffn(x.double(), w13.double(), w2.double(), 10.0)["y"]
+    out = mx.gated_ffn(x, w13, w2, out_fp32=True)
+    check(out, y, bound, "fp32", l2=2.0 ** -15)
+    saving, (_, h) = mx.gated_ffn(x, w13, w2, save=True, out_fp32=True)
+    assert torch.equal(saving, out)
+    I0 = w13[:I].double(), w13[I:].double()
+    g, u = (x.double() @ w.t() for w in I0)
+    h64 = torch.nn.functional.silu(g.clamp(max=10.0)) * u.clamp(-10.0, 10.0)
+    assert float((h.double() - h64).norm() / h64.norm()) <= U16
+
+
+def test_ffn_streamed_infinite_h():
+    """h past bf16's largest value: the output keeps its infinities apart from NaN, as bf16 operands would."""
+    H = I = 8
+    x = torch.zeros(2, H, dtype=torch.bfloat16, device=DEV)
+    x[0, 0], x[1, 1] = 3e38, 1.0
+    w13 = torch.zeros(2 * I, H, dtype=torch.bfloat16, device=DEV)
+    w13[:I, 0], w13[:I, 1], w13[I:, 0], w13[I:, 1] = 1.0, 1.0, 1.0, 1.0
+    w2 = torch.ones(H, I, dtype=torch.bfloat16, device=DEV)
+    y = mx.gated_ffn(x, w13, w2, limit=math.inf)
+    assert bool((y[0] == math.inf).all())
+    assert bool(torch.isfinite(y[1]).all())
+
+
 # the backward's products two to a launch, with every tile, and one to a launch with K split
 @pytest.mark.parametrize("T,H,I", [(2, 64, 4096), (70, 4096, 64), (400, 512, 512), (700, 1024, 1024),
                                    (1500, 2048, 1024), (2000, 1024, 4096), (3000, 4096, 2048), (5000, 256, 264)])
