@@ -25,8 +25,19 @@
 //     transposing read (16 lanes x 4 elements) hands each lane 4 consecutive
 //     k of its row.
 //   - MFMA 16x16x32 (bf16) or 16x16x128 with E8M0 scales (MXFP4), W as the A
-//     operand: lane (r, g) ends with 4 consecutive n of one m, one 8-byte
-//     bf16 store.
+//     operand: lane (r, g) ends with 4 consecutive n of one m; two blocks'
+//     lanes are joined to 16-byte stores.
+//
+// Measured (MI355X; a large copy runs at 5.1 TB/s, a large library bf16
+// product at 1.26 PFLOP/s): 8192 x 4096 x 4096, transposed W, 256 x 256 tiles
+// 205 us, 1.34 PFLOP/s, matrix cores busy 64 % of the cycles; both transposed
+// 205 us; 1000 x 4096 x 4096, 128 x 128: 34.7 us, 0.97; 300 x 4096 x 4096,
+// 64 x 128: 22.7 us; MXFP4 8192 x 4096 x 4096: 72 to 76 us, 3.6 to 3.8
+// PFLOP/s. Large tiles are bound by the MFMAs and, where a launch is one or
+// two rounds of blocks, by epilogues that nothing covers (6.5 us a round of
+// bf16 stores); the smaller ones and MXFP4 by the L2 -> LDS path (a stage of
+// 64 x 128 takes 0.26 to 0.34 us, 128 x 128 0.32 to 0.47, 256 x 128 0.47 to
+// 0.80, 256 x 256 0.95 to 1.45, with few and with all CUs at work).
 #pragma once
 
 #include <atomic>

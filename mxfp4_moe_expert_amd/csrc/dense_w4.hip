@@ -9,6 +9,11 @@
 // waves per column block; the bf16 product: 0.30). The tile's exponent bytes
 // are copied to LDS once, before the K loop (a byte per row and k-step is then
 // one LDS read).
+//
+// Measured, launch included: 33 x 8192 -> 4096, eight slices of K, 12.5 us
+// (0.37 us a stage: LDS latency, 64 MFMAs a stage and wave pair do not cover
+// it), 1000 x 4096 -> 4096 41.6 us (0.81 PFLOP/s; the bf16 product with W
+// expanded before it: 34.7 + 8.6).
 #include "dense.h"
 
 namespace moe {

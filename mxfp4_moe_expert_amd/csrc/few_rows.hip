@@ -17,7 +17,10 @@
 //     the nearest to what that leaves (16 bits together): the weights bound the
 //     pass, and h rounded to bf16 alone would cost the output as much again as
 //     its own rounding (relative L2 2.4e-3 against 1.7e-3).
-// Bound by the weight bytes; at one token by launch and load latency.
+// Bound by the weight bytes; at one token by launch and load latency; with
+// more tokens by every block's reading all activations. Measured: 1 x 4096 ->
+// 1536 (MXFP4) 5.8 us; the gated block, 1 x 4096 x 2048, 8.1 us for gate and
+// up (4.1 TB/s of weights) and 4.6 for down (3.6).
 #include "dense.h"
 
 namespace moe {

@@ -11,7 +11,10 @@
 //
 // Memory-bound in both directions. A lane takes 16 bytes per load (8 values of
 // 16 bits or 4 of 32), consecutive lanes consecutive bytes, so 4 or 8 lanes
-// share a group and its maximum is two or three lane exchanges.
+// share a group and its maximum is two or three lane exchanges. Measured,
+// 16384 x 4096 fp32: encoding 75 us (4.0 TB/s), decoding 56 to 58 us (5.2);
+// 4096 x 4096 weights to bf16 8.4 us (5.0); the operands of the 4-bit product
+// with 8192 x 4096 activations 16.5 to 17.4 us (4.9). A large copy: 5.1 TB/s.
 #include "device.h"
 #include "internal.h"
 
