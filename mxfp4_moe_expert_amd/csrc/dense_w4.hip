@@ -11,8 +11,8 @@
 // one LDS read).
 //
 // Measured, launch included: 33 x 8192 -> 4096, eight slices of K, 12.5 us
-// (0.37 us a stage: LDS latency, 64 MFMAs a stage and wave pair do not cover
-// it), 1000 x 4096 -> 4096 41.6 us (0.81 PFLOP/s; the bf16 product with W
+// (0.37 us a stage: LDS latency, which a wave's four MFMAs a k-step do not
+// cover), 1000 x 4096 -> 4096 41.6 us (0.81 PFLOP/s; the bf16 product with W
 // expanded before it: 34.7 + 8.6).
 #include "dense.h"
 

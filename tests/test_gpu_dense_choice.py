@@ -176,3 +176,45 @@ def test_ffn_long_batch():
     ref = plain64.ffn(x.double(), w13c.double(), w2[:, cols].double(), 10.0, dy.double())
     check(dw13.view(2, I, H)[:, cols].reshape(-1, H), *ref["dw13"], "dw13", l2=2 * U16)
     check(dw2[:, cols], *ref["dw2"], "dw2", l2=2 * U16)
+
+
+def test_every_path_captured_and_replayed():
+    """Each kernel family captured into a graph of its own (its first launch at that size) and replayed with eager
+    calls of the same between the replays."""
+    calls = []
+    for T, K, N, act in [(1, 256, 64, "bf16"), (100, 1024, 512, "bf16"), (700, 1024, 512, "bf16"),
+                         (3000, 1024, 2048, "bf16"), (20, 512, 96, "mxfp4"), (300, 1024, 512, "mxfp4"),
+                         (5000, 1024, 4096, "mxfp4")]:
+        codes, scales = _weight(K, N, K)
+        x = _bf16(T, T, K)
+        calls.append(lambda x=x, c=codes, s=scales, act=act: (mx.linear_mxfp4(x, c, s, act=act),))
+        if act == "bf16":
+            dy = _bf16(T + 1, T, N)
+            calls.append(lambda dy=dy, c=codes, s=scales: (mx.linear_mxfp4_dx(dy, c, s),))
+    for T, H, I in [(2, 256, 128), (200, 512, 256), (1500, 512, 1024), (4000, 2048, 2048)]:
+        x, w13 = _bf16(T, T, H), _bf16(H, 2 * I, H, scale=1.3 / math.sqrt(H))
+        w2, dy = _bf16(I, H, I, scale=1 / math.sqrt(I)), _bf16(T + 1, T, H, scale=0.1)
+
+        def step(x=x, w13=w13, w2=w2, dy=dy):
+            y, saved = mx.gated_ffn(x, w13, w2, save=True)
+            return (y,) + mx.gated_ffn_backward(dy, x, w13, w2, saved)
+
+        calls.append(step)
+    rows = _bf16(9, 70, 96)
+    calls.append(lambda: mx.quantize_mxfp4(rows))
+    torch.cuda.synchronize()
+    graphs = []
+    for call in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call()
+        graphs.append((g, out))
+    for rep in range(3):
+        for g, out in graphs:
+            for t in out:
+                t.zero_()
+            g.replay()
+        eager = [call() for call in calls]
+        torch.cuda.synchronize()
+        for i, ((_, out), ref) in enumerate(zip(graphs, eager)):
+            assert all(torch.equal(a, b) for a, b in zip(out, ref)), (rep, i)
