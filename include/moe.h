@@ -339,9 +339,9 @@ int moe_linear_mxfp4_dx(int32_t T, int32_t K, int32_t N, const uint16_t* dy, con
  *   limit  L > 0 (INFINITY: no clamp)
  *   gu_saved [T][2I] f32 (g, then u), h_saved [T][I] bf16: both given, they are written
  *   for moe_gated_ffn_backward; both NULL otherwise.
- * h enters the second product rounded to bf16 (of few rows, where the weights
- * are streamed, with 16 bits: out then differs by its own rounding only); g and
- * u are kept in fp32. NaN inputs give NaN outputs.
+ * h enters the second product rounded to bf16 (of few rows, up to 32, where the
+ * weights are streamed, with 16 bits: out then differs by its own rounding
+ * only); g and u are kept in fp32. NaN inputs give NaN outputs.
  * Two launches (both projections, activation and product in the first; more
  * where K is split, as for moe_linear_mxfp4).
  *   workspace: moe_gated_ffn_workspace_size(T, H, I) bytes, 256-byte aligned,

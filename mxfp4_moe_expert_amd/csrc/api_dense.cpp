@@ -39,18 +39,25 @@ bool linear_ok(int T, int K, int N) {
 
 // Rows up to which a product runs in the streaming pass (few_rows.hip) rather than as a tile product. Every block of
 // the pass reads all activations, T K values, through its CU's share of the L2, while the tile product splits K over
-// blocks at the price of a second launch: at 4096 x 4096 (MXFP4, bf16 activations) 11.1 against 12.4 us at 32 rows and
-// 15.8 against 13.8 at 48; at K = 8192 the two meet at 16 rows (15.2 us at 17), at K = 2048 at 64 (10.2 against 11.0).
-// Activations that the pass encodes to MXFP4 itself cost it a little more (9.5 against 10.4 us at 17 rows of 4096,
-// 11.9 against 11.2 at 32).
+// blocks at the price of a second launch: at 4096 x 4096 (MXFP4, bf16 activations) 9.8 us at 24 rows and 11.1 at 32
+// against 10.9 at 33, at K = 8192 11.9 at 12 rows and 13.2 at 16 against 12.1 at 17, at 2048 x 2048 6.7 against 7.6 at 32
+// rows. Activations that the pass encodes to MXFP4 itself cost it a little more (4096 x 4096: 10.6 us at 24 rows, the
+// tile product 11.1 at 28; K = 8192: 12.4 at 12 rows, 11.5 at 16).
 bool linear_few(int T, int K, int act) {
-  if (act == MOE_ACT_MXFP4) return T <= 32 && (long long)T * K <= 98304;
-  return T <= kSmallT && (long long)T * K <= 131072;
+  return T <= kFewRows && (long long)T * K <= (act == MOE_ACT_MXFP4 ? 81920 : 98304);
 }
-// The gated block: the same bytes over both products, by rounds of 256 blocks (of 8 gate rows; of 16). Measured to meet
-// at 42 rows of 4096 x 2048 (hidden x intermediate), 32 of 1024 x 4096, and past 64 of 2048 x 1024.
+// The gated block: two passes, by their weights and by what each CU's blocks (of 8 gate and 8 up rows; of 16) read of the
+// activations (h in two parts), against the tile products' estimate. 4096 x 2048 (hidden x intermediate):
+// 20.1 us at 17 rows and 22.5 at 24 against 20.8 at 24; 2048 x 1024: 12.7 at 24 and 14.1 at 32 against 13.6 at 33; 1024 x
+// 4096: 14.4 at 8 and 16.8 at 12 against 14.4 at 17.
 bool ffn_few(int T, int H, int I) {
-  return T <= kSmallT && (long long)T * ((long long)H * ((I + 2047) / 2048) + (long long)I * ((H + 4095) / 4096)) <= 220000;
+  if (T <= 8 || T > kFewRows) return T <= 8;  // without the estimates' microsecond on the host where calls are shortest
+  const double values = (double)T * ((double)H * ((I + 2047) / 2048) + 2.0 * I * ((H + 4095) / 4096));
+  const double few_us = 7.0 + 6.0 * H * I / 1e7 + 5.7e-5 * values;
+  double up_us, down_us;
+  dense_plan(kDenseBf16, kDenseNT, T, 2 * I, H, &up_us);
+  dense_plan(kDenseBf16, kDenseNT, T, H, I, &down_us);
+  return few_us < up_us + down_us;
 }
 
 // ---- workspace layouts
@@ -130,6 +137,7 @@ constexpr int kStore = 0, kGate = 1, kGrad = 2;  // epilogues of dense.h
 
 struct FfnLayout {
   DensePlan up, down;
+  bool few;               // streamed
   size_t h, part, total;  // h: [T][I] bf16; of few rows followed by what its rounding left, another [T][I]
 };
 
@@ -137,10 +145,10 @@ FfnLayout ffn_layout(int T, int H, int I) {
   FfnLayout L;
   memset(&L, 0, sizeof(L));
   L.h = 0;
-  const bool few = ffn_few(T, H, I);
-  size_t o = align256((size_t)T * I * (few ? 4 : 2));
+  L.few = ffn_few(T, H, I);
+  size_t o = align256((size_t)T * I * (L.few ? 4 : 2));
   L.part = o;
-  if (!few) {
+  if (!L.few) {
     L.up = dense_plan(kDenseBf16, kDenseNT, T, 2 * I, H);
     L.down = dense_plan(kDenseBf16, kDenseNT, T, H, I);
     o = align256(o + max_of(dense_part_bytes(L.up, T, 2 * I), dense_part_bytes(L.down, T, H)));
@@ -319,7 +327,7 @@ int moe_gated_ffn(int32_t T, int32_t H, int32_t I, float limit, const uint16_t* 
   if (rc) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint16_t* h = h_saved ? h_saved : at<uint16_t>(workspace, L.h);
-  if (ffn_few(T, H, I)) {
+  if (L.few) {
     uint16_t* h_lo = at<uint16_t>(workspace, L.h) + (size_t)T * I;
     FewRowsArgs a;
     memset(&a, 0, sizeof(a));

@@ -24,10 +24,10 @@ constexpr size_t tile_lds(const TileCfg& t, bool fp4) {
 // Sums the slices of a split K in order, then the epilogue of the product.
 // Thread: four consecutive columns of one row.
 template <int EPI>
-__global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
+__global__ __launch_bounds__(64) void k_dense_reduce(DenseArgs a, int slices) {
   const int cols = EPI == kEpiGate ? a.I : a.N;
   const int per = (cols + 3) / 4;
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long id = (long long)blockIdx.x * 64 + threadIdx.x;
   const int m = (int)(id / per), n = (int)(id - (long long)m * per) * 4;
   if (m >= a.M) return;
   const size_t plane = (size_t)a.M * a.N;
@@ -35,10 +35,20 @@ __global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
   auto sum = [&](int col) {
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
     const float* p = a.part + (size_t)m * a.N + col;
-    for (int s = 0; s < slices; ++s, p += plane) {
-      if (wide) {
-        v += *reinterpret_cast<const f32x4_t*>(p);
-      } else {
+    if (wide) {
+      // eight slices' loads in flight together (past the last slice: the last again, not added)
+      constexpr int AHEAD = 8;
+      for (int s0 = 0; s0 < slices; s0 += AHEAD) {
+        f32x4_t t[AHEAD];
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s)
+          t[s] = *reinterpret_cast<const f32x4_t*>(p + (size_t)min(s0 + s, slices - 1) * plane);
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s)
+          if (s0 + s < slices) v += t[s];
+      }
+    } else {
+      for (int s = 0; s < slices; ++s, p += plane) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (col + i < a.N) v[i] += p[i];
@@ -58,10 +68,10 @@ __global__ __launch_bounds__(256) void k_dense_reduce(DenseArgs a, int slices) {
       *reinterpret_cast<f32x4_t*>(o + a.I) = u;
     }
   } else if constexpr (EPI == kEpiGrad) {
-    const f32x4_t dh = sum(n);
     const float* s = a.gu_in + (size_t)m * 2 * a.I + n;
+    const f32x4_t g = *reinterpret_cast<const f32x4_t*>(s), u = *reinterpret_cast<const f32x4_t*>(s + a.I);
     f32x4_t dg, du;
-    ffn_act_grad4(*reinterpret_cast<const f32x4_t*>(s), *reinterpret_cast<const f32x4_t*>(s + a.I), dh, a.limit, dg, du);
+    ffn_act_grad4(g, u, sum(n), a.limit, dg, du);
     uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)m * 2 * a.I + n;
     *reinterpret_cast<uint2*>(o) = pack4_bf16(dg);
     *reinterpret_cast<uint2*>(o + a.I) = pack4_bf16(du);
@@ -139,7 +149,7 @@ DensePlan dense_plan(DenseKind kind, DenseLayout layout, int M, int N, int K, do
       const long long blocks = tiles * slices;
       const double stage = stage_us(t, (double)blocks) * (layout == kDenseTN ? kTnCost : 1.0);
       double us = (double)((blocks + places(t) - 1) / places(t)) * (per * stage + kStartUs);
-      if (slices > 1) us += 3.0 + 2.0 * slices * M * (double)N * 4 / 4e6;
+      if (slices > 1) us += 2.5 + 2.0 * slices * M * (double)N * 4 / 4e6;
       if (us < best_us) {
         best_us = us;
         best = {t, slices};
@@ -281,10 +291,10 @@ hipError_t launch_dense_pair(int epi, const DensePairPlan& p, DenseArgs a, Dense
 hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st) {
   const int cols = epi == kEpiGate ? a.I : a.N;
   const long long threads = (long long)a.M * ((cols + 3) / 4);
-  const unsigned nb = (unsigned)((threads + 255) / 256);
-  if (epi == kEpiGate) k_dense_reduce<kEpiGate><<<nb, 256, 0, st>>>(a, slices);
-  else if (epi == kEpiGrad) k_dense_reduce<kEpiGrad><<<nb, 256, 0, st>>>(a, slices);
-  else k_dense_reduce<kEpiStore><<<nb, 256, 0, st>>>(a, slices);
+  const unsigned nb = (unsigned)((threads + 63) / 64);
+  if (epi == kEpiGate) k_dense_reduce<kEpiGate><<<nb, 64, 0, st>>>(a, slices);
+  else if (epi == kEpiGrad) k_dense_reduce<kEpiGrad><<<nb, 64, 0, st>>>(a, slices);
+  else k_dense_reduce<kEpiStore><<<nb, 64, 0, st>>>(a, slices);
   return hipGetLastError();
 }
 

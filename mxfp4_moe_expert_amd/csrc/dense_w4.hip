@@ -221,7 +221,7 @@ DensePlan dense_w4_plan(int M, int N, int K, double* us_out) {
       if (w4_lds(kW4[t], per) > kLdsBlockMax) continue;
       const long long blocks = tiles * slices;
       double us = (double)((blocks + 255) / 256) * (per * stage_us[t] + start_us);
-      if (slices > 1) us += 3.0 + 2.0 * slices * M * (double)N * 4 / 4e6;
+      if (slices > 1) us += 2.5 + 2.0 * slices * M * (double)N * 4 / 4e6;
       if (us < best_us) {
         best_us = us;
         best = {t, slices};

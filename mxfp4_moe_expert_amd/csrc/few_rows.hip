@@ -1,4 +1,4 @@
-// Products of at most 64 rows with a weight matrix that is streamed once:
+// Products of at most 32 rows with a weight matrix that is streamed once:
 // MXFP4 weights (moe_linear_mxfp4) and bf16 weights (the gated block).
 //
 // A block owns 16 weight rows (gate: 8 gate rows and the matching 8 up rows)
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
   constexpr int PV = STEP / 32;                        // 16-byte activation pieces per lane, token block and step
   constexpr int XV = FMT == kRowsTwo ? 2 * PV : PV;    // and those of the second part
   constexpr int WV = BF ? 2 : 1;                       // 16-byte weight pieces per lane and step
-  constexpr int U = CT == 1 ? 4 : CT == 2 ? 2 : 1;     // steps whose loads are in flight together
+  constexpr int U = CT == 1 ? 4 : 2;                   // steps whose loads are in flight together
   __shared__ __align__(16) float red[NW][CT * 256];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -205,13 +205,11 @@ static hipError_t go_waves(const FewRowsArgs& a, hipStream_t st) {
 template <int FMT>
 static hipError_t go_tokens(const FewRowsArgs& a, hipStream_t st) {
   if (a.T <= 16) return go_waves<FMT, 1>(a, st);
-  if (a.T <= 32) return go_waves<FMT, 2>(a, st);
-  if constexpr (FMT == kRowsMxA4) return hipErrorInvalidValue;  // the caller takes the tile product there
-  else return go_waves<FMT, 4>(a, st);
+  return go_waves<FMT, 2>(a, st);
 }
 
 static bool few_rows_ok(const FewRowsArgs& a, int step) {
-  return a.T > 0 && a.T <= kSmallT && a.N > 0 && a.K > 0 && a.K % step == 0;
+  return a.T > 0 && a.T <= kFewRows && a.N > 0 && a.K > 0 && a.K % step == 0;
 }
 
 hipError_t launch_few_rows_mxfp4(const FewRowsArgs& a, hipStream_t st) {

@@ -447,7 +447,8 @@ hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, u
 hipError_t launch_mxfp4_expand(int N, int K, const uint8_t* codes, const uint8_t* scales, uint16_t* w, int T,
                                const uint16_t* dy, uint16_t* dyp, int ld, hipStream_t st);
 
-// Up to kSmallT rows: K split over the waves of a block (few_rows.hip)
+// The streaming pass (few_rows.hip): K split over the waves of a block
+constexpr int kFewRows = 32;  // rows it takes
 struct FewRowsArgs {
   int T, N, K;
   const uint16_t* x;       // [T][K] bf16
