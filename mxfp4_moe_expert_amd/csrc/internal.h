@@ -387,7 +387,7 @@ struct DenseArgs {
   int M, N, K;               // K in values
   int stages, slice_stages;  // K stages (128 bytes of a K-contiguous row each), stages per slice of a split K
   int tm, tn;                // tiles along M and N
-  const uint32_t* x_scales;  // packed E8M0 bytes (MXFP4 operands), see mxfp4_pack_at
+  const uint32_t* x_scales;  // packed E8M0 bytes (MXFP4 operands), see mxfp4.hip
   const uint32_t* w_scales;
   int x_blocks, w_blocks;    // their 16-row blocks
   void* out;                 // [M][N]; gate: h [M][I] bf16; grad: dgu [M][2I] bf16
