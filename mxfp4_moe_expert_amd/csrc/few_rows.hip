@@ -16,7 +16,8 @@
 //     block's h enters its second product as two bf16 values, the nearest and
 //     the nearest to what that leaves (16 bits together): the weights bound the
 //     pass, and h rounded to bf16 alone would cost the output as much again as
-//     its own rounding (relative L2 2.4e-3 against 1.7e-3).
+//     its own rounding (relative L2 2.4e-3 against 1.7e-3). The parts' sums stay
+//     apart until the first is known to be finite (two_parts).
 // Bound by the weight bytes; at one token by launch and load latency; with
 // more tokens by every block's reading all activations. Measured: 1 x 4096 ->
 // 1536 (MXFP4) 5.8 us; the gated block, 1 x 4096 x 2048, 8.1 us for gate and
@@ -53,6 +54,18 @@ __device__ __forceinline__ u32x4_t lane_encode(const u32x4_t (&x)[4], uint32_t& 
     c[i] = bad ? 0u : d;
   }
   return c;
+}
+
+// The sum of h's first parts and that of the second. An infinite weight, or a product past the largest value, makes the
+// first infinite and the second NaN (a second part of 0) or infinite with either sign: the first alone is the answer.
+// Where the first is finite so is the second, 2^-8 of it term by term.
+__device__ __forceinline__ float two_parts(float hi, float lo) {
+  return __builtin_fabsf(hi) < __builtin_inff() ? hi + lo : hi;
+}
+
+// The value of the lane 8 further on in its 16.
+__device__ __forceinline__ float from_lane_8_on(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x128, 0xf, 0xf, true));  // row_ror:8
 }
 
 enum RowsFmt {
@@ -96,7 +109,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
     if constexpr (FMT == kRowsTwo) lorow[c] = a.x_lo + (size_t)t * a.K + kl;
   }
 
-  constexpr int LOW = FMT == kRowsTwo && CT == 1 ? 1 : 0;  // one block of tokens: the lo parts' sums apart, for two chains
+  constexpr int LOW = FMT == kRowsTwo ? CT : 0;  // the second parts' sums
   f32x4_t acc[CT + LOW];
 #pragma unroll
   for (int c = 0; c < CT + LOW; ++c) acc[c] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
@@ -152,7 +165,14 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
       }
     }
   }
-  if constexpr (LOW) acc[0] += acc[1];
+#pragma unroll
+  for (int c = 0; c < LOW; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[c][i] = two_parts(acc[c][i], acc[c + LOW][i]);
+  if constexpr (FMT == kRowsPair) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[0][i] = two_parts(acc[0][i], from_lane_8_on(acc[0][i]));
+  }
 #pragma unroll
   for (int c = 0; c < CT; ++c) *reinterpret_cast<f32x4_t*>(&red[wave][(c * 64 + lane) * 4]) = acc[c];
   __syncthreads();
@@ -183,7 +203,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
       if (n0 + n >= a.N) continue;
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) v += FMT == kRowsPair ? red[w][j] + red[w][j + 32] : red[w][j];  // + token t + 8
+      for (int w = 0; w < NW; ++w) v += red[w][j];
       const size_t at = (size_t)t * a.N + n0 + n;
       if (a.out_is_fp32) static_cast<float*>(a.out)[at] = v;
       else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);

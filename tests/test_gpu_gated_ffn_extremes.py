@@ -66,3 +66,51 @@ def test_gradients_of_large_gates(T, H, I, need, limit):
     absw = torch.cat((dg, du), 1).abs() @ w.abs()
     bound = eg @ w[:I].abs() + eu @ w[I:].abs() + sum_err(absw, 2 * I) + 2 * U16 * ref.abs()
     assert bool(((dx.double() - ref).abs() <= bound).all())
+
+
+# streamed rows: h's two parts in one product's columns (up to 8 rows), as two products of one and of two token blocks,
+# by blocks of 16, 8 and 4 waves; then tile products
+@pytest.mark.parametrize("T,H,I", [(1, 64, 64), (5, 264, 1032), (8, 64, 136), (3, 5144, 72), (2, 10264, 72), (9, 64, 64),
+                                   (16, 264, 1032), (10, 5144, 72), (9, 10272, 72), (17, 64, 64), (32, 264, 520),
+                                   (18, 5144, 72), (40, 64, 64), (100, 264, 136)])
+def test_infinite_down_weights(T, H, I):
+    """An infinite w2[n][i] makes column n of y infinite with the sign of h[t][i], whatever the rounding of h to bf16
+    leaves or however that is signed; every other column is as without it."""
+    g_ = _gen(T + H + I)
+    x = torch.randn(T, H, generator=g_, device=DEV).to(torch.bfloat16)
+    w13 = (torch.randn(2 * I, H, generator=g_, device=DEV) * 1.3 / math.sqrt(H)).to(torch.bfloat16)
+    w2 = (torch.randn(H, I, generator=g_, device=DEV) / math.sqrt(I)).to(torch.bfloat16)
+    clean, (_, h) = mx.gated_ffn(x, w13, w2, save=True, out_fp32=True)
+    places = [(0, 3, math.inf), (1, I - 1, -math.inf), (17, 40, -math.inf), (H - 1, I // 2, math.inf), (33, 0, math.inf)]
+    bad = w2.clone()
+    for n, i, v in places:
+        bad[n, i] = v
+    for fp32 in (True, False):
+        y = mx.gated_ffn(x, w13, bad, out_fp32=fp32)
+        for n, i, v in places:
+            assert bool((h[:, i] != 0).all())
+            want = torch.sign(h[:, i].float()) * v
+            assert torch.equal(y[:, n].float(), want), (n, i, v, y[:, n][:8], want[:8])
+        keep = torch.ones(H, dtype=torch.bool, device=DEV)
+        keep[[n for n, _, _ in places]] = False
+        assert torch.equal(y[:, keep], clean[:, keep].to(y.dtype))
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 16, 17, 32, 50])
+def test_products_past_the_largest_value(T):
+    """h = 1029 and 1027 under weights of 3e38 and -3e38: both parts' products pass fp32's range (bf16 holds 1032 and
+    1024: the rest, -3 and 3, has either sign), and y is infinite, not NaN."""
+    H = I = 64
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 1.0, 1.0
+    w13 = torch.zeros(2 * I, H, dtype=torch.bfloat16, device=DEV)
+    w13[0, 0], w13[0, 1] = 1024.0, 5.0
+    w13[1, 0], w13[1, 1] = 1024.0, 3.0
+    w13[I:, 2] = 1.0
+    w2 = torch.zeros(H, I, dtype=torch.bfloat16, device=DEV)
+    w2[0, 0], w2[1, 0], w2[2, 1], w2[3, 1], w2[4, 0] = 3e38, -3e38, 3e38, -3e38, 1.0
+    y = mx.gated_ffn(x, w13, w2, limit=math.inf, out_fp32=True)
+    for n, v in ((0, math.inf), (1, -math.inf), (2, math.inf), (3, -math.inf)):
+        assert bool((y[:, n] == v).all()), (n, y[:, n][:4])
+    assert bool((y[:, 4] == (1029.0 if T <= 32 else 1032.0)).all())
+    assert not bool(y[:, 5:].any())
