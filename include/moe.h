@@ -274,7 +274,10 @@ int moe_linear_w8a16(int32_t T, int32_t K, int32_t N, int32_t groups, const uint
  * w13_codes / w13_scales and w2_codes / w2_scales, so that weights encoded
  * here go straight into moe_expert_ffn and moe_forward. A scale byte 255
  * stands for NaN: such a group reads as NaN and so does every product with it
- * (moe_mxfp4_quantize writes it only for a group that holds an Inf or NaN). */
+ * (moe_mxfp4_quantize writes it only for a group that holds an Inf or NaN).
+ * Pointers are 16-byte aligned as everywhere here, those of scales too: a
+ * matrix of a stack whose N K / 32 is not a multiple of 16 needs its scales
+ * at such a border of their own (the Python binding copies them there). */
 
 /* Element types of the conversions. */
 enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F16 = 2 };

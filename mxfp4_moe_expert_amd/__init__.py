@@ -552,13 +552,34 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _border(p, name, bytes_=16):
+    """Pointer p, at a border of ``bytes_`` as the library needs it."""
+    if p & (bytes_ - 1):
+        raise MoEError(MOE_EINVAL, f"{name}: not {bytes_}-byte aligned")
+    return p
+
+
 def _arg(t, dtype, shape, index, name):
-    """t's pointer, t being a contiguous ``dtype`` tensor of ``shape`` on device ``index``."""
+    """t's pointer, t being a contiguous, 16-byte aligned ``dtype`` tensor of ``shape`` on device ``index``."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous()):
-        return t.data_ptr()
+        p = t.data_ptr()
+        return _border(p, name) if p & 15 else p
     _need(t, dtype, shape, name)
     raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+
+
+def _scale_bytes(t, shape, index):
+    """Pointer of an MXFP4 tensor's scales, and the tensor it belongs to (to be kept until the call is queued). Cut out
+    of a stacked tensor they start at any byte, N K / 32 being any number: the call then reads an aligned copy."""
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        p = t.data_ptr()
+        if p & 15:
+            t = t.clone()
+            p = t.data_ptr()
+        return p, t
+    return _arg(t, torch.uint8, shape, index, "scales"), t
 
 
 def _matrix(t, dtype, name):
@@ -592,7 +613,7 @@ def _scratch(need, like, ws, what):
     if ws is None:
         ws = like.new_empty((need,), dtype=torch.uint8)
         return ws.data_ptr(), need, ws
-    return _arg(ws, torch.uint8, ws.shape, like.get_device(), "ws"), ws.numel(), ws
+    return _border(_arg(ws, torch.uint8, ws.shape, like.get_device(), "ws"), "ws", 256), ws.numel(), ws
 
 
 def _result(out, shape, dtype, like, name="out"):
@@ -627,13 +648,16 @@ def quantize_mxfp4(x, out=None):
     c, s = out if out is not None else (None, None)
     codes = _result(c, lead + (K // 2,), torch.uint8, x, "codes")
     scales = _result(s, lead + (K // 32,), torch.uint8, x, "scales")
-    _call(x.get_device(), "moe_mxfp4_quantize", x.numel() // K, K, dt, x.data_ptr(), ldx, codes.data_ptr(),
-          scales.data_ptr())
+    px = _border(x.data_ptr(), "x")
+    if ldx * x.element_size() % 16:
+        raise MoEError(MOE_EINVAL, "x: rows not 16-byte aligned")
+    _call(x.get_device(), "moe_mxfp4_quantize", x.numel() // K, K, dt, px, ldx, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None):
-    """(codes [..., K/2], scales [..., K/32]) -> [..., K] in bf16 or fp32, exact (moe_mxfp4_dequantize)."""
+    """(codes [..., K/2], scales [..., K/32]) -> [..., K] in bf16 or fp32, exact (moe_mxfp4_dequantize). The scales
+    may start at any byte, as those of one matrix of a stack do (here and in the products)."""
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"dtype {dtype}, expected bfloat16 or float32")
     if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
@@ -644,19 +668,21 @@ def dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None):
         raise ValueError("codes: last dimension must be a positive multiple of 16")
     lead = tuple(shape[:-1])
     pc = _arg(codes, torch.uint8, shape, index, "codes")
-    ps = _arg(scales, torch.uint8, lead + (K // 32,), index, "scales")
+    ps, scales = _scale_bytes(scales, lead + (K // 32,), index)
     out = _result(out, lead + (K,), dtype, codes)
     _call(index, "moe_mxfp4_dequantize", codes.numel() * 2 // K, K, pc, ps, _DTYPES[dtype], out.data_ptr())
     return out
 
 
 def _mxfp4_weight(codes, scales, index):
-    """N, K and the pointers of an MXFP4 matrix [N][K] on device ``index``."""
+    """N, K and the pointers of an MXFP4 matrix [N][K] on device ``index``, and its scales' tensor (to be kept)."""
     if (isinstance(codes, torch.Tensor) and codes.dtype is torch.uint8 and codes.dim() == 2
             and codes.get_device() == index and codes.is_contiguous()):
         N, half = codes.shape
         if half and half % 16 == 0:
-            return N, half * 2, codes.data_ptr(), _arg(scales, torch.uint8, (N, half // 16), index, "scales")
+            ps, scales = _scale_bytes(scales, (N, half // 16), index)
+            p = codes.data_ptr()
+            return N, half * 2, _border(p, "codes") if p & 15 else p, ps, scales
     _matrix(codes, torch.uint8, "codes")
     _arg(codes, torch.uint8, codes.shape, index, "codes")
     raise ValueError("codes: shape [N, K/2] with K a positive multiple of 32 expected")
@@ -670,9 +696,12 @@ def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None
     if mode is None:
         raise ValueError(f"act {act!r}, expected one of {sorted(_ACTS)}")
     T, cols, index = _matrix(x, torch.bfloat16, "x")
-    N, K, pc, ps = _mxfp4_weight(codes, scales, index)
+    N, K, pc, ps, scales = _mxfp4_weight(codes, scales, index)
     if cols != K or not x.is_contiguous():
         _need(x, torch.bfloat16, (T, K), "x")
+    px = x.data_ptr()
+    if px & 15:
+        _border(px, "x")
     if out is None:
         out = x.new_empty((T, N), dtype=torch.float32) if out_fp32 else x.new_empty((T, N))
     else:
@@ -682,7 +711,7 @@ def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None
         need = lib().moe_linear_mxfp4_workspace_size(T, K, N, mode)
         if need != 256 or ws is not None:
             pw, nw, ws = _scratch(need, x, ws, "moe_linear_mxfp4")
-    _call(index, "moe_linear_mxfp4", T, K, N, x.data_ptr(), pc, ps, mode, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
+    _call(index, "moe_linear_mxfp4", T, K, N, px, pc, ps, mode, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
     return out
 
 
@@ -690,7 +719,7 @@ def linear_mxfp4_dx(dy, codes, scales, out_fp32=False, out=None, ws=None):
     """dx = dy W, the input gradient of ``linear_mxfp4`` through frozen
     weights (moe_linear_mxfp4_dx): dy [T][N] bf16 -> [T][K] (bf16 or fp32)."""
     T, _, index = _matrix(dy, torch.bfloat16, "dy")
-    N, K, pc, ps = _mxfp4_weight(codes, scales, index)
+    N, K, pc, ps, scales = _mxfp4_weight(codes, scales, index)
     py = _arg(dy, torch.bfloat16, (T, N), index, "dy")
     out = _result(out, (T, K), torch.float32 if out_fp32 else torch.bfloat16, dy)
     pw, nw, ws = _scratch(lib().moe_linear_mxfp4_dx_workspace_size(T, K, N), dy, ws, "moe_linear_mxfp4_dx")
