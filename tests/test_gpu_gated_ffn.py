@@ -34,6 +34,8 @@ def _ref(x, w13, w2, L, dy=None):
 # steps on the way: y and dw2: h and the output; dx and dw13: dg / du and the output.
 L2_OUT, L2_GRAD = 2 * U16, 2 * U16
 
+# The streaming pass ends at 32 rows, or earlier by size: 33 and 64 rows below run as tile products. Its variants by
+# waves, and the tiles with K split, are in test_gpu_dense_variants.py.
 SHAPES = [  # T, H, I: the streaming pass (1 .. 64), then every tile size, splits and ragged edges
     (1, 8, 8), (1, 4096, 2048), (2, 264, 136), (16, 1024, 512), (17, 2048, 72), (33, 512, 1024), (64, 4096, 512),
     (65, 8, 8), (65, 1024, 264), (100, 4096, 2048), (129, 264, 520), (300, 4096, 2048), (777, 2048, 1024),

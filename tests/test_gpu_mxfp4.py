@@ -138,6 +138,8 @@ def test_quantize_refusals_on_device():
 
 # ---------------------------------------------------------------- products
 
+# The streaming pass ends at 32 rows, or earlier by size: 33 and 64 rows below run as tile products. Its variants by
+# waves, and the tiles with K split, are in test_gpu_dense_variants.py.
 SHAPES = [  # T, K, N: the streaming pass (1 .. 64), then every tile size and splits of K
     (1, 32, 1), (1, 4096, 1536), (1, 96, 17), (2, 8192, 256), (15, 2080, 100), (16, 4096, 4096), (17, 512, 12000),
     (32, 1024, 48), (33, 8192, 640), (64, 2048, 1000), (64, 288, 20000),
