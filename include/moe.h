@@ -275,6 +275,10 @@ int moe_linear_w8a16(int32_t T, int32_t K, int32_t N, int32_t groups, const uint
  * here go straight into moe_expert_ffn and moe_forward. A scale byte 255
  * stands for NaN: such a group reads as NaN and so does every product with it
  * (moe_mxfp4_quantize writes it only for a group that holds an Inf or NaN).
+ * Bytes 253 and 254 reach past fp32 and bf16: values of 2^128 and more (codes
+ * 4 and 6, and from 2 on; no encoding of finite values has them) read as
+ * infinities and are infinite in products, except where activations enter as
+ * MXFP4 too (MOE_ACT_MXFP4: the codes are multiplied, exactly).
  * Pointers are 16-byte aligned as everywhere here, those of scales too: a
  * matrix of a stack whose N K / 32 is not a multiple of 16 needs its scales
  * at such a border of their own (the Python binding copies them there). */
@@ -293,7 +297,7 @@ enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F16 = 2 };
 int moe_mxfp4_quantize(int64_t rows, int32_t K, int32_t dtype, const void* x, int64_t ldx, uint8_t* codes,
                        uint8_t* scales, void* stream);
 
-/* codes, scales -> out [rows][K] contiguous, exact. dtype: MOE_DTYPE_BF16 or
+/* codes, scales -> out [rows][K] contiguous, exact (below 2^128). dtype: MOE_DTYPE_BF16 or
  * _F32 (binary16 does not hold every value: MOE_EUNSUPPORTED). */
 int moe_mxfp4_dequantize(int64_t rows, int32_t K, const uint8_t* codes, const uint8_t* scales, int32_t dtype,
                          void* out, void* stream);
