@@ -212,13 +212,16 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(FewRowsArgs a) {
 }
 
 // Waves per block: enough that the blocks of 16 rows give each of the 256 CUs
-// about 16 waves, and no more than there are k-steps.
+// about 16 waves. (Where K has fewer steps than the block has waves, the others
+// add zeros.) With 17 and more rows the gated block runs as tile products before
+// it has more than 640 blocks: its estimate is 16 % above theirs at the least.
 template <int FMT, int CT>
 static hipError_t go_waves(const FewRowsArgs& a, hipStream_t st) {
+  constexpr bool FOUR = CT == 1 || FMT == kRowsMx || FMT == kRowsMxA4;
   const int blocks = FMT == kRowsGate ? a.N / 8 : (a.N + 15) / 16;
   if (blocks <= 320) k_few_rows<FMT, CT, 16><<<blocks, 16 * 64, 0, st>>>(a);
-  else if (blocks <= 640) k_few_rows<FMT, CT, 8><<<blocks, 8 * 64, 0, st>>>(a);
-  else k_few_rows<FMT, CT, 4><<<blocks, 4 * 64, 0, st>>>(a);
+  else if (blocks <= 640 || !FOUR) k_few_rows<FMT, CT, 8><<<blocks, 8 * 64, 0, st>>>(a);
+  else if constexpr (FOUR) k_few_rows<FMT, CT, 4><<<blocks, 4 * 64, 0, st>>>(a);
   return hipGetLastError();
 }
 
