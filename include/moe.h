@@ -328,8 +328,10 @@ int moe_linear_mxfp4(int32_t T, int32_t K, int32_t N, const uint16_t* x, const u
 
 /* The input gradient of the same product through frozen weights:
  *   dx [T][K] = dy [T][N] W, dy bf16, dx bf16 or f32.
- * Sizes, workspace and errors as for moe_linear_mxfp4; every T uses the
- * workspace. */
+ * Sizes, workspace and errors as for moe_linear_mxfp4. Every T takes the same
+ * route: W is expanded to bf16 in the workspace (N K 2 bytes of it, for one
+ * row too), then multiplied. Of few rows the expansion is a large part of the
+ * call (4096 x 4096: 24 us at 1 to 64 rows). */
 size_t moe_linear_mxfp4_dx_workspace_size(int32_t T, int32_t K, int32_t N);
 int moe_linear_mxfp4_dx(int32_t T, int32_t K, int32_t N, const uint16_t* dy, const uint8_t* codes,
                         const uint8_t* scales, void* dx, int32_t out_is_fp32, void* workspace, size_t workspace_bytes,
@@ -348,7 +350,9 @@ int moe_linear_mxfp4_dx(int32_t T, int32_t K, int32_t N, const uint16_t* dy, con
  *   for moe_gated_ffn_backward; both NULL otherwise.
  * h enters the second product rounded to bf16 (of few rows, up to 32, where the
  * weights are streamed, with 16 bits: out then differs by its own rounding
- * only); g and u are kept in fp32. NaN inputs give NaN outputs.
+ * only), whatever the type of out: a token's output depends in its last bits on
+ * how many rows stand beside it. g and u are kept in fp32. NaN inputs give NaN
+ * outputs.
  * Two launches (both projections, activation and product in the first; more
  * where K is split, as for moe_linear_mxfp4).
  *   workspace: moe_gated_ffn_workspace_size(T, H, I) bytes, 256-byte aligned,

@@ -541,7 +541,9 @@ def linear_w8a16(x, q, scale, groups=1, out_fp32=False, out=None, ws=None):
 # These calls take their scratch from torch's allocator per call (or from
 # ``ws``, a uint8 tensor of at least the size the C ABI names), so calls on
 # different streams and captured graphs never share one by accident. They run
-# on the device of their tensors, whatever the current device is.
+# on the device of their tensors, whatever the current device is. They are no
+# autograd operations: outputs have no history, whatever their inputs require.
+# Outputs and workspaces must not overlap each other or an input.
 
 # Small calls last a few microseconds, so the argument checks here are the
 # short forms; a check that fails is repeated by ``_need``, which words it.
@@ -691,7 +693,8 @@ def _mxfp4_weight(codes, scales, index):
 def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None):
     """y = x W^T (moe_linear_mxfp4): x [T][K] bf16, W [N][K] as codes
     [N][K/2] and scales [N][K/32] -> [T][N] (bf16 or fp32). act: "bf16", or
-    "mxfp4" to round x to MXFP4 first."""
+    "mxfp4" to round x to MXFP4 first. Autograd does not see it: its input
+    gradient is ``linear_mxfp4_dx``."""
     mode = _ACTS.get(act)
     if mode is None:
         raise ValueError(f"act {act!r}, expected one of {sorted(_ACTS)}")
@@ -741,7 +744,8 @@ def gated_ffn(x, w13, w2, limit=10.0, save=False, out_fp32=False, out=None, ws=N
     """The expert's block with bf16 weights (moe_gated_ffn): x [T][H], w13
     [2I][H] (gate rows, then up rows), w2 [H][I] -> y [T][H] (bf16 or fp32).
     save=True returns (y, saved), ``saved`` being what ``gated_ffn_backward``
-    takes: (g and u [T][2I] fp32, h [T][I] bf16)."""
+    takes: (g and u [T][2I] fp32, h [T][I] bf16). Autograd does not see it: the
+    gradients are ``gated_ffn_backward``'s."""
     T, H, I, index, px, p13, p2 = _ffn_args(x, w13, w2)
     out = _result(out, (T, H), torch.float32 if out_fp32 else torch.bfloat16, x)
     saved = (x.new_empty((T, 2 * I), dtype=torch.float32), x.new_empty((T, I))) if save else None

@@ -41,8 +41,11 @@ bool linear_ok(int T, int K, int N) {
 // the pass reads all activations, T K values, through its CU's share of the L2, while the tile product splits K over
 // blocks at the price of a second launch: at 4096 x 4096 (MXFP4, bf16 activations) 9.8 us at 24 rows and 11.1 at 32
 // against 10.9 at 33, at K = 8192 11.9 at 12 rows and 13.2 at 16 against 12.1 at 17, at 2048 x 2048 6.7 against 7.6 at 32
-// rows. Activations that the pass encodes to MXFP4 itself cost it a little more (4096 x 4096: 10.6 us at 24 rows, the
-// tile product 11.1 at 28; K = 8192: 12.4 at 12 rows, 11.5 at 16).
+// rows. The rule does not know N: at 4096 -> 1536 tiles lead from about 18 rows on (9.6 us streamed at 24 rows, 8.6 in
+// tiles at 28), at 1024 -> 8192 the pass still does at 32 (6.9 us; tiles 8.8 at 33).
+// Activations that the pass encodes to MXFP4 itself cost it more. 81920 lies between 4096 x 4096, where it would lead at
+// 24 rows (10.6 us; tiles 11.1 at 28), and K = 8192, where it would trail at 12 (12.4 us; tiles 11.5 at 16); at 1024 ->
+// 8192 it trails from 17 rows on (8.0 us at 32; tiles 6.8 at 33).
 bool linear_few(int T, int K, int act) {
   return T <= kFewRows && (long long)T * K <= (act == MOE_ACT_MXFP4 ? 81920 : 98304);
 }

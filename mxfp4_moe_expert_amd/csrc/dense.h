@@ -35,9 +35,12 @@
 // 64 x 128: 22.7 us; MXFP4 8192 x 4096 x 4096: 72 to 76 us, 3.6 to 3.8
 // PFLOP/s. Large tiles are bound by the MFMAs and, where a launch is one or
 // two rounds of blocks, by epilogues that nothing covers (6.5 us a round of
-// bf16 stores); the smaller ones and MXFP4 by the L2 -> LDS path (a stage of
-// 64 x 128 takes 0.26 to 0.34 us, 128 x 128 0.32 to 0.47, 256 x 128 0.47 to
-// 0.80, 256 x 256 0.95 to 1.45, with few and with all CUs at work).
+// bf16 stores); the smaller ones by the L2 -> LDS path (a stage of 64 x 128
+// takes 0.26 to 0.34 us, 128 x 128 0.32 to 0.47, 256 x 128 0.47 to 0.80, 256 x
+// 256 0.95 to 1.45, with few and with all CUs at work). MXFP4 at 256 x 256 fills
+// neither: a stage of 64 KB takes about 1.6 us (40 KB/us per CU, where the small
+// tiles reach 70), its MFMAs about half of that. Its ring holds two stages, so
+// each load is waited for one stage after its issue.
 #pragma once
 
 #include <atomic>

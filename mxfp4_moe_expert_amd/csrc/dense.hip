@@ -124,7 +124,8 @@ inline int slice_stages(DenseKind kind, int nst, int slices) {
 // Microseconds per stage of a block, by tile, where few CUs are busy and on a full chip, and the rest of a block's time
 // (launch, first loads, epilogue). A block is bound by its share of the L2 -> LDS path, then by the matrix cores.
 // Measured on 4096 x 4096 weights at 33 to 4096 rows: of the cuts tried for each size, the rule takes the fastest or one
-// within a few percent of it.
+// within a few percent of it. MXFP4 products are cut by the same times, though a stage of theirs is other work; their
+// cuts were not timed one against another.
 constexpr double kFewUs[kNumTiles] = {0.95, 0.47, 0.32, 0.26}, kFullUs[kNumTiles] = {1.45, 0.80, 0.47, 0.34};
 constexpr double kStartUs = 4.5;
 constexpr double kPairUs = 0.56;  // 64 x 128: a stage of both blocks of a CU

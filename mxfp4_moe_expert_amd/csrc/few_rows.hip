@@ -19,9 +19,10 @@
 //     its own rounding (relative L2 2.4e-3 against 1.7e-3). The parts' sums stay
 //     apart until the first is known to be finite (two_parts).
 // Bound by the weight bytes; at one token by launch and load latency; with
-// more tokens by every block's reading all activations. Measured: 1 x 4096 ->
-// 1536 (MXFP4) 5.8 us; the gated block, 1 x 4096 x 2048, 8.1 us for gate and
-// up (4.1 TB/s of weights) and 4.6 for down (3.6).
+// more tokens by every block's reading all activations. Measured (kernels in a
+// trace, median and least of 20): 1 x 4096 -> 1536 (MXFP4) 6.0 and 5.8 us; the
+// gated block, 1 x 4096 x 2048, 9.0 and 8.7 us for gate and up (3.7 TB/s of
+// weights), 5.6 and 4.5 for down (3.0).
 #include "dense.h"
 
 namespace moe {
