@@ -10,13 +10,13 @@
 // are copied to LDS once, before the K loop (a byte per row and k-step is then
 // one LDS read).
 //
-// Measured (the kernel in a trace, medians; calls among others take 37 to 38 us
-// of the one that takes 41.9 here): 33 x 8192 -> 4096, eight slices of K, 12.7 us, of which
-// the 16 stages are 6 (0.37 us each: LDS latency, which a wave's four MFMAs a
-// k-step do not cover) and the rest is before and after them: the exponent
-// bytes pass through registers, everything loaded first is waited for
-// together, and 4 MB of partial sums are stored. 1000 x 4096 -> 4096 41.9 us
-// (0.80 PFLOP/s; the bf16 product with W expanded before it: 34.7 + 8.6).
+// Measured (the kernel in a trace, medians): 33 x 8192 -> 4096, eight slices of
+// K, 12.7 us, of which the 16 stages are 6 (0.37 us each: LDS latency, which a
+// wave's four MFMAs a k-step do not cover) and the rest is before and after
+// them: the exponent bytes pass through registers, everything loaded first is
+// waited for together, and 4 MB of partial sums are stored. 1000 x 4096 ->
+// 4096 41.9 us (0.80 PFLOP/s; untraced, a call among others 37 to 39 us; the
+// bf16 product with W expanded before it: 34.7 + 8.6).
 #include "dense.h"
 
 namespace moe {
