@@ -554,19 +554,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _border(p, name, bytes_=16):
-    """Pointer p, at a border of ``bytes_`` as the library needs it."""
-    if p & (bytes_ - 1):
-        raise MoEError(MOE_EINVAL, f"{name}: not {bytes_}-byte aligned")
-    return p
-
-
 def _arg(t, dtype, shape, index, name):
-    """t's pointer, t being a contiguous, 16-byte aligned ``dtype`` tensor of ``shape`` on device ``index``."""
+    """t's pointer, t being a contiguous ``dtype`` tensor of ``shape`` on device ``index``."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous()):
-        p = t.data_ptr()
-        return _border(p, name) if p & 15 else p
+        return t.data_ptr()
     _need(t, dtype, shape, name)
     raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
 
@@ -605,7 +597,28 @@ def _call(index, name, *args):
         with torch.cuda.device(index):
             status = fn(*args, _raw_stream(index))
     if status != MOE_OK:
-        raise MoEError(status, name)
+        raise MoEError(status, _misaligned(name, args) if status == MOE_EINVAL else name)
+
+
+# The pointer arguments of the calls, in order.
+_POINTERS = {
+    "moe_mxfp4_quantize": ("x", "codes", "scales"),
+    "moe_mxfp4_dequantize": ("codes", "scales", "out"),
+    "moe_linear_mxfp4": ("x", "codes", "scales", "out", "ws"),
+    "moe_linear_mxfp4_dx": ("dy", "codes", "scales", "out", "ws"),
+    "moe_gated_ffn": ("x", "w13", "w2", "saved[0]", "saved[1]", "out", "ws"),
+    "moe_gated_ffn_backward": ("dy", "x", "w13", "w2", "saved[0]", "saved[1]", "dx", "dw13", "dw2", "ws"),
+}
+
+
+def _misaligned(name, args):
+    """What a refused call is about: its first tensor off its border (16 bytes, workspaces 256), else the call."""
+    pointers = [a for a, t in zip(args, _SIGNATURES[name][0]) if t is _VP]
+    for what, p in zip(_POINTERS[name], pointers):
+        border = 256 if what == "ws" else 16
+        if p and p % border:
+            return f"{name}, {what}: not {border}-byte aligned"
+    return name
 
 
 def _scratch(need, like, ws, what):
@@ -615,7 +628,7 @@ def _scratch(need, like, ws, what):
     if ws is None:
         ws = like.new_empty((need,), dtype=torch.uint8)
         return ws.data_ptr(), need, ws
-    return _border(_arg(ws, torch.uint8, ws.shape, like.get_device(), "ws"), "ws", 256), ws.numel(), ws
+    return _arg(ws, torch.uint8, ws.shape, like.get_device(), "ws"), ws.numel(), ws
 
 
 def _result(out, shape, dtype, like, name="out"):
@@ -650,10 +663,8 @@ def quantize_mxfp4(x, out=None):
     c, s = out if out is not None else (None, None)
     codes = _result(c, lead + (K // 2,), torch.uint8, x, "codes")
     scales = _result(s, lead + (K // 32,), torch.uint8, x, "scales")
-    px = _border(x.data_ptr(), "x")
-    if ldx * x.element_size() % 16:
-        raise MoEError(MOE_EINVAL, "x: rows not 16-byte aligned")
-    _call(x.get_device(), "moe_mxfp4_quantize", x.numel() // K, K, dt, px, ldx, codes.data_ptr(), scales.data_ptr())
+    _call(x.get_device(), "moe_mxfp4_quantize", x.numel() // K, K, dt, x.data_ptr(), ldx, codes.data_ptr(),
+          scales.data_ptr())
     return codes, scales
 
 
@@ -683,8 +694,7 @@ def _mxfp4_weight(codes, scales, index):
         N, half = codes.shape
         if half and half % 16 == 0:
             ps, scales = _scale_bytes(scales, (N, half // 16), index)
-            p = codes.data_ptr()
-            return N, half * 2, _border(p, "codes") if p & 15 else p, ps, scales
+            return N, half * 2, codes.data_ptr(), ps, scales
     _matrix(codes, torch.uint8, "codes")
     _arg(codes, torch.uint8, codes.shape, index, "codes")
     raise ValueError("codes: shape [N, K/2] with K a positive multiple of 32 expected")
@@ -702,9 +712,6 @@ def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None
     N, K, pc, ps, scales = _mxfp4_weight(codes, scales, index)
     if cols != K or not x.is_contiguous():
         _need(x, torch.bfloat16, (T, K), "x")
-    px = x.data_ptr()
-    if px & 15:
-        _border(px, "x")
     if out is None:
         out = x.new_empty((T, N), dtype=torch.float32) if out_fp32 else x.new_empty((T, N))
     else:
@@ -714,7 +721,7 @@ def linear_mxfp4(x, codes, scales, act="bf16", out_fp32=False, out=None, ws=None
         need = lib().moe_linear_mxfp4_workspace_size(T, K, N, mode)
         if need != 256 or ws is not None:
             pw, nw, ws = _scratch(need, x, ws, "moe_linear_mxfp4")
-    _call(index, "moe_linear_mxfp4", T, K, N, px, pc, ps, mode, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
+    _call(index, "moe_linear_mxfp4", T, K, N, x.data_ptr(), pc, ps, mode, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
     return out
 
 

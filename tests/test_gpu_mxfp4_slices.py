@@ -84,3 +84,15 @@ def test_refusals_name_the_argument():
             with pytest.raises(mx.MoEError, match=rf"\b{name}: .*aligned") as e:
                 f()
             assert e.value.status == mx.MOE_EINVAL
+
+
+def test_what_a_call_does_not_use_is_not_refused():
+    """A workspace at any address where none is used, and empty batches beside misaligned tensors."""
+    c, s, g = _stack()
+    x = torch.randn(5, K, generator=g, device=DEV).to(torch.bfloat16)
+    odd = torch.empty(4096, dtype=torch.uint8, device=DEV)[1:]
+    for n in (1, 5):
+        assert torch.equal(mx.linear_mxfp4(x[:n], c[0], s[0], ws=odd), mx.linear_mxfp4(x[:n], c[0], s[0]))
+    assert mx.linear_mxfp4(x[:0], c[1], s[1], ws=odd).shape == (0, N)
+    w = torch.zeros(1 + 64 * K, dtype=torch.bfloat16, device=DEV)[1:]
+    assert mx.gated_ffn(x[:0], w.view(64, K), w[:32 * K].view(K, 32)).shape == (0, K)
