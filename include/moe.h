@@ -337,6 +337,45 @@ int moe_linear_mxfp4_dx(int32_t T, int32_t K, int32_t N, const uint16_t* dy, con
                         const uint8_t* scales, void* dx, int32_t out_is_fp32, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/* ---- int8 tensors and the product of two of them ("w8a8")
+ *
+ * The storage format of the model's int8 projections (linears_w8a16 above:
+ * symmetric, one fp32 scale per output channel) made from a tensor, read back,
+ * and multiplied with activations of 8 bits too, one scale per token. A tensor
+ * of `rows` rows of K values (K % 16 == 0) is codes [rows][K] i8 and scales
+ * [rows] f32, value = scale * code. Scales may start at any multiple of 4
+ * bytes; every other pointer is 16-byte aligned. */
+
+/* x [rows][K] (row r at x + r ldx, in elements) -> codes, scales. Per row with
+ * largest magnitude m: scale = m / 127, rounded to fp32 (1 if m = 0, at least
+ * 2^-126); code = x / scale rounded to the nearest whole number, ties to even
+ * (decided on the exact quotient). A row with an Inf or NaN: scale NaN, codes 0.
+ * dtype: MOE_DTYPE_BF16, _F32 or _F16. ldx >= K and rows 16-byte aligned.
+ * 0 <= rows, 16 <= K <= 65536, rows K <= 2^36. */
+int moe_int8_quantize(int64_t rows, int32_t K, int32_t dtype, const void* x, int64_t ldx, int8_t* codes, float* scales,
+                      void* stream);
+
+/* codes, scales -> out [rows][K] contiguous, code * scale rounded once. dtype: MOE_DTYPE_BF16 or _F32. */
+int moe_int8_dequantize(int64_t rows, int32_t K, const int8_t* codes, const float* scales, int32_t dtype, void* out,
+                        void* stream);
+
+/* y = x W^T with W [N][K] in int8 and x in int8:
+ *   y[t][n] = x_scale[t] * scale[n] * sum_k x_code[t][k] * q[n][k], the sum
+ *   exact in 32 bits; out [T][N] bf16 (out_is_fp32 = 0) or f32.
+ *   x        [T][K] bf16, encoded here as moe_int8_quantize does, or NULL, and
+ *   x_codes  [T][K] i8 with x_scales [T] f32: activations encoded before.
+ *   A token or channel with a NaN scale gives NaN. Codes of -128 are allowed.
+ *   Results do not depend on how many rows stand beside a row.
+ *   workspace: moe_linear_w8a8_workspace_size(T, K, N, encoded) bytes
+ *   (encoded: x_codes is given), 256-byte aligned, any contents; calls sharing
+ *   one must be ordered on one stream. A size of 256 means that none is used:
+ *   workspace may then be NULL.
+ * Supported: K a multiple of 16 up to 65536, 1 <= N <= 65536, 0 <= T <= 65536. */
+size_t moe_linear_w8a8_workspace_size(int32_t T, int32_t K, int32_t N, int32_t encoded);
+int moe_linear_w8a8(int32_t T, int32_t K, int32_t N, const uint16_t* x, const int8_t* x_codes, const float* x_scales,
+                    const int8_t* q, const float* scale, void* out, int32_t out_is_fp32, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
 /* ---- The gated feed-forward block with bf16 weights, and its gradients
  *
  * The layer's expert (clamped SwiGLU; page "DeepSeek-V4-Flash-0731", section

@@ -92,6 +92,10 @@ _SIGNATURES = {
     "moe_linear_mxfp4": ([_I32, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
     "moe_linear_mxfp4_dx_workspace_size": ([_I32, _I32, _I32], _SZ),
     "moe_linear_mxfp4_dx": ([_I32, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
+    "moe_int8_quantize": ([_I64, _I32, _I32, _VP, _I64, _VP, _VP, _VP], ctypes.c_int),
+    "moe_int8_dequantize": ([_I64, _I32, _VP, _VP, _I32, _VP, _VP], ctypes.c_int),
+    "moe_linear_w8a8_workspace_size": ([_I32, _I32, _I32, _I32], _SZ),
+    "moe_linear_w8a8": ([_I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
     "moe_gated_ffn_workspace_size": ([_I32, _I32, _I32], _SZ),
     "moe_gated_ffn": ([_I32, _I32, _I32, _F32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
     "moe_gated_ffn_backward_workspace_size": ([_I32, _I32, _I32], _SZ),
@@ -606,16 +610,20 @@ _POINTERS = {
     "moe_mxfp4_dequantize": ("codes", "scales", "out"),
     "moe_linear_mxfp4": ("x", "codes", "scales", "out", "ws"),
     "moe_linear_mxfp4_dx": ("dy", "codes", "scales", "out", "ws"),
+    "moe_int8_quantize": ("x", "codes", "row scales"),
+    "moe_int8_dequantize": ("codes", "row scales", "out"),
+    "moe_linear_w8a8": ("x", "x", "x_scale", "q", "scale", "out", "ws"),
     "moe_gated_ffn": ("x", "w13", "w2", "saved[0]", "saved[1]", "out", "ws"),
     "moe_gated_ffn_backward": ("dy", "x", "w13", "w2", "saved[0]", "saved[1]", "dx", "dw13", "dw2", "ws"),
 }
+_BORDERS = {"ws": 256, "scale": 4, "x_scale": 4, "row scales": 4}
 
 
 def _misaligned(name, args):
-    """What a refused call is about: its first tensor off its border (16 bytes, workspaces 256), else the call."""
+    """What a refused call is about: its first tensor off its border (``_BORDERS``, else 16 bytes), else the call."""
     pointers = [a for a, t in zip(args, _SIGNATURES[name][0]) if t is _VP]
     for what, p in zip(_POINTERS[name], pointers):
-        border = 256 if what == "ws" else 16
+        border = _BORDERS.get(what, 16)
         if p and p % border:
             return f"{name}, {what}: not {border}-byte aligned"
     return name
@@ -638,11 +646,8 @@ def _result(out, shape, dtype, like, name="out"):
     return out
 
 
-def quantize_mxfp4(x, out=None):
-    """x [..., K] (bf16, fp32 or fp16; K a multiple of 32) -> (codes uint8
-    [..., K/2], scales uint8 [..., K/32]), the layer's MXFP4 layout
-    (moe_mxfp4_quantize). x is contiguous, or 2-D with unit column stride and
-    16-byte aligned rows."""
+def _rows_to_encode(x, group):
+    """Last dimension (a multiple of ``group``), row stride, dtype code and leading dimensions of x."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x: torch.Tensor expected")
     if not x.is_cuda:
@@ -652,14 +657,22 @@ def quantize_mxfp4(x, out=None):
         raise TypeError(f"x: dtype {x.dtype}, expected bfloat16, float32 or float16")
     shape = x.shape
     K = shape[-1] if len(shape) else 0
-    if K == 0 or K % 32:
-        raise ValueError("x: last dimension must be a positive multiple of 32")
+    if K == 0 or K % group:
+        raise ValueError(f"x: last dimension must be a positive multiple of {group}")
     ldx = K
     if not x.is_contiguous():
         if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < K:
             raise ValueError("x: contiguous, or 2-D with unit column stride, expected")
         ldx = x.stride(0)
-    lead = tuple(shape[:-1])
+    return K, ldx, dt, tuple(shape[:-1])
+
+
+def quantize_mxfp4(x, out=None):
+    """x [..., K] (bf16, fp32 or fp16; K a multiple of 32) -> (codes uint8
+    [..., K/2], scales uint8 [..., K/32]), the layer's MXFP4 layout
+    (moe_mxfp4_quantize). x is contiguous, or 2-D with unit column stride and
+    16-byte aligned rows."""
+    K, ldx, dt, lead = _rows_to_encode(x, 32)
     c, s = out if out is not None else (None, None)
     codes = _result(c, lead + (K // 2,), torch.uint8, x, "codes")
     scales = _result(s, lead + (K // 32,), torch.uint8, x, "scales")
@@ -734,6 +747,63 @@ def linear_mxfp4_dx(dy, codes, scales, out_fp32=False, out=None, ws=None):
     out = _result(out, (T, K), torch.float32 if out_fp32 else torch.bfloat16, dy)
     pw, nw, ws = _scratch(lib().moe_linear_mxfp4_dx_workspace_size(T, K, N), dy, ws, "moe_linear_mxfp4_dx")
     _call(index, "moe_linear_mxfp4_dx", T, K, N, py, pc, ps, out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
+    return out
+
+
+def quantize_int8(x, out=None):
+    """x [..., K] (bf16, fp32 or fp16; K a multiple of 16) -> (codes int8
+    [..., K], scales fp32 [...]), symmetric with one scale per row
+    (moe_int8_quantize): the format of ``linear_w8a16``'s and ``linear_w8a8``'s
+    weights, and of activations of 8 bits. x is contiguous, or 2-D with unit
+    column stride and 16-byte aligned rows."""
+    K, ldx, dt, lead = _rows_to_encode(x, 16)
+    c, s = out if out is not None else (None, None)
+    codes = _result(c, lead + (K,), torch.int8, x, "codes")
+    scales = _result(s, lead, torch.float32, x, "scales")
+    _call(x.get_device(), "moe_int8_quantize", x.numel() // K, K, dt, x.data_ptr(), ldx, codes.data_ptr(),
+          scales.data_ptr())
+    return codes, scales
+
+
+def dequantize_int8(codes, scales, dtype=torch.bfloat16, out=None):
+    """(codes [..., K], scales [...]) -> codes * scales [..., K] in bf16 or fp32, rounded once (moe_int8_dequantize)."""
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"dtype {dtype}, expected bfloat16 or float32")
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        _need(codes, torch.int8, None, "codes")
+    shape, index = codes.shape, codes.get_device()
+    K = shape[-1] if len(shape) else 0
+    if K == 0 or K % 16:
+        raise ValueError("codes: last dimension must be a positive multiple of 16")
+    pc = _arg(codes, torch.int8, shape, index, "codes")
+    ps = _arg(scales, torch.float32, tuple(shape[:-1]), index, "scales")
+    out = _result(out, tuple(shape), dtype, codes)
+    _call(index, "moe_int8_dequantize", codes.numel() // K, K, pc, ps, _DTYPES[dtype], out.data_ptr())
+    return out
+
+
+def linear_w8a8(x, q, scale, x_scale=None, out_fp32=False, out=None, ws=None):
+    """y = x W^T with both sides in int8 (moe_linear_w8a8): q int8 [N][K] with
+    scale fp32 [N], as for ``linear_w8a16``, -> [T][N] (bf16 or fp32). x is
+    bf16 [T][K], encoded on the way with a scale per token, or, with x_scale
+    fp32 [T], int8 codes [T][K] as ``quantize_int8`` gives them. K is a multiple
+    of 16. Autograd does not see it."""
+    encoded = x_scale is not None
+    T, K, index = _matrix(x, torch.int8 if encoded else torch.bfloat16, "x")
+    N, cols, _ = _matrix(q, torch.int8, "q")
+    if cols != K or not x.is_contiguous():
+        _need(x, None, (T, cols), "x")
+    pq = _arg(q, torch.int8, (N, K), index, "q")
+    ps = _arg(scale, torch.float32, (N,), index, "scale")
+    pxs = _arg(x_scale, torch.float32, (T,), index, "x_scale") if encoded else None
+    out = _result(out, (T, N), torch.float32 if out_fp32 else torch.bfloat16, x)
+    px = x.data_ptr()
+    need = lib().moe_linear_w8a8_workspace_size(T, K, N, 1 if encoded else 0)
+    pw, nw = None, 0
+    if need != 256 or ws is not None:
+        pw, nw, ws = _scratch(need, x, ws, "moe_linear_w8a8")
+    _call(index, "moe_linear_w8a8", T, K, N, None if encoded else px, px if encoded else None, pxs, pq, ps,
+          out.data_ptr(), 1 if out_fp32 else 0, pw, nw)
     return out
 
 

@@ -1,4 +1,4 @@
-// Host entry points of the plain MXFP4 operators and the gated block
+// Host entry points of the plain MXFP4 and int8 operators and the gated block
 // (include/moe.h): argument checks, workspace carving and dispatch on the
 // caller's stream. Nothing here allocates device memory or synchronises.
 #include <hip/hip_runtime.h>
@@ -17,6 +17,7 @@ constexpr int kMaxLinear = 65536; // K and N of a linear
 constexpr int kMaxFfn = 16384;    // H and I of the gated block: 2 I H values stay below 2^30
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline int status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 inline size_t max_of(size_t a, size_t b) { return a > b ? a : b; }
@@ -101,6 +102,38 @@ LinearLayout linear_layout(int T, int K, int N, int act) {
       L.wpack = take(mxfp4_pack_bytes(N, K));
     } else if (!L.codes_direct) {
       L.w = take((size_t)N * K * 2);
+    }
+    L.part = take(dense_part_bytes(L.plan, T, N));
+  }
+  L.total = o == 0 ? kNoWorkspace : o < 512 ? 512 : o;
+  return L;
+}
+
+// int8 x int8: K a multiple of 16 (16-byte pieces of codes); sums of 65536 products of magnitude 2^14 stay below 2^31.
+constexpr int kI8Step = 16;
+bool w8a8_ok(int T, int K, int N) {
+  return T >= 0 && T <= kMaxRows && K >= kI8Step && K % kI8Step == 0 && K <= kMaxLinear && N >= 1 && N <= kMaxLinear;
+}
+
+struct W8a8Layout {
+  DensePlan plan;
+  size_t codes, scales, part, total;  // codes, scales: of activations that come as bf16
+};
+
+W8a8Layout w8a8_layout(int T, int K, int N, bool encoded) {
+  W8a8Layout L;
+  memset(&L, 0, sizeof(L));
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t p = o;
+    o = align256(o + bytes);
+    return p;
+  };
+  if (T > 0) {
+    L.plan = dense_plan(kDenseI8, kDenseNT, T, N, K);
+    if (!encoded) {
+      L.codes = take((size_t)T * K);
+      L.scales = take((size_t)T * 4);
     }
     L.part = take(dense_part_bytes(L.plan, T, N));
   }
@@ -309,6 +342,63 @@ int moe_linear_mxfp4_dx(int32_t T, int32_t K, int32_t N, const uint16_t* dy, con
   return status(launch_dense(kDenseBf16, kDenseNN, kStore, L.plan,
                              dense_args(pad ? dyp : dy, L.ldy, w, K, T, K, N, dx, out_is_fp32,
                                         at<float>(workspace, L.part)), st));
+}
+
+int moe_int8_quantize(int64_t rows, int32_t K, int32_t dtype, const void* x, int64_t ldx, int8_t* codes, float* scales,
+                      void* stream) {
+  if (rows < 0 || K <= 0 || ldx < K) return MOE_EINVAL;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_F16) return MOE_EUNSUPPORTED;
+  if (K % kI8Step || K > kMaxLinear || rows > ((int64_t)1 << 36) / K) return MOE_EUNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned4(scales)) return MOE_EINVAL;
+  if (ldx % (dtype == MOE_DTYPE_F32 ? 4 : 8)) return MOE_EINVAL;
+  return status(launch_int8_quantize(rows, K, dtype, x, ldx, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+int moe_int8_dequantize(int64_t rows, int32_t K, const int8_t* codes, const float* scales, int32_t dtype, void* out,
+                        void* stream) {
+  if (rows < 0 || K <= 0) return MOE_EINVAL;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return MOE_EUNSUPPORTED;
+  if (K % kI8Step || K > kMaxLinear || rows > ((int64_t)1 << 36) / K) return MOE_EUNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!out || !codes || !scales || !aligned16(out) || !aligned16(codes) || !aligned4(scales)) return MOE_EINVAL;
+  return status(launch_int8_dequantize(rows, K, codes, scales, dtype, out, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_linear_w8a8_workspace_size(int32_t T, int32_t K, int32_t N, int32_t encoded) {
+  return w8a8_ok(T, K, N) ? w8a8_layout(T, K, N, encoded != 0).total : 0;
+}
+
+int moe_linear_w8a8(int32_t T, int32_t K, int32_t N, const uint16_t* x, const int8_t* x_codes, const float* x_scales,
+                    const int8_t* q, const float* scale, void* out, int32_t out_is_fp32, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (T < 0 || K <= 0 || N <= 0) return MOE_EINVAL;
+  if (!w8a8_ok(T, K, N)) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const bool encoded = x_codes != nullptr;
+  if (encoded == (x != nullptr) || encoded != (x_scales != nullptr) || !q || !scale || !out) return MOE_EINVAL;
+  if (!aligned16(x) || !aligned16(x_codes) || !aligned4(x_scales) || !aligned16(q) || !aligned4(scale) ||
+      !aligned16(out))
+    return MOE_EINVAL;
+  const W8a8Layout L = w8a8_layout(T, K, N, encoded);
+  if (L.total != kNoWorkspace) {
+    const int rc = check_ws(workspace, workspace_bytes, L.total);
+    if (rc) return rc;
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (!encoded) {
+    int8_t* codes = at<int8_t>(workspace, L.codes);
+    float* scales = at<float>(workspace, L.scales);
+    const hipError_t e = launch_int8_quantize(T, K, kDtBf16, x, K, codes, scales, st);
+    if (e != hipSuccess) return status(e);
+    x_codes = codes;
+    x_scales = scales;
+  }
+  DenseArgs a = dense_args(x_codes, (size_t)K / 2, q, (size_t)K / 2, T, N, K, out, out_is_fp32,
+                           at<float>(workspace, L.part));
+  a.x_scale = x_scales;
+  a.w_scale = scale;
+  return status(launch_dense(kDenseI8, kDenseNT, kStore, L.plan, a, st));
 }
 
 size_t moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I) {

@@ -2,10 +2,11 @@
 // projections on gfx950's matrix cores: one kernel template,
 //   C[m][n] = sum_k X(m, k) W(n, k),
 // with each operand stored either along k ([row][k], "K-contiguous") or
-// across it ([k][row], "transposed"), in bf16 or (both K-contiguous) MXFP4.
+// across it ([k][row], "transposed"), in bf16 or (both K-contiguous) MXFP4 or
+// int8.
 //
 // Tile BM x BN, one block of WGM x WGN waves. K runs in stages of two MFMA
-// k-steps (128 bytes per row: 64 bf16 or 256 E2M1 values); LDS holds NX stages
+// k-steps (128 bytes per row: 64 bf16, 128 int8 or 256 E2M1 values); LDS holds NX stages
 // of the X tile and NW of the W tile:
 //   - Operands go from global memory straight to LDS (16 bytes per lane, the
 //     64 lanes of a wave filling 1 KB), whole 128-byte lines at a time (half
@@ -24,8 +25,8 @@
 //     k rows; its 32-byte units are stored at unit ^ f(k), and the LDS
 //     transposing read (16 lanes x 4 elements) hands each lane 4 consecutive
 //     k of its row.
-//   - MFMA 16x16x32 (bf16) or 16x16x128 with E8M0 scales (MXFP4), W as the A
-//     operand: lane (r, g) ends with 4 consecutive n of one m; two blocks'
+//   - MFMA 16x16x32 (bf16), 16x16x64 (int8) or 16x16x128 with E8M0 scales
+//     (MXFP4), W as the A operand: lane (r, g) ends with 4 consecutive n of one m; two blocks'
 //     lanes are joined to 16-byte stores.
 //
 // Measured (MI355X; a large copy runs at 5.1 TB/s, a large library bf16
@@ -51,6 +52,7 @@
 
 namespace moe {
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
@@ -169,6 +171,9 @@ struct Reader {
 __device__ __forceinline__ f32x4_t mfma_bf16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
   return mfma_16x16x32(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c);
 }
+__device__ __forceinline__ i32x4_t mfma_i8(const u32x4_t& a, const u32x4_t& b, const i32x4_t& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+}
 template <int KK>
 __device__ __forceinline__ f32x4_t mfma_mx4(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c, uint32_t sa,
                                             uint32_t sb) {
@@ -240,10 +245,9 @@ __device__ __forceinline__ void ffn_act_grad4(const f32x4_t& g4, const f32x4_t& 
   }
 }
 
-// The wave's accumulators to out [M][N]: lane (r, g) holds acc[b][c][i] = C[m0 + 16 c + r][n0 + 16 b + 4 g + i].
-template <int MB, int NB>
-__device__ __forceinline__ void store_tile(const f32x4_t (&acc)[NB][MB], void* out, bool fp32, int M, int N, int m0,
-                                           int n0, int lane) {
+// The wave's values to out [M][N]: lane (r, g) holds value(b, c)[i] = C[m0 + 16 c + r][n0 + 16 b + 4 g + i].
+template <int MB, int NB, class F>
+__device__ __forceinline__ void store_values(F&& value, void* out, bool fp32, int M, int N, int m0, int n0, int lane) {
   const int r = lane & 15, g = lane >> 4;
   // 16-byte pieces of bf16 rows exist whole or not at all
   const bool joined = NB % 2 == 0 && !fp32 && (N & 7) == 0;
@@ -255,7 +259,7 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[NB][MB], void* o
 #pragma unroll
       for (int b = 0; b + 1 < NB; b += 2) {
         const int n = n0 + b * 16 + 8 * g;
-        const u32x4_t v = join_blocks(pack4_bf16(acc[b][c]), pack4_bf16(acc[b + 1][c]));
+        const u32x4_t v = join_blocks(pack4_bf16(value(b, c)), pack4_bf16(value(b + 1, c)));
         if (m < M && n < N) *reinterpret_cast<u32x4_t*>(row + n) = v;
       }
     } else if (m < M) {
@@ -263,10 +267,31 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[NB][MB], void* o
       for (int b = 0; b < NB; ++b) {
         const int n = n0 + b * 16 + 4 * g;
         if (n >= N) continue;
-        store4(out, fp32, (size_t)m * N + n, acc[b][c], N - n, (N & 3) == 0);
+        store4(out, fp32, (size_t)m * N + n, value(b, c), N - n, (N & 3) == 0);
       }
     }
   }
+}
+
+template <int MB, int NB>
+__device__ __forceinline__ void store_tile(const f32x4_t (&acc)[NB][MB], void* out, bool fp32, int M, int N, int m0,
+                                           int n0, int lane) {
+  store_values<MB, NB>([&](int b, int c) { return acc[b][c]; }, out, fp32, M, N, m0, n0, lane);
+}
+
+// Four sums of int8 products times the scales of their row and columns.
+__device__ __forceinline__ f32x4_t scaled(const i32x4_t& v, float row, const f32x4_t& col) {
+  f32x4_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (float)v[i] * row * col[i];
+  return o;
+}
+// Four consecutive scales from column n on (those past N as 0): fp32 values at any multiple of 4 bytes.
+__device__ __forceinline__ f32x4_t four_scales(const float* s, int n, int N) {
+  f32x4_t v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = n + i < N ? s[n + i] : 0.0f;
+  return v;
 }
 
 enum DenseEpi {
@@ -298,8 +323,9 @@ __device__ __forceinline__ void dense_tile(int bid, int tm, int tn, int& im, int
 // The LDS rings of a tile and the loads that fill them: NX stages of X, NW of W, then (MXFP4) NS sets of the packed
 // scales of two stages (see mxfp4.hip). Past the slice's stages a load writes zeros, so that every stage has its loads
 // and the waits can count them.
-template <bool XT, bool WT, int BM, int BN, int W, int NX, int NW, bool FP4, int NS, bool GATE>
+template <bool XT, bool WT, int BM, int BN, int W, int NX, int NW, int OP, int NS, bool GATE>
 struct TileLoads {
+  static constexpr bool FP4 = OP == kDenseFp4;
   static constexpr int XB = BM * kStageB, WB = BN * kStageB;              // bytes per stage
   static constexpr int SXB = FP4 ? BM * 16 : 0, SWB = FP4 ? BN * 16 : 0;  // scales of two stages
   static constexpr uint32_t WBASE = NX * XB, SCALES = WBASE + NW * WB, SCB = SXB + SWB;
@@ -307,7 +333,7 @@ struct TileLoads {
   using SW = Stager<WT, BN, W>;
   static constexpr int LX = SX::NI, LW = SW::NI;  // loads per wave and stage
   static_assert(LX * 1024 * W == XB && LW * 1024 * W == WB, "tiles split evenly over the waves");
-  static_assert(!FP4 || (!XT && !WT), "MXFP4 operands are K-contiguous");
+  static_assert((OP != kDenseFp4 && OP != kDenseI8) || (!XT && !WT), "operands of less than 16 bits are K-contiguous");
   // Where the next stage of one operand comes from and goes to. Past the slice kleft is 0 or less: every lane is out of
   // range and nothing is read.
   struct Feed {
@@ -333,7 +359,7 @@ struct TileLoads {
     st0 = blockIdx.y * a.slice_stages;
     nst = min(a.slice_stages, a.stages - st0);
     const int m0 = im * BM, n0 = in * (GATE ? BN / 2 : BN);
-    const int kb = a.K * 2 / (FP4 ? 4 : 1);  // bytes along k (K-contiguous operands)
+    const int kb = FP4 ? a.K / 2 : OP == kDenseI8 ? a.K : a.K * 2;  // bytes along k (K-contiguous operands)
     const char *xbase = static_cast<const char*>(a.x), *wbase = static_cast<const char*>(a.w);
     if constexpr (XT) {
       sx.init_tr(wave, lane, a.x_ld, a.M - m0);
@@ -396,6 +422,23 @@ struct TileLoads {
 
 // What a wave does with its sums: lane (r, g) holds acc[b][c][i] = C[m0 + 16 c + r][n0 + 16 b + 4 g + i] (gate: blocks b
 // alternate between gate and up, n0 is the first h column).
+template <int EPI, int MB, int NB>
+__device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const i32x4_t (&acc)[NB][MB], int m0, int n0,
+                                               int lane) {
+  if constexpr (EPI == kEpiPartial) {  // whole numbers, in the place of fp32 values
+    store_values<MB, NB>([&](int b, int c) { return __builtin_bit_cast(f32x4_t, acc[b][c]); },
+                         a.part + (size_t)blockIdx.y * a.M * a.N, true, a.M, a.N, m0, n0, lane);
+  } else {
+    float row[MB];
+    f32x4_t col[NB];
+#pragma unroll
+    for (int c = 0; c < MB; ++c) row[c] = a.x_scale[min(m0 + c * 16 + (lane & 15), a.M - 1)];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) col[b] = four_scales(a.w_scale, n0 + b * 16 + 4 * (lane >> 4), a.N);
+    store_values<MB, NB>([&](int b, int c) { return scaled(acc[b][c], row[c], col[b]); }, a.out, a.out_is_fp32, a.M,
+                         a.N, m0, n0, lane);
+  }
+}
 template <int EPI, int MB, int NB>
 __device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t (&acc)[NB][MB], int m0, int n0,
                                                int lane) {
@@ -481,15 +524,16 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t
   }
 }
 
-// One tile (block `bid` of the product's a.tm a.tn) of the product. FP4: both operands MXFP4 K-contiguous, with packed
-// scales.
-template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, bool FP4, int EPI>
+// One tile (block `bid` of the product's a.tm a.tn) of the product of operands OP (a DenseKind). MXFP4: both operands
+// K-contiguous, with packed scales; int8: both K-contiguous.
+template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, int OP, int EPI>
 __device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
+  constexpr bool FP4 = OP == kDenseFp4;
   constexpr int W = WGM * WGN;
   constexpr int MB = BM / WGM / 16, NB = BN / WGN / 16;  // 16-row blocks per wave
   // scales are loaded SD pairs of stages ahead, so that the waits below cover them
   constexpr int SD = NW <= 2 ? 1 : (NW + 1) / 2 - (NW & 1);
-  using L = TileLoads<XT, WT, BM, BN, W, NX, NW, FP4, SD + 1, EPI == kEpiGate>;
+  using L = TileLoads<XT, WT, BM, BN, W, NX, NW, OP, SD + 1, EPI == kEpiGate>;
   constexpr int XB = L::XB, WB = L::WB, LX = L::LX, LW = L::LW;
   constexpr uint32_t WBASE = L::WBASE;
   static_assert(2 * SD - 1 >= NW - 2, "a stage's scales land with it");
@@ -514,11 +558,12 @@ __device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
   rx.init(wm * MB * 16, lane);
   rw.init(wn * NB * 16, lane);
 
-  f32x4_t acc[NB][MB];
+  using V = std::conditional_t<OP == kDenseI8, i32x4_t, f32x4_t>;
+  V acc[NB][MB];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int c = 0; c < MB; ++c) acc[b][c] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < MB; ++c) acc[b][c] = (V){0, 0, 0, 0};
 
   // Registers: the W operands of this k-step and the next; of the X operands the first half once (xr[c] is read again,
   // for the next k-step, after its last MFMA of this one) and the second half twice, so that every read of a k-step is
@@ -545,6 +590,7 @@ __device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
       const int c = m / NB, b = m % NB;
       const u32x4_t& x = c < XR ? xr[c < XR ? c : 0] : xd[kk][c < XR ? 0 : c - XR];
       if constexpr (FP4) acc[b][c] = mfma_mx4<kk + 2 * q>(wf[kk][b], x, acc[b][c], swv[b], sxv[c]);
+      else if constexpr (OP == kDenseI8) acc[b][c] = mfma_i8(wf[kk][b], x, acc[b][c]);
       else acc[b][c] = mfma_bf16(wf[kk][b], x, acc[b][c]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -632,9 +678,9 @@ __device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
                               EPI == kEpiGate ? in * (BN / 2) + wn * NB * 8 : in * BN + wn * NB * 16, lane);
 }
 
-template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, bool FP4, int EPI>
+template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, int OP, int EPI>
 __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
-  dense_block<XT, WT, BM, BN, WGM, WGN, NX, NW, FP4, EPI>(a, blockIdx.x);
+  dense_block<XT, WT, BM, BN, WGM, WGN, NX, NW, OP, EPI>(a, blockIdx.x);
 }
 
 // Two independent products in one launch: the weight gradient `a` (both operands transposed) and a product `b` with W
@@ -645,9 +691,9 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_dense_pair(DenseArgs a, Dense
   const int in_first = (int)blockIdx.x < second;
   const int bid = in_first ? (int)blockIdx.x : (int)blockIdx.x - second;
   if (in_first != b_first) {
-    if (bid < a.tm * a.tn) dense_block<true, true, BM, BN, WGM, WGN, NX, NW, false, kEpiStore>(a, bid);
+    if (bid < a.tm * a.tn) dense_block<true, true, BM, BN, WGM, WGN, NX, NW, kDenseBf16, kEpiStore>(a, bid);
   } else {
-    if (bid < b.tm * b.tn) dense_block<false, true, BM, BN, WGM, WGN, NX, NW, false, EPI>(b, bid);
+    if (bid < b.tm * b.tn) dense_block<false, true, BM, BN, WGM, WGN, NX, NW, kDenseBf16, EPI>(b, bid);
   }
 }
 

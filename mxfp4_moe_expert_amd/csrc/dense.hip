@@ -23,8 +23,10 @@ constexpr size_t tile_lds(const TileCfg& t, bool fp4) {
 
 // Sums the slices of a split K in order, then the epilogue of the product.
 // Thread: four consecutive columns of one row.
-template <int EPI>
+template <int EPI, bool I8 = false>
 __global__ __launch_bounds__(64) void k_dense_reduce(DenseArgs a, int slices) {
+  using V = std::conditional_t<I8, i32x4_t, f32x4_t>;
+  using S = std::conditional_t<I8, int, float>;
   const int cols = EPI == kEpiGate ? a.I : a.N;
   const int per = (cols + 3) / 4;
   const long long id = (long long)blockIdx.x * 64 + threadIdx.x;
@@ -33,16 +35,16 @@ __global__ __launch_bounds__(64) void k_dense_reduce(DenseArgs a, int slices) {
   const size_t plane = (size_t)a.M * a.N;
   const bool wide = (a.N & 3) == 0;
   auto sum = [&](int col) {
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    const float* p = a.part + (size_t)m * a.N + col;
+    V v = {0, 0, 0, 0};
+    const S* p = reinterpret_cast<const S*>(a.part) + (size_t)m * a.N + col;
     if (wide) {
       // eight slices' loads in flight together (past the last slice: the last again, not added)
       constexpr int AHEAD = 8;
       for (int s0 = 0; s0 < slices; s0 += AHEAD) {
-        f32x4_t t[AHEAD];
+        V t[AHEAD];
 #pragma unroll
         for (int s = 0; s < AHEAD; ++s)
-          t[s] = *reinterpret_cast<const f32x4_t*>(p + (size_t)min(s0 + s, slices - 1) * plane);
+          t[s] = *reinterpret_cast<const V*>(p + (size_t)min(s0 + s, slices - 1) * plane);
 #pragma unroll
         for (int s = 0; s < AHEAD; ++s)
           if (s0 + s < slices) v += t[s];
@@ -56,7 +58,10 @@ __global__ __launch_bounds__(64) void k_dense_reduce(DenseArgs a, int slices) {
     }
     return v;
   };
-  if constexpr (EPI == kEpiGate) {
+  if constexpr (I8) {
+    store4(a.out, a.out_is_fp32, (size_t)m * a.N + n, scaled(sum(n), a.x_scale[m], four_scales(a.w_scale, n, a.N)),
+           a.N - n, wide);
+  } else if constexpr (EPI == kEpiGate) {
     const f32x4_t g = sum(n), u = sum(a.I + n);
     f32x4_t h;
 #pragma unroll
@@ -89,30 +94,35 @@ hipError_t run(const TileCfg& t, bool fp4, int slices, const DenseArgs& a, hipSt
   return hipGetLastError();
 }
 
-template <bool XT, bool WT, bool FP4, int EPI>
+template <bool XT, bool WT, int OP, int EPI>
 hipError_t run_tile(int tile, int slices, const DenseArgs& a, hipStream_t st) {
+  constexpr bool FP4 = OP == kDenseFp4;
   constexpr const TileCfg* t = FP4 ? kTilesFp4 : kTiles;
-  if (tile == 0) return run<&k_dense<XT, WT, 256, 256, 2, 4, t[0].nx, t[0].nw, FP4, EPI>>(t[0], FP4, slices, a, st);
-  if (tile == 1) return run<&k_dense<XT, WT, 256, 128, 2, 4, t[1].nx, t[1].nw, FP4, EPI>>(t[1], FP4, slices, a, st);
-  if (tile == 2) return run<&k_dense<XT, WT, 128, 128, 2, 4, t[2].nx, t[2].nw, FP4, EPI>>(t[2], FP4, slices, a, st);
-  return run<&k_dense<XT, WT, 64, 128, 2, 4, t[3].nx, t[3].nw, FP4, EPI>>(t[3], FP4, slices, a, st);
+  if (tile == 0) return run<&k_dense<XT, WT, 256, 256, 2, 4, t[0].nx, t[0].nw, OP, EPI>>(t[0], FP4, slices, a, st);
+  if (tile == 1) return run<&k_dense<XT, WT, 256, 128, 2, 4, t[1].nx, t[1].nw, OP, EPI>>(t[1], FP4, slices, a, st);
+  if (tile == 2) return run<&k_dense<XT, WT, 128, 128, 2, 4, t[2].nx, t[2].nw, OP, EPI>>(t[2], FP4, slices, a, st);
+  return run<&k_dense<XT, WT, 64, 128, 2, 4, t[3].nx, t[3].nw, OP, EPI>>(t[3], FP4, slices, a, st);
 }
 
 template <int EPI>
 hipError_t run_bf16(DenseLayout layout, int tile, int slices, const DenseArgs& a, hipStream_t st) {
   if constexpr (EPI == kEpiGate) {
-    return layout == kDenseNT ? run_tile<false, false, false, EPI>(tile, slices, a, st) : hipErrorInvalidValue;
+    return layout == kDenseNT ? run_tile<false, false, kDenseBf16, EPI>(tile, slices, a, st) : hipErrorInvalidValue;
   } else if constexpr (EPI == kEpiGrad) {
-    return layout == kDenseNN ? run_tile<false, true, false, EPI>(tile, slices, a, st) : hipErrorInvalidValue;
+    return layout == kDenseNN ? run_tile<false, true, kDenseBf16, EPI>(tile, slices, a, st) : hipErrorInvalidValue;
   } else {
-    if (layout == kDenseNT) return run_tile<false, false, false, EPI>(tile, slices, a, st);
-    if (layout == kDenseNN) return run_tile<false, true, false, EPI>(tile, slices, a, st);
-    return run_tile<true, true, false, EPI>(tile, slices, a, st);
+    if (layout == kDenseNT) return run_tile<false, false, kDenseBf16, EPI>(tile, slices, a, st);
+    if (layout == kDenseNN) return run_tile<false, true, kDenseBf16, EPI>(tile, slices, a, st);
+    return run_tile<true, true, kDenseBf16, EPI>(tile, slices, a, st);
   }
 }
 
-inline int stages_of(DenseKind kind, int K) { return kind == kDenseFp4 ? (K + 255) / 256 : (K + 63) / 64; }
+inline int stages_of(DenseKind kind, int K) {
+  const int k = kind == kDenseFp4 ? 256 : kind == kDenseI8 ? 128 : 64;
+  return (K + k - 1) / k;
+}
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+inline unsigned reduce_blocks(int M, int cols) { return (unsigned)(((long long)M * ((cols + 3) / 4) + 63) / 64); }
 // stages per slice; MXFP4 slices are whole pairs of stages (their scales are packed so)
 inline int slice_stages(DenseKind kind, int nst, int slices) {
   const int per = ceil_div(nst, slices);
@@ -183,8 +193,15 @@ hipError_t launch_dense(DenseKind kind, DenseLayout layout, int epi, const Dense
   const int first = split ? (int)kEpiPartial : epi;
   if (kind == kDenseFp4) {
     if (layout != kDenseNT || epi != kEpiStore) return hipErrorInvalidValue;
-    e = split ? run_tile<false, false, true, kEpiPartial>(p.tile, p.slices, a, st)
-              : run_tile<false, false, true, kEpiStore>(p.tile, p.slices, a, st);
+    e = split ? run_tile<false, false, kDenseFp4, kEpiPartial>(p.tile, p.slices, a, st)
+              : run_tile<false, false, kDenseFp4, kEpiStore>(p.tile, p.slices, a, st);
+  } else if (kind == kDenseI8) {
+    if (layout != kDenseNT || epi != kEpiStore || !a.x_scale || !a.w_scale) return hipErrorInvalidValue;
+    if (!split) return run_tile<false, false, kDenseI8, kEpiStore>(p.tile, 1, a, st);
+    e = run_tile<false, false, kDenseI8, kEpiPartial>(p.tile, p.slices, a, st);
+    if (e != hipSuccess) return e;
+    k_dense_reduce<kEpiStore, true><<<reduce_blocks(a.M, a.N), 64, 0, st>>>(a, p.slices);
+    return hipGetLastError();
   } else if (first == kEpiGate) {
     e = run_bf16<kEpiGate>(layout, p.tile, p.slices, a, st);
   } else if (first == kEpiGrad) {
@@ -291,8 +308,7 @@ hipError_t launch_dense_pair(int epi, const DensePairPlan& p, DenseArgs a, Dense
 
 hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st) {
   const int cols = epi == kEpiGate ? a.I : a.N;
-  const long long threads = (long long)a.M * ((cols + 3) / 4);
-  const unsigned nb = (unsigned)((threads + 63) / 64);
+  const unsigned nb = reduce_blocks(a.M, cols);
   if (epi == kEpiGate) k_dense_reduce<kEpiGate><<<nb, 64, 0, st>>>(a, slices);
   else if (epi == kEpiGrad) k_dense_reduce<kEpiGrad><<<nb, 64, 0, st>>>(a, slices);
   else k_dense_reduce<kEpiStore><<<nb, 64, 0, st>>>(a, slices);

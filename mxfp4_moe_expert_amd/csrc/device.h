@@ -147,6 +147,29 @@ __device__ __forceinline__ f32x4_t mfma_16x16x32(bf16x8_t a, bf16x8_t b, f32x4_t
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// The scale of an int8 row from the bits of its largest magnitude (Inf and NaN: scale NaN), and its reciprocal.
+struct RowScale {
+  float scale, inverse;
+  bool finite;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  RowScale s;
+  s.finite = top < 0x7f800000u;
+  const float v = fmaxf(__uint_as_float(s.finite ? top : 0u) / 127.0f, 1.1754943508222875e-38f);
+  s.scale = !s.finite ? __uint_as_float(0x7fc00000u) : top == 0u ? 1.0f : v;
+  s.inverse = 1.0f / v;
+  return s;
+}
+// The code of v under the scale of its row: RNE(v / s), exact (see int8.hip).
+__device__ __forceinline__ int int8_code(float v, const RowScale& s) {
+  if (!s.finite) return 0;
+  float c = rintf(v * s.inverse);
+  const float rest = __builtin_fmaf(-c, s.scale, v), twice = 2.0f * __builtin_fabsf(rest);
+  const bool odd = (int)c & 1;
+  if (twice > s.scale || (twice == s.scale && odd)) c += __builtin_copysignf(1.0f, rest);
+  return (int)c;
+}
+
 __device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z))); }
 
 // silu(z) = z / (1 + e^-z) with the hardware base-2 exponential and

@@ -1,0 +1,205 @@
+// int8 encoding and decoding on gfx950 (page "deepseek-v4-mxfp4-int8
+// config.json", quantization_config, linears_w8a16: int8, symmetric, one scale
+// per output channel; here one scale per row, a weight's channel or an
+// activation's token): per row with largest magnitude m,
+//   s = m / 127 (fp32, rounded once; 1 if m = 0; at least 2^-126),
+//   code = v / s rounded to the nearest whole number, ties to even.
+// A row with an Inf or NaN gets the scale NaN and codes 0, and reads as NaN.
+//
+// The code is that of the exact quotient: a product with 1 / s lies within a few
+// units in its last place, so it can only miss a code next to a border, and the
+// remainder v - c s, exact in one fma (|v - c s| <= s and both are multiples of
+// the smaller one's last place), says on which side v lies.
+//
+// Memory-bound both ways: a row is read once, held in registers between its
+// maximum and its codes (up to 2048 16-byte pieces; longer rows are read twice,
+// the second time from the L2).
+#include <type_traits>
+
+#include "device.h"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+template <int DT>
+constexpr int kPer = DT == kDtF32 ? 4 : 8;  // values of a 16-byte piece
+
+template <int DT>
+__device__ __forceinline__ float value_of(const u32x4_t& p, int i) {
+  if constexpr (DT == kDtF32) return __uint_as_float(p[i]);
+  const uint32_t h = i & 1 ? p[i >> 1] >> 16 : p[i >> 1] & 0xffffu;
+  return DT == kDtBf16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
+}
+
+// Largest magnitude as bits: magnitudes compare as integers, Inf and NaN above every finite value.
+template <int DT>
+__device__ __forceinline__ uint32_t piece_top(const u32x4_t& p, uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < kPer<DT>; ++i) m = max(m, __float_as_uint(value_of<DT>(p, i)) & 0x7fffffffu);
+  return m;
+}
+
+// The codes of a piece: 8 bytes (16-bit values) or 4.
+template <int DT>
+__device__ __forceinline__ uint2 piece_codes(const u32x4_t& p, const RowScale& s) {
+  uint2 o = make_uint2(0u, 0u);
+#pragma unroll
+  for (int i = 0; i < kPer<DT>; ++i) {
+    const uint32_t c = (uint32_t)int8_code(value_of<DT>(p, i), s) & 255u;
+    if (i < 4) o.x |= c << (8 * i);
+    else o.y |= c << (8 * (i - 4));
+  }
+  return o;
+}
+
+template <int DT>
+__device__ __forceinline__ void put_codes(int8_t* row, int piece, const uint2& c) {
+  if constexpr (DT == kDtF32) *reinterpret_cast<uint32_t*>(row + 4 * piece) = c.x;
+  else *reinterpret_cast<uint2*>(row + 8 * piece) = c;
+}
+
+// WPR waves (of the block's four) per row, PER pieces per lane in registers (0: any number, read twice).
+template <int DT, int WPR, int PER>
+__global__ __launch_bounds__(256) void k_int8_quantize(long long rows, int K, const char* __restrict__ x,
+                                                       long long ld_bytes, int8_t* __restrict__ codes,
+                                                       float* __restrict__ scales) {
+  constexpr int TPR = WPR * 64;
+  const int lane = (int)threadIdx.x % TPR, sub = (int)threadIdx.x / TPR;
+  const long long row = (long long)blockIdx.x * (256 / TPR) + sub;
+  const bool live = row < rows;
+  const int P = live ? K / kPer<DT> : 0;
+  const u32x4_t* src = reinterpret_cast<const u32x4_t*>(x + (live ? row : 0) * ld_bytes);
+  u32x4_t v[PER ? PER : 1];
+  uint32_t top = 0;
+  if constexpr (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = lane + i * TPR < P ? src[lane + i * TPR] : (u32x4_t){0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) top = piece_top<DT>(v[i], top);
+  } else {
+    for (int i = lane; i < P; i += TPR) top = piece_top<DT>(src[i], top);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  if constexpr (WPR > 1) {
+    __shared__ uint32_t tops[4];
+    if (threadIdx.x % 64 == 0) tops[threadIdx.x / 64] = top;
+    __syncthreads();
+    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+  }
+  if (!live) return;
+  const RowScale s = row_scale(top);
+  int8_t* out = codes + row * K;
+  if constexpr (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (lane + i * TPR < P) put_codes<DT>(out, lane + i * TPR, piece_codes<DT>(v[i], s));
+  } else {
+    for (int i = lane; i < P; i += TPR) put_codes<DT>(out, i, piece_codes<DT>(src[i], s));
+  }
+  if (lane == 0) scales[row] = s.scale;
+}
+
+template <int DT>
+hipError_t quantize(long long rows, int K, const char* x, long long ld, int8_t* codes, float* scales, hipStream_t st) {
+  const int P = K / kPer<DT>;
+  auto go = [&](auto wpr, auto per) {
+    const long long nb = (rows + 4 / wpr - 1) / (4 / wpr);
+    k_int8_quantize<DT, wpr, per><<<(unsigned)nb, 256, 0, st>>>(rows, K, x, ld, codes, scales);
+    return hipGetLastError();
+  };
+  using W1 = std::integral_constant<int, 1>;
+  using W4 = std::integral_constant<int, 4>;
+  // a wave per row while its lanes hold two pieces at most, then a block per row
+  if (P <= 64) return go(W1{}, std::integral_constant<int, 1>{});
+  if (P <= 128) return go(W1{}, std::integral_constant<int, 2>{});
+  if (P <= 256) return go(W4{}, std::integral_constant<int, 1>{});
+  if (P <= 512) return go(W4{}, std::integral_constant<int, 2>{});
+  if (P <= 1024) return go(W4{}, std::integral_constant<int, 4>{});
+  if (P <= 2048) return go(W4{}, std::integral_constant<int, 8>{});
+  return go(W4{}, std::integral_constant<int, 0>{});
+}
+
+// A thread takes pieces of 16 output bytes. Rows of fewer than 256 pieces share a block (RPB rows), longer ones are cut
+// into segments of 256 * AHEAD pieces.
+constexpr int kDeqAhead = 4;
+
+template <bool F32>
+__global__ __launch_bounds__(256) void k_int8_dequantize(long long rows, int K, int rpb, int segs,
+                                                         const int8_t* __restrict__ codes,
+                                                         const float* __restrict__ scales, void* __restrict__ out) {
+  constexpr int V = F32 ? 4 : 8;
+  const int P = K / V;
+  long long row;
+  int first, step;
+  if (rpb > 1) {
+    const int sub = (int)threadIdx.x / P;
+    row = (long long)blockIdx.x * rpb + sub;
+    if (sub >= rpb || row >= rows) return;
+    first = (int)threadIdx.x - sub * P;
+    step = P;  // one piece each
+  } else {
+    row = blockIdx.x / (unsigned)segs;
+    first = (int)(blockIdx.x - (unsigned)row * (unsigned)segs) * 256 * kDeqAhead + (int)threadIdx.x;
+    step = 256;
+  }
+  const float s = scales[row];
+  const int8_t* c = codes + row * K;
+  uint2 q[kDeqAhead];
+#pragma unroll
+  for (int i = 0; i < kDeqAhead; ++i) {
+    const int p = first + i * step;
+    q[i] = make_uint2(0u, 0u);
+    if (p >= P) continue;
+    if constexpr (F32) q[i].x = *reinterpret_cast<const uint32_t*>(c + 4 * p);
+    else q[i] = *reinterpret_cast<const uint2*>(c + 8 * p);
+  }
+#pragma unroll
+  for (int i = 0; i < kDeqAhead; ++i) {
+    const int p = first + i * step;
+    if (p >= P) continue;
+    float f[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = (float)(int8_t)((j < 4 ? q[i].x : q[i].y) >> (8 * (j & 3))) * s;
+    u32x4_t o;
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = __float_as_uint(f[j]);
+      reinterpret_cast<u32x4_t*>(static_cast<float*>(out) + row * K)[p] = o;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = bf16x2_rne(f[2 * j], f[2 * j + 1]);
+      reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + row * K)[p] = o;
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_int8_quantize(long long rows, int K, int dtype, const void* x, long long ldx, int8_t* codes,
+                                float* scales, hipStream_t st) {
+  if (rows <= 0 || K <= 0 || K % 16 || rows > (1ll << 32)) return hipErrorInvalidValue;
+  const char* p = static_cast<const char*>(x);
+  if (dtype == kDtF32) return quantize<kDtF32>(rows, K, p, ldx * 4, codes, scales, st);
+  if (dtype == kDtBf16) return quantize<kDtBf16>(rows, K, p, ldx * 2, codes, scales, st);
+  return quantize<kDtF16>(rows, K, p, ldx * 2, codes, scales, st);
+}
+
+hipError_t launch_int8_dequantize(long long rows, int K, const int8_t* codes, const float* scales, int dtype, void* out,
+                                  hipStream_t st) {
+  if (rows <= 0 || K <= 0 || K % 16 || rows > (1ll << 32)) return hipErrorInvalidValue;
+  const int P = K / (dtype == kDtF32 ? 4 : 8);
+  const int rpb = P <= 128 ? 256 / P : 1;
+  const int segs = rpb > 1 ? 1 : (P + 256 * kDeqAhead - 1) / (256 * kDeqAhead);
+  const long long nb = (rows + rpb - 1) / rpb * segs;
+  if (nb > 0x7fffffffll) return hipErrorInvalidValue;
+  if (dtype == kDtF32)
+    k_int8_dequantize<true><<<(unsigned)nb, 256, 0, st>>>(rows, K, rpb, segs, codes, scales, out);
+  else
+    k_int8_dequantize<false><<<(unsigned)nb, 256, 0, st>>>(rows, K, rpb, segs, codes, scales, out);
+  return hipGetLastError();
+}
+
+}  // namespace moe

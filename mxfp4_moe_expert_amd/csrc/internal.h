@@ -390,16 +390,18 @@ struct DenseArgs {
   const uint32_t* x_scales;  // packed E8M0 bytes (MXFP4 operands), see mxfp4.hip
   const uint32_t* w_scales;
   int x_blocks, w_blocks;    // their 16-row blocks
+  const float* x_scale;      // int8 operands: the scales of x's rows [M] and of w's [N]
+  const float* w_scale;
   void* out;                 // [M][N]; gate: h [M][I] bf16; grad: dgu [M][2I] bf16
   int out_is_fp32;
   int I;
   float limit;
   float* gu_out;             // gate: the pre-activations [M][2I] for the backward pass, or null
   const float* gu_in;        // grad: the same
-  float* part;               // split K: fp32 partial sums [slices][M][N] (gate: N = 2I)
+  float* part;               // split K: fp32 (int8: int32) partial sums [slices][M][N] (gate: N = 2I)
 };
 
-enum DenseKind { kDenseBf16 = 0, kDenseFp4 = 1 };
+enum DenseKind { kDenseBf16 = 0, kDenseFp4 = 1, kDenseI8 = 2 };
 enum DenseLayout { kDenseNT = 0, kDenseNN = 1, kDenseTN = 2 };  // X, W along k; W transposed; both transposed
 
 // How a product is cut: the tile configuration and the slices of K.
@@ -423,7 +425,7 @@ struct DensePairPlan {
 DensePairPlan dense_pair_plan(int Ma, int Na, int Ka, int Mb, int Nb, int Kb, int epi_bytes);
 hipError_t launch_dense_pair(int epi, const DensePairPlan& p, DenseArgs a, DenseArgs b, hipStream_t st);
 
-hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st);  // of a split's partials
+hipError_t launch_dense_reduce(int epi, const DenseArgs& a, int slices, hipStream_t st);  // of a split's partials (fp32)
 
 // The product with W read as MXFP4 codes (dense_w4.hip): the plan and its estimated microseconds (tile -1: K too long
 // for its LDS), and its launch on x bf16 (a.x, a.x_ld), codes (a.w, a.w_ld) and exponent bytes.
@@ -446,6 +448,12 @@ hipError_t launch_mxfp4_prep(int T, int K, const uint16_t* x, uint8_t* xcodes, u
 // W codes -> bf16 [N][K]; dy [T][N] -> rows padded to ld values with zeros (dy may be null)
 hipError_t launch_mxfp4_expand(int N, int K, const uint8_t* codes, const uint8_t* scales, uint16_t* w, int T,
                                const uint16_t* dy, uint16_t* dyp, int ld, hipStream_t st);
+
+// int8 encoding and decoding (int8.hip): one fp32 scale per row
+hipError_t launch_int8_quantize(long long rows, int K, int dtype, const void* x, long long ldx, int8_t* codes,
+                                float* scales, hipStream_t st);
+hipError_t launch_int8_dequantize(long long rows, int K, const int8_t* codes, const float* scales, int dtype, void* out,
+                                  hipStream_t st);
 
 // The streaming pass (few_rows.hip): K split over the waves of a block
 constexpr int kFewRows = 32;  // rows it takes
