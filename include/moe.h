@@ -108,9 +108,11 @@ enum {
 enum {
   MOE_FLAG_TOKEN_ID = 1,      /* a hash-layer token id outside [0, V) */
   MOE_FLAG_TABLE_ENTRY = 2,   /* a tid2eid entry outside [0, E) */
-  MOE_FLAG_EXPERT_ID = 4,     /* an expert id outside [0, E) given to moe_permute */
+  MOE_FLAG_EXPERT_ID = 4,     /* an expert id outside [0, E) given to moe_permute, moe_balance_loss or
+                               * moe_route_backward */
   MOE_FLAG_WAIT_EXPIRED = 8,  /* a bounded wait between blocks of one launch expired */
-  MOE_FLAG_PERMUTATION = 16   /* offsets or sorted slots given to moe_expert_ffn are inconsistent */
+  MOE_FLAG_PERMUTATION = 16,  /* offsets or sorted slots given to moe_expert_ffn are inconsistent */
+  MOE_FLAG_SEQUENCE = 32      /* sequence offsets given to moe_balance_loss do not ascend within [0, T] */
 };
 
 /* Reads the current device's error flags into *flags (if not NULL) after the
@@ -159,6 +161,13 @@ int moe_workspace_init(void* workspace, size_t workspace_bytes, void* stream);
 int moe_route(const moe_config* cfg, int32_t T, const uint16_t* x, const float* gate_w,
               const float* bias, const float* logit_offset, int32_t* topk_ids, float* topk_w,
               void* workspace, size_t workspace_bytes, void* stream);
+
+/* moe_route that also writes the logits (logit_offset added) its scores come
+ * from, [T][E] f32: what moe_balance_loss and moe_route_backward start from.
+ * logits may be NULL: moe_route. */
+int moe_route_logits(const moe_config* cfg, int32_t T, const uint16_t* x, const float* gate_w,
+                     const float* bias, const float* logit_offset, int32_t* topk_ids, float* topk_w,
+                     float* logits, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Hash router of the first num_hash_layers layers (page "Tidalluna/
  * DeepSeek-V4-Flash-0731-Tina-CQ4KM", section "Compatibility", item 2):
@@ -263,6 +272,52 @@ size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t groups
 int moe_linear_w8a16(int32_t T, int32_t K, int32_t N, int32_t groups, const uint16_t* x, const int8_t* q,
                      const float* scale, void* out, int32_t out_is_fp32, void* workspace, size_t workspace_bytes,
                      void* stream);
+
+/* ---- Training the router: balance loss, per-expert counts, gradient of the logits
+ *
+ * The selection bias balances the experts' loads over batches (page
+ * "DeepSeek-V4-Flash-0731", section "Checked in its code", row
+ * "Auxiliary-loss-free load balancing (selection bias)"), by the counts below;
+ * the loss holds them apart within a sequence. With s = sqrt(softplus(logits)),
+ * p_te = s_te / sum_j s_tj, and sequence q of n_q tokens with c_qe slots on
+ * expert e:
+ *   loss = alpha / Q sum_q sum_e (c_qe E / (k n_q)) (1 / n_q) sum_t p_te
+ * over the Q sequences that are not empty (0 if all are).
+ *   logits       [T][E] f32 (moe_route_logits)
+ *   topk_ids     [T][k] i32, of moe_route or moe_hash_route; an id outside
+ *                [0, E) is not counted and sets MOE_FLAG_EXPERT_ID; an id that
+ *                stands in two slots of a token counts twice
+ *   seq_offsets  [S+1] i32, ascending within [0, T]: sequence q is tokens
+ *                [offsets[q], offsets[q+1]); tokens outside all of them take
+ *                no part. NULL: one sequence of all tokens (S = 1). Offsets
+ *                that do not ascend within [0, T] set MOE_FLAG_SEQUENCE, and
+ *                the loss is NaN (coef and counts: any values)
+ *   loss   [1] f32 out; counts [E] i32 out (over all sequences)
+ *   coef   [S E + 1] f32 out: what moe_route_backward takes
+ * An expert with the logit -inf has the share 0 (and gets no gradient); a token
+ * all of whose logits are has no shares. NaN logits give a NaN loss. Sums are
+ * fp32 in an order that does not depend on timing.
+ *   workspace: moe_balance_workspace_size(T, E, S) bytes, 256-byte aligned, any
+ *   contents; calls sharing one must be ordered on one stream. Two launches.
+ * Supported: 1 <= E <= 256, 1 <= k <= 8, 0 <= T <= 65536, 1 <= S <= 65536. */
+size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S);
+int moe_balance_loss(int32_t T, int32_t E, int32_t k, int32_t S, const float* logits, const int32_t* topk_ids,
+                     const int32_t* seq_offsets, float alpha, float* loss, int32_t* counts, float* coef,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the logits from the balance loss, from the routing weights
+ * w[t][j] = scale s_j / sum_i s_i over the token's slots, or from both:
+ *   coef   of moe_balance_loss (with the same seq_offsets and S), or NULL
+ *   dloss  [1] f32: the gradient of the loss, or NULL for 1
+ *   dw     [T][k] f32: the gradient of topk_w, or NULL; scale:
+ *          routed_scaling_factor
+ *   dlogits [T][E] f32 out: zeros for tokens outside every sequence
+ * One of coef and dw at least is given. A slot whose id is outside [0, E) passes
+ * nothing (MOE_FLAG_EXPERT_ID). The counts and the selection pass no gradient.
+ * topk_ids is read only if dw is given. One launch, no workspace. */
+int moe_route_backward(int32_t T, int32_t E, int32_t k, int32_t S, const float* logits, const int32_t* topk_ids,
+                       const int32_t* seq_offsets, const float* coef, const float* dloss, const float* dw, float scale,
+                       float* dlogits, void* stream);
 
 /* ---- MXFP4 tensors and their products
  *

@@ -73,6 +73,10 @@ _SIGNATURES = {
     "moe_workspace_size": ([_CFGP, _I32], _SZ),
     "moe_workspace_init": ([_VP, _SZ, _VP], ctypes.c_int),
     "moe_route": ([_CFGP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "moe_route_logits": ([_CFGP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "moe_balance_workspace_size": ([_I32, _I32, _I32], _SZ),
+    "moe_balance_loss": ([_I32, _I32, _I32, _I32, _VP, _VP, _VP, _F32, _VP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "moe_route_backward": ([_I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _F32, _VP, _VP], ctypes.c_int),
     "moe_hash_route": ([_CFGP, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP], ctypes.c_int),
     "moe_permute": ([_CFGP, _I32, _VP, _VP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
     "moe_expert_ffn": ([_CFGP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
@@ -184,7 +188,7 @@ def set_option(name: str, value: int):
     return prev
 
 
-FLAGS = {"token_id": 1, "table_entry": 2, "expert_id": 4, "wait_expired": 8, "permutation": 16}
+FLAGS = {"token_id": 1, "table_entry": 2, "expert_id": 4, "wait_expired": 8, "permutation": 16, "sequence": 32}
 
 
 def read_probe(buf, blocks: int, sink, device=None) -> None:
@@ -293,8 +297,9 @@ def bf16_from_numpy(a, device="cuda") -> torch.Tensor:
 
 # ------------------------------------------------------------------ entry points
 
-def route(cfg: MoeConfig, x, gate_w, bias, logit_offset=None, ws=None, out=None):
-    """Learned router -> (topk_ids int32 [T,k], topk_w fp32 [T,k])."""
+def route(cfg: MoeConfig, x, gate_w, bias, logit_offset=None, ws=None, out=None, return_logits=False):
+    """Learned router -> (topk_ids int32 [T,k], topk_w fp32 [T,k]), with return_logits (topk_ids, topk_w, logits fp32
+    [T,E]): what ``balance_loss`` and ``route_backward`` start from."""
     T, H, E, k = x.shape[0], cfg.hidden_size, cfg.n_routed_experts, cfg.top_k
     _need(x, _BF16, (T, H), "x")
     _need(gate_w, torch.float32, (E, H), "gate_w")
@@ -304,6 +309,12 @@ def route(cfg: MoeConfig, x, gate_w, bias, logit_offset=None, ws=None, out=None)
     ids, w = out if out is not None else (torch.empty(T, k, dtype=torch.int32, device=x.device),
                                           torch.empty(T, k, dtype=torch.float32, device=x.device))
     buf, nb = _ws(cfg, T, x.device, ws)
+    if return_logits:
+        logits = torch.empty(T, E, dtype=torch.float32, device=x.device)
+        _check(lib().moe_route_logits(ctypes.byref(cfg), T, _ptr(x), _ptr(gate_w), _ptr(bias), _ptr(logit_offset),
+                                      _ptr(ids), _ptr(w), _ptr(logits), _ptr(buf), nb, _stream(x.device)),
+               "moe_route_logits")
+        return ids, w, logits
     _check(lib().moe_route(ctypes.byref(cfg), T, _ptr(x), _ptr(gate_w), _ptr(bias), _ptr(logit_offset),
                            _ptr(ids), _ptr(w), _ptr(buf), nb, _stream(x.device)), "moe_route")
     return ids, w
@@ -613,10 +624,13 @@ _POINTERS = {
     "moe_int8_quantize": ("x", "codes", "row scales"),
     "moe_int8_dequantize": ("codes", "row scales", "out"),
     "moe_linear_w8a8": ("x", "x", "x_scale", "q", "scale", "out", "ws"),
+    "moe_balance_loss": ("logits", "topk_ids", "seq_offsets", "loss", "counts", "coef", "ws"),
+    "moe_route_backward": ("logits", "topk_ids", "seq_offsets", "coef", "dloss", "dw", "dlogits"),
     "moe_gated_ffn": ("x", "w13", "w2", "saved[0]", "saved[1]", "out", "ws"),
     "moe_gated_ffn_backward": ("dy", "x", "w13", "w2", "saved[0]", "saved[1]", "dx", "dw13", "dw2", "ws"),
 }
-_BORDERS = {"ws": 256, "scale": 4, "x_scale": 4, "row scales": 4}
+_BORDERS = {"ws": 256, "scale": 4, "x_scale": 4, "row scales": 4, "topk_ids": 4, "seq_offsets": 4, "loss": 4,
+            "counts": 4, "coef": 4, "dloss": 4, "dw": 4}
 
 
 def _misaligned(name, args):
@@ -850,3 +864,58 @@ def gated_ffn_backward(dy, x, w13, w2, saved, limit=10.0, need=(True, True, True
           None if dx is None else dx.data_ptr(), None if dw13 is None else dw13.data_ptr(),
           None if dw2 is None else dw2.data_ptr(), 1 if dw_fp32 else 0, pw, nw)
     return dx, dw13, dw2
+
+
+# ------------------------------------------------------------------ training the router
+
+def _routed(logits, topk_ids, seq_offsets):
+    """T, E, k, S, the device index and the pointers of a routed batch."""
+    T, E, index = _matrix(logits, torch.float32, "logits")
+    _, k, _ = _matrix(topk_ids, torch.int32, "topk_ids")
+    S, po = 1, None
+    if seq_offsets is not None:
+        if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+            raise ValueError("seq_offsets: int32 tensor of the sequences' borders [S + 1], S >= 1, expected")
+        S = seq_offsets.shape[0] - 1
+        po = _arg(seq_offsets, torch.int32, (S + 1,), index, "seq_offsets")
+    return (T, E, k, S, index, _arg(logits, torch.float32, (T, E), index, "logits"),
+            _arg(topk_ids, torch.int32, (T, k), index, "topk_ids"), po)
+
+
+def balance_loss(logits, topk_ids, seq_offsets=None, alpha=1e-4, ws=None):
+    """Sequence-wise balance loss of a routed batch (moe_balance_loss): logits
+    fp32 [T][E] (``route`` with return_logits), topk_ids int32 [T][k],
+    seq_offsets int32 [S+1] (None: one sequence) -> (loss fp32 [], counts int32
+    [E], saved). ``counts`` are the slots on each expert, ``saved`` is what
+    ``route_backward`` takes. Autograd does not see it."""
+    T, E, k, S, index, pl, pi, po = _routed(logits, topk_ids, seq_offsets)
+    loss = logits.new_empty(())
+    counts = topk_ids.new_empty((E,))
+    coef = logits.new_empty((S * E + 1,))
+    pw, nw, ws = _scratch(lib().moe_balance_workspace_size(T, E, S), logits, ws, "moe_balance_loss")
+    _call(index, "moe_balance_loss", T, E, k, S, pl, pi, po, alpha, loss.data_ptr(), counts.data_ptr(),
+          coef.data_ptr(), pw, nw)
+    return loss, counts, (coef, seq_offsets)
+
+
+def route_backward(logits, topk_ids, dw=None, saved=None, scale=1.5, dloss=None, out=None):
+    """Gradient of the router's logits, fp32 [T][E] (moe_route_backward): from
+    the routing weights' gradient dw fp32 [T][k] (scale: the config's
+    routed_scaling_factor), from the balance loss (``saved`` of
+    ``balance_loss``; dloss: its gradient, a one-element fp32 tensor, None for
+    1), or from both. The gradients of gate_w and x follow as dlogits^T x and
+    dlogits gate_w."""
+    coef, seq_offsets = saved if saved is not None else (None, None)
+    T, E, k, S, index, pl, pi, po = _routed(logits, topk_ids, seq_offsets)
+    if coef is None and dw is None:
+        raise ValueError("route_backward: neither dw nor saved given")
+    pc = None if coef is None else _arg(coef, torch.float32, (S * E + 1,), index, "coef")
+    pd = None
+    if dloss is not None:
+        if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
+            raise ValueError("dloss: tensor of one element expected")
+        pd = _arg(dloss, torch.float32, dloss.shape, index, "dloss")
+    pw = None if dw is None else _arg(dw, torch.float32, (T, k), index, "dw")
+    out = _result(out, (T, E), torch.float32, logits)
+    _call(index, "moe_route_backward", T, E, k, S, pl, pi, po, pc, pd, pw, scale, out.data_ptr())
+    return out

@@ -538,6 +538,7 @@ RouterArgs router_args(const moe_config& c, int T, const uint16_t* x, const floa
   a.tid2eid = nullptr;
   a.V = 0;
   a.flags = device_flags();
+  a.logits = nullptr;
   return a;
 }
 
@@ -653,21 +654,23 @@ int moe_workspace_init(void* workspace, size_t workspace_bytes, void* stream) {
   return status(launch_fill_zero(workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
 }
 
-int moe_route(const moe_config* cfg, int32_t T, const uint16_t* x, const float* gate_w, const float* bias,
-              const float* logit_offset, int32_t* topk_ids, float* topk_w, void* workspace,
-              size_t workspace_bytes, void* stream) {
+int moe_route_logits(const moe_config* cfg, int32_t T, const uint16_t* x, const float* gate_w, const float* bias,
+                     const float* logit_offset, int32_t* topk_ids, float* topk_w, float* logits, void* workspace,
+                     size_t workspace_bytes, void* stream) {
   if (!cfg) return MOE_EINVAL;
   if (!cfg_ok(cfg) || T > kMaxT) return MOE_EUNSUPPORTED;
   if (T < 0) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
   if (!x || !gate_w || !bias || !topk_ids || !topk_w) return MOE_EINVAL;
-  if (!aligned16(x) || !aligned16(gate_w) || !aligned16(topk_ids) || !aligned16(topk_w)) return MOE_EINVAL;
+  if (!aligned16(x) || !aligned16(gate_w) || !aligned16(topk_ids) || !aligned16(topk_w) || !aligned16(logits))
+    return MOE_EINVAL;
   int rc = check_ws(*cfg, T, workspace, workspace_bytes);
   if (rc) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Layout L = layout(*cfg, T);
   RouterArgs a = router_args(*cfg, T, x, gate_w, bias, logit_offset, at<float>(workspace, L.scores), topk_ids,
                              topk_w);
+  a.logits = logits;
   if (T <= kSmallT) {
     Perm p = perm_of(workspace, L, at<int32_t>(workspace, L.offsets), at<int32_t>(workspace, L.sorted),
                      at<int32_t>(workspace, L.slot_pos));
@@ -676,6 +679,13 @@ int moe_route(const moe_config* cfg, int32_t T, const uint16_t* x, const float* 
     return status(launch_topk_permute_small(a, p, at<int32_t>(workspace, L.counters) + kArrivalsInt, st));
   }
   return status(launch_router_mfma(a, at<uint16_t>(workspace, L.wsplit), at<float>(workspace, L.plog), st));
+}
+
+int moe_route(const moe_config* cfg, int32_t T, const uint16_t* x, const float* gate_w, const float* bias,
+              const float* logit_offset, int32_t* topk_ids, float* topk_w, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  return moe_route_logits(cfg, T, x, gate_w, bias, logit_offset, topk_ids, topk_w, nullptr, workspace, workspace_bytes,
+                          stream);
 }
 
 int moe_hash_route(const moe_config* cfg, int32_t T, const uint16_t* x, const int32_t* token_ids,

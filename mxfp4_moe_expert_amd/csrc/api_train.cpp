@@ -1,0 +1,123 @@
+// Host entry points of the training operators beside the gated block
+// (include/moe.h): argument checks, workspace carving and dispatch on the
+// caller's stream. Nothing here allocates device memory or synchronises.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "internal.h"
+#include "moe.h"
+
+namespace {
+
+using namespace moe;
+
+constexpr int kMaxRows = 65536;  // T and S
+constexpr int kMaxExperts = 256;
+
+inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline int status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
+
+template <class P>
+inline P* at(void* ws, size_t off) {
+  return reinterpret_cast<P*>(static_cast<char*>(ws) + off);
+}
+
+// MOE_OK if the workspace holds `need` bytes at 256-byte alignment.
+int check_ws(const void* ws, size_t have, size_t need) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255)) return MOE_EINVAL;
+  return have < need ? MOE_EWORKSPACE : MOE_OK;
+}
+
+bool balance_ok(int T, int E, int S) {
+  return T >= 0 && T <= kMaxRows && E >= 1 && E <= kMaxExperts && S >= 1 && S <= kMaxRows;
+}
+
+struct BalanceLayout {
+  size_t sum, count, loss, ticket, total;
+};
+BalanceLayout balance_layout(int T, int E, int S) {
+  BalanceLayout L;
+  const size_t rows = align256((size_t)balance_rows(T, S) * E * 4);
+  L.ticket = 0;
+  L.sum = 256;
+  L.count = L.sum + rows;
+  L.loss = L.count + rows;
+  L.total = L.loss + align256((size_t)S * 4);
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S) {
+  return balance_ok(T, E, S) ? balance_layout(T, E, S).total : 0;
+}
+
+int moe_balance_loss(int32_t T, int32_t E, int32_t k, int32_t S, const float* logits, const int32_t* topk_ids,
+                     const int32_t* seq_offsets, float alpha, float* loss, int32_t* counts, float* coef,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (T < 0 || E <= 0 || k <= 0 || S <= 0) return MOE_EINVAL;
+  if (!balance_ok(T, E, S) || k > kMaxTopK) return MOE_EUNSUPPORTED;
+  if (!loss || !counts || !coef || (!seq_offsets && S != 1)) return MOE_EINVAL;
+  if (T > 0 && (!logits || !topk_ids)) return MOE_EINVAL;
+  if (!aligned16(logits) || !aligned4(topk_ids) || !aligned4(seq_offsets) || !aligned4(loss) || !aligned4(counts) ||
+      !aligned4(coef))
+    return MOE_EINVAL;
+  const BalanceLayout L = balance_layout(T, E, S);
+  const int rc = check_ws(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  BalanceArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.S = S;
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.offsets = seq_offsets;
+  a.alpha = alpha;
+  a.loss = loss;
+  a.counts = counts;
+  a.coef = coef;
+  a.part_sum = at<float>(workspace, L.sum);
+  a.part_count = at<int32_t>(workspace, L.count);
+  a.seq_loss = at<float>(workspace, L.loss);
+  a.ticket = at<int32_t>(workspace, L.ticket);
+  a.flags = device_flags();
+  return status(launch_balance(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_route_backward(int32_t T, int32_t E, int32_t k, int32_t S, const float* logits, const int32_t* topk_ids,
+                       const int32_t* seq_offsets, const float* coef, const float* dloss, const float* dw, float scale,
+                       float* dlogits, void* stream) {
+  if (T < 0 || E <= 0 || k <= 0 || S <= 0) return MOE_EINVAL;
+  if (!balance_ok(T, E, S) || k > kMaxTopK) return MOE_EUNSUPPORTED;
+  if ((!coef && !dw) || (!seq_offsets && S != 1)) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!logits || !dlogits || (dw && !topk_ids)) return MOE_EINVAL;
+  if (!aligned16(logits) || !aligned16(dlogits) || !aligned4(topk_ids) || !aligned4(seq_offsets) || !aligned4(coef) ||
+      !aligned4(dloss) || !aligned4(dw))
+    return MOE_EINVAL;
+  BalanceArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.S = S;
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.offsets = seq_offsets;
+  a.coef = const_cast<float*>(coef);
+  a.dloss = dloss;
+  a.dw = dw;
+  a.scale = scale;
+  a.dlogits = dlogits;
+  a.flags = device_flags();
+  return status(launch_route_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -62,6 +62,7 @@ struct RouterArgs {
   const int32_t* tid2eid;    // [V][k]
   int V;
   uint32_t* flags;           // device error-flag word
+  float* logits;             // [T][E] copy of the logits, or null
 };
 
 struct HashArgs {
@@ -375,7 +376,7 @@ hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
 // library-owned device memory; the address for the current device, or null
 // if it cannot be obtained.
 constexpr uint32_t kFlagTokenId = 1u, kFlagTableEntry = 2u, kFlagExpertId = 4u, kFlagWaitExpired = 8u,
-                   kFlagPermutation = 16u;
+                   kFlagPermutation = 16u, kFlagSequence = 32u;
 uint32_t* device_flags();
 
 // ---- dense products (dense.h, dense.hip, few_rows.hip): plain MXFP4 linears and the gated block
@@ -474,5 +475,31 @@ struct FewRowsArgs {
 hipError_t launch_few_rows_mxfp4(const FewRowsArgs& a, hipStream_t st);
 hipError_t launch_few_rows_gate(const FewRowsArgs& a, hipStream_t st);
 hipError_t launch_few_rows_two(const FewRowsArgs& a, hipStream_t st);
+
+// ---- the router's training operators (balance.hip)
+struct BalanceArgs {
+  int T, E, k, S;          // S sequences
+  const float* logits;     // [T][E]
+  const int32_t* ids;      // [T][k]
+  const int32_t* offsets;  // [S + 1], or null: one sequence of all tokens
+  float alpha;
+  float* loss;             // [1]
+  int32_t* counts;         // [E]
+  float* coef;             // [S][E] alpha f / n, then [1] 1 / Q (backward: read; null: no balance loss)
+  int run;                 // tokens per block of the forward pass
+  float* part_sum;         // [balance_rows][E] partial rows: of run r and sequence q at r + q
+  int32_t* part_count;
+  float* seq_loss;         // [S]
+  int32_t* ticket;
+  const float* dloss;      // backward: the loss's gradient, or null for 1
+  const float* dw;         // [T][k], or null
+  float scale;
+  float* dlogits;          // [T][E]
+  uint32_t* flags;
+};
+int balance_run(int T);
+int balance_rows(int T, int S);
+hipError_t launch_balance(BalanceArgs a, hipStream_t st);
+hipError_t launch_route_backward(const BalanceArgs& a, hipStream_t st);
 
 }  // namespace moe

@@ -33,6 +33,7 @@ namespace moe {
 // once here so that every top-k reader only compares.
 __device__ __forceinline__ void store_score(const RouterArgs& a, int t, int e, float logit) {
   const float sc = sqrtf(softplus(logit));
+  if (a.logits) a.logits[(size_t)t * a.E + e] = logit;
   a.scores[(size_t)t * a.E + e] = sc;
   a.keys[(size_t)t * a.E + e] = sc + (a.bias ? a.bias[e] : 0.0f);  // no bias on hash layers
 }

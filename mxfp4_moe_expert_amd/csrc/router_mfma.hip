@@ -179,6 +179,7 @@ __global__ __launch_bounds__(256) void k_topk_sum(RouterArgs a, const float* __r
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) logit += part[q][ks];
     if (a.logit_offset) logit += off[q];
+    if (a.logits && lane + 64 * q < a.E) a.logits[(size_t)t * a.E + lane + 64 * q] = logit;
     row.s[q] = sqrtf(softplus(logit));
     row.b[q] = row.s[q] + bias[q];
   }
