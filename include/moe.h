@@ -472,6 +472,31 @@ int moe_gated_ffn_backward(int32_t T, int32_t H, int32_t I, float limit, const u
                            const uint16_t* h_saved, uint16_t* dx, void* dw13, void* dw2, int32_t dw_is_fp32,
                            void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The update of a weight matrix made orthogonal
+ *
+ * Newton-Schulz products on a gradient (of moe_gated_ffn_backward, or a
+ * momentum of such gradients), as an optimiser that steps along the
+ * orthogonal factor takes them. For each of the B matrices of a stack:
+ *   X = G / (|G|_F + eps), then `steps` times
+ *   A = X X^T, X = a X + (b A + c A A) X
+ * (on the shorter side: of a matrix taller than wide, A = X^T X and X = a X +
+ * X (b A + c A A)); out = X.
+ *   g    [B][R][C] bf16, f32 or f16 (dtype), at any element of an array (one
+ *        matrix of a stack); out [B][R][C] bf16, 16-byte aligned
+ *   a, b, c  with which singular values of at most 1 stay below about 64 (the
+ *        usual 3.4445, -4.7750, 2.0315 hold them below 1.3); eps >= 0
+ * The norm is taken in 64 bits, the products in fp16 with fp32 sums, X being held
+ * in 22 bits: the result is within about 3e-3 (relative L2) of the same steps in
+ * 64 bits. A matrix of zeros gives zeros (eps > 0); one with an Inf or NaN gives
+ * NaN and leaves the others as they are. A matrix's bits do not depend on which
+ * others stand beside it as long as B is the same.
+ *   workspace: moe_orthogonalize_workspace_size(B, R, C) bytes, 256-byte
+ *   aligned, any contents; calls sharing one must be ordered on one stream.
+ * Supported: 1 <= R, C <= 16384, 0 <= B <= 65535, 1 <= steps <= 64. */
+size_t moe_orthogonalize_workspace_size(int32_t B, int32_t R, int32_t C);
+int moe_orthogonalize(int32_t B, int32_t R, int32_t C, int32_t dtype, const void* g, int32_t steps, float a, float b,
+                      float c, float eps, uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* One MoE layer's parameters for moe_forward_stack (device pointers, layouts
  * as for moe_forward). tid2eid != NULL makes it a hash layer (V rows); then
  * bias and logit_offset are ignored. */

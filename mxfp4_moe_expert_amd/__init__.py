@@ -105,6 +105,9 @@ _SIGNATURES = {
     "moe_gated_ffn_backward_workspace_size": ([_I32, _I32, _I32], _SZ),
     "moe_gated_ffn_backward": ([_I32, _I32, _I32, _F32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ,
                                 _VP], ctypes.c_int),
+    "moe_orthogonalize_workspace_size": ([_I32, _I32, _I32], _SZ),
+    "moe_orthogonalize": ([_I32, _I32, _I32, _I32, _VP, _I32, _F32, _F32, _F32, _F32, _VP, _VP, _SZ, _VP],
+                          ctypes.c_int),
     "moe_forward_stack": ([_CFGP, _I32, _VP, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], ctypes.c_int),
     "moe_forward_noalloc": ([_CFGP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP,
                              _VP, _VP, _VP, _I32, _VP, _VP, _VP], ctypes.c_int),
@@ -626,11 +629,12 @@ _POINTERS = {
     "moe_linear_w8a8": ("x", "x", "x_scale", "q", "scale", "out", "ws"),
     "moe_balance_loss": ("logits", "topk_ids", "seq_offsets", "loss", "counts", "coef", "ws"),
     "moe_route_backward": ("logits", "topk_ids", "seq_offsets", "coef", "dloss", "dw", "dlogits"),
+    "moe_orthogonalize": ("g", "out", "ws"),
     "moe_gated_ffn": ("x", "w13", "w2", "saved[0]", "saved[1]", "out", "ws"),
     "moe_gated_ffn_backward": ("dy", "x", "w13", "w2", "saved[0]", "saved[1]", "dx", "dw13", "dw2", "ws"),
 }
 _BORDERS = {"ws": 256, "scale": 4, "x_scale": 4, "row scales": 4, "topk_ids": 4, "seq_offsets": 4, "loss": 4,
-            "counts": 4, "coef": 4, "dloss": 4, "dw": 4}
+            "counts": 4, "coef": 4, "dloss": 4, "dw": 4, "g": 2}
 
 
 def _misaligned(name, args):
@@ -918,4 +922,33 @@ def route_backward(logits, topk_ids, dw=None, saved=None, scale=1.5, dloss=None,
     pw = None if dw is None else _arg(dw, torch.float32, (T, k), index, "dw")
     out = _result(out, (T, E), torch.float32, logits)
     _call(index, "moe_route_backward", T, E, k, S, pl, pi, po, pc, pd, pw, scale, out.data_ptr())
+    return out
+
+
+# ------------------------------------------------------------------ orthogonalised updates
+
+def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None, ws=None):
+    """Newton-Schulz orthogonalisation (moe_orthogonalize) of a gradient or
+    momentum g [..., R, C] (bf16, fp32 or fp16; leading dimensions are a stack
+    of matrices, e.g. ``dw13.view(2, I, H)``) -> bf16 of the same shape: X = g /
+    (|g| + eps), then ``steps`` times X = a X + (b A + c A A) X with A = X X^T."""
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g: torch.Tensor expected")
+    if not g.is_cuda:
+        raise ValueError("g: must be a device (cuda/hip) tensor")
+    dt = _DTYPES.get(g.dtype)
+    if dt is None:
+        raise TypeError(f"g: dtype {g.dtype}, expected bfloat16, float32 or float16")
+    shape, index = g.shape, g.get_device()
+    if len(shape) < 2 or shape[-1] == 0 or shape[-2] == 0:
+        raise ValueError("g: [..., R, C] with R, C >= 1 expected")
+    pg = _arg(g, g.dtype, shape, index, "g")
+    a, b, c = coefficients
+    R, C = shape[-2], shape[-1]
+    B = 1
+    for n in shape[:-2]:
+        B *= n
+    out = _result(out, shape, torch.bfloat16, g)
+    pw, nw, ws = _scratch(lib().moe_orthogonalize_workspace_size(B, R, C), g, ws, "moe_orthogonalize")
+    _call(index, "moe_orthogonalize", B, R, C, dt, pg, steps, a, b, c, eps, out.data_ptr(), pw, nw)
     return out

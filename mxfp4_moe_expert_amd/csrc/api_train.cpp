@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <cmath>
+
 #include "internal.h"
 #include "moe.h"
 
@@ -33,6 +35,11 @@ int check_ws(const void* ws, size_t have, size_t need) {
 
 bool balance_ok(int T, int E, int S) {
   return T >= 0 && T <= kMaxRows && E >= 1 && E <= kMaxExperts && S >= 1 && S <= kMaxRows;
+}
+
+constexpr int kMaxSteps = 64;
+bool newton_ok(int B, int R, int C) {
+  return B >= 0 && B <= kNewtonMaxBatch && R >= 1 && R <= kNewtonMaxSide && C >= 1 && C <= kNewtonMaxSide;
 }
 
 struct BalanceLayout {
@@ -118,6 +125,39 @@ int moe_route_backward(int32_t T, int32_t E, int32_t k, int32_t S, const float* 
   a.dlogits = dlogits;
   a.flags = device_flags();
   return status(launch_route_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_orthogonalize_workspace_size(int32_t B, int32_t R, int32_t C) {
+  return newton_ok(B, R, C) ? newton_workspace(B, R, C) : 0;
+}
+
+int moe_orthogonalize(int32_t B, int32_t R, int32_t C, int32_t dtype, const void* g, int32_t steps, float a, float b,
+                      float c, float eps, uint16_t* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || R <= 0 || C <= 0 || steps <= 0 || !(eps >= 0.0f) || !std::isfinite(a) || !std::isfinite(b) ||
+      !std::isfinite(c))
+    return MOE_EINVAL;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_F16) return MOE_EUNSUPPORTED;
+  if (!newton_ok(B, R, C) || steps > kMaxSteps) return MOE_EUNSUPPORTED;
+  if (B == 0) return MOE_OK;
+  // one matrix of a stack of odd sizes starts at any element
+  const uintptr_t element = dtype == MOE_DTYPE_F32 ? 4 : 2;
+  if (!g || !out || reinterpret_cast<uintptr_t>(g) % element || !aligned16(out)) return MOE_EINVAL;
+  const int rc = check_ws(workspace, workspace_bytes, newton_workspace(B, R, C));
+  if (rc) return rc;
+  NewtonArgs n;
+  n.B = B;
+  n.R = R;
+  n.C = C;
+  n.steps = steps;
+  n.dtype = dtype;
+  n.g = g;
+  n.a = a;
+  n.b = b;
+  n.c = c;
+  n.eps = eps;
+  n.out = out;
+  n.workspace = workspace;
+  return status(launch_newton(n, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -2,8 +2,8 @@
 // projections on gfx950's matrix cores: one kernel template,
 //   C[m][n] = sum_k X(m, k) W(n, k),
 // with each operand stored either along k ([row][k], "K-contiguous") or
-// across it ([k][row], "transposed"), in bf16 or (both K-contiguous) MXFP4 or
-// int8.
+// across it ([k][row], "transposed"), in bf16, fp16 or (both K-contiguous) MXFP4
+// or int8.
 //
 // Tile BM x BN, one block of WGM x WGN waves. K runs in stages of two MFMA
 // k-steps (128 bytes per row: 64 bf16, 128 int8 or 256 E2M1 values); LDS holds NX stages
@@ -25,7 +25,7 @@
 //     k rows; its 32-byte units are stored at unit ^ f(k), and the LDS
 //     transposing read (16 lanes x 4 elements) hands each lane 4 consecutive
 //     k of its row.
-//   - MFMA 16x16x32 (bf16), 16x16x64 (int8) or 16x16x128 with E8M0 scales
+//   - MFMA 16x16x32 (bf16, fp16), 16x16x64 (int8) or 16x16x128 with E8M0 scales
 //     (MXFP4), W as the A operand: lane (r, g) ends with 4 consecutive n of one m; two blocks'
 //     lanes are joined to 16-byte stores.
 //
@@ -52,6 +52,7 @@
 
 namespace moe {
 
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
@@ -170,6 +171,9 @@ struct Reader {
 
 __device__ __forceinline__ f32x4_t mfma_bf16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
   return mfma_16x16x32(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c);
+}
+__device__ __forceinline__ f32x4_t mfma_f16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 __device__ __forceinline__ i32x4_t mfma_i8(const u32x4_t& a, const u32x4_t& b, const i32x4_t& c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
@@ -524,10 +528,10 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& a, const f32x4_t
   }
 }
 
-// One tile (block `bid` of the product's a.tm a.tn) of the product of operands OP (a DenseKind). MXFP4: both operands
-// K-contiguous, with packed scales; int8: both K-contiguous.
-template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, int OP, int EPI>
-__device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
+// Tile (im, in) of the product of operands OP (a DenseKind). MXFP4: both operands K-contiguous, with packed scales; int8:
+// both K-contiguous. ARGS is DenseArgs or extends it, with an epilogue of its own.
+template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, int OP, int EPI, class ARGS>
+__device__ __forceinline__ void dense_block(const ARGS& a, int im, int in) {
   constexpr bool FP4 = OP == kDenseFp4;
   constexpr int W = WGM * WGN;
   constexpr int MB = BM / WGM / 16, NB = BN / WGN / 16;  // 16-row blocks per wave
@@ -546,8 +550,6 @@ __device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int im, in;
-  dense_tile(bid, a.tm, a.tn, im, in);
   L t;
   t.init(a, (uint32_t)(uintptr_t)lds, wave, lane, im, in);
   const int nst = t.nst;
@@ -591,6 +593,7 @@ __device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
       const u32x4_t& x = c < XR ? xr[c < XR ? c : 0] : xd[kk][c < XR ? 0 : c - XR];
       if constexpr (FP4) acc[b][c] = mfma_mx4<kk + 2 * q>(wf[kk][b], x, acc[b][c], swv[b], sxv[c]);
       else if constexpr (OP == kDenseI8) acc[b][c] = mfma_i8(wf[kk][b], x, acc[b][c]);
+      else if constexpr (OP == kDenseF16) acc[b][c] = mfma_f16(wf[kk][b], x, acc[b][c]);
       else acc[b][c] = mfma_bf16(wf[kk][b], x, acc[b][c]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -680,7 +683,9 @@ __device__ __forceinline__ void dense_block(const DenseArgs& a, int bid) {
 
 template <bool XT, bool WT, int BM, int BN, int WGM, int WGN, int NX, int NW, int OP, int EPI>
 __global__ __launch_bounds__(WGM* WGN * 64) void k_dense(DenseArgs a) {
-  dense_block<XT, WT, BM, BN, WGM, WGN, NX, NW, OP, EPI>(a, blockIdx.x);
+  int im, in;
+  dense_tile(blockIdx.x, a.tm, a.tn, im, in);
+  dense_block<XT, WT, BM, BN, WGM, WGN, NX, NW, OP, EPI>(a, im, in);
 }
 
 // Two independent products in one launch: the weight gradient `a` (both operands transposed) and a product `b` with W
@@ -690,10 +695,15 @@ template <int BM, int BN, int WGM, int WGN, int NX, int NW, int EPI>
 __global__ __launch_bounds__(WGM* WGN * 64) void k_dense_pair(DenseArgs a, DenseArgs b, int second, int b_first) {
   const int in_first = (int)blockIdx.x < second;
   const int bid = in_first ? (int)blockIdx.x : (int)blockIdx.x - second;
+  int im, in;
   if (in_first != b_first) {
-    if (bid < a.tm * a.tn) dense_block<true, true, BM, BN, WGM, WGN, NX, NW, kDenseBf16, kEpiStore>(a, bid);
+    if (bid >= a.tm * a.tn) return;
+    dense_tile(bid, a.tm, a.tn, im, in);
+    dense_block<true, true, BM, BN, WGM, WGN, NX, NW, kDenseBf16, kEpiStore>(a, im, in);
   } else {
-    if (bid < b.tm * b.tn) dense_block<false, true, BM, BN, WGM, WGN, NX, NW, kDenseBf16, EPI>(b, bid);
+    if (bid >= b.tm * b.tn) return;
+    dense_tile(bid, b.tm, b.tn, im, in);
+    dense_block<false, true, BM, BN, WGM, WGN, NX, NW, kDenseBf16, EPI>(b, im, in);
   }
 }
 

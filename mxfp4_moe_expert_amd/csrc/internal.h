@@ -402,7 +402,7 @@ struct DenseArgs {
   float* part;               // split K: fp32 (int8: int32) partial sums [slices][M][N] (gate: N = 2I)
 };
 
-enum DenseKind { kDenseBf16 = 0, kDenseFp4 = 1, kDenseI8 = 2 };
+enum DenseKind { kDenseBf16 = 0, kDenseFp4 = 1, kDenseI8 = 2, kDenseF16 = 3 };  // kDenseF16: newton.hip alone
 enum DenseLayout { kDenseNT = 0, kDenseNN = 1, kDenseTN = 2 };  // X, W along k; W transposed; both transposed
 
 // How a product is cut: the tile configuration and the slices of K.
@@ -501,5 +501,19 @@ int balance_run(int T);
 int balance_rows(int T, int S);
 hipError_t launch_balance(BalanceArgs a, hipStream_t st);
 hipError_t launch_route_backward(const BalanceArgs& a, hipStream_t st);
+
+// ---- Newton-Schulz orthogonalisation (newton.hip)
+constexpr int kNewtonMaxSide = 16384;
+constexpr int kNewtonMaxBatch = 65535;
+struct NewtonArgs {
+  int B, R, C, steps;
+  int dtype;        // of g
+  const void* g;    // [B][R][C]
+  double a, b, c, eps;
+  uint16_t* out;    // [B][R][C] bf16
+  void* workspace;  // newton_workspace(B, R, C) bytes
+};
+size_t newton_workspace(int B, int R, int C);
+hipError_t launch_newton(const NewtonArgs& a, hipStream_t st);
 
 }  // namespace moe

@@ -1,0 +1,435 @@
+// Newton-Schulz orthogonalisation of a stack of matrices on gfx950: with
+// X = G / (|G|_F + eps), `steps` times
+//   A = X X^T,  X = a X + (b A + c A A) X
+// (of a matrix taller than wide A = X^T X and X = a X + X (b A + c A A)), which
+// drives the singular values of X towards 1 and keeps its singular vectors.
+//
+// The products run in fp16 on the tile product of dense.h, sums in fp32. What
+// has to be more exact is the term a X: a small singular value grows by a in
+// each step, and so does an error of X beside it. X is therefore held in two
+// fp16 values, the nearest and the nearest to what it leaves (22 bits): the
+// products take the first, a X both. (Relative L2 error of the result against 64
+// bits, a 1024 x 2048 matrix of 16 strong directions over a floor of 1e-2: 3e-2
+// with X held in one fp16 value, 1e-3 in two; in bf16, 3e-1.) The last step has
+// no step after it, and takes the first value alone, which loses least there.
+// X is stored times 2^8: a singular value is at most about 1.2, a value of X at
+// the largest size 2^-14, so that neither end leaves fp16's normal range. A and
+// b A + c A A are stored as they are; their error, absolute, is measured against a.
+//
+// A and A A are symmetric: tiles below the diagonal are computed and stored twice.
+// Rows and columns are padded with zeros to multiples of 8, which every step keeps.
+#include "dense.h"
+
+namespace moe {
+
+namespace {
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kXScale = 256.0f;
+
+struct NsArgs : DenseArgs {
+  size_t x_batch, w_batch;        // bytes between the matrices of a stack
+  size_t in_batch, out_batch;     // values: of hi / lo / mat, and of out
+  float ca, cb;                   // kNsGram: acc * ca; kNsPoly: mat * ca + acc * cb; kNsNext, kNsLast: x * ca + acc
+  const uint16_t *hi, *lo;        // kNsPoly: hi is A
+  uint16_t *hi_out, *lo_out;      // lo_out may be null
+  int in_ld, out_ld;              // values per row of hi / lo, and of out
+};
+
+enum NsEpi { kNsGram = 10, kNsPoly = 11, kNsNext = 12, kNsLast = 13 };
+
+__device__ __forceinline__ uint32_t f16x2_rne(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, f16x2_t));
+}
+__device__ __forceinline__ uint2 pack4_f16(const f32x4_t& v) {
+  return make_uint2(f16x2_rne(v[0], v[1]), f16x2_rne(v[2], v[3]));
+}
+__device__ __forceinline__ f32x4_t unpack4_f16(const uint2& p) {
+  return __builtin_convertvector(__builtin_bit_cast(f16x4_t, p), f32x4_t);
+}
+
+// Four lanes of a quad hold four 16-bit values each, of one row; -> four values of one column each (lane j: column j).
+__device__ __forceinline__ uint2 quad_transpose(const uint2& d, int lane) {
+  auto swap1 = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true); };
+  auto swap2 = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true); };
+  const uint32_t e0 = swap1(d.x), e1 = swap1(d.y);
+  // even lanes: the pair's low halves (own first); odd lanes: its high halves (the neighbour's first)
+  const bool odd = lane & 1;
+  const uint32_t sel = odd ? 0x03020706u : 0x05040100u;  // bytes of (d, e): d is 0..3, e is 4..7
+  const uint32_t p0 = __builtin_amdgcn_perm(e0, d.x, sel), p1 = __builtin_amdgcn_perm(e1, d.y, sel);
+  const bool high = lane & 2;
+  const uint32_t f = swap2(high ? p0 : p1);
+  return high ? make_uint2(f, p1) : make_uint2(p0, f);
+}
+
+template <int EPI, int MB, int NB>
+__device__ __forceinline__ void dense_epilogue(const NsArgs& a, const f32x4_t (&acc)[NB][MB], int m0, int n0, int lane) {
+  const int r = lane & 15, g = lane >> 4;
+  if constexpr (EPI == kNsGram || EPI == kNsPoly) {
+    // the tile and its mirror image; M and N are the same multiple of 8
+#pragma unroll
+    for (int c = 0; c < MB; ++c) {
+      const int m = m0 + c * 16 + r;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int n = n0 + b * 16 + 4 * g;
+        f32x4_t v;
+        if constexpr (EPI == kNsGram) {
+          v = acc[b][c] * a.ca;
+        } else {
+          const size_t at = (size_t)min(m, a.M - 1) * a.in_ld + (n < a.N ? n : 0);
+          v = unpack4_f16(*reinterpret_cast<const uint2*>(a.hi + at)) * a.ca + acc[b][c] * a.cb;
+        }
+        const uint2 p = pack4_f16(v), t = quad_transpose(p, lane);
+        if (m < a.M && n < a.N) *reinterpret_cast<uint2*>(a.hi_out + (size_t)m * a.out_ld + n) = p;
+        const int mt = m0 + c * 16 + (r & 12), nt = n + (r & 3);
+        if (mt < a.M && nt < a.N) *reinterpret_cast<uint2*>(a.hi_out + (size_t)nt * a.out_ld + mt) = t;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < MB; ++c) {
+      const int m = m0 + c * 16 + r;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int n = n0 + b * 16 + 4 * g;
+        if (m >= a.M || n >= a.N) continue;
+        const size_t at = (size_t)m * a.in_ld + n;
+        f32x4_t x = unpack4_f16(*reinterpret_cast<const uint2*>(a.hi + at));
+        if (a.lo) x += unpack4_f16(*reinterpret_cast<const uint2*>(a.lo + at));
+        const f32x4_t y = x * a.ca + acc[b][c];
+        if constexpr (EPI == kNsNext) {
+          const uint2 h = pack4_f16(y);
+          *reinterpret_cast<uint2*>(a.hi_out + at) = h;
+          if (a.lo_out) *reinterpret_cast<uint2*>(a.lo_out + at) = pack4_f16(y - unpack4_f16(h));
+        } else {
+          store4(a.out, false, (size_t)m * a.out_ld + n, y * (1.0f / kXScale), a.N - n, (a.out_ld & 3) == 0);
+        }
+      }
+    }
+  }
+}
+
+// Tile of block bid among those at and below the diagonal (a contiguous run of them per XCD, as in dense_tile).
+__device__ __forceinline__ void lower_tile(int bid, int n, int& im, int& in) {
+  const int tiles = n * (n + 1) / 2, per = tiles >> 3, extra = tiles & 7, x = bid & 7;
+  const int t = x * per + min(x, extra) + (bid >> 3);
+  int i = (int)((__builtin_amdgcn_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+  while (i * (i + 1) / 2 > t) --i;
+  while ((i + 1) * (i + 2) / 2 <= t) ++i;
+  im = i;
+  in = t - i * (i + 1) / 2;
+}
+
+template <bool XT, bool WT, int BM, int BN, int NX, int NW, int EPI>
+__global__ __launch_bounds__(512) void k_newton(NsArgs a) {
+  int im, in;
+  if constexpr (EPI == kNsGram || EPI == kNsPoly) lower_tile(blockIdx.x, a.tm, im, in);
+  else dense_tile(blockIdx.x, a.tm, a.tn, im, in);
+  const size_t z = blockIdx.z;
+  a.x = static_cast<const char*>(a.x) + z * a.x_batch;
+  a.w = static_cast<const char*>(a.w) + z * a.w_batch;
+  a.hi += z * a.in_batch;
+  if (a.lo) a.lo += z * a.in_batch;
+  if (EPI == kNsLast) a.out = static_cast<uint16_t*>(a.out) + z * a.out_batch;
+  else a.hi_out += z * a.out_batch;
+  if (a.lo_out) a.lo_out += z * a.out_batch;
+  dense_block<XT, WT, BM, BN, 2, 4, NX, NW, kDenseF16, EPI>(a, im, in);
+}
+
+// ---- |G|_F and the first X
+
+constexpr int kNormThreads = 256, kNormBlocks = 256;
+
+template <int DT>
+__device__ __forceinline__ double value_at(const void* p, size_t i) {
+  if constexpr (DT == kDtF32) return static_cast<const float*>(p)[i];
+  const uint32_t h = static_cast<const uint16_t*>(p)[i];
+  return DT == kDtBf16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
+}
+template <int DT>
+__device__ __forceinline__ void eight_values(const u32x4_t* p, double (&v)[8]) {
+  if constexpr (DT == kDtF32) {
+    const u32x4_t a = p[0], b = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(a[i]);
+      v[4 + i] = __uint_as_float(b[i]);
+    }
+  } else {
+    const u32x4_t a = p[0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t h = i & 1 ? a[i >> 1] >> 16 : a[i >> 1] & 0xffffu;
+      v[i] = DT == kDtBf16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
+    }
+  }
+}
+
+// Sum over the block (kNormThreads) in a fixed order; every thread has it.
+__device__ __forceinline__ double block_sum(double v, double* lds) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kNormThreads / 64; ++w) s += lds[w];
+  return s;
+}
+
+// Sums of squares in 64 bits: no magnitude of G leaves their range.
+template <int DT>
+__global__ __launch_bounds__(kNormThreads) void k_newton_norm(const void* g, size_t n, double* part) {
+  constexpr size_t SIZE = DT == kDtF32 ? 4 : 2;
+  __shared__ double lds[kNormThreads / 64];
+  const char* p = static_cast<const char*>(g) + blockIdx.y * n * SIZE;
+  const size_t head = min(n, ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / SIZE);
+  const size_t pieces = (n - head) / 8, tail = head + pieces * 8;
+  const u32x4_t* body = reinterpret_cast<const u32x4_t*>(p + head * SIZE);
+  double s = 0.0;
+  const size_t step = (size_t)gridDim.x * kNormThreads;
+  for (size_t i = (size_t)blockIdx.x * kNormThreads + threadIdx.x; i < pieces; i += step) {
+    double v[8];
+    eight_values<DT>(body + i * (SIZE / 2), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += v[j] * v[j];
+  }
+  if (blockIdx.x == 0) {
+    const size_t ends = head + (n - tail);  // fewer than 16
+    if (threadIdx.x < ends) {
+      const double v = value_at<DT>(p, threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head);
+      s += v * v;
+    }
+  }
+  s = block_sum(s, lds);
+  if (threadIdx.x == 0) part[blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+// X = G / (|G| + eps), times kXScale, in two fp16 values; zeros in the padding. A thread takes 8 columns of a row.
+template <int DT>
+__global__ __launch_bounds__(kNormThreads) void k_newton_first(const void* g, int R, int C, int Rp, int Cp,
+                                                               const double* part, int parts, double eps, uint16_t* hi,
+                                                               uint16_t* lo) {
+  constexpr size_t SIZE = DT == kDtF32 ? 4 : 2;
+  __shared__ double lds[kNormThreads / 64];
+  const double sum = block_sum((int)threadIdx.x < parts ? part[(size_t)blockIdx.y * parts + threadIdx.x] : 0.0, lds);
+  const double inv = (double)kXScale / (__builtin_sqrt(sum) + eps);
+  const char* p = static_cast<const char*>(g) + (size_t)blockIdx.y * R * C * SIZE;
+  const bool whole = C % 8 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+  const long long n = (long long)Rp * (Cp / 8);
+  for (long long i = (long long)blockIdx.x * kNormThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kNormThreads) {
+    const int row = (int)(i / (Cp / 8)), col = (int)(i - (long long)row * (Cp / 8)) * 8;
+    double v[8];
+    if (row < R && whole) {
+      eight_values<DT>(reinterpret_cast<const u32x4_t*>(p + ((size_t)row * C + col) * SIZE), v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = row < R && col + j < C ? value_at<DT>(p, (size_t)row * C + col + j) : 0.0;
+    }
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = (float)(v[2 * j] * inv), y = (float)(v[2 * j + 1] * inv);
+      h[j] = f16x2_rne(x, y);
+      const f16x2_t hv = __builtin_bit_cast(f16x2_t, h[j]);
+      l[j] = f16x2_rne(x - (float)hv[0], y - (float)hv[1]);
+    }
+    const size_t at = ((size_t)blockIdx.y * Rp + row) * Cp + col;
+    *reinterpret_cast<u32x4_t*>(hi + at) = (u32x4_t){h[0], h[1], h[2], h[3]};
+    *reinterpret_cast<u32x4_t*>(lo + at) = (u32x4_t){l[0], l[1], l[2], l[3]};
+  }
+}
+
+// ---- host
+
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+struct Tile {
+  int bm, bn, nx, nw;
+};
+constexpr Tile kTiles[] = {{256, 256, 3, 2}, {256, 128, 3, 3}, {128, 128, 4, 4}, {64, 128, 3, 3}};
+
+template <bool XT, bool WT, int T, int EPI>
+hipError_t run(const NsArgs& a, int blocks, int batch, hipStream_t st) {
+  constexpr Tile t = kTiles[T];
+  constexpr auto kernel = &k_newton<XT, WT, t.bm, t.bn, t.nx, t.nw, EPI>;
+  constexpr int lds = (t.nx * t.bm + t.nw * t.bn) * kStageB;
+  const hipError_t e = allow_lds<kernel>(lds);
+  if (e != hipSuccess) return e;
+  kernel<<<dim3((unsigned)blocks, 1, (unsigned)batch), 512, lds, st>>>(a);
+  return hipGetLastError();
+}
+
+// A symmetric product: tiles of 256 or of 128, whichever ends first by the times per stage of dense.hip.
+template <bool TRANSPOSED, int EPI>
+hipError_t symmetric(NsArgs a, int batch, hipStream_t st) {
+  a.stages = a.slice_stages = ceil_div(a.K, 64);
+  auto blocks = [&](int side) {
+    const int n = ceil_div(a.M, side);
+    return n * (n + 1) / 2;
+  };
+  auto rounds = [&](int side) { return (double)ceil_div(blocks(side) * batch, 256); };
+  const bool large = rounds(256) * 1.45 < rounds(128) * 0.47;
+  a.tm = a.tn = ceil_div(a.M, large ? 256 : 128);
+  return large ? run<TRANSPOSED, TRANSPOSED, 0, EPI>(a, blocks(256), batch, st)
+               : run<TRANSPOSED, TRANSPOSED, 2, EPI>(a, blocks(128), batch, st);
+}
+
+template <bool WT, int EPI>
+hipError_t general(NsArgs a, int batch, hipStream_t st) {
+  a.stages = a.slice_stages = ceil_div(a.K, 64);
+  constexpr double stage_us[4] = {1.45, 0.80, 0.47, 0.56};
+  int best = 0;
+  double best_us = 1e30;
+  for (int t = 0; t < 4; ++t) {
+    const long long n = (long long)ceil_div(a.M, kTiles[t].bm) * ceil_div(a.N, kTiles[t].bn) * batch;
+    const int places = t == 3 ? 512 : 256;
+    const double us = (double)((n + places - 1) / places) * (a.stages * stage_us[t] + 4.5);
+    if (us < best_us) {
+      best_us = us;
+      best = t;
+    }
+  }
+  a.tm = ceil_div(a.M, kTiles[best].bm);
+  a.tn = ceil_div(a.N, kTiles[best].bn);
+  const int blocks = a.tm * a.tn;
+  if (best == 0) return run<false, WT, 0, EPI>(a, blocks, batch, st);
+  if (best == 1) return run<false, WT, 1, EPI>(a, blocks, batch, st);
+  if (best == 2) return run<false, WT, 2, EPI>(a, blocks, batch, st);
+  return run<false, WT, 3, EPI>(a, blocks, batch, st);
+}
+
+// Matrices of a stack are worked on `chunk` at a time, so that the workspace stays below about 1 GB.
+struct Layout {
+  int chunk, Rp, Cp, m;  // m: the shorter side, padded
+  size_t x, sq;          // values of an X and of a square matrix
+  size_t hi0, hi1, lo, gram, poly, part, total;
+};
+Layout layout_of(int B, int R, int C) {
+  Layout L;
+  L.Rp = (R + 7) & ~7;
+  L.Cp = (C + 7) & ~7;
+  L.m = L.Rp <= L.Cp ? L.Rp : L.Cp;
+  L.x = (size_t)L.Rp * L.Cp;
+  L.sq = (size_t)L.m * L.m;
+  const size_t each = 2 * (3 * L.x + 2 * L.sq);
+  const size_t most = ((size_t)1 << 30) / each;
+  L.chunk = (size_t)B <= most ? B : most < 1 ? 1 : (int)most;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t p = o;
+    o += align256(bytes);
+    return p;
+  };
+  L.hi0 = take(2 * L.x * L.chunk);
+  L.hi1 = take(2 * L.x * L.chunk);
+  L.lo = take(2 * L.x * L.chunk);
+  L.gram = take(2 * L.sq * L.chunk);
+  L.poly = take(2 * L.sq * L.chunk);
+  L.part = take(sizeof(double) * kNormBlocks * L.chunk);
+  L.total = o;
+  return L;
+}
+
+template <int DT>
+hipError_t first(const NewtonArgs& n, const Layout& L, const void* g, int count, double* part, uint16_t* hi, uint16_t* lo,
+                 hipStream_t st) {
+  const size_t values = (size_t)n.R * n.C;
+  const int parts = (int)(values / (kNormThreads * 32) < kNormBlocks ? values / (kNormThreads * 32) + 1 : kNormBlocks);
+  k_newton_norm<DT><<<dim3((unsigned)parts, (unsigned)count), kNormThreads, 0, st>>>(g, values, part);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const size_t pieces = L.x / 8;
+  const size_t nb = (pieces + kNormThreads - 1) / kNormThreads;
+  k_newton_first<DT><<<dim3((unsigned)(nb < 2048 ? nb : 2048), (unsigned)count), kNormThreads, 0, st>>>(
+      g, n.R, n.C, L.Rp, L.Cp, part, parts, n.eps, hi, lo);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t newton_workspace(int B, int R, int C) { return layout_of(B > 0 ? B : 1, R, C).total; }
+
+hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
+  if (n.B <= 0 || n.B > kNewtonMaxBatch || n.R <= 0 || n.C <= 0 || n.R > kNewtonMaxSide || n.C > kNewtonMaxSide ||
+      n.steps <= 0)
+    return hipErrorInvalidValue;
+  const Layout L = layout_of(n.B, n.R, n.C);
+  char* ws = static_cast<char*>(n.workspace);
+  uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(ws + L.hi0), reinterpret_cast<uint16_t*>(ws + L.hi1)};
+  uint16_t* lo = reinterpret_cast<uint16_t*>(ws + L.lo);
+  uint16_t* gram = reinterpret_cast<uint16_t*>(ws + L.gram);
+  uint16_t* poly = reinterpret_cast<uint16_t*>(ws + L.poly);
+  double* part = reinterpret_cast<double*>(ws + L.part);
+  const bool tall = L.Rp > L.Cp;
+  const size_t each = (size_t)n.R * n.C, size = n.dtype == kDtF32 ? 4 : 2;
+  for (int b = 0; b < n.B; b += L.chunk) {
+    const int count = n.B - b < L.chunk ? n.B - b : L.chunk;
+    const void* g = static_cast<const char*>(n.g) + (size_t)b * each * size;
+    hipError_t e = n.dtype == kDtF32    ? first<kDtF32>(n, L, g, count, part, hi[0], lo, st)
+                   : n.dtype == kDtBf16 ? first<kDtBf16>(n, L, g, count, part, hi[0], lo, st)
+                                        : first<kDtF16>(n, L, g, count, part, hi[0], lo, st);
+    if (e != hipSuccess) return e;
+    for (int i = 0; i < n.steps; ++i) {
+      const bool last = i + 1 == n.steps;
+      uint16_t *x = hi[i & 1], *y = hi[1 - (i & 1)];
+      NsArgs p;
+      __builtin_memset(&p, 0, sizeof(p));
+      // A
+      p.x = p.w = x;
+      p.x_ld = p.w_ld = (uint32_t)L.Cp * 2;
+      p.x_batch = p.w_batch = L.x * 2;
+      p.M = p.N = L.m;
+      p.K = tall ? L.Rp : L.Cp;
+      p.ca = 1.0f / (kXScale * kXScale);
+      p.hi_out = gram;
+      p.out_ld = L.m;
+      p.out_batch = L.sq;
+      e = tall ? symmetric<true, kNsGram>(p, count, st) : symmetric<false, kNsGram>(p, count, st);
+      if (e != hipSuccess) return e;
+      // b A + c A A
+      p.x = p.w = gram;
+      p.x_ld = p.w_ld = (uint32_t)L.m * 2;
+      p.x_batch = p.w_batch = L.sq * 2;
+      p.K = L.m;
+      p.ca = (float)n.b;
+      p.cb = (float)n.c;
+      p.hi = gram;
+      p.in_ld = L.m;
+      p.in_batch = L.sq;
+      p.hi_out = poly;
+      e = symmetric<false, kNsPoly>(p, count, st);
+      if (e != hipSuccess) return e;
+      // a X + (b A + c A A) X; tall: a X + X (b A + c A A)
+      p.x = tall ? x : poly;
+      p.w = tall ? poly : x;
+      p.x_ld = (uint32_t)(tall ? L.Cp : L.m) * 2;
+      p.w_ld = (uint32_t)(tall ? L.m : L.Cp) * 2;
+      p.x_batch = (tall ? L.x : L.sq) * 2;
+      p.w_batch = (tall ? L.sq : L.x) * 2;
+      p.M = last ? n.R : L.Rp;
+      p.N = last ? n.C : L.Cp;
+      p.K = L.m;
+      p.ca = (float)n.a;
+      p.hi = x;
+      p.in_ld = L.Cp;
+      p.in_batch = L.x;
+      p.lo = last ? nullptr : lo;
+      p.hi_out = y;
+      p.lo_out = i + 2 < n.steps ? lo : nullptr;
+      p.out = n.out + (size_t)b * each;
+      p.out_ld = last ? n.C : L.Cp;
+      p.out_batch = last ? each : L.x;
+      if (last) e = tall ? general<false, kNsLast>(p, count, st) : general<true, kNsLast>(p, count, st);
+      else e = tall ? general<false, kNsNext>(p, count, st) : general<true, kNsNext>(p, count, st);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe
