@@ -199,6 +199,16 @@ __device__ __forceinline__ u32x4_t join_blocks(const uint2& p, const uint2& q) {
   const auto d = __builtin_amdgcn_permlane16_swap(b[0], b[1], false, false);
   return (u32x4_t){c[0], d[0], c[1], d[1]};
 }
+// The same of two blocks' fp32 values: lane row g -> columns 8 g .. 8 g + 3 (lo) and 8 g + 4 .. 8 g + 7 (hi).
+__device__ __forceinline__ void join_values(const f32x4_t& p, const f32x4_t& q, f32x4_t& lo, f32x4_t& hi) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(p[i]), __float_as_uint(q[i]), false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
+    lo[i] = __uint_as_float(c[0]);
+    hi[i] = __uint_as_float(c[1]);
+  }
+}
 // Four consecutive outputs out[at .. at+3], of which `live` (1..4) exist;
 // wide: at is a multiple of 4 elements and all four exist.
 __device__ __forceinline__ void store4(void* out, bool fp32, size_t at, const f32x4_t& v, int live, bool wide) {
@@ -354,7 +364,8 @@ struct TileLoads {
   uint32_t lds0;
   int wave, lane, st0, nst, im, in;
 
-  __device__ __forceinline__ void init(const DenseArgs& a, uint32_t lds, int wave_, int lane_, int im_, int in_) {
+  template <class ARGS>
+  __device__ __forceinline__ void init(const ARGS& a, uint32_t lds, int wave_, int lane_, int im_, int in_) {
     lds0 = lds;
     wave = wave_;
     lane = lane_;
@@ -364,7 +375,7 @@ struct TileLoads {
     nst = min(a.slice_stages, a.stages - st0);
     const int m0 = im * BM, n0 = in * (GATE ? BN / 2 : BN);
     const int kb = FP4 ? a.K / 2 : OP == kDenseI8 ? a.K : a.K * 2;  // bytes along k (K-contiguous operands)
-    const char *xbase = static_cast<const char*>(a.x), *wbase = static_cast<const char*>(a.w);
+    const char *xbase = static_cast<const char*>(a.x_base()), *wbase = static_cast<const char*>(a.w_base());
     if constexpr (XT) {
       sx.init_tr(wave, lane, a.x_ld, a.M - m0);
       xbase += (size_t)m0 * 2;

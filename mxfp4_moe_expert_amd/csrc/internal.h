@@ -400,6 +400,9 @@ struct DenseArgs {
   float* gu_out;             // gate: the pre-activations [M][2I] for the backward pass, or null
   const float* gu_in;        // grad: the same
   float* part;               // split K: fp32 (int8: int32) partial sums [slices][M][N] (gate: N = 2I)
+
+  __device__ const void* x_base() const { return x; }
+  __device__ const void* w_base() const { return w; }
 };
 
 enum DenseKind { kDenseBf16 = 0, kDenseFp4 = 1, kDenseI8 = 2, kDenseF16 = 3 };  // kDenseF16: newton.hip alone

@@ -36,9 +36,13 @@ struct NsArgs : DenseArgs {
   const uint16_t *hi, *lo;        // kNsPoly: hi is A
   uint16_t *hi_out, *lo_out;      // lo_out may be null
   int in_ld, out_ld;              // values per row of hi / lo, and of out
+
+  __device__ const void* x_base() const { return static_cast<const char*>(x) + blockIdx.z * x_batch; }
+  __device__ const void* w_base() const { return static_cast<const char*>(w) + blockIdx.z * w_batch; }
 };
 
-enum NsEpi { kNsGram = 10, kNsPoly = 11, kNsNext = 12, kNsLast = 13 };
+// Epilogues: A from its sums; b A + c A A; X of the next step; the result; fp32 partial sums of A (of a split K)
+enum NsEpi { kNsGram = 10, kNsPoly = 11, kNsNext = 12, kNsLast = 13, kNsPartial = 14 };
 
 __device__ __forceinline__ uint32_t f16x2_rne(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, f16x2_t));
@@ -64,79 +68,146 @@ __device__ __forceinline__ uint2 quad_transpose(const uint2& d, int lane) {
   return high ? make_uint2(f, p1) : make_uint2(p0, f);
 }
 
+// Eight 16-bit values.
+__device__ __forceinline__ void unpack8_f16(const u32x4_t& p, f32x4_t& lo, f32x4_t& hi) {
+  lo = unpack4_f16(make_uint2(p[0], p[1]));
+  hi = unpack4_f16(make_uint2(p[2], p[3]));
+}
+__device__ __forceinline__ u32x4_t both(const uint2& a, const uint2& b) { return (u32x4_t){a.x, a.y, b.x, b.y}; }
+
+// Lane (r, g) takes eight consecutive columns of row m0 + 16 c + r at a time, from two blocks of 16. What it reads of the
+// next 16 rows is requested before this one's stores, which the compiler may not move loads across.
 template <int EPI, int MB, int NB>
 __device__ __forceinline__ void dense_epilogue(const NsArgs& a, const f32x4_t (&acc)[NB][MB], int m0, int n0, int lane) {
+  static_assert(NB % 2 == 0, "columns are taken by pairs of blocks");
+  constexpr int NP = NB / 2;
   const int r = lane & 15, g = lane >> 4;
-  if constexpr (EPI == kNsGram || EPI == kNsPoly) {
-    // the tile and its mirror image; M and N are the same multiple of 8
+  const size_t z = blockIdx.z;
+  if constexpr (EPI == kNsPartial) {
+    float* out = a.part + ((size_t)blockIdx.y * gridDim.z + z) * a.M * a.N;
+    store_tile<MB, NB>(acc, out, true, a.M, a.N, m0, n0, lane);
+    return;
+  }
+  constexpr bool READS = EPI != kNsGram;
+  const uint16_t* hi = READS ? a.hi + z * a.in_batch : nullptr;
+  const uint16_t* lo = EPI == kNsNext ? a.lo + z * a.in_batch : nullptr;
+  u32x4_t hv[2][NP], lv[2][NP];
+  auto fetch = [&](int c) {  // past the edges: the last row, the first columns (never stored)
+    const size_t row = (size_t)min(m0 + c * 16 + r, a.M - 1) * a.in_ld;
 #pragma unroll
-    for (int c = 0; c < MB; ++c) {
-      const int m = m0 + c * 16 + r;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int n = n0 + b * 16 + 4 * g;
-        f32x4_t v;
-        if constexpr (EPI == kNsGram) {
-          v = acc[b][c] * a.ca;
-        } else {
-          const size_t at = (size_t)min(m, a.M - 1) * a.in_ld + (n < a.N ? n : 0);
-          v = unpack4_f16(*reinterpret_cast<const uint2*>(a.hi + at)) * a.ca + acc[b][c] * a.cb;
-        }
-        const uint2 p = pack4_f16(v), t = quad_transpose(p, lane);
-        if (m < a.M && n < a.N) *reinterpret_cast<uint2*>(a.hi_out + (size_t)m * a.out_ld + n) = p;
-        const int mt = m0 + c * 16 + (r & 12), nt = n + (r & 3);
-        if (mt < a.M && nt < a.N) *reinterpret_cast<uint2*>(a.hi_out + (size_t)nt * a.out_ld + mt) = t;
-      }
+    for (int b = 0; b < NP; ++b) {
+      const int n = n0 + b * 32 + 8 * g, col = n < a.N ? n : 0;
+      if constexpr (READS) hv[c & 1][b] = *reinterpret_cast<const u32x4_t*>(hi + row + col);
+      if constexpr (EPI == kNsNext) lv[c & 1][b] = *reinterpret_cast<const u32x4_t*>(lo + row + col);
     }
-  } else {
+  };
+  fetch(0);
 #pragma unroll
-    for (int c = 0; c < MB; ++c) {
-      const int m = m0 + c * 16 + r;
+  for (int c = 0; c < MB; ++c) {
+    if (c + 1 < MB) fetch(c + 1);
+    const int m = m0 + c * 16 + r;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int n = n0 + b * 16 + 4 * g;
-        if (m >= a.M || n >= a.N) continue;
-        const size_t at = (size_t)m * a.in_ld + n;
-        f32x4_t x = unpack4_f16(*reinterpret_cast<const uint2*>(a.hi + at));
-        if (a.lo) x += unpack4_f16(*reinterpret_cast<const uint2*>(a.lo + at));
-        const f32x4_t y = x * a.ca + acc[b][c];
-        if constexpr (EPI == kNsNext) {
-          const uint2 h = pack4_f16(y);
-          *reinterpret_cast<uint2*>(a.hi_out + at) = h;
-          if (a.lo_out) *reinterpret_cast<uint2*>(a.lo_out + at) = pack4_f16(y - unpack4_f16(h));
+    for (int b = 0; b < NP; ++b) {
+      const int n = n0 + b * 32 + 8 * g;
+      const bool live = m < a.M && n < a.N;
+      f32x4_t v0, v1, x0, x1;
+      join_values(acc[2 * b][c], acc[2 * b + 1][c], v0, v1);
+      if constexpr (READS) unpack8_f16(hv[c & 1][b], x0, x1);
+      if constexpr (EPI == kNsGram || EPI == kNsPoly) {
+        // the tile and its mirror image; M and N are the same multiple of 8
+        if constexpr (EPI == kNsGram) {
+          v0 *= a.ca;
+          v1 *= a.ca;
         } else {
-          store4(a.out, false, (size_t)m * a.out_ld + n, y * (1.0f / kXScale), a.N - n, (a.out_ld & 3) == 0);
+          v0 = x0 * a.ca + v0 * a.cb;
+          v1 = x1 * a.ca + v1 * a.cb;
+        }
+        uint16_t* out = a.hi_out + z * a.out_batch;
+        const uint2 p0 = pack4_f16(v0), p1 = pack4_f16(v1);
+        const uint2 t0 = quad_transpose(p0, lane), t1 = quad_transpose(p1, lane);
+        if (live) *reinterpret_cast<u32x4_t*>(out + (size_t)m * a.out_ld + n) = both(p0, p1);
+        const int mt = m0 + c * 16 + (r & 12), nt = n + (r & 3);
+        if (mt < a.M && n < a.N) {
+          *reinterpret_cast<uint2*>(out + (size_t)nt * a.out_ld + mt) = t0;
+          *reinterpret_cast<uint2*>(out + (size_t)(nt + 4) * a.out_ld + mt) = t1;
+        }
+      } else if constexpr (EPI == kNsNext) {
+        f32x4_t l0, l1;
+        unpack8_f16(lv[c & 1][b], l0, l1);
+        v0 += (x0 + l0) * a.ca;
+        v1 += (x1 + l1) * a.ca;
+        const size_t at = z * a.out_batch + (size_t)m * a.out_ld + n;
+        const uint2 h0 = pack4_f16(v0), h1 = pack4_f16(v1);
+        if (live) *reinterpret_cast<u32x4_t*>(a.hi_out + at) = both(h0, h1);
+        if (a.lo_out) {
+          const u32x4_t l = both(pack4_f16(v0 - unpack4_f16(h0)), pack4_f16(v1 - unpack4_f16(h1)));
+          if (live) *reinterpret_cast<u32x4_t*>(a.lo_out + at) = l;
+        }
+      } else {
+        v0 = (v0 + x0 * a.ca) * (1.0f / kXScale);
+        v1 = (v1 + x1 * a.ca) * (1.0f / kXScale);
+        uint16_t* out = static_cast<uint16_t*>(a.out) + z * a.out_batch;
+        const size_t at = (size_t)m * a.out_ld + n;
+        if (!live) continue;
+        if ((a.out_ld & 7) == 0) {
+          *reinterpret_cast<u32x4_t*>(out + at) = both(pack4_bf16(v0), pack4_bf16(v1));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (n + i < a.N) out[at + i] = f32_to_bf16(v0[i]);
+            if (n + 4 + i < a.N) out[at + 4 + i] = f32_to_bf16(v1[i]);
+          }
         }
       }
     }
   }
 }
 
-// Tile of block bid among those at and below the diagonal (a contiguous run of them per XCD, as in dense_tile).
-__device__ __forceinline__ void lower_tile(int bid, int n, int& im, int& in) {
-  const int tiles = n * (n + 1) / 2, per = tiles >> 3, extra = tiles & 7, x = bid & 7;
+// Tile of block bid among those of a symmetric product that reach the diagonal or lie below it, SH = BM / BN of them
+// more in each row than in the one before (a contiguous run of them per XCD, as in dense_tile).
+template <int SH>
+__device__ __forceinline__ void lower_tile(int bid, int tiles, int& im, int& in) {
+  const int per = tiles >> 3, extra = tiles & 7, x = bid & 7;
   const int t = x * per + min(x, extra) + (bid >> 3);
-  int i = (int)((__builtin_amdgcn_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-  while (i * (i + 1) / 2 > t) --i;
-  while ((i + 1) * (i + 2) / 2 <= t) ++i;
+  // SH i (i + 1) / 2 tiles lie above row i
+  int i = (int)((__builtin_amdgcn_sqrtf(8.0f * (float)t / SH + 1.0f) - 1.0f) * 0.5f);
+  while (SH * i * (i + 1) / 2 > t) --i;
+  while (SH * (i + 1) * (i + 2) / 2 <= t) ++i;
   im = i;
-  in = t - i * (i + 1) / 2;
+  in = t - SH * i * (i + 1) / 2;
 }
 
 template <bool XT, bool WT, int BM, int BN, int NX, int NW, int EPI>
 __global__ __launch_bounds__(512) void k_newton(NsArgs a) {
   int im, in;
-  if constexpr (EPI == kNsGram || EPI == kNsPoly) lower_tile(blockIdx.x, a.tm, im, in);
-  else dense_tile(blockIdx.x, a.tm, a.tn, im, in);
-  const size_t z = blockIdx.z;
-  a.x = static_cast<const char*>(a.x) + z * a.x_batch;
-  a.w = static_cast<const char*>(a.w) + z * a.w_batch;
-  a.hi += z * a.in_batch;
-  if (a.lo) a.lo += z * a.in_batch;
-  if (EPI == kNsLast) a.out = static_cast<uint16_t*>(a.out) + z * a.out_batch;
-  else a.hi_out += z * a.out_batch;
-  if (a.lo_out) a.lo_out += z * a.out_batch;
+  if constexpr (EPI == kNsNext || EPI == kNsLast) dense_tile(blockIdx.x, a.tm, a.tn, im, in);
+  else lower_tile<BM / BN>(blockIdx.x, gridDim.x, im, in);
   dense_block<XT, WT, BM, BN, 2, 4, NX, NW, kDenseF16, EPI>(a, im, in);
+}
+
+// A from the partial sums of a split K, [slice][matrix][m][m] of which the tiles k_newton computed exist: a thread adds
+// four columns of one row, slices in order, and stores them and their mirror image.
+__global__ __launch_bounds__(256) void k_newton_gram_sum(NsArgs a, int slices, int side) {
+  const int per = a.N / 4, id = blockIdx.x * 256 + threadIdx.x, m = id / per, n = (id - m * per) * 4;
+  if (m >= a.M || n / side > m / side) return;
+  const size_t z = blockIdx.z, plane = (size_t)a.M * a.N;
+  const float* p = a.part + z * plane + (size_t)m * a.N + n;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  constexpr int AHEAD = 8;
+  for (int s0 = 0; s0 < slices; s0 += AHEAD) {
+    f32x4_t t[AHEAD];
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s)
+      t[s] = *reinterpret_cast<const f32x4_t*>(p + (size_t)min(s0 + s, slices - 1) * gridDim.z * plane);
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s)
+      if (s0 + s < slices) v += t[s];
+  }
+  const uint2 h = pack4_f16(v * a.ca);
+  uint16_t* out = a.hi_out + z * a.out_batch;
+  *reinterpret_cast<uint2*>(out + (size_t)m * a.out_ld + n) = h;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[(size_t)(n + i) * a.out_ld + m] = (uint16_t)((i < 2 ? h.x : h.y) >> (16 * (i & 1)));
 }
 
 // ---- |G|_F and the first X
@@ -254,41 +325,93 @@ struct Tile {
 constexpr Tile kTiles[] = {{256, 256, 3, 2}, {256, 128, 3, 3}, {128, 128, 4, 4}, {64, 128, 3, 3}};
 
 template <bool XT, bool WT, int T, int EPI>
-hipError_t run(const NsArgs& a, int blocks, int batch, hipStream_t st) {
+hipError_t run(const NsArgs& a, int blocks, int slices, int batch, hipStream_t st) {
   constexpr Tile t = kTiles[T];
   constexpr auto kernel = &k_newton<XT, WT, t.bm, t.bn, t.nx, t.nw, EPI>;
   constexpr int lds = (t.nx * t.bm + t.nw * t.bn) * kStageB;
   const hipError_t e = allow_lds<kernel>(lds);
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)blocks, 1, (unsigned)batch), 512, lds, st>>>(a);
+  kernel<<<dim3((unsigned)blocks, (unsigned)slices, (unsigned)batch), 512, lds, st>>>(a);
   return hipGetLastError();
 }
 
-// A symmetric product: tiles of 256 or of 128, whichever ends first by the times per stage of dense.hip.
+// Microseconds per stage of a tile with few and with all CUs at work (dense.hip), and of the rest of a block.
+constexpr double kFewUs[4] = {0.95, 0.47, 0.32, 0.26}, kFullUs[4] = {1.45, 0.80, 0.47, 0.34}, kStartUs = 4.5;
+inline double stage_us(int tile, double blocks) {
+  const double full = blocks < 256 ? blocks / 256 : 1.0;
+  return kFewUs[tile] + full * (kFullUs[tile] - kFewUs[tile]);
+}
+
+inline int lower_tiles(int tile, int m) {
+  const int sh = kTiles[tile].bm / kTiles[tile].bn, n = ceil_div(m, kTiles[tile].bm);
+  // the last row may end before its last column of tiles
+  return sh * n * (n + 1) / 2 - (sh * n - ceil_div(m, kTiles[tile].bn));
+}
+
+// How a symmetric product is cut: tile (0 to 2) and slices of K.
+struct Cut {
+  int tile, slices;
+};
+Cut symmetric_cut(int m, int K, int batch, bool split) {
+  const int stages = ceil_div(K, 64);
+  Cut best = {2, 1};
+  double best_us = 1e30;
+  for (int t = 0; t < 3; ++t) {
+    const int tiles = lower_tiles(t, m);
+    for (int s = 1; s == 1 || (split && s <= 16 && s * 4 <= stages + 3); s *= 2) {
+      const int per = ceil_div(stages, s), slices = ceil_div(stages, per);
+      const double blocks = (double)tiles * slices * batch;
+      double us = __builtin_ceil(blocks / 256) * (per * stage_us(t, blocks) + kStartUs);
+      if (slices > 1) us += 2.5 + 1.5 * slices * m * (double)m * batch * 4 / 4e6;
+      if (us < best_us) {
+        best_us = us;
+        best = {t, slices};
+      }
+    }
+  }
+  return best;
+}
+inline size_t partial_bytes(int m, int K, int batch) {
+  const Cut c = symmetric_cut(m, K, batch, true);
+  return c.slices > 1 ? (size_t)c.slices * batch * m * m * sizeof(float) : 0;
+}
+
 template <bool TRANSPOSED, int EPI>
-hipError_t symmetric(NsArgs a, int batch, hipStream_t st) {
-  a.stages = a.slice_stages = ceil_div(a.K, 64);
-  auto blocks = [&](int side) {
-    const int n = ceil_div(a.M, side);
-    return n * (n + 1) / 2;
-  };
-  auto rounds = [&](int side) { return (double)ceil_div(blocks(side) * batch, 256); };
-  const bool large = rounds(256) * 1.45 < rounds(128) * 0.47;
-  a.tm = a.tn = ceil_div(a.M, large ? 256 : 128);
-  return large ? run<TRANSPOSED, TRANSPOSED, 0, EPI>(a, blocks(256), batch, st)
-               : run<TRANSPOSED, TRANSPOSED, 2, EPI>(a, blocks(128), batch, st);
+hipError_t symmetric(NsArgs a, const Cut& cut, int batch, hipStream_t st) {
+  a.stages = ceil_div(a.K, 64);
+  a.slice_stages = ceil_div(a.stages, cut.slices);
+  const int tiles = lower_tiles(cut.tile, a.M);
+  if (cut.tile == 0) return run<TRANSPOSED, TRANSPOSED, 0, EPI>(a, tiles, cut.slices, batch, st);
+  if (cut.tile == 1) return run<TRANSPOSED, TRANSPOSED, 1, EPI>(a, tiles, cut.slices, batch, st);
+  return run<TRANSPOSED, TRANSPOSED, 2, EPI>(a, tiles, cut.slices, batch, st);
+}
+
+// A = X X^T or X^T X
+hipError_t gram_of(const NsArgs& a, bool tall, int batch, hipStream_t st) {
+  const Cut cut = symmetric_cut(a.M, a.K, batch, true);
+  if (cut.slices == 1)
+    return tall ? symmetric<true, kNsGram>(a, cut, batch, st) : symmetric<false, kNsGram>(a, cut, batch, st);
+  const hipError_t e =
+      tall ? symmetric<true, kNsPartial>(a, cut, batch, st) : symmetric<false, kNsPartial>(a, cut, batch, st);
+  if (e != hipSuccess) return e;
+  // every tile is whole in rows and columns of the tile's longer side
+  const long long threads = (long long)a.M * (a.N / 4);
+  k_newton_gram_sum<<<dim3((unsigned)((threads + 255) / 256), 1, (unsigned)batch), 256, 0, st>>>(a, cut.slices,
+                                                                                               kTiles[cut.tile].bm);
+  return hipGetLastError();
 }
 
 template <bool WT, int EPI>
 hipError_t general(NsArgs a, int batch, hipStream_t st) {
   a.stages = a.slice_stages = ceil_div(a.K, 64);
-  constexpr double stage_us[4] = {1.45, 0.80, 0.47, 0.56};
+  constexpr double kPairUs = 0.56;  // 64 x 128: a stage of both blocks of a CU
   int best = 0;
   double best_us = 1e30;
   for (int t = 0; t < 4; ++t) {
     const long long n = (long long)ceil_div(a.M, kTiles[t].bm) * ceil_div(a.N, kTiles[t].bn) * batch;
     const int places = t == 3 ? 512 : 256;
-    const double us = (double)((n + places - 1) / places) * (a.stages * stage_us[t] + 4.5);
+    const double stage = t == 3 && n > 256 ? kPairUs : stage_us(t, (double)n);
+    const double us = (double)((n + places - 1) / places) * (a.stages * stage + kStartUs);
     if (us < best_us) {
       best_us = us;
       best = t;
@@ -297,17 +420,17 @@ hipError_t general(NsArgs a, int batch, hipStream_t st) {
   a.tm = ceil_div(a.M, kTiles[best].bm);
   a.tn = ceil_div(a.N, kTiles[best].bn);
   const int blocks = a.tm * a.tn;
-  if (best == 0) return run<false, WT, 0, EPI>(a, blocks, batch, st);
-  if (best == 1) return run<false, WT, 1, EPI>(a, blocks, batch, st);
-  if (best == 2) return run<false, WT, 2, EPI>(a, blocks, batch, st);
-  return run<false, WT, 3, EPI>(a, blocks, batch, st);
+  if (best == 0) return run<false, WT, 0, EPI>(a, blocks, 1, batch, st);
+  if (best == 1) return run<false, WT, 1, EPI>(a, blocks, 1, batch, st);
+  if (best == 2) return run<false, WT, 2, EPI>(a, blocks, 1, batch, st);
+  return run<false, WT, 3, EPI>(a, blocks, 1, batch, st);
 }
 
 // Matrices of a stack are worked on `chunk` at a time, so that the workspace stays below about 1 GB.
 struct Layout {
   int chunk, Rp, Cp, m;  // m: the shorter side, padded
   size_t x, sq;          // values of an X and of a square matrix
-  size_t hi0, hi1, lo, gram, poly, part, total;
+  size_t hi0, hi1, lo, gram, poly, norm, part, total;
 };
 Layout layout_of(int B, int R, int C) {
   Layout L;
@@ -330,7 +453,12 @@ Layout layout_of(int B, int R, int C) {
   L.lo = take(2 * L.x * L.chunk);
   L.gram = take(2 * L.sq * L.chunk);
   L.poly = take(2 * L.sq * L.chunk);
-  L.part = take(sizeof(double) * kNormBlocks * L.chunk);
+  L.norm = take(sizeof(double) * kNormBlocks * L.chunk);
+  // the last part of a stack may be shorter, and cut otherwise
+  const int K = L.Rp > L.Cp ? L.Rp : L.Cp, rest = B % L.chunk;
+  size_t p = partial_bytes(L.m, K, L.chunk);
+  if (rest) p = p > partial_bytes(L.m, K, rest) ? p : partial_bytes(L.m, K, rest);
+  L.part = take(p);
   L.total = o;
   return L;
 }
@@ -364,15 +492,15 @@ hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
   uint16_t* lo = reinterpret_cast<uint16_t*>(ws + L.lo);
   uint16_t* gram = reinterpret_cast<uint16_t*>(ws + L.gram);
   uint16_t* poly = reinterpret_cast<uint16_t*>(ws + L.poly);
-  double* part = reinterpret_cast<double*>(ws + L.part);
+  double* norm = reinterpret_cast<double*>(ws + L.norm);
   const bool tall = L.Rp > L.Cp;
   const size_t each = (size_t)n.R * n.C, size = n.dtype == kDtF32 ? 4 : 2;
   for (int b = 0; b < n.B; b += L.chunk) {
     const int count = n.B - b < L.chunk ? n.B - b : L.chunk;
     const void* g = static_cast<const char*>(n.g) + (size_t)b * each * size;
-    hipError_t e = n.dtype == kDtF32    ? first<kDtF32>(n, L, g, count, part, hi[0], lo, st)
-                   : n.dtype == kDtBf16 ? first<kDtBf16>(n, L, g, count, part, hi[0], lo, st)
-                                        : first<kDtF16>(n, L, g, count, part, hi[0], lo, st);
+    hipError_t e = n.dtype == kDtF32    ? first<kDtF32>(n, L, g, count, norm, hi[0], lo, st)
+                   : n.dtype == kDtBf16 ? first<kDtBf16>(n, L, g, count, norm, hi[0], lo, st)
+                                        : first<kDtF16>(n, L, g, count, norm, hi[0], lo, st);
     if (e != hipSuccess) return e;
     for (int i = 0; i < n.steps; ++i) {
       const bool last = i + 1 == n.steps;
@@ -389,7 +517,8 @@ hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
       p.hi_out = gram;
       p.out_ld = L.m;
       p.out_batch = L.sq;
-      e = tall ? symmetric<true, kNsGram>(p, count, st) : symmetric<false, kNsGram>(p, count, st);
+      p.part = reinterpret_cast<float*>(ws + L.part);
+      e = gram_of(p, tall, count, st);
       if (e != hipSuccess) return e;
       // b A + c A A
       p.x = p.w = gram;
@@ -402,7 +531,7 @@ hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
       p.in_ld = L.m;
       p.in_batch = L.sq;
       p.hi_out = poly;
-      e = symmetric<false, kNsPoly>(p, count, st);
+      e = symmetric<false, kNsPoly>(p, symmetric_cut(L.m, L.m, count, false), count, st);
       if (e != hipSuccess) return e;
       // a X + (b A + c A A) X; tall: a X + X (b A + c A A)
       p.x = tall ? x : poly;

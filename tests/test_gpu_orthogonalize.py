@@ -92,13 +92,16 @@ def test_singular_values_end_near_one():
 
 @pytest.mark.parametrize("R,C", [(40, 100), (1000, 72), (513, 513)])
 def test_stack(R, C):
-    """A stack is its matrices one by one, whatever their sizes (the products add in the same order)."""
+    """A stack is its matrices one by one, and a matrix's bits do not depend on the others'."""
     G = gradient(5, R, C, "strong", B=5) * torch.tensor([1.0, 1e-4, 1e5, 3.0, 1.0], device=DEV).view(5, 1, 1)
     got = mx.orthogonalize(G.view(5, 1, R, C))
     assert got.shape == (5, 1, R, C) and got.dtype == torch.bfloat16
     for i in range(5):
         hold(got[i, 0], G[i])
-        assert torch.equal(got[i, 0], mx.orthogonalize(G[i]))
+        hold(mx.orthogonalize(G[i]), G[i])
+        others = gradient(50 + i, R, C, B=5)
+        others[i] = G[i]
+        assert torch.equal(mx.orthogonalize(others)[i], got[i, 0])
 
 
 def test_stack_in_parts():
