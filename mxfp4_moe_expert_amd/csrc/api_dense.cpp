@@ -115,7 +115,21 @@ bool w8a8_ok(int T, int K, int N) {
   return T >= 0 && T <= kMaxRows && K >= kI8Step && K % kI8Step == 0 && K <= kMaxLinear && N >= 1 && N <= kMaxLinear;
 }
 
+// Whether an int8 product is streamed (few_i8.hip) rather than cut into tiles: its weights, and the codes that every
+// block of 16 weight rows reads, against the tile products' estimate (both without the encoding). 4096 x 4096 9.0 us at
+// 33 rows and 10.8 at 49 against 9.5 and 10.7; 8192 -> 4096 10.5 at 16 and 11.4 at 17 against 11.0 and 11.2; 2048 x 2048
+// 6.8 at 64 against 8.0; 1024 -> 8192 5.6 at 32 and 6.0 at 33 against 5.9 and 5.8.
+bool w8a8_few(int T, int K, int N) {
+  if (T <= 8 && T * K <= 131072) return true;  // without the estimates' microsecond on the host where calls are shortest
+  if (T > kFewI8Rows) return false;
+  const double few_us = 3.0 + (double)N * K / 6.2e6 + 2.5e-5 * T * K * ((N + 4095) / 4096);
+  double tile_us;
+  dense_plan(kDenseI8, kDenseNT, T, N, K, &tile_us);
+  return few_us < tile_us;
+}
+
 struct W8a8Layout {
+  bool few;  // streamed
   DensePlan plan;
   size_t codes, scales, part, total;  // codes, scales: of activations that come as bf16
 };
@@ -129,13 +143,14 @@ W8a8Layout w8a8_layout(int T, int K, int N, bool encoded) {
     o = align256(o + bytes);
     return p;
   };
+  L.few = w8a8_few(T, K, N);
   if (T > 0) {
-    L.plan = dense_plan(kDenseI8, kDenseNT, T, N, K);
-    if (!encoded) {
+    if (!L.few) L.plan = dense_plan(kDenseI8, kDenseNT, T, N, K);
+    if (!encoded && !(L.few && few_i8_encodes(T, K))) {
       L.codes = take((size_t)T * K);
       L.scales = take((size_t)T * 4);
     }
-    L.part = take(dense_part_bytes(L.plan, T, N));
+    if (!L.few) L.part = take(dense_part_bytes(L.plan, T, N));
   }
   L.total = o == 0 ? kNoWorkspace : o < 512 ? 512 : o;
   return L;
@@ -386,13 +401,29 @@ int moe_linear_w8a8(int32_t T, int32_t K, int32_t N, const uint16_t* x, const in
     if (rc) return rc;
   }
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (!encoded) {
+  FewI8Args few;
+  memset(&few, 0, sizeof(few));
+  if (!encoded && L.few && few_i8_encodes(T, K)) {
+    few.x = x;
+  } else if (!encoded) {
     int8_t* codes = at<int8_t>(workspace, L.codes);
     float* scales = at<float>(workspace, L.scales);
     const hipError_t e = launch_int8_quantize(T, K, kDtBf16, x, K, codes, scales, st);
     if (e != hipSuccess) return status(e);
     x_codes = codes;
     x_scales = scales;
+  }
+  if (L.few) {
+    few.T = T;
+    few.N = N;
+    few.K = K;
+    few.x_codes = x_codes;
+    few.x_scales = x_scales;
+    few.q = q;
+    few.scale = scale;
+    few.out = out;
+    few.out_is_fp32 = out_is_fp32 ? 1 : 0;
+    return status(launch_few_i8(few, st));
   }
   DenseArgs a = dense_args(x_codes, (size_t)K / 2, q, (size_t)K / 2, T, N, K, out, out_is_fp32,
                            at<float>(workspace, L.part));

@@ -1,0 +1,163 @@
+// Products of at most 64 rows of int8 activations with int8 weights that are
+// streamed once (moe_linear_w8a8).
+//
+// As in few_rows.hip a block owns 16 weight rows and its NW waves split K, wave
+// w taking k-steps w, w + NW, ... of 128 values: lane (r, g) reads 32 bytes of
+// row r, which are its operands of two MFMA 16x16x64 (the order of k is the same
+// on both sides). The waves' sums meet in LDS; they are whole numbers, so no
+// order of adding them changes a result.
+//   Activations that come as codes: a lane reads its tokens' codes as it reads
+//     the weights.
+//   Up to four tokens in bf16 (K short enough, see fits()): every block encodes
+//     them itself, while its first weights are under way, and keeps the codes in
+//     LDS. One token 4096 -> 1536 costs one launch then, not three.
+// Bound by the weight bytes; at one token by launch and load latency.
+#include <type_traits>
+
+#include "dense.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kStep = 128;       // k values per wave and step
+constexpr int kEncodeMax = 16384;  // values that a block encodes (rows rounded up to a power of two)
+constexpr int kEncodeRows = 4;
+
+// CT: blocks of 16 tokens. ENCODE: x is bf16, encoded here.
+template <bool ENCODE, int CT, int NW>
+__global__ __launch_bounds__(NW * 64) void k_few_i8(FewI8Args a) {
+  constexpr int U = CT == 1 ? 4 : CT == 2 ? 2 : 1;  // steps whose loads are in flight together
+  __shared__ __align__(16) int red[NW][CT * 256];
+  extern __shared__ __align__(16) unsigned char codes[];  // ENCODE: [T][K]
+  __shared__ float scale_of[ENCODE ? kEncodeRows : 1];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * 16;
+  const int S = (a.K + kStep - 1) / kStep, kl = g * 32;
+  const int8_t* wrow = a.q + (size_t)min(n0 + r, a.N - 1) * a.K + kl;  // past the end: the last row again, never stored
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
+
+  u32x4_t w[U][2], x[U][CT][2];
+  auto load_w = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int k = (s0 + u * NW) * kStep + kl + v * 16;  // K % 16 == 0: a piece exists whole or not at all
+        w[u][v] = k < a.K ? *reinterpret_cast<const u32x4_t*>(wrow + (size_t)(s0 + u * NW) * kStep + v * 16) : zero;
+      }
+  };
+  load_w(wave);
+
+  if constexpr (ENCODE) {
+    // the waves share the rows evenly: rp rows (a power of two), NW / rp waves on each
+    const int rp = a.T <= 1 ? 1 : a.T <= 2 ? 2 : 4, wpr = NW / rp;
+    const int row = wave / wpr, first = (wave % wpr) * 64 + lane, step = wpr * 64, P = a.K / 8;
+    constexpr int PER = kEncodeMax / 8 / (NW * 64);  // pieces per lane at most
+    static_assert(PER >= 1, "");
+    u32x4_t p[PER];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = first + i * step;
+      p[i] = row < a.T && at < P ? reinterpret_cast<const u32x4_t*>(a.x + (size_t)row * a.K)[at] : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max((p[i][j] << 16) & 0x7fff0000u, p[i][j] & 0x7fff0000u));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    if (lane == 0) red[wave][0] = (int)top;
+    __syncthreads();
+    for (int i = 0; i < wpr; ++i) top = max(top, (uint32_t)red[row * wpr + i][0]);
+    const RowScale s = row_scale(top);
+    if (row < a.T) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = first + i * step;
+        if (at >= P) continue;
+        uint2 c = make_uint2(0u, 0u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t lo = (uint32_t)int8_code(__uint_as_float(p[i][j] << 16), s) & 255u;
+          const uint32_t hi = (uint32_t)int8_code(__uint_as_float(p[i][j] & 0xffff0000u), s) & 255u;
+          (j < 2 ? c.x : c.y) |= (lo | hi << 8) << (16 * (j & 1));
+        }
+        *reinterpret_cast<uint2*>(codes + row * a.K + at * 8) = c;
+      }
+      if (first == 0) scale_of[row] = s.scale;
+    }
+    __syncthreads();
+  }
+
+  i32x4_t acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) acc[c] = (i32x4_t){0, 0, 0, 0};
+  for (int s0 = wave; s0 < S; s0 += NW * U) {
+    if (s0 != wave) load_w(s0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int t = min(16 * c + r, a.T - 1), k = (s0 + u * NW) * kStep + kl + v * 16;
+          if constexpr (ENCODE)
+            x[u][c][v] = k < a.K ? *reinterpret_cast<const u32x4_t*>(codes + t * a.K + k) : zero;
+          else
+            x[u][c][v] = k < a.K ? *reinterpret_cast<const u32x4_t*>(a.x_codes + (size_t)t * a.K + k) : zero;
+        }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[c] = mfma_i8(w[u][v], x[u][c][v], acc[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c) *reinterpret_cast<i32x4_t*>(&red[wave][(c * 64 + lane) * 4]) = acc[c];
+  __syncthreads();
+  // value j: row 4 (lane / 16) + j % 4, token 16 c + lane % 16, where (c, lane) = j / 4
+  for (int j = tid; j < CT * 256; j += NW * 64) {
+    const int l = (j >> 2) & 63, t = (j >> 8) * 16 + (l & 15), n = n0 + 4 * (l >> 4) + (j & 3);
+    if (t >= a.T || n >= a.N) continue;
+    int v = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v += red[i][j];
+    const float y = (float)v * (ENCODE ? scale_of[ENCODE ? t : 0] : a.x_scales[t]) * a.scale[n];
+    const size_t at = (size_t)t * a.N + n;
+    if (a.out_is_fp32) static_cast<float*>(a.out)[at] = y;
+    else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(y);
+  }
+}
+
+// Waves per block: enough that the blocks of 16 rows give each of the 256 CUs about 16 waves.
+template <bool ENCODE, int CT>
+hipError_t go(const FewI8Args& a, hipStream_t st) {
+  const int blocks = (a.N + 15) / 16;
+  const size_t lds = ENCODE ? (size_t)a.T * a.K : 0;
+  if (blocks <= 320) k_few_i8<ENCODE, CT, 16><<<blocks, 16 * 64, lds, st>>>(a);
+  else if (blocks <= 640) k_few_i8<ENCODE, CT, 8><<<blocks, 8 * 64, lds, st>>>(a);
+  else k_few_i8<ENCODE, CT, 4><<<blocks, 4 * 64, lds, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool few_i8_encodes(int T, int K) {
+  const int rows = T <= 1 ? 1 : T <= 2 ? 2 : 4;
+  return T <= kEncodeRows && rows * K <= kEncodeMax;
+}
+
+hipError_t launch_few_i8(const FewI8Args& a, hipStream_t st) {
+  if (a.T <= 0 || a.T > kFewI8Rows || a.N <= 0 || a.K <= 0 || a.K % 16) return hipErrorInvalidValue;
+  if (a.x) return few_i8_encodes(a.T, a.K) ? go<true, 1>(a, st) : hipErrorInvalidValue;
+  if (a.T <= 16) return go<false, 1>(a, st);
+  if (a.T <= 32) return go<false, 2>(a, st);
+  if (a.T <= 48) return go<false, 3>(a, st);
+  return go<false, 4>(a, st);
+}
+
+}  // namespace moe

@@ -11,9 +11,10 @@
 // remainder v - c s, exact in one fma (|v - c s| <= s and both are multiples of
 // the smaller one's last place), says on which side v lies.
 //
-// Memory-bound both ways: a row is read once, held in registers between its
-// maximum and its codes (up to 2048 16-byte pieces; longer rows are read twice,
-// the second time from the L2).
+// Memory-bound both ways: a row is read once and held in registers between its
+// maximum and its codes. Measured (a large copy: 5.1 TB/s): 16384 x 4096 fp32
+// 61 us to encode (5.5 TB/s, part of it from the last-level cache) and 61 to
+// decode, bf16 41 and 38; 33 x 8192 bf16 3.4 us.
 #include <type_traits>
 
 #include "device.h"
@@ -60,66 +61,70 @@ __device__ __forceinline__ void put_codes(int8_t* row, int piece, const uint2& c
   else *reinterpret_cast<uint2*>(row + 8 * piece) = c;
 }
 
-// WPR waves (of the block's four) per row, PER pieces per lane in registers (0: any number, read twice).
-template <int DT, int WPR, int PER>
-__global__ __launch_bounds__(256) void k_int8_quantize(long long rows, int K, const char* __restrict__ x,
+// TPR threads per row (8 to 64: a part of a wave; 256, 1024: whole waves), PER pieces per thread.
+template <int DT, int TPR, int PER>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_int8_quantize(long long rows, int K, const char* __restrict__ x,
                                                        long long ld_bytes, int8_t* __restrict__ codes,
                                                        float* __restrict__ scales) {
-  constexpr int TPR = WPR * 64;
+  constexpr int BLOCK = TPR > 256 ? TPR : 256, WPR = TPR / 64;
   const int lane = (int)threadIdx.x % TPR, sub = (int)threadIdx.x / TPR;
-  const long long row = (long long)blockIdx.x * (256 / TPR) + sub;
+  const long long row = (long long)blockIdx.x * (BLOCK / TPR) + sub;
   const bool live = row < rows;
   const int P = live ? K / kPer<DT> : 0;
   const u32x4_t* src = reinterpret_cast<const u32x4_t*>(x + (live ? row : 0) * ld_bytes);
-  u32x4_t v[PER ? PER : 1];
+  u32x4_t v[PER];
   uint32_t top = 0;
-  if constexpr (PER > 0) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = lane + i * TPR < P ? src[lane + i * TPR] : (u32x4_t){0u, 0u, 0u, 0u};
+  for (int i = 0; i < PER; ++i) v[i] = lane + i * TPR < P ? src[lane + i * TPR] : (u32x4_t){0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < PER; ++i) top = piece_top<DT>(v[i], top);
-  } else {
-    for (int i = lane; i < P; i += TPR) top = piece_top<DT>(src[i], top);
-  }
+  for (int i = 0; i < PER; ++i) top = piece_top<DT>(v[i], top);
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  for (int o = (TPR < 64 ? TPR : 64) / 2; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
   if constexpr (WPR > 1) {
-    __shared__ uint32_t tops[4];
+    __shared__ uint32_t tops[WPR];
     if (threadIdx.x % 64 == 0) tops[threadIdx.x / 64] = top;
     __syncthreads();
-    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) top = max(top, tops[i]);
   }
   if (!live) return;
   const RowScale s = row_scale(top);
   int8_t* out = codes + row * K;
-  if constexpr (PER > 0) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + i * TPR < P) put_codes<DT>(out, lane + i * TPR, piece_codes<DT>(v[i], s));
-  } else {
-    for (int i = lane; i < P; i += TPR) put_codes<DT>(out, i, piece_codes<DT>(src[i], s));
-  }
+  for (int i = 0; i < PER; ++i)
+    if (lane + i * TPR < P) put_codes<DT>(out, lane + i * TPR, piece_codes<DT>(v[i], s));
   if (lane == 0) scales[row] = s.scale;
 }
 
 template <int DT>
 hipError_t quantize(long long rows, int K, const char* x, long long ld, int8_t* codes, float* scales, hipStream_t st) {
   const int P = K / kPer<DT>;
-  auto go = [&](auto wpr, auto per) {
-    const long long nb = (rows + 4 / wpr - 1) / (4 / wpr);
-    k_int8_quantize<DT, wpr, per><<<(unsigned)nb, 256, 0, st>>>(rows, K, x, ld, codes, scales);
+  auto go = [&](auto tpr, auto per) {
+    constexpr int threads = tpr > 256 ? tpr : 256, rpb = threads / tpr;
+    k_int8_quantize<DT, tpr, per><<<(unsigned)((rows + rpb - 1) / rpb), threads, 0, st>>>(rows, K, x, ld, codes, scales);
     return hipGetLastError();
   };
-  using W1 = std::integral_constant<int, 1>;
-  using W4 = std::integral_constant<int, 4>;
-  // a wave per row while its lanes hold two pieces at most, then a block per row
-  if (P <= 64) return go(W1{}, std::integral_constant<int, 1>{});
-  if (P <= 128) return go(W1{}, std::integral_constant<int, 2>{});
-  if (P <= 256) return go(W4{}, std::integral_constant<int, 1>{});
-  if (P <= 512) return go(W4{}, std::integral_constant<int, 2>{});
-  if (P <= 1024) return go(W4{}, std::integral_constant<int, 4>{});
-  if (P <= 2048) return go(W4{}, std::integral_constant<int, 8>{});
-  return go(W4{}, std::integral_constant<int, 0>{});
+#define ROW(tpr, per) go(std::integral_constant<int, tpr>{}, std::integral_constant<int, per>{})
+  // Few rows: latency counts, and a row's pieces are spread over 1024 threads (33 x 8192 bf16 5.3 -> 3.4 us); rows past
+  // 2048 pieces take as many anyway.
+  if ((rows <= 512 && P > 256) || P > 2048) {
+    if (P <= 1024) return ROW(1024, 1);
+    if (P <= 2048) return ROW(1024, 2);
+    if (P <= 4096) return ROW(1024, 4);
+    if (P <= 8192) return ROW(1024, 8);
+    return ROW(1024, 16);  // fp32, K up to 65536
+  }
+  // as many lanes as a short row has pieces, a wave while they hold two each, then a block per row
+  if (P <= 8) return ROW(8, 1);
+  if (P <= 16) return ROW(16, 1);
+  if (P <= 32) return ROW(32, 1);
+  if (P <= 64) return ROW(64, 1);
+  if (P <= 128) return ROW(64, 2);
+  if (P <= 256) return ROW(256, 1);
+  if (P <= 512) return ROW(256, 2);
+  if (P <= 1024) return ROW(256, 4);
+  return ROW(256, 8);
+#undef ROW
 }
 
 // A thread takes pieces of 16 output bytes. Rows of fewer than 256 pieces share a block (RPB rows), longer ones are cut

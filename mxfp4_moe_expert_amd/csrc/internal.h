@@ -459,6 +459,21 @@ hipError_t launch_int8_quantize(long long rows, int K, int dtype, const void* x,
 hipError_t launch_int8_dequantize(long long rows, int K, const int8_t* codes, const float* scales, int dtype, void* out,
                                   hipStream_t st);
 
+// The streaming pass of int8 products (few_i8.hip)
+constexpr int kFewI8Rows = 64;  // rows it takes
+struct FewI8Args {
+  int T, N, K;
+  const uint16_t* x;       // [T][K] bf16 where the pass encodes it (few_i8_encodes), else null
+  const int8_t* x_codes;   // [T][K], x_scales [T]
+  const float* x_scales;
+  const int8_t* q;         // [N][K], scale [N]
+  const float* scale;
+  void* out;               // [T][N]
+  int out_is_fp32;
+};
+bool few_i8_encodes(int T, int K);
+hipError_t launch_few_i8(const FewI8Args& a, hipStream_t st);
+
 // The streaming pass (few_rows.hip): K split over the waves of a block
 constexpr int kFewRows = 32;  // rows it takes
 struct FewRowsArgs {
