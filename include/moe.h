@@ -298,7 +298,9 @@ int moe_linear_w8a16(int32_t T, int32_t K, int32_t N, int32_t groups, const uint
  * all of whose logits are has no shares. NaN logits give a NaN loss. Sums are
  * fp32 in an order that does not depend on timing.
  *   workspace: moe_balance_workspace_size(T, E, S) bytes, 256-byte aligned, any
- *   contents; calls sharing one must be ordered on one stream. Two launches.
+ *   contents; calls sharing one must be ordered on one stream. A size of 256
+ *   means that none is used (small batches: one launch; else two): workspace may
+ *   then be NULL.
  * Supported: 1 <= E <= 256, 1 <= k <= 8, 0 <= T <= 65536, 1 <= S <= 65536. */
 size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S);
 int moe_balance_loss(int32_t T, int32_t E, int32_t k, int32_t S, const float* logits, const int32_t* topk_ids,
@@ -491,7 +493,9 @@ int moe_gated_ffn_backward(int32_t T, int32_t H, int32_t I, float limit, const u
  * NaN and leaves the others as they are. A matrix's bits do not depend on which
  * others stand beside it as long as B is the same.
  *   workspace: moe_orthogonalize_workspace_size(B, R, C) bytes, 256-byte
- *   aligned, any contents; calls sharing one must be ordered on one stream.
+ *   aligned, any contents; calls sharing one must be ordered on one stream. A
+ *   size of 256 means that none is used (small matrices: one launch): workspace
+ *   may then be NULL.
  * Supported: 1 <= R, C <= 16384, 0 <= B <= 65535, 1 <= steps <= 64. */
 size_t moe_orthogonalize_workspace_size(int32_t B, int32_t R, int32_t C);
 int moe_orthogonalize(int32_t B, int32_t R, int32_t C, int32_t dtype, const void* g, int32_t steps, float a, float b,

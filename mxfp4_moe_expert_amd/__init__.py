@@ -875,15 +875,18 @@ def gated_ffn_backward(dy, x, w13, w2, saved, limit=10.0, need=(True, True, True
 def _routed(logits, topk_ids, seq_offsets):
     """T, E, k, S, the device index and the pointers of a routed batch."""
     T, E, index = _matrix(logits, torch.float32, "logits")
-    _, k, _ = _matrix(topk_ids, torch.int32, "topk_ids")
+    if not logits.is_contiguous():
+        _need(logits, torch.float32, (T, E), "logits")
+    rows, k, at = _matrix(topk_ids, torch.int32, "topk_ids")
+    if rows != T or at != index or not topk_ids.is_contiguous():
+        _arg(topk_ids, torch.int32, (T, k), index, "topk_ids")
     S, po = 1, None
     if seq_offsets is not None:
         if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
             raise ValueError("seq_offsets: int32 tensor of the sequences' borders [S + 1], S >= 1, expected")
         S = seq_offsets.shape[0] - 1
         po = _arg(seq_offsets, torch.int32, (S + 1,), index, "seq_offsets")
-    return (T, E, k, S, index, _arg(logits, torch.float32, (T, E), index, "logits"),
-            _arg(topk_ids, torch.int32, (T, k), index, "topk_ids"), po)
+    return T, E, k, S, index, logits.data_ptr(), topk_ids.data_ptr(), po
 
 
 def balance_loss(logits, topk_ids, seq_offsets=None, alpha=1e-4, ws=None):
@@ -895,11 +898,20 @@ def balance_loss(logits, topk_ids, seq_offsets=None, alpha=1e-4, ws=None):
     T, E, k, S, index, pl, pi, po = _routed(logits, topk_ids, seq_offsets)
     loss = logits.new_empty(())
     counts = topk_ids.new_empty((E,))
-    coef = logits.new_empty((S * E + 1,))
-    pw, nw, ws = _scratch(lib().moe_balance_workspace_size(T, E, S), logits, ws, "moe_balance_loss")
+    need = lib().moe_balance_workspace_size(T, E, S)
+    n = S * E + 1
+    pw, nw = None, 0
+    if ws is None and 256 < need <= 1 << 20:  # behind the coefficients, in one allocation
+        first = (n + 63) // 64 * 64
+        coef = logits.new_empty((first + need // 4,))
+        pw, nw = coef.data_ptr() + 4 * first, need
+    else:
+        coef = logits.new_empty((n,))
+        if need != 256 or ws is not None:
+            pw, nw, ws = _scratch(need, logits, ws, "moe_balance_loss")
     _call(index, "moe_balance_loss", T, E, k, S, pl, pi, po, alpha, loss.data_ptr(), counts.data_ptr(),
           coef.data_ptr(), pw, nw)
-    return loss, counts, (coef, seq_offsets)
+    return loss, counts, (coef, seq_offsets, n)
 
 
 def route_backward(logits, topk_ids, dw=None, saved=None, scale=1.5, dloss=None, out=None):
@@ -909,11 +921,15 @@ def route_backward(logits, topk_ids, dw=None, saved=None, scale=1.5, dloss=None,
     ``balance_loss``; dloss: its gradient, a one-element fp32 tensor, None for
     1), or from both. The gradients of gate_w and x follow as dlogits^T x and
     dlogits gate_w."""
-    coef, seq_offsets = saved if saved is not None else (None, None)
+    coef, seq_offsets, n = saved if saved is not None else (None, None, 0)
     T, E, k, S, index, pl, pi, po = _routed(logits, topk_ids, seq_offsets)
     if coef is None and dw is None:
         raise ValueError("route_backward: neither dw nor saved given")
-    pc = None if coef is None else _arg(coef, torch.float32, (S * E + 1,), index, "coef")
+    pc = None
+    if coef is not None:
+        if n != S * E + 1 or coef.numel() < n:
+            raise ValueError("saved: not that of these logits and offsets")
+        pc = _arg(coef, torch.float32, coef.shape, index, "coef")
     pd = None
     if dloss is not None:
         if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
@@ -949,6 +965,9 @@ def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     for n in shape[:-2]:
         B *= n
     out = _result(out, shape, torch.bfloat16, g)
-    pw, nw, ws = _scratch(lib().moe_orthogonalize_workspace_size(B, R, C), g, ws, "moe_orthogonalize")
+    need = lib().moe_orthogonalize_workspace_size(B, R, C)
+    pw, nw = None, 0
+    if need != 256 or ws is not None:
+        pw, nw, ws = _scratch(need, g, ws, "moe_orthogonalize")
     _call(index, "moe_orthogonalize", B, R, C, dt, pg, steps, a, b, c, eps, out.data_ptr(), pw, nw)
     return out

@@ -16,6 +16,7 @@ using namespace moe;
 
 constexpr int kMaxRows = 65536;  // T and S
 constexpr int kMaxExperts = 256;
+constexpr size_t kNoWorkspace = 256;  // the stated size where none is used (0 stands for unsupported)
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
@@ -52,7 +53,7 @@ BalanceLayout balance_layout(int T, int E, int S) {
   L.sum = 256;
   L.count = L.sum + rows;
   L.loss = L.count + rows;
-  L.total = L.loss + align256((size_t)S * 4);
+  L.total = balance_one(T, E, S) ? kNoWorkspace : L.loss + align256((size_t)S * 4);
   return L;
 }
 
@@ -75,7 +76,7 @@ int moe_balance_loss(int32_t T, int32_t E, int32_t k, int32_t S, const float* lo
       !aligned4(coef))
     return MOE_EINVAL;
   const BalanceLayout L = balance_layout(T, E, S);
-  const int rc = check_ws(workspace, workspace_bytes, L.total);
+  const int rc = L.total == kNoWorkspace ? MOE_OK : check_ws(workspace, workspace_bytes, L.total);
   if (rc) return rc;
   BalanceArgs a;
   memset(&a, 0, sizeof(a));
@@ -142,7 +143,8 @@ int moe_orthogonalize(int32_t B, int32_t R, int32_t C, int32_t dtype, const void
   // one matrix of a stack of odd sizes starts at any element
   const uintptr_t element = dtype == MOE_DTYPE_F32 ? 4 : 2;
   if (!g || !out || reinterpret_cast<uintptr_t>(g) % element || !aligned16(out)) return MOE_EINVAL;
-  const int rc = check_ws(workspace, workspace_bytes, newton_workspace(B, R, C));
+  const size_t need = newton_workspace(B, R, C);
+  const int rc = need == kNewtonNoWorkspace ? MOE_OK : check_ws(workspace, workspace_bytes, need);
   if (rc) return rc;
   NewtonArgs n;
   n.B = B;

@@ -17,8 +17,8 @@
 // shares of its tokens in registers (a group of G lanes per token, four experts
 // per lane), then over the block in LDS, and writes one partial row per (run,
 // sequence). A second launch adds each sequence's partial rows in order and the
-// losses of the sequences in order: results do not depend on timing. Backward:
-// one pass over the logits.
+// losses of the sequences in order: results do not depend on timing. Of small
+// batches one block does both. Backward: one pass over the logits.
 #include <type_traits>
 
 #include "device.h"
@@ -29,7 +29,7 @@ namespace moe {
 namespace {
 
 constexpr int kBalWaves = 16, kBalThreads = kBalWaves * 64;
-constexpr int kBalRuns = 256;    // runs of tokens at most: one block per CU
+constexpr int kBalRuns = 512;    // runs of tokens at most: two blocks per CU
 constexpr int kBalRunMin = 32;
 
 // h = exp(-|z| / 2), one hardware exponential. Above, e = h h = exp(-|z|): softplus(z) = max(z, 0) + log1p(e), with
@@ -53,12 +53,29 @@ __device__ __forceinline__ float score_slope(float z, const Score& v) {
   return z < -17.0f ? 0.5f * v.h : 0.5f * sig * __builtin_amdgcn_rsqf(v.sp);
 }
 
+// The sum over each group of G lanes, in every lane of it (lane exchanges inside the vector unit, no LDS).
+template <int CTRL>
+__device__ __forceinline__ float plus_lane(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  v = plus_lane<0xB1>(v);                              // quad_perm [1,0,3,2]
+  v = plus_lane<0x4E>(v);                              // quad_perm [2,3,0,1]
+  v = plus_lane<0x141>(v);                             // row_half_mirror
+  if constexpr (G > 8) v = plus_lane<0x140>(v);        // row_mirror
+  if constexpr (G > 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if constexpr (G > 32) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
   return v;
 }
+// 1 / v, 0 for 0 (a row whose scores are all 0 has no shares).
+__device__ __forceinline__ float inverse(float v) { return v != 0.0f ? __builtin_amdgcn_rcpf(v) : 0.0f; }
 
 // A token's four logits of lane l of its group; experts past E as -inf (score 0).
 template <bool VEC>
@@ -80,75 +97,30 @@ __device__ __forceinline__ f32x4_t four_logits(const float* row, int l, int E) {
 __device__ __forceinline__ int offset_of(const BalanceArgs& a, int q) {
   return a.offsets ? min(max(a.offsets[q], 0), a.T) : q > 0 ? a.T : 0;
 }
-// The last sequence that starts at or before t (-1: none).
+// The last sequence that starts at or before t (0 if none does), t the same in all lanes: a wave looks at 64 borders at a
+// time; of very many it searches by halves.
 __device__ __forceinline__ int sequence_of(const BalanceArgs& a, int t) {
+  if (!a.offsets) return 0;
+  if (a.S <= 1024) {
+    int n = 0;
+    for (int i = 0; i < a.S; i += 64) {
+      const int q = i + (int)(threadIdx.x & 63);
+      n += __builtin_popcountll(__ballot(q < a.S && offset_of(a, q) <= t));
+    }
+    return max(n - 1, 0);
+  }
   int lo = 0, hi = a.S;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (offset_of(a, mid) <= t) lo = mid + 1;
     else hi = mid;
   }
-  return lo - 1;
-}
-
-template <int G, bool VEC>
-__global__ __launch_bounds__(kBalThreads) void k_balance_runs(BalanceArgs a) {
-  constexpr int TPW = 64 / G, NG = kBalWaves * TPW;  // tokens per wave and block at a time
-  __shared__ __align__(16) float red[kBalWaves][256];
-  __shared__ int hist[256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (G - 1);
-  const int group = wave * TPW + lane / G;
-  if (blockIdx.x == 0) {  // for the next launch
-    if (tid < a.E) a.counts[tid] = 0;
-    if (tid == 0) *a.ticket = 0;
-  }
-  const int t0 = blockIdx.x * a.run, t1 = min(t0 + a.run, a.T);
-  int q = max(sequence_of(a, t0), 0);
-  for (int t = t0; t < t1 && q < a.S; ++q) {
-    const int first = max(t, offset_of(a, q)), end = min(t1, offset_of(a, q + 1));
-    if (first >= end) continue;
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-    constexpr int U = 4;  // tokens whose logits are in flight together
-    for (int b = first + group; b < end; b += U * NG) {
-      f32x4_t z[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) z[u] = four_logits<VEC>(a.logits + (size_t)min(b + u * NG, end - 1) * a.E, l, a.E);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        f32x4_t s;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = score_of(z[u][i]).s;
-        const float total = group_sum<G>((s[0] + s[1]) + (s[2] + s[3]));
-        // a row whose scores are all 0 has no shares
-        const float inv = b + u * NG < end && total != 0.0f ? 1.0f / total : 0.0f;
-        if (b + u * NG < end) sum += s * inv;
-      }
-    }
-    *reinterpret_cast<f32x4_t*>(&red[wave][lane * 4]) = sum;
-    for (int i = first * a.k + tid; i < end * a.k; i += kBalThreads) {
-      const int e = a.ids[i];
-      if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
-      else if (a.flags) atomicOr(a.flags, kFlagExpertId);
-    }
-    __syncthreads();
-    if (tid < a.E) {
-      float v = 0.0f;
-#pragma unroll 8
-      for (int w = 0; w < NG; ++w) v += red[w / TPW][(w % TPW) * (4 * G) + tid];
-      const size_t at = (size_t)(blockIdx.x + q) * a.E + tid;
-      a.part_sum[at] = v;
-      a.part_count[at] = hist[tid];
-    }
-    __syncthreads();
-    t = end;
-  }
+  return max(lo - 1, 0);
 }
 
 // Sum over the block in a fixed order; every thread has the result.
 __device__ __forceinline__ float block_sum(float v, float* lds) {
-  v = wave_sum(v);
+  v = group_sum<64>(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -156,6 +128,128 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
 #pragma unroll
   for (int w = 0; w < kBalWaves; ++w) s += lds[w];
   return s;
+}
+
+// A sequence's loss (thread e < E: the sum of its shares of expert e and its slots on it; the result in every thread) and
+// its coefficients.
+__device__ __forceinline__ float sequence_loss(const BalanceArgs& a, int q, int e, int n, float sum, int count, float* lds) {
+  float loss = 0.0f;
+  if (e < a.E) {
+    const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+    const float f = (float)count * ((float)a.E / (float)a.k) * inv;
+    loss = f * (sum * inv);
+    a.coef[(size_t)q * a.E + e] = a.alpha * f * inv;
+  }
+  return block_sum(loss, lds);
+}
+// Whether a sequence's borders are what they have to be (flagged if not).
+__device__ __forceinline__ bool bad_borders(const BalanceArgs& a, int q) {
+  if (!a.offsets) return false;
+  const int lo = a.offsets[q], hi = a.offsets[q + 1];
+  const bool bad = lo < 0 || hi < lo || hi > a.T;
+  if (bad && threadIdx.x == 0 && a.flags) atomicOr(a.flags, kFlagSequence);
+  return bad;
+}
+
+// ONE: a single block with all tokens does the whole of the forward pass.
+template <int G, bool VEC, bool ONE>
+__global__ __launch_bounds__(kBalThreads) void k_balance_runs(BalanceArgs a) {
+  constexpr int TPW = 64 / G, NG = kBalWaves * TPW;  // tokens per wave and block at a time
+  constexpr int U = 4;                               // a group's tokens whose logits are in flight together
+  constexpr int SLOTS = 2;                           // ids a thread holds: of the first 2048 slots of the run
+  __shared__ __align__(16) float red[kBalWaves][256];
+  __shared__ int hist[256];
+  __shared__ float lds[kBalWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (G - 1);
+  const int group = wave * TPW + lane / G;
+  const int t0 = blockIdx.x * a.run, t1 = min(t0 + a.run, a.T);
+  // the run's first logits and its ids are requested before its sequences are looked up
+  f32x4_t z[U];
+  auto load = [&](int b, int end) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) z[u] = four_logits<VEC>(a.logits + (size_t)min(b + u * NG, end - 1) * a.E, l, a.E);
+  };
+  if (t0 < t1) load(t0 + group, t1);
+  int held[SLOTS];
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    const int at = t0 * a.k + i * kBalThreads + tid;
+    held[i] = at < t1 * a.k ? a.ids[at] : 0;
+  }
+  if (!ONE && blockIdx.x == 0) {  // for the next launch
+    if (tid < a.E) a.counts[tid] = 0;
+    if (tid == 0) *a.ticket = 0;
+  }
+  int q = ONE ? 0 : sequence_of(a, t0);
+  int counted = 0;                 // ONE: of expert tid
+  float total = 0.0f, live = 0.0f;
+  int loaded = t0 + group;         // z holds the logits of this token on
+  for (int t = t0; (ONE || t < t1) && q < a.S; ++q) {
+    const int from = offset_of(a, q), to = offset_of(a, q + 1);
+    const int first = max(t, from), end = min(t1, to);
+    const bool some = first < end;
+    if (!ONE && !some) continue;
+    float v = 0.0f;
+    int count = 0;
+    if (some) {
+      if (tid < 256) hist[tid] = 0;
+      f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+      for (int b = first + group; b < end; b += U * NG) {
+        if (b != loaded) load(b, end);
+        loaded = -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          f32x4_t s;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] = score_of(z[u][i]).s;
+          const float inv = inverse(group_sum<G>((s[0] + s[1]) + (s[2] + s[3])));
+          if (b + u * NG < end) sum += s * inv;
+        }
+      }
+      *reinterpret_cast<f32x4_t*>(&red[wave][lane * 4]) = sum;
+      __syncthreads();
+      auto slot = [&](int e) {
+        if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
+        else if (a.flags) atomicOr(a.flags, kFlagExpertId);
+      };
+      const int lo = first * a.k, hi = end * a.k;
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) {
+        const int at = t0 * a.k + i * kBalThreads + tid;
+        if (at >= lo && at < hi) slot(held[i]);
+      }
+      for (int at = max(lo, t0 * a.k + SLOTS * kBalThreads) + tid; at < hi; at += kBalThreads) slot(a.ids[at]);
+      if (tid < a.E) {
+#pragma unroll 16
+        for (int w = 0; w < NG; ++w) v += red[w / TPW][(w % TPW) * (4 * G) + tid];
+      }
+      __syncthreads();
+      if (tid < a.E) count = hist[tid];
+      t = end;
+    }
+    if constexpr (ONE) {
+      const bool bad = bad_borders(a, q);
+      const float one = sequence_loss(a, q, tid, to - from, v, count, lds);
+      total += bad ? __uint_as_float(0x7fc00000u) : one;
+      live += some ? 1.0f : 0.0f;
+      counted += count;
+    } else {
+      if (tid < a.E) {
+        const size_t at = (size_t)(blockIdx.x + q) * a.E + tid;
+        a.part_sum[at] = v;
+        a.part_count[at] = count;
+      }
+    }
+    __syncthreads();
+  }
+  if constexpr (ONE) {
+    live = fmaxf(live, 1.0f);
+    if (tid < a.E) a.counts[tid] = counted;
+    if (tid == 0) {
+      *a.loss = a.alpha * total / live;
+      a.coef[(size_t)a.S * a.E] = 1.0f / live;
+    }
+  }
 }
 
 // Block q: sequence q's partial rows -> its loss, its coefficients (alpha f / n; 1 / Q follows them) and its counts; the
@@ -166,12 +260,7 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fold(BalanceArgs a) {
   __shared__ int pcount[SUB][256], last;
   const int tid = threadIdx.x, e = tid & 255, sub = tid >> 8, q = blockIdx.x;
   const int b = offset_of(a, q), end = offset_of(a, q + 1), n = end - b;
-  bool bad = false;
-  if (a.offsets) {
-    const int lo = a.offsets[q], hi = a.offsets[q + 1];
-    bad = lo < 0 || hi < lo || hi > a.T;
-    if (bad && tid == 0 && a.flags) atomicOr(a.flags, kFlagSequence);
-  }
+  const bool bad = bad_borders(a, q);
   float sum = 0.0f;
   int count = 0;
   if (n > 0 && e < a.E) {
@@ -199,20 +288,15 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fold(BalanceArgs a) {
   psum[sub][e] = sum;
   pcount[sub][e] = count;
   __syncthreads();
-  float loss = 0.0f;
-  if (sub == 0 && e < a.E) {
+  if (sub == 0) {
 #pragma unroll
     for (int i = 1; i < SUB; ++i) {
       sum += psum[i][e];
       count += pcount[i][e];
     }
-    const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-    const float f = (float)count * ((float)a.E / (float)a.k) * inv;
-    loss = f * (sum * inv);
-    a.coef[(size_t)q * a.E + e] = a.alpha * f * inv;
     if (count) atomicAdd(&a.counts[e], count);
   }
-  loss = block_sum(loss, lds);
+  float loss = sequence_loss(a, q, tid, n, sum, count, lds);
   if (bad) loss = __uint_as_float(0x7fc00000u);
   if (tid == 0) {
     __hip_atomic_store(&a.seq_loss[q], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -241,13 +325,29 @@ constexpr int kGradWaves = 4;
 template <int G, bool VEC, bool DW>
 __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs a, int per_group) {
   constexpr int TPW = 64 / G;
+  constexpr int U = 2;  // tokens at a time; the next ones' logits are in flight meanwhile
   const int lane = threadIdx.x & 63, l = lane & (G - 1);
-  const long long group = ((long long)blockIdx.x * kGradWaves + (threadIdx.x >> 6)) * TPW + lane / G;
+  const long long wave = (long long)blockIdx.x * kGradWaves + (threadIdx.x >> 6), group = wave * TPW + lane / G;
   const int t0 = (int)min(group * per_group, (long long)a.T), t1 = min(t0 + per_group, a.T);
+  f32x4_t zn[U];
+  int idn[U];
+  float dwn[U];
+  auto load = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = min(t0 + b + u, a.T - 1);
+      zn[u] = four_logits<VEC>(a.logits + (size_t)t * a.E, l, a.E);
+      if constexpr (DW) {
+        idn[u] = l < a.k ? a.ids[(size_t)t * a.k + l] : -1;
+        dwn[u] = l < a.k ? a.dw[(size_t)t * a.k + l] : 0.0f;
+      }
+    }
+  };
+  load(0);
   const float lead = a.coef ? a.coef[(size_t)a.S * a.E] * (a.dloss ? *a.dloss : 1.0f) : 0.0f;
-  int q = t0 < t1 ? sequence_of(a, t0) : a.S, begin = 0, end = 0;  // tokens [begin, end) are sequence q's
-  if (q < 0) q = 0;
-  f32x4_t g = {0.f, 0.f, 0.f, 0.f};
+  // tokens [begin, end) are sequence q's, with coefficients g
+  int q = sequence_of(a, (int)min(wave * TPW * per_group, (long long)a.T)), begin, end;
+  f32x4_t g;
   auto enter = [&]() {
     begin = offset_of(a, q);
     end = offset_of(a, q + 1);
@@ -255,8 +355,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs 
     for (int i = 0; i < 4; ++i)
       g[i] = a.coef && 4 * l + i < a.E ? a.coef[(size_t)q * a.E + 4 * l + i] * lead : 0.0f;
   };
-  if (q < a.S) enter();
-  constexpr int U = 2;  // tokens whose logits are in flight together
+  enter();
   // every group makes the same number of steps: the lanes of a wave exchange values
   for (int b = 0; b < per_group; b += U) {
     f32x4_t z[U];
@@ -264,17 +363,17 @@ __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs 
     float dw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = min(t0 + b + u, a.T - 1);
-      z[u] = four_logits<VEC>(a.logits + (size_t)t * a.E, l, a.E);
+      z[u] = zn[u];
       if constexpr (DW) {
-        id[u] = l < a.k ? a.ids[(size_t)t * a.k + l] : -1;
-        dw[u] = l < a.k ? a.dw[(size_t)t * a.k + l] : 0.0f;
+        id[u] = idn[u];
+        dw[u] = dwn[u];
         if ((unsigned)id[u] >= (unsigned)a.E) {
           if (l < a.k && a.flags) atomicOr(a.flags, kFlagExpertId);
           id[u] = -1;
         }
       }
     }
+    if (b + U < per_group) load(b + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = t0 + b + u;
@@ -287,9 +386,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs 
       f32x4_t ds;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = score_of(z[u][i]);
-      const float total = group_sum<G>((v[0].s + v[1].s) + (v[2].s + v[3].s));
+      const float inv = inverse(group_sum<G>((v[0].s + v[1].s) + (v[2].s + v[3].s)));
       const float dot = group_sum<G>((g[0] * v[0].s + g[1] * v[1].s) + (g[2] * v[2].s + g[3] * v[3].s));
-      const float inv = total != 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) ds[i] = (g[i] - dot * inv) * inv;
       if constexpr (DW) {
@@ -298,8 +396,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs 
         const float a0 = __shfl(v[0].s, from), a1 = __shfl(v[1].s, from), a2 = __shfl(v[2].s, from),
                     a3 = __shfl(v[3].s, from);
         const float sj = id[u] < 0 ? 0.0f : c == 0 ? a0 : c == 1 ? a1 : c == 2 ? a2 : a3;
-        const float norm = group_sum<8>(sj), wdot = group_sum<8>(id[u] < 0 ? 0.0f : dw[u] * sj);
-        const float ninv = norm != 0.0f ? 1.0f / norm : 0.0f;
+        const float ninv = inverse(group_sum<8>(sj)), wdot = group_sum<8>(id[u] < 0 ? 0.0f : dw[u] * sj);
         const float dsj = a.scale * ninv * (dw[u] - wdot * ninv);
         for (int j = 0; j < a.k; ++j) {  // in slot order
           const int at = (lane & ~(G - 1)) + j, ej = __shfl(id[u], at);
@@ -349,15 +446,28 @@ int balance_rows(int T, int S) {
   return (T > 0 ? (T + run - 1) / run : 1) + S;
 }
 
+// Whether one block does the whole forward pass, in at most four steps of 64 tokens (of 256 experts; more of fewer): one
+// launch for two.
+bool balance_one(int T, int E, int S) {
+  const int lanes = E > 128 ? 64 : E > 64 ? 32 : E > 32 ? 16 : 8;
+  return (long long)T * lanes <= 16384 && S <= 8;
+}
+
 hipError_t launch_balance(BalanceArgs a, hipStream_t st) {
   if (!balance_args_ok(a)) return hipErrorInvalidValue;
-  a.run = balance_run(a.T);
-  const unsigned runs = (unsigned)(balance_rows(a.T, a.S) - a.S);
+  const bool one = balance_one(a.T, a.E, a.S);
+  a.run = one ? a.T : balance_run(a.T);
+  const unsigned runs = one ? 1u : (unsigned)(balance_rows(a.T, a.S) - a.S);
   const hipError_t e = by_group(a.E, [&](auto g) {
-    if (a.E % 4 == 0) k_balance_runs<g, true><<<runs, kBalThreads, 0, st>>>(a);
-    else k_balance_runs<g, false><<<runs, kBalThreads, 0, st>>>(a);
+    if (a.E % 4 == 0) {
+      if (one) k_balance_runs<g, true, true><<<1, kBalThreads, 0, st>>>(a);
+      else k_balance_runs<g, true, false><<<runs, kBalThreads, 0, st>>>(a);
+    } else {
+      if (one) k_balance_runs<g, false, true><<<1, kBalThreads, 0, st>>>(a);
+      else k_balance_runs<g, false, false><<<runs, kBalThreads, 0, st>>>(a);
+    }
   });
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || one) return e;
   k_balance_fold<<<(unsigned)a.S, kBalThreads, 0, st>>>(a);
   return hipGetLastError();
 }

@@ -515,6 +515,7 @@ struct BalanceArgs {
   float* dlogits;          // [T][E]
   uint32_t* flags;
 };
+bool balance_one(int T, int E, int S);  // no workspace used
 int balance_run(int T);
 int balance_rows(int T, int S);
 hipError_t launch_balance(BalanceArgs a, hipStream_t st);
@@ -531,6 +532,7 @@ struct NewtonArgs {
   uint16_t* out;    // [B][R][C] bf16
   void* workspace;  // newton_workspace(B, R, C) bytes
 };
+constexpr size_t kNewtonNoWorkspace = 256;  // the size where none is used
 size_t newton_workspace(int B, int R, int C);
 hipError_t launch_newton(const NewtonArgs& a, hipStream_t st);
 

@@ -12,22 +12,17 @@
 // bits, a 1024 x 2048 matrix of 16 strong directions over a floor of 1e-2: 3e-2
 // with X held in one fp16 value, 1e-3 in two; in bf16, 3e-1.) The last step has
 // no step after it, and takes the first value alone, which loses least there.
-// X is stored times 2^8: a singular value is at most about 1.2, a value of X at
-// the largest size 2^-14, so that neither end leaves fp16's normal range. A and
-// b A + c A A are stored as they are; their error, absolute, is measured against a.
+// X is stored times 2^8. A and b A + c A A are stored as they are; their error,
+// absolute, is measured against a.
 //
 // A and A A are symmetric: tiles below the diagonal are computed and stored twice.
 // Rows and columns are padded with zeros to multiples of 8, which every step keeps.
-#include "dense.h"
+// Matrices with a side of at most 256 take the way of newton_small.hip.
+#include "newton.h"
 
 namespace moe {
 
 namespace {
-
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
-
-constexpr float kXScale = 256.0f;
 
 struct NsArgs : DenseArgs {
   size_t x_batch, w_batch;        // bytes between the matrices of a stack
@@ -43,16 +38,6 @@ struct NsArgs : DenseArgs {
 
 // Epilogues: A from its sums; b A + c A A; X of the next step; the result; fp32 partial sums of A (of a split K)
 enum NsEpi { kNsGram = 10, kNsPoly = 11, kNsNext = 12, kNsLast = 13, kNsPartial = 14 };
-
-__device__ __forceinline__ uint32_t f16x2_rne(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, f16x2_t));
-}
-__device__ __forceinline__ uint2 pack4_f16(const f32x4_t& v) {
-  return make_uint2(f16x2_rne(v[0], v[1]), f16x2_rne(v[2], v[3]));
-}
-__device__ __forceinline__ f32x4_t unpack4_f16(const uint2& p) {
-  return __builtin_convertvector(__builtin_bit_cast(f16x4_t, p), f32x4_t);
-}
 
 // Four lanes of a quad hold four 16-bit values each, of one row; -> four values of one column each (lane j: column j).
 __device__ __forceinline__ uint2 quad_transpose(const uint2& d, int lane) {
@@ -212,14 +197,9 @@ __global__ __launch_bounds__(256) void k_newton_gram_sum(NsArgs a, int slices, i
 
 // ---- |G|_F and the first X
 
-constexpr int kNormThreads = 256, kNormBlocks = 256;
+constexpr int kNormThreads = 256;
+static_assert(kNormBlocks <= kNormThreads, "");
 
-template <int DT>
-__device__ __forceinline__ double value_at(const void* p, size_t i) {
-  if constexpr (DT == kDtF32) return static_cast<const float*>(p)[i];
-  const uint32_t h = static_cast<const uint16_t*>(p)[i];
-  return DT == kDtBf16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
-}
 template <int DT>
 __device__ __forceinline__ void eight_values(const u32x4_t* p, double (&v)[8]) {
   if constexpr (DT == kDtF32) {
@@ -237,18 +217,6 @@ __device__ __forceinline__ void eight_values(const u32x4_t* p, double (&v)[8]) {
       v[i] = DT == kDtBf16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
     }
   }
-}
-
-// Sum over the block (kNormThreads) in a fixed order; every thread has it.
-__device__ __forceinline__ double block_sum(double v, double* lds) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kNormThreads / 64; ++w) s += lds[w];
-  return s;
 }
 
 // Sums of squares in 64 bits: no magnitude of G leaves their range.
@@ -275,7 +243,7 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_norm(const void* g, siz
       s += v * v;
     }
   }
-  s = block_sum(s, lds);
+  s = block_sum<kNormThreads / 64>(s, lds);
   if (threadIdx.x == 0) part[blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
@@ -286,7 +254,8 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_first(const void* g, in
                                                                uint16_t* lo) {
   constexpr size_t SIZE = DT == kDtF32 ? 4 : 2;
   __shared__ double lds[kNormThreads / 64];
-  const double sum = block_sum((int)threadIdx.x < parts ? part[(size_t)blockIdx.y * parts + threadIdx.x] : 0.0, lds);
+  const double sum =
+      block_sum<kNormThreads / 64>((int)threadIdx.x < parts ? part[(size_t)blockIdx.y * parts + threadIdx.x] : 0.0, lds);
   const double inv = (double)kXScale / (__builtin_sqrt(sum) + eps);
   const char* p = static_cast<const char*>(g) + (size_t)blockIdx.y * R * C * SIZE;
   const bool whole = C % 8 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
@@ -463,29 +432,96 @@ Layout layout_of(int B, int R, int C) {
   return L;
 }
 
+inline int norm_parts(size_t values) {
+  return (int)(values / (kNormThreads * 32) < kNormBlocks ? values / (kNormThreads * 32) + 1 : kNormBlocks);
+}
 template <int DT>
-hipError_t first(const NewtonArgs& n, const Layout& L, const void* g, int count, double* part, uint16_t* hi, uint16_t* lo,
+hipError_t norm_of(const void* g, size_t values, int count, double* norm, hipStream_t st) {
+  k_newton_norm<DT><<<dim3((unsigned)norm_parts(values), (unsigned)count), kNormThreads, 0, st>>>(g, values, norm);
+  return hipGetLastError();
+}
+template <int DT>
+hipError_t first(const NewtonArgs& n, const Layout& L, const void* g, int count, double* norm, uint16_t* hi, uint16_t* lo,
                  hipStream_t st) {
   const size_t values = (size_t)n.R * n.C;
-  const int parts = (int)(values / (kNormThreads * 32) < kNormBlocks ? values / (kNormThreads * 32) + 1 : kNormBlocks);
-  k_newton_norm<DT><<<dim3((unsigned)parts, (unsigned)count), kNormThreads, 0, st>>>(g, values, part);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = norm_of<DT>(g, values, count, norm, st);
   if (e != hipSuccess) return e;
-  const size_t pieces = L.x / 8;
-  const size_t nb = (pieces + kNormThreads - 1) / kNormThreads;
+  const size_t nb = (L.x / 8 + kNormThreads - 1) / kNormThreads;
   k_newton_first<DT><<<dim3((unsigned)(nb < 2048 ? nb : 2048), (unsigned)count), kNormThreads, 0, st>>>(
-      g, n.R, n.C, L.Rp, L.Cp, part, parts, n.eps, hi, lo);
+      g, n.R, n.C, L.Rp, L.Cp, norm, norm_parts(values), n.eps, hi, lo);
   return hipGetLastError();
+}
+
+// The ways to do it: all in one launch, in panels, or in tile products.
+enum Way { kInOne, kPanels, kTileProducts };
+Way way_of(int R, int C) {
+  const int m = R < C ? R : C, n = R < C ? C : R;
+  return newton_in_one(m, n) ? kInOne : m <= kNewtonSmall ? kPanels : kTileProducts;
+}
+// matrices at a time in panels: the workspace stays below about 1 GB
+int panels_chunk(int B, int R, int C) {
+  const int m = R < C ? R : C, n = R < C ? C : R;
+  const size_t most = ((size_t)1 << 30) / newton_small_layout(m, n, 1).total;
+  return (size_t)B <= most ? B : most < 1 ? 1 : (int)most;
 }
 
 }  // namespace
 
-size_t newton_workspace(int B, int R, int C) { return layout_of(B > 0 ? B : 1, R, C).total; }
+size_t newton_workspace(int B, int R, int C) {
+  const Way way = way_of(R, C);
+  if (way == kInOne) return kNewtonNoWorkspace;
+  if (B <= 0) B = 1;
+  if (way == kTileProducts) return layout_of(B, R, C).total;
+  const int m = R < C ? R : C, n = R < C ? C : R, chunk = panels_chunk(B, R, C);
+  // the last part of a stack may be smaller, and cut otherwise
+  const size_t a = newton_small_layout(m, n, chunk).total;
+  const size_t b = B % chunk ? newton_small_layout(m, n, B % chunk).total : 0;
+  return a > b ? a : b;
+}
+
+static hipError_t launch_small(const NewtonArgs& n, Way way, hipStream_t st) {
+  SmallArgs a;
+  __builtin_memset(&a, 0, sizeof(a));
+  a.tall = n.R > n.C;
+  a.m = a.tall ? n.C : n.R;
+  a.n = a.tall ? n.R : n.C;
+  a.steps = n.steps;
+  a.ca = (float)n.a;
+  a.cb = (float)n.b;
+  a.cc = (float)n.c;
+  a.eps = n.eps;
+  a.g = n.g;
+  a.out = n.out;
+  if (way == kInOne) return launch_newton_one(a, n.B, n.dtype, st);
+  const size_t values = (size_t)n.R * n.C, size = n.dtype == kDtF32 ? 4 : 2;
+  const int chunk = panels_chunk(n.B, n.R, n.C);
+  char* ws = static_cast<char*>(n.workspace);
+  for (int b = 0; b < n.B; b += chunk) {
+    const int count = n.B - b < chunk ? n.B - b : chunk;
+    const SmallLayout L = newton_small_layout(a.m, a.n, count);
+    double* norm = reinterpret_cast<double*>(ws + L.norm);
+    a.g = static_cast<const char*>(n.g) + (size_t)b * values * size;
+    a.out = n.out + (size_t)b * values;
+    a.norm = norm;
+    a.norm_parts = norm_parts(values);
+    a.state = reinterpret_cast<u32x4_t*>(ws + L.state);
+    a.square = reinterpret_cast<uint16_t*>(ws + L.square);
+    a.part = reinterpret_cast<f32x4_t*>(ws + L.part);
+    hipError_t e = n.dtype == kDtF32    ? norm_of<kDtF32>(a.g, values, count, norm, st)
+                   : n.dtype == kDtBf16 ? norm_of<kDtBf16>(a.g, values, count, norm, st)
+                                        : norm_of<kDtF16>(a.g, values, count, norm, st);
+    if (e == hipSuccess) e = launch_newton_panels(a, count, n.dtype, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
   if (n.B <= 0 || n.B > kNewtonMaxBatch || n.R <= 0 || n.C <= 0 || n.R > kNewtonMaxSide || n.C > kNewtonMaxSide ||
       n.steps <= 0)
     return hipErrorInvalidValue;
+  const Way way = way_of(n.R, n.C);
+  if (way != kTileProducts) return launch_small(n, way, st);
   const Layout L = layout_of(n.B, n.R, n.C);
   char* ws = static_cast<char*>(n.workspace);
   uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(ws + L.hi0), reinterpret_cast<uint16_t*>(ws + L.hi1)};

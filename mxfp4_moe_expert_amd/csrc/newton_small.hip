@@ -1,0 +1,472 @@
+// Newton-Schulz orthogonalisation (newton.hip) of matrices whose shorter side m
+// is at most 256, in column panels that one block takes through a whole step.
+//
+// With X taken as m x n (n the longer side), a step is
+//   Y = A X,  X' = a X + b Y + c A Y,  A' = X' X'^T.
+// Y and X' of a panel of 64 columns need that panel of X alone, so a block holds
+// A in registers (each wave the rows it computes), passes its panel through LDS
+// three times, as operand of A X, of A Y and, read transposed, of X' X'^T, and
+// ends with its part of A'. A second launch adds the blocks' parts in order: two
+// launches a step, where tile products take four (A with K split, its sum, b A +
+// c A A, the update). Small matrices (m up to 128, few panels) stay in one
+// block's registers over all steps: one launch in all.
+//
+// Roundings as in newton.hip: X in two fp16 values times 2^8, operands the first;
+// A and Y in fp16; sums, and a X + b Y + c A Y, in fp32.
+//
+// X is kept as the lanes hold it: lane (r, g) of a wave has X[i .. i + 3][j] of
+// its tiles, i = 16 tile row + 4 g, j = 16 tile column + r, and stores both parts
+// of the four values as 16 bytes.
+#include <type_traits>
+
+#include "dense.h"
+#include "newton.h"
+
+namespace moe {
+
+namespace {
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) u32x2_t lds_u32x2;
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+
+constexpr int kThreads = 512, kWaves = 8;
+constexpr int kPanel = 64;
+
+// MT: 16-row tiles of the padded shorter side.
+template <int MT>
+struct Shape {
+  static constexpr int M = 16 * MT, PITCH = 2 * M + 16;  // bytes per panel column in LDS: 16 columns in distinct banks
+  static constexpr int RT = MT >= 4 ? 2 : 1, WR = MT / RT, WC = kWaves / WR, CT = 4 / WC;  // tiles of a wave: RT x CT
+  static constexpr int KS = M / 32;                                                        // k-steps of a product with A
+  static constexpr int TILES = MT * (MT + 1) / 2, SLOTS = (TILES + kWaves - 1) / kWaves;
+  static_assert(WR * RT == MT && WR * WC == kWaves && WC * CT == 4, "");
+};
+
+__device__ __forceinline__ void lower_of(int t, int& i, int& j) {
+  i = 0;
+  while ((i + 1) * (i + 2) / 2 <= t) ++i;
+  j = t - i * (i + 1) / 2;
+}
+
+template <int MT>
+struct Small {
+  using S = Shape<MT>;
+  const SmallArgs& a;
+  lds_u8* panel;  // [64 columns][PITCH]
+  int lane, wave, r, g, row0, col0;  // first tile row and column of the wave
+  u32x4_t af[S::RT][S::KS];          // A's rows of the wave
+  f32x4_t gram[S::SLOTS];            // tiles first_tile .. of the lower triangle of A'
+
+  __device__ __forceinline__ Small(const SmallArgs& args, lds_u8* p)
+      : a(args), panel(p), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {
+    r = lane & 15;
+    g = lane >> 4;
+    row0 = (wave % S::WR) * S::RT;
+    col0 = (wave / S::WR) * S::CT;
+  }
+  // slots past the last tile compute one again that is not kept
+  __device__ __forceinline__ int first_tile() const { return wave * S::SLOTS; }
+  __device__ __forceinline__ bool kept(int slot) const { return first_tile() + slot < S::TILES; }
+  __device__ __forceinline__ void clear_gram() {
+#pragma unroll
+    for (int s = 0; s < S::SLOTS; ++s) gram[s] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  }
+  // rows of A from memory (pitch bytes), global or LDS
+  template <class P>
+  __device__ __forceinline__ void load_a(P base, int pitch) {
+    typedef const u32x4_t __attribute__((may_alias)) piece;
+#pragma unroll
+    for (int t = 0; t < S::RT; ++t)
+#pragma unroll
+      for (int k = 0; k < S::KS; ++k) {
+        const auto* p = base + ((row0 + t) * 16 + r) * pitch + k * 64 + g * 16;
+        if constexpr (std::is_same_v<P, lds_u8*>) af[t][k] = *(const lds_u32x4*)p;
+        else af[t][k] = *(piece*)p;
+      }
+  }
+  // the four values of tile (t, c), as fp16, to the panel
+  __device__ __forceinline__ void put(int t, int c, const uint2& v) {
+    *(lds_u32x2*)(panel + ((col0 + c) * 16 + r) * S::PITCH + ((row0 + t) * 16 + 4 * g) * 2) = (u32x2_t){v.x, v.y};
+  }
+  // A times columns c0 .. c0 + C - 1 of the wave's tiles of the panel
+  template <int C>
+  __device__ __forceinline__ void product(int c0, f32x4_t (&acc)[S::RT][C]) {
+#pragma unroll
+    for (int t = 0; t < S::RT; ++t)
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[t][c] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    // operands are read a k-step ahead; the order is pinned, or the compiler reads all of them first (registers)
+    u32x4_t b[2][C];
+    auto read = [&](int k) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        b[k & 1][c] = *(const lds_u32x4*)(panel + ((col0 + c0 + c) * 16 + r) * S::PITCH + k * 64 + g * 16);
+    };
+    read(0);
+#pragma unroll
+    for (int k = 0; k < S::KS; ++k) {
+      if (k + 1 < S::KS) read(k + 1);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int t = 0; t < S::RT; ++t) acc[t][c] = mfma_f16(af[t][k], b[k & 1][c], acc[t][c]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // eight columns of row 16 tile + r of the panel's X (the panel is stored by columns: transposing reads)
+  __device__ __forceinline__ u32x4_t row_piece(int tile, int k) const {
+    const lds_u8* p = panel + (32 * k + 8 * g + (r >> 2)) * S::PITCH + (16 * tile + 4 * (r & 3)) * 2;
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * S::PITCH));
+    const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
+    return (u32x4_t){x.x, x.y, y.x, y.y};
+  }
+  // A' += panel panel^T; a tile's operands are read under the MFMAs of the one before
+  __device__ __forceinline__ void add_gram() {
+    int i, j;
+    lower_of(min(first_tile(), S::TILES - 1), i, j);
+    u32x4_t x[2], y[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      x[k] = row_piece(i, k);
+      y[0][k] = row_piece(j, k);
+    }
+#pragma unroll
+    for (int s = 0; s < S::SLOTS; ++s) {
+      const bool turn = j == i;  // the next tile is the first of the next row
+      i = turn ? min(i + 1, MT - 1) : i;
+      j = turn ? 0 : j + 1;
+      if (s + 1 < S::SLOTS) {
+        y[(s + 1) & 1][0] = row_piece(j, 0);
+        y[(s + 1) & 1][1] = row_piece(j, 1);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) gram[s] = mfma_f16(x[k], y[s & 1][k], gram[s]);
+      if (s + 1 < S::SLOTS) {
+        x[0] = row_piece(i, 0);
+        x[1] = row_piece(i, 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // One panel through a step: x holds both parts of the wave's values; -> those of the next step, or (LAST) the result's
+  // values in y. The panel may be read by the other waves until the caller's next barrier.
+  template <bool LAST>
+  __device__ __forceinline__ void step(u32x4_t (&x)[S::RT][S::CT], f32x4_t (&y)[S::RT][S::CT]) {
+    each([&](int t, int c) { put(t, c, make_uint2(x[t][c][0], x[t][c][1])); });
+    __syncthreads();
+    product<S::CT>(0, y);
+    __syncthreads();
+    each([&](int t, int c) { put(t, c, pack4_f16(y[t][c])); });
+    __syncthreads();
+    // A Y two tile columns at a time (registers)
+    constexpr int C = S::CT < 2 ? S::CT : 2;
+#pragma unroll
+    for (int c0 = 0; c0 < S::CT; c0 += C) {
+      f32x4_t z[S::RT][C];
+      product<C>(c0, z);
+#pragma unroll
+      for (int t = 0; t < S::RT; ++t)
+#pragma unroll
+        for (int d = 0; d < C; ++d) {
+          const int c = c0 + d;
+          f32x4_t v = unpack4_f16(make_uint2(x[t][c][0], x[t][c][1]));
+          if (!LAST) v += unpack4_f16(make_uint2(x[t][c][2], x[t][c][3]));
+          y[t][c] = v * a.ca + y[t][c] * a.cb + z[t][d] * a.cc;
+        }
+    }
+    __syncthreads();
+    if constexpr (!LAST) next(x, y);
+  }
+  // x: both parts of the values y; A' takes the panel's share
+  __device__ __forceinline__ void next(u32x4_t (&x)[S::RT][S::CT], const f32x4_t (&y)[S::RT][S::CT]) {
+    each([&](int t, int c) {
+      const uint2 h = pack4_f16(y[t][c]), l = pack4_f16(y[t][c] - unpack4_f16(h));
+      x[t][c] = (u32x4_t){h.x, h.y, l.x, l.y};
+      put(t, c, h);
+    });
+    __syncthreads();
+    add_gram();
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F&& f) {
+#pragma unroll
+    for (int t = 0; t < S::RT; ++t)
+#pragma unroll
+      for (int c = 0; c < S::CT; ++c) f(t, c);
+  }
+  __device__ __forceinline__ int row_of(int t) const { return (row0 + t) * 16 + 4 * g; }
+  __device__ __forceinline__ int col_of(int panel_at, int c) const { return panel_at * kPanel + (col0 + c) * 16 + r; }
+
+  // G's values (exact in fp32) at the wave's places of a panel, zeros past its edges
+  template <int DT>
+  __device__ __forceinline__ void load_g(const void* gp, int at, f32x4_t (&v)[S::RT][S::CT]) const {
+#pragma unroll
+    for (int t = 0; t < S::RT; ++t)
+#pragma unroll
+      for (int c = 0; c < S::CT; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = row_of(t) + e, j = col_of(at, c);
+          const bool in = i < a.m && j < a.n;
+          const size_t o = a.tall ? (size_t)j * a.m + i : (size_t)i * a.n + j;
+          v[t][c][e] = in ? (float)value_at<DT>(gp, o) : 0.0f;
+        }
+  }
+  __device__ __forceinline__ void store_out(uint16_t* out, int at, const f32x4_t (&y)[S::RT][S::CT]) const {
+#pragma unroll
+    for (int t = 0; t < S::RT; ++t)
+#pragma unroll
+      for (int c = 0; c < S::CT; ++c) {
+        const int i = row_of(t), j = col_of(at, c);
+        if (j >= a.n) continue;
+        const f32x4_t v = y[t][c] * (1.0f / kXScale);
+        if (a.tall) {
+          store4(out, false, (size_t)j * a.m + i, v, a.m - i, (a.m & 3) == 0 && i < a.m);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < a.m) out[(size_t)(i + e) * a.n + j] = f32_to_bf16(v[e]);
+        }
+      }
+  }
+};
+
+// ---- one step per launch
+
+enum { kFirst = 0, kStep = 1, kLast = 2 };
+
+// Block (p, z): panels p q .. of matrix z. kFirst: X from G, and its A; kLast: the result.
+template <int MT, int MODE, int DT>
+__global__ __launch_bounds__(kThreads) void k_newton_panel(SmallArgs a) {
+  using S = Shape<MT>;
+  __shared__ __align__(16) unsigned char buf[kPanel * S::PITCH];
+  Small<MT> w(a, (lds_u8*)buf);
+  const size_t z = blockIdx.y, values = (size_t)a.n * a.m;
+  const int first = blockIdx.x * a.per_block, end = min(first + a.per_block, a.panels);
+  u32x4_t* state = a.state + ((size_t)z * a.panels * S::RT * S::CT) * kThreads + threadIdx.x;
+  double inv = 0.0;
+  if constexpr (MODE == kFirst) {
+    __shared__ double lds[kWaves];
+    const double* part = a.norm + z * a.norm_parts;
+    inv = (double)kXScale / (__builtin_sqrt(block_sum<kWaves>((int)threadIdx.x < a.norm_parts ? part[threadIdx.x] : 0.0, lds)) + a.eps);
+  } else {
+    w.load_a(reinterpret_cast<const unsigned char*>(a.square + z * S::M * S::M), 2 * S::M);
+  }
+  w.clear_gram();
+  for (int p = first; p < end; ++p) {
+    u32x4_t x[S::RT][S::CT];
+    f32x4_t y[S::RT][S::CT];
+    u32x4_t* at = state + (size_t)p * S::RT * S::CT * kThreads;
+    if constexpr (MODE == kFirst) {
+      w.template load_g<DT>(static_cast<const char*>(a.g) + z * values * (DT == kDtF32 ? 4 : 2), p, y);
+      w.each([&](int t, int c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[t][c][e] = (float)((double)y[t][c][e] * inv);
+      });
+      w.next(x, y);
+    } else {
+      w.each([&](int t, int c) { x[t][c] = at[(t * S::CT + c) * kThreads]; });
+      w.template step<MODE == kLast>(x, y);
+    }
+    if constexpr (MODE == kLast) {
+      w.store_out(a.out + z * values, p, y);
+    } else {
+      w.each([&](int t, int c) { at[(t * S::CT + c) * kThreads] = x[t][c]; });
+      __syncthreads();
+    }
+  }
+  if constexpr (MODE != kLast) {
+    f32x4_t* part = a.part + ((size_t)(z * gridDim.x + blockIdx.x) * S::TILES + w.first_tile()) * 64 + w.lane;
+#pragma unroll
+    for (int s = 0; s < S::SLOTS; ++s)
+      if (w.kept(s)) part[s * 64] = w.gram[s];
+  }
+}
+
+// A from the blocks' parts: four threads per 16 bytes of a tile add a quarter of the parts each, in order.
+template <int MT>
+__global__ __launch_bounds__(256) void k_newton_panel_sum(SmallArgs a, int parts) {
+  using S = Shape<MT>;
+  __shared__ f32x4_t sums[4][64];
+  const int tile = blockIdx.x, lane = threadIdx.x & 63, sub = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const size_t z = blockIdx.y;
+  const f32x4_t* p = a.part + (z * parts * S::TILES + tile) * 64 + lane;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  constexpr int AHEAD = 8;
+  for (int s0 = sub; s0 < parts; s0 += 4 * AHEAD) {
+    f32x4_t t[AHEAD];
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) t[s] = p[(size_t)min(s0 + 4 * s, parts - 1) * S::TILES * 64];
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s)
+      if (s0 + 4 * s < parts) v += t[s];
+  }
+  sums[sub][lane] = v;
+  __syncthreads();
+  if (sub) return;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) v += sums[i][lane];
+  int ti, tj;
+  lower_of(tile, ti, tj);
+  const uint2 h = pack4_f16(v * (1.0f / (kXScale * kXScale)));
+  uint16_t* out = a.square + z * S::M * S::M;
+  const int i = ti * 16 + 4 * g, j = tj * 16 + r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[(i + e) * S::M + j] = (uint16_t)((e < 2 ? h.x : h.y) >> (16 * (e & 1)));
+  *reinterpret_cast<uint2*>(out + j * S::M + i) = h;
+}
+
+// ---- all steps in one launch
+
+// NP: panels at most. X stays in registers, A passes from step to step through LDS.
+template <int MT, int NP, int DT>
+__global__ __launch_bounds__(kThreads) void k_newton_one(SmallArgs a) {
+  using S = Shape<MT>;
+  __shared__ __align__(16) unsigned char buf[kPanel * S::PITCH], square[S::M * S::PITCH];
+  __shared__ double lds[kWaves];
+  Small<MT> w(a, (lds_u8*)buf);
+  const size_t z = blockIdx.x, values = (size_t)a.n * a.m;
+  const void* gp = static_cast<const char*>(a.g) + z * values * (DT == kDtF32 ? 4 : 2);
+  u32x4_t x[NP][S::RT][S::CT];
+  f32x4_t y[S::RT][S::CT];
+  double sum = 0.0;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    if (p >= a.panels) continue;
+    w.template load_g<DT>(gp, p, y);
+    w.each([&](int t, int c) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum += (double)y[t][c][e] * y[t][c][e];
+        x[p][t][c][e] = __float_as_uint(y[t][c][e]);
+      }
+    });
+  }
+  const double inv = (double)kXScale / (__builtin_sqrt(block_sum<kWaves>(sum, lds)) + a.eps);
+  w.clear_gram();
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    if (p >= a.panels) continue;
+    w.each([&](int t, int c) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[t][c][e] = (float)((double)__uint_as_float(x[p][t][c][e]) * inv);
+    });
+    w.next(x[p], y);
+    __syncthreads();
+  }
+  for (int s = 0; s < a.steps; ++s) {
+    // A: the tiles the waves hold and their mirror images
+    lds_u8* sq = (lds_u8*)square;
+#pragma unroll
+    for (int k = 0; k < S::SLOTS; ++k) {
+      if (!w.kept(k)) continue;
+      int ti, tj;
+      lower_of(w.first_tile() + k, ti, tj);
+      const uint2 h = pack4_f16(w.gram[k] * (1.0f / (kXScale * kXScale)));
+      const int i = ti * 16 + 4 * w.g, j = tj * 16 + w.r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *(lds_u16*)(sq + (i + e) * S::PITCH + j * 2) = (uint16_t)((e < 2 ? h.x : h.y) >> (16 * (e & 1)));
+      *(lds_u32x2*)(sq + j * S::PITCH + i * 2) = (u32x2_t){h.x, h.y};
+    }
+    __syncthreads();
+    w.load_a(sq, S::PITCH);
+    w.clear_gram();
+    const bool last = s + 1 == a.steps;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      if (p >= a.panels) continue;
+      if (last) {
+        w.template step<true>(x[p], y);
+        w.store_out(a.out + z * values, p, y);
+      } else {
+        w.template step<false>(x[p], y);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <int MT, int MODE>
+hipError_t panel(const SmallArgs& a, int blocks, int batch, int dtype, hipStream_t st) {
+  const dim3 grid((unsigned)blocks, (unsigned)batch);
+  if (MODE != kFirst || dtype == kDtBf16) k_newton_panel<MT, MODE, kDtBf16><<<grid, kThreads, 0, st>>>(a);
+  else if (dtype == kDtF32) k_newton_panel<MT, MODE, MODE == kFirst ? kDtF32 : kDtBf16><<<grid, kThreads, 0, st>>>(a);
+  else k_newton_panel<MT, MODE, MODE == kFirst ? kDtF16 : kDtBf16><<<grid, kThreads, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int MT>
+hipError_t panels(SmallArgs a, int batch, int dtype, hipStream_t st) {
+  const int blocks = (a.panels + a.per_block - 1) / a.per_block;
+  hipError_t e = panel<MT, kFirst>(a, blocks, batch, dtype, st);
+  for (int s = 0; s < a.steps && e == hipSuccess; ++s) {
+    k_newton_panel_sum<MT><<<dim3((unsigned)Shape<MT>::TILES, (unsigned)batch), 256, 0, st>>>(a, blocks);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    e = s + 1 < a.steps ? panel<MT, kStep>(a, blocks, batch, dtype, st) : panel<MT, kLast>(a, blocks, batch, dtype, st);
+  }
+  return e;
+}
+
+template <int MT, int NP>
+hipError_t one(const SmallArgs& a, int batch, int dtype, hipStream_t st) {
+  if (dtype == kDtBf16) k_newton_one<MT, NP, kDtBf16><<<(unsigned)batch, kThreads, 0, st>>>(a);
+  else if (dtype == kDtF32) k_newton_one<MT, NP, kDtF32><<<(unsigned)batch, kThreads, 0, st>>>(a);
+  else k_newton_one<MT, NP, kDtF16><<<(unsigned)batch, kThreads, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+// tile rows the kernels are made for
+inline int tile_rows(int m) { return m <= 32 ? 2 : m <= 64 ? 4 : m <= 128 ? 8 : 16; }
+// panels that one block's registers hold
+inline int most_panels(int m) { return m <= 32 ? 16 : m <= 64 ? 8 : m <= 128 ? 4 : 0; }
+inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+}  // namespace
+
+bool newton_in_one(int m, int n) { return (n + kPanel - 1) / kPanel <= most_panels(m); }
+
+// Panels per block: the chip's 256 CUs filled once, and at most 64 parts of a matrix's A to add.
+int newton_per_block(int n, int batch) {
+  const int count = (n + kPanel - 1) / kPanel;
+  const int fill = (int)(((long long)count * batch + 255) / 256), sums = (count + 63) / 64;
+  const int per = fill > sums ? fill : sums;
+  return per < count ? per : count;
+}
+
+SmallLayout newton_small_layout(int m, int n, int batch) {
+  SmallLayout L;
+  const size_t count = (n + kPanel - 1) / kPanel, M = 16 * tile_rows(m), tiles = M / 16 * (M / 16 + 1) / 2;
+  const int per = newton_per_block(n, batch);
+  L.state = 0;
+  L.square = align256(count * kPanel * M * 4 * batch);
+  L.norm = L.square + align256(M * M * 2 * batch);
+  L.part = L.norm + align256(sizeof(double) * kNormBlocks * batch);
+  L.total = L.part + align256((count + per - 1) / per * tiles * 1024 * batch);
+  return L;
+}
+
+hipError_t launch_newton_one(SmallArgs a, int batch, int dtype, hipStream_t st) {
+  if (a.m > a.n || !newton_in_one(a.m, a.n) || batch <= 0) return hipErrorInvalidValue;
+  a.panels = (a.n + kPanel - 1) / kPanel;
+  if (a.m <= 32) return one<2, 16>(a, batch, dtype, st);
+  if (a.m <= 64) return one<4, 8>(a, batch, dtype, st);
+  return one<8, 4>(a, batch, dtype, st);
+}
+
+hipError_t launch_newton_panels(SmallArgs a, int batch, int dtype, hipStream_t st) {
+  if (a.m > a.n || a.m > kNewtonSmall || batch <= 0 || batch > 65535) return hipErrorInvalidValue;
+  a.panels = (a.n + kPanel - 1) / kPanel;
+  a.per_block = newton_per_block(a.n, batch);
+  switch (tile_rows(a.m)) {
+    case 2: return panels<2>(a, batch, dtype, st);
+    case 4: return panels<4>(a, batch, dtype, st);
+    case 8: return panels<8>(a, batch, dtype, st);
+    default: return panels<16>(a, batch, dtype, st);
+  }
+}
+
+}  // namespace moe

@@ -62,7 +62,10 @@ def hold(got, G, steps=5, coef=COEF, eps=1e-7):
     return e
 
 
-SIZES = [(1, 1), (1, 9), (9, 1), (2, 3), (7, 8), (8, 8), (16, 5), (17, 33), (33, 17), (64, 64), (100, 300), (300, 100),
+# m x n on both sides of every change of way: tile rows (32, 64, 128, 256), what one block holds (32 x 1024, 64 x 512,
+# 128 x 256), panels of 64; above 256 tile products, K split or whole
+SIZES = [(32, 1024), (1025, 31), (33, 512), (513, 64), (65, 256), (257, 128), (128, 1000), (129, 64), (200, 3000), (256, 257),
+         (1, 1), (1, 9), (9, 1), (2, 3), (7, 8), (8, 8), (16, 5), (17, 33), (33, 17), (64, 64), (100, 300), (300, 100),
          (127, 129), (129, 128), (256, 256), (257, 520), (520, 257), (64, 2050), (2050, 72), (256, 4096), (1001, 600),
          (1024, 1024), (1000, 2000), (2048, 640)]
 
@@ -90,7 +93,7 @@ def test_singular_values_end_near_one():
     assert 0.6 < float(s.min()) and float(s.max()) < 1.25
 
 
-@pytest.mark.parametrize("R,C", [(40, 100), (1000, 72), (513, 513)])
+@pytest.mark.parametrize("R,C", [(40, 100), (1000, 72), (150, 1300), (513, 513)])
 def test_stack(R, C):
     """A stack is its matrices one by one, and a matrix's bits do not depend on the others'."""
     G = gradient(5, R, C, "strong", B=5) * torch.tensor([1.0, 1e-4, 1e5, 3.0, 1.0], device=DEV).view(5, 1, 1)
@@ -104,13 +107,14 @@ def test_stack(R, C):
         assert torch.equal(mx.orthogonalize(others)[i], got[i, 0])
 
 
-def test_stack_in_parts():
+@pytest.mark.parametrize("B,R,C", [(1500, 200, 1104), (300, 700, 600)])
+def test_stack_in_parts(B, R, C):
     """More matrices than the workspace holds at a time."""
-    B, R, C = 1500, 200, 1104
     G = gradient(6, R, C, B=B).to(torch.bfloat16)
-    assert mx.lib().moe_orthogonalize_workspace_size(B, R, C) < B * 2 * (3 * R * C + 2 * R * R)
+    size = mx.lib().moe_orthogonalize_workspace_size
+    assert size(4 * B, R, C) < 1.5 * size(B, R, C)
     got = mx.orthogonalize(G)
-    for i in (0, 1, 720, 760, 1498, 1499):
+    for i in list(range(0, B, B // 12)) + [B - 2, B - 1]:
         hold(got[i], G[i])
 
 
@@ -151,7 +155,7 @@ def test_rank_deficient_and_tied_directions():
 
 def test_empty_stack_outputs_and_workspace():
     assert mx.orthogonalize(torch.empty(0, 8, 9, device=DEV)).shape == (0, 8, 9)
-    for R, C in ((33, 50), (50, 33), (64, 128)):
+    for R, C in ((33, 50), (50, 33), (64, 128), (200, 700), (700, 200), (300, 290)):
         G = gradient(11, R, C)
         need = mx.lib().moe_orthogonalize_workspace_size(1, R, C)
         ws = torch.full((need + 256,), 0xAB, dtype=torch.uint8, device=DEV)
@@ -173,7 +177,7 @@ def test_refusals_on_device():
             bad()
     for bad in (lambda: mx.orthogonalize(torch.zeros(1, 16392, device=DEV)), lambda: mx.orthogonalize(G, steps=0),
                 lambda: mx.orthogonalize(G, eps=-1.0), lambda: mx.orthogonalize(G, coefficients=(1.0, float("nan"), 0.0)),
-                lambda: mx.orthogonalize(G, ws=torch.empty(256, dtype=torch.uint8, device=DEV))):
+                lambda: mx.orthogonalize(gradient(12, 300, 280), ws=torch.empty(256, dtype=torch.uint8, device=DEV))):
         with pytest.raises(mx.MoEError):
             bad()
     with pytest.raises(mx.MoEError, match="out: not 16-byte"):
@@ -192,8 +196,9 @@ def test_input_at_any_element(R, C, dtype):
         assert torch.equal(mx.orthogonalize(at), want), skip
 
 
-def test_on_two_streams_and_in_graphs():
-    Gs = [gradient(20 + i, 260, 390, "strong") for i in range(4)]
+@pytest.mark.parametrize("R,C", [(60, 100), (1200, 160), (260, 390)])
+def test_on_two_streams_and_in_graphs(R, C):
+    Gs = [gradient(20 + i, R, C, "strong") for i in range(4)]
     want = [mx.orthogonalize(G) for G in Gs]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]

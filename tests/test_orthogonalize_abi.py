@@ -17,10 +17,12 @@ def test_refusals():
     size, f = L.moe_orthogonalize_workspace_size, L.moe_orthogonalize
     for B, R, C in ((-1, 8, 8), (65536, 8, 8), (1, 0, 8), (1, 8, 0), (1, 16385, 8), (1, 8, 16385)):
         assert size(B, R, C) == 0, (B, R, C)
-    need = size(2, 100, 64)
-    assert need >= 2 * 2 * (3 * 104 * 64 + 2 * 64 * 64)
+    need = size(2, 1001, 640)
+    assert need >= 2 * 2 * (3 * 1008 * 640 + 2 * 640 * 640)
+    assert size(9, 60, 100) == 256                                   # none used
+    assert size(1, 256, 4096) >= 4 * 256 * 4096                      # X in 32 bits
     assert size(65535, 256, 512) < 3 << 30                           # a stack is worked on in parts
-    good = [2, 100, 64, 0, P, 5, 3.4, -4.7, 2.0, 1e-7, P, P, need, None]
+    good = [2, 1001, 640, 0, P, 5, 3.4, -4.7, 2.0, 1e-7, P, P, need, None]
 
     def call(**kw):
         a = list(good)

@@ -16,8 +16,8 @@ def test_balance_loss_refusals():
     size, f = L.moe_balance_workspace_size, L.moe_balance_loss
     for T, E, S in ((-1, 8, 1), (65537, 8, 1), (8, 0, 1), (8, 257, 1), (8, 8, 0), (8, 8, 65537)):
         assert size(T, E, S) == 0
-    need = size(100, 64, 3)
-    good = [100, 64, 6, 3, P, P, P, 1e-3, P, P, P, P, need, None]
+    need = size(5000, 64, 3)
+    good = [5000, 64, 6, 3, P, P, P, 1e-3, P, P, P, P, need, None]
 
     def call(**kw):
         a = list(good)
@@ -30,6 +30,7 @@ def test_balance_loss_refusals():
         assert call(**{f"a{i}": BYTE}) == EINVAL, i
     assert call(a4=ODD) == EINVAL and call(a11=P + 16) == EINVAL
     assert call(a12=need - 1) == EWS
+    assert size(64, 256, 1) == 256                                  # none used
     assert call(a0=-1) == EINVAL and call(a1=0) == EINVAL and call(a2=0) == EINVAL and call(a3=0) == EINVAL
     assert call(a0=65537) == EUNSUP and call(a1=257) == EUNSUP and call(a2=9) == EUNSUP and call(a3=65537) == EUNSUP
 
