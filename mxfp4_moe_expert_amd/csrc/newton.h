@@ -62,7 +62,7 @@ struct SmallArgs {
 struct SmallLayout {
   size_t state, square, norm, part, total;
 };
-bool newton_in_one(int m, int n);
+bool newton_in_one(int m, int n, int batch);
 SmallLayout newton_small_layout(int m, int n, int batch);
 hipError_t launch_newton_one(SmallArgs a, int batch, int dtype, hipStream_t st);     // all of it
 hipError_t launch_newton_panels(SmallArgs a, int batch, int dtype, hipStream_t st);  // from |G|^2 on

@@ -454,9 +454,9 @@ hipError_t first(const NewtonArgs& n, const Layout& L, const void* g, int count,
 
 // The ways to do it: all in one launch, in panels, or in tile products.
 enum Way { kInOne, kPanels, kTileProducts };
-Way way_of(int R, int C) {
+Way way_of(int B, int R, int C) {
   const int m = R < C ? R : C, n = R < C ? C : R;
-  return newton_in_one(m, n) ? kInOne : m <= kNewtonSmall ? kPanels : kTileProducts;
+  return newton_in_one(m, n, B) ? kInOne : m <= kNewtonSmall ? kPanels : kTileProducts;
 }
 // matrices at a time in panels: the workspace stays below about 1 GB
 int panels_chunk(int B, int R, int C) {
@@ -468,9 +468,9 @@ int panels_chunk(int B, int R, int C) {
 }  // namespace
 
 size_t newton_workspace(int B, int R, int C) {
-  const Way way = way_of(R, C);
-  if (way == kInOne) return kNewtonNoWorkspace;
   if (B <= 0) B = 1;
+  const Way way = way_of(B, R, C);
+  if (way == kInOne) return kNewtonNoWorkspace;
   if (way == kTileProducts) return layout_of(B, R, C).total;
   const int m = R < C ? R : C, n = R < C ? C : R, chunk = panels_chunk(B, R, C);
   // the last part of a stack may be smaller, and cut otherwise
@@ -520,7 +520,7 @@ hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
   if (n.B <= 0 || n.B > kNewtonMaxBatch || n.R <= 0 || n.C <= 0 || n.R > kNewtonMaxSide || n.C > kNewtonMaxSide ||
       n.steps <= 0)
     return hipErrorInvalidValue;
-  const Way way = way_of(n.R, n.C);
+  const Way way = way_of(n.B, n.R, n.C);
   if (way != kTileProducts) return launch_small(n, way, st);
   const Layout L = layout_of(n.B, n.R, n.C);
   char* ws = static_cast<char*>(n.workspace);

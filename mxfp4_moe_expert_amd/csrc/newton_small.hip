@@ -31,16 +31,16 @@ typedef __attribute__((address_space(3))) u32x2_t lds_u32x2;
 typedef __attribute__((address_space(3))) uint16_t lds_u16;
 
 constexpr int kThreads = 512, kWaves = 8;
-constexpr int kPanel = 64;
 
-// MT: 16-row tiles of the padded shorter side.
-template <int MT>
+// MT: 16-row tiles of the padded shorter side; PC: columns of a panel.
+template <int MT, int PC>
 struct Shape {
-  static constexpr int M = 16 * MT, PITCH = 2 * M + 16;  // bytes per panel column in LDS: 16 columns in distinct banks
-  static constexpr int RT = MT >= 4 ? 2 : 1, WR = MT / RT, WC = kWaves / WR, CT = 4 / WC;  // tiles of a wave: RT x CT
-  static constexpr int KS = M / 32;                                                        // k-steps of a product with A
+  // bytes per panel column in LDS: 16 columns in distinct banks, and the four of a transposing read nearly so
+  static constexpr int M = 16 * MT, PITCH = 2 * M + 48;
+  static constexpr int RT = MT * PC >= 256 ? 2 : 1, WR = MT / RT, WC = kWaves / WR, CT = PC / 16 / WC;  // a wave: RT x CT tiles
+  static constexpr int KS = M / 32, KG = PC / 32;  // k-steps of a product with A, and of the panel's share of A'
   static constexpr int TILES = MT * (MT + 1) / 2, SLOTS = (TILES + kWaves - 1) / kWaves;
-  static_assert(WR * RT == MT && WR * WC == kWaves && WC * CT == 4, "");
+  static_assert(CT >= 1 && WR * RT == MT && WR * WC == kWaves && WC * CT * 16 == PC, "");
 };
 
 __device__ __forceinline__ void lower_of(int t, int& i, int& j) {
@@ -49,11 +49,11 @@ __device__ __forceinline__ void lower_of(int t, int& i, int& j) {
   j = t - i * (i + 1) / 2;
 }
 
-template <int MT>
+template <int MT, int PC>
 struct Small {
-  using S = Shape<MT>;
+  using S = Shape<MT, PC>;
   const SmallArgs& a;
-  lds_u8* panel;  // [64 columns][PITCH]
+  lds_u8* panel;  // [PC columns][PITCH]
   int lane, wave, r, g, row0, col0;  // first tile row and column of the wave
   u32x4_t af[S::RT][S::KS];          // A's rows of the wave
   f32x4_t gram[S::SLOTS];            // tiles first_tile .. of the lower triangle of A'
@@ -72,18 +72,21 @@ struct Small {
 #pragma unroll
     for (int s = 0; s < S::SLOTS; ++s) gram[s] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   }
-  // rows of A from memory (pitch bytes), global or LDS
-  template <class P>
-  __device__ __forceinline__ void load_a(P base, int pitch) {
-    typedef const u32x4_t __attribute__((may_alias)) piece;
+  // the wave's rows of A: its MFMA operands, stored as such in global memory (operand_at)
+  __device__ __forceinline__ void load_a(const uint16_t* square) {
 #pragma unroll
     for (int t = 0; t < S::RT; ++t)
 #pragma unroll
-      for (int k = 0; k < S::KS; ++k) {
-        const auto* p = base + ((row0 + t) * 16 + r) * pitch + k * 64 + g * 16;
-        if constexpr (std::is_same_v<P, lds_u8*>) af[t][k] = *(const lds_u32x4*)p;
-        else af[t][k] = *(piece*)p;
-      }
+      for (int k = 0; k < S::KS; ++k)
+        af[t][k] = reinterpret_cast<const u32x4_t*>(square)[((row0 + t) * S::KS + k) * 64 + lane];
+  }
+  // the same from LDS, rows of PITCH bytes
+  __device__ __forceinline__ void load_a(const lds_u8* square) {
+#pragma unroll
+    for (int t = 0; t < S::RT; ++t)
+#pragma unroll
+      for (int k = 0; k < S::KS; ++k)
+        af[t][k] = *(const lds_u32x4*)(square + ((row0 + t) * 16 + r) * S::PITCH + k * 64 + g * 16);
   }
   // the four values of tile (t, c), as fp16, to the panel
   __device__ __forceinline__ void put(int t, int c, const uint2& v) {
@@ -126,27 +129,22 @@ struct Small {
   __device__ __forceinline__ void add_gram() {
     int i, j;
     lower_of(min(first_tile(), S::TILES - 1), i, j);
-    u32x4_t x[2], y[2][2];
+    u32x4_t x[S::KG], y[2][S::KG];
+    auto rows = [&](int tile, u32x4_t (&v)[S::KG]) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      x[k] = row_piece(i, k);
-      y[0][k] = row_piece(j, k);
-    }
+      for (int k = 0; k < S::KG; ++k) v[k] = row_piece(tile, k);
+    };
+    rows(i, x);
+    rows(j, y[0]);
 #pragma unroll
     for (int s = 0; s < S::SLOTS; ++s) {
       const bool turn = j == i;  // the next tile is the first of the next row
       i = turn ? min(i + 1, MT - 1) : i;
       j = turn ? 0 : j + 1;
-      if (s + 1 < S::SLOTS) {
-        y[(s + 1) & 1][0] = row_piece(j, 0);
-        y[(s + 1) & 1][1] = row_piece(j, 1);
-      }
+      if (s + 1 < S::SLOTS) rows(j, y[(s + 1) & 1]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) gram[s] = mfma_f16(x[k], y[s & 1][k], gram[s]);
-      if (s + 1 < S::SLOTS) {
-        x[0] = row_piece(i, 0);
-        x[1] = row_piece(i, 1);
-      }
+      for (int k = 0; k < S::KG; ++k) gram[s] = mfma_f16(x[k], y[s & 1][k], gram[s]);
+      if (s + 1 < S::SLOTS && turn) rows(i, x);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -197,7 +195,7 @@ struct Small {
       for (int c = 0; c < S::CT; ++c) f(t, c);
   }
   __device__ __forceinline__ int row_of(int t) const { return (row0 + t) * 16 + 4 * g; }
-  __device__ __forceinline__ int col_of(int panel_at, int c) const { return panel_at * kPanel + (col0 + c) * 16 + r; }
+  __device__ __forceinline__ int col_of(int panel_at, int c) const { return panel_at * PC + (col0 + c) * 16 + r; }
 
   // G's values (exact in fp32) at the wave's places of a panel, zeros past its edges
   template <int DT>
@@ -238,11 +236,11 @@ struct Small {
 enum { kFirst = 0, kStep = 1, kLast = 2 };
 
 // Block (p, z): panels p q .. of matrix z. kFirst: X from G, and its A; kLast: the result.
-template <int MT, int MODE, int DT>
+template <int MT, int PC, int MODE, int DT>
 __global__ __launch_bounds__(kThreads) void k_newton_panel(SmallArgs a) {
-  using S = Shape<MT>;
-  __shared__ __align__(16) unsigned char buf[kPanel * S::PITCH];
-  Small<MT> w(a, (lds_u8*)buf);
+  using S = Shape<MT, PC>;
+  __shared__ __align__(16) unsigned char buf[PC * S::PITCH];
+  Small<MT, PC> w(a, (lds_u8*)buf);
   const size_t z = blockIdx.y, values = (size_t)a.n * a.m;
   const int first = blockIdx.x * a.per_block, end = min(first + a.per_block, a.panels);
   u32x4_t* state = a.state + ((size_t)z * a.panels * S::RT * S::CT) * kThreads + threadIdx.x;
@@ -252,7 +250,7 @@ __global__ __launch_bounds__(kThreads) void k_newton_panel(SmallArgs a) {
     const double* part = a.norm + z * a.norm_parts;
     inv = (double)kXScale / (__builtin_sqrt(block_sum<kWaves>((int)threadIdx.x < a.norm_parts ? part[threadIdx.x] : 0.0, lds)) + a.eps);
   } else {
-    w.load_a(reinterpret_cast<const unsigned char*>(a.square + z * S::M * S::M), 2 * S::M);
+    w.load_a(a.square + z * S::M * S::M);
   }
   w.clear_gram();
   for (int p = first; p < end; ++p) {
@@ -285,48 +283,55 @@ __global__ __launch_bounds__(kThreads) void k_newton_panel(SmallArgs a) {
   }
 }
 
-// A from the blocks' parts: four threads per 16 bytes of a tile add a quarter of the parts each, in order.
+// Where A[i][j] lies among the operands of load_a (j, j + 1 .. of an aligned group of eight side by side).
 template <int MT>
-__global__ __launch_bounds__(256) void k_newton_panel_sum(SmallArgs a, int parts) {
-  using S = Shape<MT>;
-  __shared__ f32x4_t sums[4][64];
+__device__ __forceinline__ int operand_at(int i, int j) {
+  return (((i >> 4) * (MT / 2) + (j >> 5)) * 64 + (i & 15) + 16 * ((j >> 3) & 3)) * 8 + (j & 7);
+}
+
+// A from the blocks' parts: eight threads per 16 bytes of a tile add an eighth of the parts each, in order.
+template <int MT>
+__global__ __launch_bounds__(512) void k_newton_panel_sum(SmallArgs a, int parts) {
+  using S = Shape<MT, 64>;
+  constexpr int SUB = 8;
+  __shared__ f32x4_t sums[SUB][64];
   const int tile = blockIdx.x, lane = threadIdx.x & 63, sub = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const size_t z = blockIdx.y;
   const f32x4_t* p = a.part + (z * parts * S::TILES + tile) * 64 + lane;
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
   constexpr int AHEAD = 8;
-  for (int s0 = sub; s0 < parts; s0 += 4 * AHEAD) {
+  for (int s0 = sub; s0 < parts; s0 += SUB * AHEAD) {
     f32x4_t t[AHEAD];
 #pragma unroll
-    for (int s = 0; s < AHEAD; ++s) t[s] = p[(size_t)min(s0 + 4 * s, parts - 1) * S::TILES * 64];
+    for (int s = 0; s < AHEAD; ++s) t[s] = p[(size_t)min(s0 + SUB * s, parts - 1) * S::TILES * 64];
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s)
-      if (s0 + 4 * s < parts) v += t[s];
+      if (s0 + SUB * s < parts) v += t[s];
   }
   sums[sub][lane] = v;
   __syncthreads();
   if (sub) return;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) v += sums[i][lane];
+  for (int i = 1; i < SUB; ++i) v += sums[i][lane];
   int ti, tj;
   lower_of(tile, ti, tj);
   const uint2 h = pack4_f16(v * (1.0f / (kXScale * kXScale)));
   uint16_t* out = a.square + z * S::M * S::M;
   const int i = ti * 16 + 4 * g, j = tj * 16 + r;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) out[(i + e) * S::M + j] = (uint16_t)((e < 2 ? h.x : h.y) >> (16 * (e & 1)));
-  *reinterpret_cast<uint2*>(out + j * S::M + i) = h;
+  for (int e = 0; e < 4; ++e) out[operand_at<MT>(i + e, j)] = (uint16_t)((e < 2 ? h.x : h.y) >> (16 * (e & 1)));
+  *reinterpret_cast<uint2*>(out + operand_at<MT>(j, i)) = h;
 }
 
 // ---- all steps in one launch
 
 // NP: panels at most. X stays in registers, A passes from step to step through LDS.
-template <int MT, int NP, int DT>
+template <int MT, int PC, int NP, int DT>
 __global__ __launch_bounds__(kThreads) void k_newton_one(SmallArgs a) {
-  using S = Shape<MT>;
-  __shared__ __align__(16) unsigned char buf[kPanel * S::PITCH], square[S::M * S::PITCH];
+  using S = Shape<MT, PC>;
+  __shared__ __align__(16) unsigned char buf[PC * S::PITCH], square[S::M * S::PITCH];
   __shared__ double lds[kWaves];
-  Small<MT> w(a, (lds_u8*)buf);
+  Small<MT, PC> w(a, (lds_u8*)buf);
   const size_t z = blockIdx.x, values = (size_t)a.n * a.m;
   const void* gp = static_cast<const char*>(a.g) + z * values * (DT == kDtF32 ? 4 : 2);
   u32x4_t x[NP][S::RT][S::CT];
@@ -372,7 +377,7 @@ __global__ __launch_bounds__(kThreads) void k_newton_one(SmallArgs a) {
       *(lds_u32x2*)(sq + j * S::PITCH + i * 2) = (u32x2_t){h.x, h.y};
     }
     __syncthreads();
-    w.load_a(sq, S::PITCH);
+    w.load_a((const lds_u8*)sq);
     w.clear_gram();
     const bool last = s + 1 == a.steps;
 #pragma unroll
@@ -389,69 +394,81 @@ __global__ __launch_bounds__(kThreads) void k_newton_one(SmallArgs a) {
   }
 }
 
-template <int MT, int MODE>
+template <int MT, int PC, int MODE>
 hipError_t panel(const SmallArgs& a, int blocks, int batch, int dtype, hipStream_t st) {
   const dim3 grid((unsigned)blocks, (unsigned)batch);
-  if (MODE != kFirst || dtype == kDtBf16) k_newton_panel<MT, MODE, kDtBf16><<<grid, kThreads, 0, st>>>(a);
-  else if (dtype == kDtF32) k_newton_panel<MT, MODE, MODE == kFirst ? kDtF32 : kDtBf16><<<grid, kThreads, 0, st>>>(a);
-  else k_newton_panel<MT, MODE, MODE == kFirst ? kDtF16 : kDtBf16><<<grid, kThreads, 0, st>>>(a);
+  if (MODE != kFirst || dtype == kDtBf16) k_newton_panel<MT, PC, MODE, kDtBf16><<<grid, kThreads, 0, st>>>(a);
+  else if (dtype == kDtF32) k_newton_panel<MT, PC, MODE, MODE == kFirst ? kDtF32 : kDtBf16><<<grid, kThreads, 0, st>>>(a);
+  else k_newton_panel<MT, PC, MODE, MODE == kFirst ? kDtF16 : kDtBf16><<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <int MT>
+template <int MT, int PC>
 hipError_t panels(SmallArgs a, int batch, int dtype, hipStream_t st) {
   const int blocks = (a.panels + a.per_block - 1) / a.per_block;
-  hipError_t e = panel<MT, kFirst>(a, blocks, batch, dtype, st);
+  hipError_t e = panel<MT, PC, kFirst>(a, blocks, batch, dtype, st);
   for (int s = 0; s < a.steps && e == hipSuccess; ++s) {
-    k_newton_panel_sum<MT><<<dim3((unsigned)Shape<MT>::TILES, (unsigned)batch), 256, 0, st>>>(a, blocks);
+    k_newton_panel_sum<MT><<<dim3((unsigned)Shape<MT, 64>::TILES, (unsigned)batch), 512, 0, st>>>(a, blocks);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    e = s + 1 < a.steps ? panel<MT, kStep>(a, blocks, batch, dtype, st) : panel<MT, kLast>(a, blocks, batch, dtype, st);
+    e = s + 1 < a.steps ? panel<MT, PC, kStep>(a, blocks, batch, dtype, st)
+                        : panel<MT, PC, kLast>(a, blocks, batch, dtype, st);
   }
   return e;
 }
 
 template <int MT, int NP>
 hipError_t one(const SmallArgs& a, int batch, int dtype, hipStream_t st) {
-  if (dtype == kDtBf16) k_newton_one<MT, NP, kDtBf16><<<(unsigned)batch, kThreads, 0, st>>>(a);
-  else if (dtype == kDtF32) k_newton_one<MT, NP, kDtF32><<<(unsigned)batch, kThreads, 0, st>>>(a);
-  else k_newton_one<MT, NP, kDtF16><<<(unsigned)batch, kThreads, 0, st>>>(a);
+  if (dtype == kDtBf16) k_newton_one<MT, 64, NP, kDtBf16><<<(unsigned)batch, kThreads, 0, st>>>(a);
+  else if (dtype == kDtF32) k_newton_one<MT, 64, NP, kDtF32><<<(unsigned)batch, kThreads, 0, st>>>(a);
+  else k_newton_one<MT, 64, NP, kDtF16><<<(unsigned)batch, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
 // tile rows the kernels are made for
 inline int tile_rows(int m) { return m <= 32 ? 2 : m <= 64 ? 4 : m <= 128 ? 8 : 16; }
-// panels that one block's registers hold
-inline int most_panels(int m) { return m <= 32 ? 16 : m <= 64 ? 8 : m <= 128 ? 4 : 0; }
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// How a stack is cut in panels: columns of a panel, panels per block. Few panels are halved (256 x 1024 88 -> 81 us, 128 x
+// 320 51 -> 47; of many, their parts of A cost more: 256 x 4096 119 us with 32 columns, 107 with 64). A block takes as many
+// as fill the chip's 256 CUs once and leave at most 128 parts of a matrix's A to add.
+struct PanelCut {
+  int columns, count, per;
+};
+PanelCut cut_of(int m, int n, int batch) {
+  PanelCut c;
+  c.columns = m > 32 && (long long)ceil_div(n, 64) * batch <= 24 ? 32 : 64;
+  c.count = ceil_div(n, c.columns);
+  const int fill = (int)(((long long)c.count * batch + 255) / 256), sums = ceil_div(c.count, 128);
+  c.per = fill > sums ? fill : sums;
+  return c;
+}
 
 }  // namespace
 
-bool newton_in_one(int m, int n) { return (n + kPanel - 1) / kPanel <= most_panels(m); }
-
-// Panels per block: the chip's 256 CUs filled once, and at most 64 parts of a matrix's A to add.
-int newton_per_block(int n, int batch) {
-  const int count = (n + kPanel - 1) / kPanel;
-  const int fill = (int)(((long long)count * batch + 255) / 256), sums = (count + 63) / 64;
-  const int per = fill > sums ? fill : sums;
-  return per < count ? per : count;
+// Panels of 64 columns that one block takes through all steps sooner than two launches a step do: few, or more in a
+// large stack, whose matrices run side by side.
+bool newton_in_one(int m, int n, int batch) {
+  const int most = m <= 32 ? 16 : m <= 64 ? 8 : m <= 128 ? 4 : 0;
+  return ceil_div(n, 64) <= (batch >= 32 ? most : most / 2);
 }
 
 SmallLayout newton_small_layout(int m, int n, int batch) {
   SmallLayout L;
-  const size_t count = (n + kPanel - 1) / kPanel, M = 16 * tile_rows(m), tiles = M / 16 * (M / 16 + 1) / 2;
-  const int per = newton_per_block(n, batch);
+  const size_t M = 16 * tile_rows(m), tiles = M / 16 * (M / 16 + 1) / 2;
+  const PanelCut c = cut_of(m, n, batch);
   L.state = 0;
-  L.square = align256(count * kPanel * M * 4 * batch);
+  L.square = align256((size_t)c.count * c.columns * M * 4 * batch);
   L.norm = L.square + align256(M * M * 2 * batch);
   L.part = L.norm + align256(sizeof(double) * kNormBlocks * batch);
-  L.total = L.part + align256((count + per - 1) / per * tiles * 1024 * batch);
+  L.total = L.part + align256((size_t)ceil_div(c.count, c.per) * tiles * 1024 * batch);
   return L;
 }
 
 hipError_t launch_newton_one(SmallArgs a, int batch, int dtype, hipStream_t st) {
-  if (a.m > a.n || !newton_in_one(a.m, a.n) || batch <= 0) return hipErrorInvalidValue;
-  a.panels = (a.n + kPanel - 1) / kPanel;
+  if (a.m > a.n || batch <= 0 || !newton_in_one(a.m, a.n, batch)) return hipErrorInvalidValue;
+  a.panels = ceil_div(a.n, 64);
   if (a.m <= 32) return one<2, 16>(a, batch, dtype, st);
   if (a.m <= 64) return one<4, 8>(a, batch, dtype, st);
   return one<8, 4>(a, batch, dtype, st);
@@ -459,13 +476,15 @@ hipError_t launch_newton_one(SmallArgs a, int batch, int dtype, hipStream_t st) 
 
 hipError_t launch_newton_panels(SmallArgs a, int batch, int dtype, hipStream_t st) {
   if (a.m > a.n || a.m > kNewtonSmall || batch <= 0 || batch > 65535) return hipErrorInvalidValue;
-  a.panels = (a.n + kPanel - 1) / kPanel;
-  a.per_block = newton_per_block(a.n, batch);
+  const PanelCut c = cut_of(a.m, a.n, batch);
+  a.panels = c.count;
+  a.per_block = c.per;
+  const bool narrow = c.columns == 32;
   switch (tile_rows(a.m)) {
-    case 2: return panels<2>(a, batch, dtype, st);
-    case 4: return panels<4>(a, batch, dtype, st);
-    case 8: return panels<8>(a, batch, dtype, st);
-    default: return panels<16>(a, batch, dtype, st);
+    case 2: return panels<2, 64>(a, batch, dtype, st);
+    case 4: return narrow ? panels<4, 32>(a, batch, dtype, st) : panels<4, 64>(a, batch, dtype, st);
+    case 8: return narrow ? panels<8, 32>(a, batch, dtype, st) : panels<8, 64>(a, batch, dtype, st);
+    default: return narrow ? panels<16, 32>(a, batch, dtype, st) : panels<16, 64>(a, batch, dtype, st);
   }
 }
 
