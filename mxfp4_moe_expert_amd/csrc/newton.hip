@@ -148,25 +148,26 @@ __device__ __forceinline__ void dense_epilogue(const NsArgs& a, const f32x4_t (&
   }
 }
 
-// Tile of block bid among those of a symmetric product that reach the diagonal or lie below it, SH = BM / BN of them
-// more in each row than in the one before (a contiguous run of them per XCD, as in dense_tile).
-template <int SH>
-__device__ __forceinline__ void lower_tile(int bid, int tiles, int& im, int& in) {
+// Tiles of a symmetric product of m rows in tile row i: those that reach the diagonal or lie below it.
+template <int BM, int BN>
+__host__ __device__ inline int tiles_in_row(int i, int m) {
+  const int reach = ((i + 1) * BM + BN - 1) / BN, all = (m + BN - 1) / BN;
+  return reach < all ? reach : all;
+}
+// Tile of block bid (a contiguous run of tiles per XCD, as in dense_tile).
+template <int BM, int BN>
+__device__ __forceinline__ void lower_tile(int bid, int tiles, int m, int& im, int& in) {
   const int per = tiles >> 3, extra = tiles & 7, x = bid & 7;
-  const int t = x * per + min(x, extra) + (bid >> 3);
-  // SH i (i + 1) / 2 tiles lie above row i
-  int i = (int)((__builtin_amdgcn_sqrtf(8.0f * (float)t / SH + 1.0f) - 1.0f) * 0.5f);
-  while (SH * i * (i + 1) / 2 > t) --i;
-  while (SH * (i + 1) * (i + 2) / 2 <= t) ++i;
-  im = i;
-  in = t - SH * i * (i + 1) / 2;
+  in = x * per + min(x, extra) + (bid >> 3);
+  im = 0;
+  while (in >= tiles_in_row<BM, BN>(im, m)) in -= tiles_in_row<BM, BN>(im++, m);
 }
 
 template <bool XT, bool WT, int BM, int BN, int NX, int NW, int EPI>
 __global__ __launch_bounds__(512) void k_newton(NsArgs a) {
   int im, in;
   if constexpr (EPI == kNsNext || EPI == kNsLast) dense_tile(blockIdx.x, a.tm, a.tn, im, in);
-  else lower_tile<BM / BN>(blockIdx.x, gridDim.x, im, in);
+  else lower_tile<BM, BN>(blockIdx.x, gridDim.x, a.M, im, in);
   dense_block<XT, WT, BM, BN, 2, 4, NX, NW, kDenseF16, EPI>(a, im, in);
 }
 
@@ -291,7 +292,8 @@ inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 struct Tile {
   int bm, bn, nx, nw;
 };
-constexpr Tile kTiles[] = {{256, 256, 3, 2}, {256, 128, 3, 3}, {128, 128, 4, 4}, {64, 128, 3, 3}};
+constexpr Tile kTiles[] = {{256, 256, 3, 2}, {256, 128, 3, 3}, {128, 128, 4, 4}, {64, 128, 3, 3}, {192, 128, 4, 4}};
+constexpr int kNumTiles = 5;
 
 template <bool XT, bool WT, int T, int EPI>
 hipError_t run(const NsArgs& a, int blocks, int slices, int batch, hipStream_t st) {
@@ -304,28 +306,40 @@ hipError_t run(const NsArgs& a, int blocks, int slices, int batch, hipStream_t s
   return hipGetLastError();
 }
 
-// Microseconds per stage of a tile with few and with all CUs at work (dense.hip), and of the rest of a block.
-constexpr double kFewUs[4] = {0.95, 0.47, 0.32, 0.26}, kFullUs[4] = {1.45, 0.80, 0.47, 0.34}, kStartUs = 4.5;
+// Microseconds per stage of a tile with few and with all CUs at work (dense.hip; 192 x 128: between its neighbours), and
+// of the rest of a block.
+constexpr double kFewUs[kNumTiles] = {0.95, 0.47, 0.32, 0.26, 0.40}, kFullUs[kNumTiles] = {1.45, 0.80, 0.47, 0.34, 0.64};
+constexpr double kStartUs = 4.5;
 inline double stage_us(int tile, double blocks) {
   const double full = blocks < 256 ? blocks / 256 : 1.0;
   return kFewUs[tile] + full * (kFullUs[tile] - kFewUs[tile]);
 }
 
+template <int T>
+int lower_tiles_of(int m) {
+  int n = 0;
+  for (int i = 0; i * kTiles[T].bm < m; ++i) n += tiles_in_row<kTiles[T].bm, kTiles[T].bn>(i, m);
+  return n;
+}
 inline int lower_tiles(int tile, int m) {
-  const int sh = kTiles[tile].bm / kTiles[tile].bn, n = ceil_div(m, kTiles[tile].bm);
-  // the last row may end before its last column of tiles
-  return sh * n * (n + 1) / 2 - (sh * n - ceil_div(m, kTiles[tile].bn));
+  switch (tile) {
+    case 0: return lower_tiles_of<0>(m);
+    case 1: return lower_tiles_of<1>(m);
+    case 2: return lower_tiles_of<2>(m);
+    default: return lower_tiles_of<4>(m);
+  }
 }
 
-// How a symmetric product is cut: tile (0 to 2) and slices of K.
+// How a symmetric product is cut: tile (not 64 x 128) and slices of K.
 struct Cut {
   int tile, slices;
 };
-Cut symmetric_cut(int m, int K, int batch, bool split) {
+Cut symmetric_cut(int m, int K, int batch, bool split, bool transposed) {
   const int stages = ceil_div(K, 64);
   Cut best = {2, 1};
   double best_us = 1e30;
-  for (int t = 0; t < 3; ++t) {
+  for (int t : {0, 1, 2, 4}) {
+    if (t == 4 && transposed) continue;  // a transposed operand's rows are a power of two
     const int tiles = lower_tiles(t, m);
     for (int s = 1; s == 1 || (split && s <= 16 && s * 4 <= stages + 3); s *= 2) {
       const int per = ceil_div(stages, s), slices = ceil_div(stages, per);
@@ -340,8 +354,8 @@ Cut symmetric_cut(int m, int K, int batch, bool split) {
   }
   return best;
 }
-inline size_t partial_bytes(int m, int K, int batch) {
-  const Cut c = symmetric_cut(m, K, batch, true);
+inline size_t partial_bytes(int m, int K, int batch, bool tall) {
+  const Cut c = symmetric_cut(m, K, batch, true, tall);
   return c.slices > 1 ? (size_t)c.slices * batch * m * m * sizeof(float) : 0;
 }
 
@@ -352,12 +366,14 @@ hipError_t symmetric(NsArgs a, const Cut& cut, int batch, hipStream_t st) {
   const int tiles = lower_tiles(cut.tile, a.M);
   if (cut.tile == 0) return run<TRANSPOSED, TRANSPOSED, 0, EPI>(a, tiles, cut.slices, batch, st);
   if (cut.tile == 1) return run<TRANSPOSED, TRANSPOSED, 1, EPI>(a, tiles, cut.slices, batch, st);
+  if constexpr (!TRANSPOSED)
+    if (cut.tile == 4) return run<false, false, 4, EPI>(a, tiles, cut.slices, batch, st);
   return run<TRANSPOSED, TRANSPOSED, 2, EPI>(a, tiles, cut.slices, batch, st);
 }
 
 // A = X X^T or X^T X
 hipError_t gram_of(const NsArgs& a, bool tall, int batch, hipStream_t st) {
-  const Cut cut = symmetric_cut(a.M, a.K, batch, true);
+  const Cut cut = symmetric_cut(a.M, a.K, batch, true, tall);
   if (cut.slices == 1)
     return tall ? symmetric<true, kNsGram>(a, cut, batch, st) : symmetric<false, kNsGram>(a, cut, batch, st);
   const hipError_t e =
@@ -424,10 +440,10 @@ Layout layout_of(int B, int R, int C) {
   L.poly = take(2 * L.sq * L.chunk);
   L.norm = take(sizeof(double) * kNormBlocks * L.chunk);
   // the last part of a stack may be shorter, and cut otherwise
-  const int K = L.Rp > L.Cp ? L.Rp : L.Cp, rest = B % L.chunk;
-  size_t p = partial_bytes(L.m, K, L.chunk);
-  if (rest) p = p > partial_bytes(L.m, K, rest) ? p : partial_bytes(L.m, K, rest);
-  L.part = take(p);
+  const bool tall = L.Rp > L.Cp;
+  const int K = tall ? L.Rp : L.Cp, rest = B % L.chunk;
+  const size_t p = partial_bytes(L.m, K, L.chunk, tall), q = rest ? partial_bytes(L.m, K, rest, tall) : 0;
+  L.part = take(p > q ? p : q);
   L.total = o;
   return L;
 }
@@ -567,7 +583,7 @@ hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
       p.in_ld = L.m;
       p.in_batch = L.sq;
       p.hi_out = poly;
-      e = symmetric<false, kNsPoly>(p, symmetric_cut(L.m, L.m, count, false), count, st);
+      e = symmetric<false, kNsPoly>(p, symmetric_cut(L.m, L.m, count, false, false), count, st);
       if (e != hipSuccess) return e;
       // a X + (b A + c A A) X; tall: a X + X (b A + c A A)
       p.x = tall ? x : poly;
