@@ -1,8 +1,8 @@
 // Newton-Schulz orthogonalisation of a stack of matrices on gfx950: with
 // X = G / (|G|_F + eps), `steps` times
 //   A = X X^T,  X = a X + (b A + c A A) X
-// (of a matrix taller than wide A = X^T X and X = a X + X (b A + c A A)), which
-// drives the singular values of X towards 1 and keeps its singular vectors.
+// (of a matrix taller than wide, on its transpose), which drives the singular
+// values of X towards 1 and keeps its singular vectors.
 //
 // The products run in fp16 on the tile product of dense.h, sums in fp32. What
 // has to be more exact is the term a X: a small singular value grows by a in
@@ -31,6 +31,7 @@ struct NsArgs : DenseArgs {
   const uint16_t *hi, *lo;        // kNsPoly: hi is A
   uint16_t *hi_out, *lo_out;      // lo_out may be null
   int in_ld, out_ld;              // values per row of hi / lo, and of out
+  int flip;                       // kNsLast: out is [N][M]
 
   __device__ const void* x_base() const { return static_cast<const char*>(x) + blockIdx.z * x_batch; }
   __device__ const void* w_base() const { return static_cast<const char*>(w) + blockIdx.z * w_batch; }
@@ -61,7 +62,8 @@ __device__ __forceinline__ void unpack8_f16(const u32x4_t& p, f32x4_t& lo, f32x4
 __device__ __forceinline__ u32x4_t both(const uint2& a, const uint2& b) { return (u32x4_t){a.x, a.y, b.x, b.y}; }
 
 // Lane (r, g) takes eight consecutive columns of row m0 + 16 c + r at a time, from two blocks of 16. What it reads of the
-// next 16 rows is requested before this one's stores, which the compiler may not move loads across.
+// next row blocks is requested ahead of this one's stores, which the compiler may not move loads across, in the registers
+// that the product no longer needs: with one row block ahead the reads' latency bounds the epilogue.
 template <int EPI, int MB, int NB>
 __device__ __forceinline__ void dense_epilogue(const NsArgs& a, const f32x4_t (&acc)[NB][MB], int m0, int n0, int lane) {
   static_assert(NB % 2 == 0, "columns are taken by pairs of blocks");
@@ -76,28 +78,36 @@ __device__ __forceinline__ void dense_epilogue(const NsArgs& a, const f32x4_t (&
   constexpr bool READS = EPI != kNsGram;
   const uint16_t* hi = READS ? a.hi + z * a.in_batch : nullptr;
   const uint16_t* lo = EPI == kNsNext ? a.lo + z * a.in_batch : nullptr;
-  u32x4_t hv[2][NP], lv[2][NP];
+  constexpr int AHEAD = MB < 4 ? MB : 4;
+  u32x4_t hv[AHEAD][NP], lv[AHEAD][NP];
   auto fetch = [&](int c) {  // past the edges: the last row, the first columns (never stored)
     const size_t row = (size_t)min(m0 + c * 16 + r, a.M - 1) * a.in_ld;
 #pragma unroll
     for (int b = 0; b < NP; ++b) {
       const int n = n0 + b * 32 + 8 * g, col = n < a.N ? n : 0;
-      if constexpr (READS) hv[c & 1][b] = *reinterpret_cast<const u32x4_t*>(hi + row + col);
-      if constexpr (EPI == kNsNext) lv[c & 1][b] = *reinterpret_cast<const u32x4_t*>(lo + row + col);
+      if constexpr (READS) hv[c % AHEAD][b] = *reinterpret_cast<const u32x4_t*>(hi + row + col);
+      if constexpr (EPI == kNsNext) lv[c % AHEAD][b] = *reinterpret_cast<const u32x4_t*>(lo + row + col);
     }
   };
-  fetch(0);
+#pragma unroll
+  for (int c = 0; c < AHEAD; ++c) fetch(c);
 #pragma unroll
   for (int c = 0; c < MB; ++c) {
-    if (c + 1 < MB) fetch(c + 1);
     const int m = m0 + c * 16 + r;
+    u32x4_t hc[NP], lc[NP];
+#pragma unroll
+    for (int b = 0; b < NP; ++b) {
+      hc[b] = hv[c % AHEAD][b];
+      lc[b] = lv[c % AHEAD][b];
+    }
+    if (c + AHEAD < MB) fetch(c + AHEAD);
 #pragma unroll
     for (int b = 0; b < NP; ++b) {
       const int n = n0 + b * 32 + 8 * g;
       const bool live = m < a.M && n < a.N;
       f32x4_t v0, v1, x0, x1;
       join_values(acc[2 * b][c], acc[2 * b + 1][c], v0, v1);
-      if constexpr (READS) unpack8_f16(hv[c & 1][b], x0, x1);
+      if constexpr (READS) unpack8_f16(hc[b], x0, x1);
       if constexpr (EPI == kNsGram || EPI == kNsPoly) {
         // the tile and its mirror image; M and N are the same multiple of 8
         if constexpr (EPI == kNsGram) {
@@ -118,7 +128,7 @@ __device__ __forceinline__ void dense_epilogue(const NsArgs& a, const f32x4_t (&
         }
       } else if constexpr (EPI == kNsNext) {
         f32x4_t l0, l1;
-        unpack8_f16(lv[c & 1][b], l0, l1);
+        unpack8_f16(lc[b], l0, l1);
         v0 += (x0 + l0) * a.ca;
         v1 += (x1 + l1) * a.ca;
         const size_t at = z * a.out_batch + (size_t)m * a.out_ld + n;
@@ -132,15 +142,28 @@ __device__ __forceinline__ void dense_epilogue(const NsArgs& a, const f32x4_t (&
         v0 = (v0 + x0 * a.ca) * (1.0f / kXScale);
         v1 = (v1 + x1 * a.ca) * (1.0f / kXScale);
         uint16_t* out = static_cast<uint16_t*>(a.out) + z * a.out_batch;
-        const size_t at = (size_t)m * a.out_ld + n;
-        if (!live) continue;
-        if ((a.out_ld & 7) == 0) {
-          *reinterpret_cast<u32x4_t*>(out + at) = both(pack4_bf16(v0), pack4_bf16(v1));
-        } else {
+        const uint2 p0 = pack4_bf16(v0), p1 = pack4_bf16(v1);
+        auto four = [&](size_t at, const uint2& p, int left) {  // values at .. at + 3, of which `left` exist
+          if (left >= 4 && (a.out_ld & 3) == 0) {
+            *reinterpret_cast<uint2*>(out + at) = p;
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (n + i < a.N) out[at + i] = f32_to_bf16(v0[i]);
-            if (n + 4 + i < a.N) out[at + 4 + i] = f32_to_bf16(v1[i]);
+            for (int i = 0; i < 4; ++i)
+              if (i < left) out[at + i] = (uint16_t)((i < 2 ? p.x : p.y) >> (16 * (i & 1)));
+          }
+        };
+        if (a.flip) {
+          const uint2 t0 = quad_transpose(p0, lane), t1 = quad_transpose(p1, lane);
+          const int mt = m0 + c * 16 + (r & 12), nt = n + (r & 3);
+          if (nt < a.N) four((size_t)nt * a.out_ld + mt, t0, a.M - mt);
+          if (nt + 4 < a.N) four((size_t)(nt + 4) * a.out_ld + mt, t1, a.M - mt);
+        } else if (live) {
+          const size_t at = (size_t)m * a.out_ld + n;
+          if ((a.out_ld & 7) == 0) {
+            *reinterpret_cast<u32x4_t*>(out + at) = both(p0, p1);
+          } else {
+            four(at, p0, a.N - n);
+            four(at + 4, p1, a.N - n - 4);
           }
         }
       }
@@ -163,12 +186,12 @@ __device__ __forceinline__ void lower_tile(int bid, int tiles, int m, int& im, i
   while (in >= tiles_in_row<BM, BN>(im, m)) in -= tiles_in_row<BM, BN>(im++, m);
 }
 
-template <bool XT, bool WT, int BM, int BN, int NX, int NW, int EPI>
+template <bool WT, int BM, int BN, int NX, int NW, int EPI>
 __global__ __launch_bounds__(512) void k_newton(NsArgs a) {
   int im, in;
   if constexpr (EPI == kNsNext || EPI == kNsLast) dense_tile(blockIdx.x, a.tm, a.tn, im, in);
   else lower_tile<BM, BN>(blockIdx.x, gridDim.x, a.M, im, in);
-  dense_block<XT, WT, BM, BN, 2, 4, NX, NW, kDenseF16, EPI>(a, im, in);
+  dense_block<false, WT, BM, BN, 2, 4, NX, NW, kDenseF16, EPI>(a, im, in);
 }
 
 // A from the partial sums of a split K, [slice][matrix][m][m] of which the tiles k_newton computed exist: a thread adds
@@ -231,11 +254,22 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_norm(const void* g, siz
   const u32x4_t* body = reinterpret_cast<const u32x4_t*>(p + head * SIZE);
   double s = 0.0;
   const size_t step = (size_t)gridDim.x * kNormThreads;
-  for (size_t i = (size_t)blockIdx.x * kNormThreads + threadIdx.x; i < pieces; i += step) {
-    double v[8];
-    eight_values<DT>(body + i * (SIZE / 2), v);
+  const size_t first = (size_t)blockIdx.x * kNormThreads + threadIdx.x;
+  constexpr int AHEAD = 4;  // loads in flight together
+  for (size_t i = first; i < pieces; i += AHEAD * step) {
+    u32x4_t p[AHEAD][SIZE / 2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += v[j] * v[j];
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+      for (int h = 0; h < (int)SIZE / 2; ++h)
+        p[k][h] = i + k * step < pieces ? body[(i + k * step) * (SIZE / 2) + h] : (u32x4_t){0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      double v[8];
+      eight_values<DT>(p[k], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j] * v[j];
+    }
   }
   if (blockIdx.x == 0) {
     const size_t ends = head + (n - tail);  // fewer than 16
@@ -284,6 +318,39 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_first(const void* g, in
   }
 }
 
+// The same of a matrix taller than wide, stored by its columns: a block takes 64 x 64 values through LDS.
+template <int DT>
+__global__ __launch_bounds__(kNormThreads) void k_newton_first_tall(const void* g, int R, int C, int m, int n,
+                                                                    const double* part, int parts, double eps,
+                                                                    uint16_t* hi, uint16_t* lo) {
+  constexpr size_t SIZE = DT == kDtF32 ? 4 : 2;
+  constexpr int LD = 72;  // values per row of the LDS tile
+  __shared__ double lds[kNormThreads / 64];
+  __shared__ __align__(16) uint16_t th[64][LD], tl[64][LD];
+  const int z = blockIdx.z;
+  const double sum =
+      block_sum<kNormThreads / 64>((int)threadIdx.x < parts ? part[(size_t)z * parts + threadIdx.x] : 0.0, lds);
+  const double inv = (double)kXScale / (__builtin_sqrt(sum) + eps);
+  const char* p = static_cast<const char*>(g) + (size_t)z * R * C * SIZE;
+  const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64, c = c0 + (int)(threadIdx.x & 63);
+#pragma unroll 8
+  for (int i = threadIdx.x >> 6; i < 64; i += kNormThreads / 64) {
+    const int r = r0 + i;
+    const float v = r < R && c < C ? (float)(value_at<DT>(p, (size_t)r * C + c) * inv) : 0.0f;
+    const _Float16 h = (_Float16)v;
+    th[c - c0][i] = __builtin_bit_cast(uint16_t, h);
+    tl[c - c0][i] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)h));
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * 8; i += kNormThreads) {
+    const int row = i >> 3, col = (i & 7) * 8;
+    if (c0 + row >= m || r0 + col >= n) continue;  // m and n are multiples of 8
+    const size_t at = ((size_t)z * m + c0 + row) * n + r0 + col;
+    *reinterpret_cast<u32x4_t*>(hi + at) = *reinterpret_cast<const u32x4_t*>(&th[row][col]);
+    *reinterpret_cast<u32x4_t*>(lo + at) = *reinterpret_cast<const u32x4_t*>(&tl[row][col]);
+  }
+}
+
 // ---- host
 
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -295,10 +362,10 @@ struct Tile {
 constexpr Tile kTiles[] = {{256, 256, 3, 2}, {256, 128, 3, 3}, {128, 128, 4, 4}, {64, 128, 3, 3}, {192, 128, 4, 4}};
 constexpr int kNumTiles = 5;
 
-template <bool XT, bool WT, int T, int EPI>
+template <bool WT, int T, int EPI>
 hipError_t run(const NsArgs& a, int blocks, int slices, int batch, hipStream_t st) {
   constexpr Tile t = kTiles[T];
-  constexpr auto kernel = &k_newton<XT, WT, t.bm, t.bn, t.nx, t.nw, EPI>;
+  constexpr auto kernel = &k_newton<WT, t.bm, t.bn, t.nx, t.nw, EPI>;
   constexpr int lds = (t.nx * t.bm + t.nw * t.bn) * kStageB;
   const hipError_t e = allow_lds<kernel>(lds);
   if (e != hipSuccess) return e;
@@ -334,12 +401,11 @@ inline int lower_tiles(int tile, int m) {
 struct Cut {
   int tile, slices;
 };
-Cut symmetric_cut(int m, int K, int batch, bool split, bool transposed) {
+Cut symmetric_cut(int m, int K, int batch, bool split) {
   const int stages = ceil_div(K, 64);
   Cut best = {2, 1};
   double best_us = 1e30;
   for (int t : {0, 1, 2, 4}) {
-    if (t == 4 && transposed) continue;  // a transposed operand's rows are a power of two
     const int tiles = lower_tiles(t, m);
     for (int s = 1; s == 1 || (split && s <= 16 && s * 4 <= stages + 3); s *= 2) {
       const int per = ceil_div(stages, s), slices = ceil_div(stages, per);
@@ -354,30 +420,27 @@ Cut symmetric_cut(int m, int K, int batch, bool split, bool transposed) {
   }
   return best;
 }
-inline size_t partial_bytes(int m, int K, int batch, bool tall) {
-  const Cut c = symmetric_cut(m, K, batch, true, tall);
+inline size_t partial_bytes(int m, int K, int batch) {
+  const Cut c = symmetric_cut(m, K, batch, true);
   return c.slices > 1 ? (size_t)c.slices * batch * m * m * sizeof(float) : 0;
 }
 
-template <bool TRANSPOSED, int EPI>
+template <int EPI>
 hipError_t symmetric(NsArgs a, const Cut& cut, int batch, hipStream_t st) {
   a.stages = ceil_div(a.K, 64);
   a.slice_stages = ceil_div(a.stages, cut.slices);
   const int tiles = lower_tiles(cut.tile, a.M);
-  if (cut.tile == 0) return run<TRANSPOSED, TRANSPOSED, 0, EPI>(a, tiles, cut.slices, batch, st);
-  if (cut.tile == 1) return run<TRANSPOSED, TRANSPOSED, 1, EPI>(a, tiles, cut.slices, batch, st);
-  if constexpr (!TRANSPOSED)
-    if (cut.tile == 4) return run<false, false, 4, EPI>(a, tiles, cut.slices, batch, st);
-  return run<TRANSPOSED, TRANSPOSED, 2, EPI>(a, tiles, cut.slices, batch, st);
+  if (cut.tile == 0) return run<false, 0, EPI>(a, tiles, cut.slices, batch, st);
+  if (cut.tile == 1) return run<false, 1, EPI>(a, tiles, cut.slices, batch, st);
+  if (cut.tile == 4) return run<false, 4, EPI>(a, tiles, cut.slices, batch, st);
+  return run<false, 2, EPI>(a, tiles, cut.slices, batch, st);
 }
 
-// A = X X^T or X^T X
-hipError_t gram_of(const NsArgs& a, bool tall, int batch, hipStream_t st) {
-  const Cut cut = symmetric_cut(a.M, a.K, batch, true, tall);
-  if (cut.slices == 1)
-    return tall ? symmetric<true, kNsGram>(a, cut, batch, st) : symmetric<false, kNsGram>(a, cut, batch, st);
-  const hipError_t e =
-      tall ? symmetric<true, kNsPartial>(a, cut, batch, st) : symmetric<false, kNsPartial>(a, cut, batch, st);
+// A = X X^T
+hipError_t gram_of(const NsArgs& a, int batch, hipStream_t st) {
+  const Cut cut = symmetric_cut(a.M, a.K, batch, true);
+  if (cut.slices == 1) return symmetric<kNsGram>(a, cut, batch, st);
+  const hipError_t e = symmetric<kNsPartial>(a, cut, batch, st);
   if (e != hipSuccess) return e;
   // every tile is whole in rows and columns of the tile's longer side
   const long long threads = (long long)a.M * (a.N / 4);
@@ -386,13 +449,14 @@ hipError_t gram_of(const NsArgs& a, bool tall, int batch, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <bool WT, int EPI>
+// (b A + c A A) X
+template <int EPI>
 hipError_t general(NsArgs a, int batch, hipStream_t st) {
   a.stages = a.slice_stages = ceil_div(a.K, 64);
   constexpr double kPairUs = 0.56;  // 64 x 128: a stage of both blocks of a CU
   int best = 0;
   double best_us = 1e30;
-  for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < kNumTiles; ++t) {
     const long long n = (long long)ceil_div(a.M, kTiles[t].bm) * ceil_div(a.N, kTiles[t].bn) * batch;
     const int places = t == 3 ? 512 : 256;
     const double stage = t == 3 && n > 256 ? kPairUs : stage_us(t, (double)n);
@@ -405,24 +469,25 @@ hipError_t general(NsArgs a, int batch, hipStream_t st) {
   a.tm = ceil_div(a.M, kTiles[best].bm);
   a.tn = ceil_div(a.N, kTiles[best].bn);
   const int blocks = a.tm * a.tn;
-  if (best == 0) return run<false, WT, 0, EPI>(a, blocks, 1, batch, st);
-  if (best == 1) return run<false, WT, 1, EPI>(a, blocks, 1, batch, st);
-  if (best == 2) return run<false, WT, 2, EPI>(a, blocks, 1, batch, st);
-  return run<false, WT, 3, EPI>(a, blocks, 1, batch, st);
+  if (best == 0) return run<true, 0, EPI>(a, blocks, 1, batch, st);
+  if (best == 4) return run<true, 4, EPI>(a, blocks, 1, batch, st);
+  if (best == 1) return run<true, 1, EPI>(a, blocks, 1, batch, st);
+  if (best == 2) return run<true, 2, EPI>(a, blocks, 1, batch, st);
+  return run<true, 3, EPI>(a, blocks, 1, batch, st);
 }
 
-// Matrices of a stack are worked on `chunk` at a time, so that the workspace stays below about 1 GB.
+// X is held wide, m x n with m <= n, m and n padded to multiples of 8 (a taller matrix by its columns). Matrices of a stack
+// are worked on `chunk` at a time, so that the workspace stays below about 1 GB.
 struct Layout {
-  int chunk, Rp, Cp, m;  // m: the shorter side, padded
-  size_t x, sq;          // values of an X and of a square matrix
+  int chunk, m, n;
+  size_t x, sq;  // values of an X and of a square matrix
   size_t hi0, hi1, lo, gram, poly, norm, part, total;
 };
 Layout layout_of(int B, int R, int C) {
   Layout L;
-  L.Rp = (R + 7) & ~7;
-  L.Cp = (C + 7) & ~7;
-  L.m = L.Rp <= L.Cp ? L.Rp : L.Cp;
-  L.x = (size_t)L.Rp * L.Cp;
+  L.m = ((R < C ? R : C) + 7) & ~7;
+  L.n = ((R < C ? C : R) + 7) & ~7;
+  L.x = (size_t)L.m * L.n;
   L.sq = (size_t)L.m * L.m;
   const size_t each = 2 * (3 * L.x + 2 * L.sq);
   const size_t most = ((size_t)1 << 30) / each;
@@ -440,9 +505,8 @@ Layout layout_of(int B, int R, int C) {
   L.poly = take(2 * L.sq * L.chunk);
   L.norm = take(sizeof(double) * kNormBlocks * L.chunk);
   // the last part of a stack may be shorter, and cut otherwise
-  const bool tall = L.Rp > L.Cp;
-  const int K = tall ? L.Rp : L.Cp, rest = B % L.chunk;
-  const size_t p = partial_bytes(L.m, K, L.chunk, tall), q = rest ? partial_bytes(L.m, K, rest, tall) : 0;
+  const int rest = B % L.chunk;
+  const size_t p = partial_bytes(L.m, L.n, L.chunk), q = rest ? partial_bytes(L.m, L.n, rest) : 0;
   L.part = take(p > q ? p : q);
   L.total = o;
   return L;
@@ -462,9 +526,14 @@ hipError_t first(const NewtonArgs& n, const Layout& L, const void* g, int count,
   const size_t values = (size_t)n.R * n.C;
   const hipError_t e = norm_of<DT>(g, values, count, norm, st);
   if (e != hipSuccess) return e;
+  if (n.R > n.C) {
+    k_newton_first_tall<DT><<<dim3((unsigned)ceil_div(L.n, 64), (unsigned)ceil_div(L.m, 64), (unsigned)count), kNormThreads,
+                              0, st>>>(g, n.R, n.C, L.m, L.n, norm, norm_parts(values), n.eps, hi, lo);
+    return hipGetLastError();
+  }
   const size_t nb = (L.x / 8 + kNormThreads - 1) / kNormThreads;
   k_newton_first<DT><<<dim3((unsigned)(nb < 2048 ? nb : 2048), (unsigned)count), kNormThreads, 0, st>>>(
-      g, n.R, n.C, L.Rp, L.Cp, norm, norm_parts(values), n.eps, hi, lo);
+      g, n.R, n.C, L.m, L.n, norm, norm_parts(values), n.eps, hi, lo);
   return hipGetLastError();
 }
 
@@ -545,7 +614,6 @@ hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
   uint16_t* gram = reinterpret_cast<uint16_t*>(ws + L.gram);
   uint16_t* poly = reinterpret_cast<uint16_t*>(ws + L.poly);
   double* norm = reinterpret_cast<double*>(ws + L.norm);
-  const bool tall = L.Rp > L.Cp;
   const size_t each = (size_t)n.R * n.C, size = n.dtype == kDtF32 ? 4 : 2;
   for (int b = 0; b < n.B; b += L.chunk) {
     const int count = n.B - b < L.chunk ? n.B - b : L.chunk;
@@ -561,16 +629,16 @@ hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
       __builtin_memset(&p, 0, sizeof(p));
       // A
       p.x = p.w = x;
-      p.x_ld = p.w_ld = (uint32_t)L.Cp * 2;
+      p.x_ld = p.w_ld = (uint32_t)L.n * 2;
       p.x_batch = p.w_batch = L.x * 2;
       p.M = p.N = L.m;
-      p.K = tall ? L.Rp : L.Cp;
+      p.K = L.n;
       p.ca = 1.0f / (kXScale * kXScale);
       p.hi_out = gram;
       p.out_ld = L.m;
       p.out_batch = L.sq;
       p.part = reinterpret_cast<float*>(ws + L.part);
-      e = gram_of(p, tall, count, st);
+      e = gram_of(p, count, st);
       if (e != hipSuccess) return e;
       // b A + c A A
       p.x = p.w = gram;
@@ -583,30 +651,27 @@ hipError_t launch_newton(const NewtonArgs& n, hipStream_t st) {
       p.in_ld = L.m;
       p.in_batch = L.sq;
       p.hi_out = poly;
-      e = symmetric<false, kNsPoly>(p, symmetric_cut(L.m, L.m, count, false, false), count, st);
+      e = symmetric<kNsPoly>(p, symmetric_cut(L.m, L.m, count, false), count, st);
       if (e != hipSuccess) return e;
-      // a X + (b A + c A A) X; tall: a X + X (b A + c A A)
-      p.x = tall ? x : poly;
-      p.w = tall ? poly : x;
-      p.x_ld = (uint32_t)(tall ? L.Cp : L.m) * 2;
-      p.w_ld = (uint32_t)(tall ? L.m : L.Cp) * 2;
-      p.x_batch = (tall ? L.x : L.sq) * 2;
-      p.w_batch = (tall ? L.sq : L.x) * 2;
-      p.M = last ? n.R : L.Rp;
-      p.N = last ? n.C : L.Cp;
-      p.K = L.m;
+      // a X + (b A + c A A) X
+      p.x = poly;
+      p.w = x;
+      p.w_ld = (uint32_t)L.n * 2;
+      p.w_batch = L.x * 2;
+      p.flip = n.R > n.C;
+      p.M = last ? (p.flip ? n.C : n.R) : L.m;
+      p.N = last ? (p.flip ? n.R : n.C) : L.n;
       p.ca = (float)n.a;
       p.hi = x;
-      p.in_ld = L.Cp;
+      p.in_ld = L.n;
       p.in_batch = L.x;
       p.lo = last ? nullptr : lo;
       p.hi_out = y;
       p.lo_out = i + 2 < n.steps ? lo : nullptr;
       p.out = n.out + (size_t)b * each;
-      p.out_ld = last ? n.C : L.Cp;
+      p.out_ld = last ? n.C : L.n;
       p.out_batch = last ? each : L.x;
-      if (last) e = tall ? general<false, kNsLast>(p, count, st) : general<true, kNsLast>(p, count, st);
-      else e = tall ? general<false, kNsNext>(p, count, st) : general<true, kNsNext>(p, count, st);
+      e = last ? general<kNsLast>(p, count, st) : general<kNsNext>(p, count, st);
       if (e != hipSuccess) return e;
     }
   }
