@@ -324,19 +324,26 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_first_tall(const void* 
                                                                     const double* part, int parts, double eps,
                                                                     uint16_t* hi, uint16_t* lo) {
   constexpr size_t SIZE = DT == kDtF32 ? 4 : 2;
-  constexpr int LD = 72;  // values per row of the LDS tile
+  constexpr int LD = 66;  // values per row of the LDS tile: a row's and a column's lie in distinct banks
   __shared__ double lds[kNormThreads / 64];
-  __shared__ __align__(16) uint16_t th[64][LD], tl[64][LD];
+  __shared__ __align__(4) uint16_t th[64][LD], tl[64][LD];
   const int z = blockIdx.z;
+  const char* p = static_cast<const char*>(g) + (size_t)z * R * C * SIZE;
+  const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64, c = c0 + (int)(threadIdx.x & 63);
+  float g16[64 / (kNormThreads / 64)];  // under way while the norm is added up
+#pragma unroll
+  for (int k = 0; k < 64 / (kNormThreads / 64); ++k) {
+    const int r = r0 + (threadIdx.x >> 6) + k * (kNormThreads / 64);
+    g16[k] = r < R && c < C ? (float)value_at<DT>(p, (size_t)r * C + c) : 0.0f;
+  }
   const double sum =
       block_sum<kNormThreads / 64>((int)threadIdx.x < parts ? part[(size_t)z * parts + threadIdx.x] : 0.0, lds);
   const double inv = (double)kXScale / (__builtin_sqrt(sum) + eps);
-  const char* p = static_cast<const char*>(g) + (size_t)z * R * C * SIZE;
-  const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64, c = c0 + (int)(threadIdx.x & 63);
-#pragma unroll 8
-  for (int i = threadIdx.x >> 6; i < 64; i += kNormThreads / 64) {
-    const int r = r0 + i;
-    const float v = r < R && c < C ? (float)(value_at<DT>(p, (size_t)r * C + c) * inv) : 0.0f;
+  constexpr int PER = 64 / (kNormThreads / 64);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int i = (threadIdx.x >> 6) + k * (kNormThreads / 64);
+    const float v = (float)(g16[k] * inv);
     const _Float16 h = (_Float16)v;
     th[c - c0][i] = __builtin_bit_cast(uint16_t, h);
     tl[c - c0][i] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)h));
@@ -346,8 +353,14 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_first_tall(const void* 
     const int row = i >> 3, col = (i & 7) * 8;
     if (c0 + row >= m || r0 + col >= n) continue;  // m and n are multiples of 8
     const size_t at = ((size_t)z * m + c0 + row) * n + r0 + col;
-    *reinterpret_cast<u32x4_t*>(hi + at) = *reinterpret_cast<const u32x4_t*>(&th[row][col]);
-    *reinterpret_cast<u32x4_t*>(lo + at) = *reinterpret_cast<const u32x4_t*>(&tl[row][col]);
+    u32x4_t h, l;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = *reinterpret_cast<const uint32_t*>(&th[row][col + 2 * j]);
+      l[j] = *reinterpret_cast<const uint32_t*>(&tl[row][col + 2 * j]);
+    }
+    *reinterpret_cast<u32x4_t*>(hi + at) = h;
+    *reinterpret_cast<u32x4_t*>(lo + at) = l;
   }
 }
 
@@ -377,8 +390,11 @@ hipError_t run(const NsArgs& a, int blocks, int slices, int batch, hipStream_t s
 // of the rest of a block.
 constexpr double kFewUs[kNumTiles] = {0.95, 0.47, 0.32, 0.26, 0.40}, kFullUs[kNumTiles] = {1.45, 0.80, 0.47, 0.34, 0.64};
 constexpr double kStartUs = 4.5;
+constexpr double kPairUs = 0.56;  // 64 x 128: a stage of both blocks of a CU
+inline int places(int tile) { return tile == 3 ? 512 : 256; }  // blocks the chip holds
 inline double stage_us(int tile, double blocks) {
   const double full = blocks < 256 ? blocks / 256 : 1.0;
+  if (tile == 3 && blocks > 256) return kPairUs;
   return kFewUs[tile] + full * (kFullUs[tile] - kFewUs[tile]);
 }
 
@@ -393,11 +409,12 @@ inline int lower_tiles(int tile, int m) {
     case 0: return lower_tiles_of<0>(m);
     case 1: return lower_tiles_of<1>(m);
     case 2: return lower_tiles_of<2>(m);
+    case 3: return lower_tiles_of<3>(m);
     default: return lower_tiles_of<4>(m);
   }
 }
 
-// How a symmetric product is cut: tile (not 64 x 128) and slices of K.
+// How a symmetric product is cut: tile and slices of K.
 struct Cut {
   int tile, slices;
 };
@@ -405,12 +422,12 @@ Cut symmetric_cut(int m, int K, int batch, bool split) {
   const int stages = ceil_div(K, 64);
   Cut best = {2, 1};
   double best_us = 1e30;
-  for (int t : {0, 1, 2, 4}) {
+  for (int t = 0; t < kNumTiles; ++t) {
     const int tiles = lower_tiles(t, m);
     for (int s = 1; s == 1 || (split && s <= 16 && s * 4 <= stages + 3); s *= 2) {
       const int per = ceil_div(stages, s), slices = ceil_div(stages, per);
       const double blocks = (double)tiles * slices * batch;
-      double us = __builtin_ceil(blocks / 256) * (per * stage_us(t, blocks) + kStartUs);
+      double us = __builtin_ceil(blocks / places(t)) * (per * stage_us(t, blocks) + kStartUs);
       if (slices > 1) us += 2.5 + 1.5 * slices * m * (double)m * batch * 4 / 4e6;
       if (us < best_us) {
         best_us = us;
@@ -432,6 +449,7 @@ hipError_t symmetric(NsArgs a, const Cut& cut, int batch, hipStream_t st) {
   const int tiles = lower_tiles(cut.tile, a.M);
   if (cut.tile == 0) return run<false, 0, EPI>(a, tiles, cut.slices, batch, st);
   if (cut.tile == 1) return run<false, 1, EPI>(a, tiles, cut.slices, batch, st);
+  if (cut.tile == 3) return run<false, 3, EPI>(a, tiles, cut.slices, batch, st);
   if (cut.tile == 4) return run<false, 4, EPI>(a, tiles, cut.slices, batch, st);
   return run<false, 2, EPI>(a, tiles, cut.slices, batch, st);
 }
@@ -453,14 +471,11 @@ hipError_t gram_of(const NsArgs& a, int batch, hipStream_t st) {
 template <int EPI>
 hipError_t general(NsArgs a, int batch, hipStream_t st) {
   a.stages = a.slice_stages = ceil_div(a.K, 64);
-  constexpr double kPairUs = 0.56;  // 64 x 128: a stage of both blocks of a CU
   int best = 0;
   double best_us = 1e30;
   for (int t = 0; t < kNumTiles; ++t) {
     const long long n = (long long)ceil_div(a.M, kTiles[t].bm) * ceil_div(a.N, kTiles[t].bn) * batch;
-    const int places = t == 3 ? 512 : 256;
-    const double stage = t == 3 && n > 256 ? kPairUs : stage_us(t, (double)n);
-    const double us = (double)((n + places - 1) / places) * (a.stages * stage + kStartUs);
+    const double us = (double)((n + places(t) - 1) / places(t)) * (a.stages * stage_us(t, (double)n) + kStartUs);
     if (us < best_us) {
       best_us = us;
       best = t;

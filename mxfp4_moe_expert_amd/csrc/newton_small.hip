@@ -245,9 +245,12 @@ __global__ __launch_bounds__(kThreads) void k_newton_panel(SmallArgs a) {
   const int first = blockIdx.x * a.per_block, end = min(first + a.per_block, a.panels);
   u32x4_t* state = a.state + ((size_t)z * a.panels * S::RT * S::CT) * kThreads + threadIdx.x;
   double inv = 0.0;
+  f32x4_t y[S::RT][S::CT];
+  const void* gp = static_cast<const char*>(a.g) + z * values * (DT == kDtF32 ? 4 : 2);
   if constexpr (MODE == kFirst) {
     __shared__ double lds[kWaves];
     const double* part = a.norm + z * a.norm_parts;
+    w.template load_g<DT>(gp, first, y);  // under way while the norm is added up
     inv = (double)kXScale / (__builtin_sqrt(block_sum<kWaves>((int)threadIdx.x < a.norm_parts ? part[threadIdx.x] : 0.0, lds)) + a.eps);
   } else {
     w.load_a(a.square + z * S::M * S::M);
@@ -255,10 +258,9 @@ __global__ __launch_bounds__(kThreads) void k_newton_panel(SmallArgs a) {
   w.clear_gram();
   for (int p = first; p < end; ++p) {
     u32x4_t x[S::RT][S::CT];
-    f32x4_t y[S::RT][S::CT];
     u32x4_t* at = state + (size_t)p * S::RT * S::CT * kThreads;
     if constexpr (MODE == kFirst) {
-      w.template load_g<DT>(static_cast<const char*>(a.g) + z * values * (DT == kDtF32 ? 4 : 2), p, y);
+      if (p > first) w.template load_g<DT>(gp, p, y);
       w.each([&](int t, int c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[t][c][e] = (float)((double)y[t][c][e] * inv);
