@@ -53,7 +53,7 @@ BalanceLayout balance_layout(int T, int E, int S) {
   L.sum = 256;
   L.count = L.sum + rows;
   L.loss = L.count + rows;
-  L.total = balance_one(T, E, S) ? kNoWorkspace : L.loss + align256((size_t)S * 4);
+  L.total = balance_one(T, E, S) ? kNoWorkspace : L.loss + align256((size_t)balance_losses(E, S) * 4);
   return L;
 }
 

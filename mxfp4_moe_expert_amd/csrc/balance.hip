@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kBalWaves = 16, kBalThreads = kBalWaves * 64;
 constexpr int kBalRuns = 512;    // runs of tokens at most: two blocks per CU
-constexpr int kBalRunMin = 32;
+constexpr int kBalRunMin = 4, kBalRunSmall = 32;
 
 // h = exp(-|z| / 2), one hardware exponential. Above, e = h h = exp(-|z|): softplus(z) = max(z, 0) + log1p(e), with
 // log1p(e) = log(1 + e) + what 1 + e lost of e (exact; it matters where e is small, and there its slope is 1). Below
@@ -252,13 +252,14 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_runs(BalanceArgs a) {
   }
 }
 
-// Block q: sequence q's partial rows -> its loss, its coefficients (alpha f / n; 1 / Q follows them) and its counts; the
-// last block to end adds the sequences' losses.
+// Block (q, y): sequence q's partial rows, experts COLS y .. -> their part of its loss, their coefficients (alpha f / n;
+// 1 / Q follows the last) and counts; the last block to end adds the losses.
+template <int COLS>
 __global__ __launch_bounds__(kBalThreads) void k_balance_fold(BalanceArgs a) {
-  constexpr int SUB = kBalThreads / 256;
-  __shared__ float psum[SUB][256], lds[kBalWaves];
-  __shared__ int pcount[SUB][256], last;
-  const int tid = threadIdx.x, e = tid & 255, sub = tid >> 8, q = blockIdx.x;
+  constexpr int SUB = kBalThreads / COLS;
+  __shared__ float psum[SUB][COLS], lds[kBalWaves];
+  __shared__ int pcount[SUB][COLS], last;
+  const int tid = threadIdx.x, sub = tid / COLS, e = blockIdx.y * COLS + tid % COLS, q = blockIdx.x;
   const int b = offset_of(a, q), end = offset_of(a, q + 1), n = end - b;
   const bool bad = bad_borders(a, q);
   float sum = 0.0f;
@@ -285,38 +286,44 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fold(BalanceArgs a) {
       }
     }
   }
-  psum[sub][e] = sum;
-  pcount[sub][e] = count;
+  psum[sub][tid % COLS] = sum;
+  pcount[sub][tid % COLS] = count;
   __syncthreads();
   if (sub == 0) {
 #pragma unroll
     for (int i = 1; i < SUB; ++i) {
-      sum += psum[i][e];
-      count += pcount[i][e];
+      sum += psum[i][tid];
+      count += pcount[i][tid];
     }
     if (count) atomicAdd(&a.counts[e], count);
   }
-  float loss = sequence_loss(a, q, tid, n, sum, count, lds);
+  float loss = sequence_loss(a, q, sub == 0 ? e : a.E, n, sum, count, lds);
   if (bad) loss = __uint_as_float(0x7fc00000u);
+  const int losses = gridDim.x * gridDim.y;
   if (tid == 0) {
-    __hip_atomic_store(&a.seq_loss[q], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(&a.seq_loss[blockIdx.y * gridDim.x + q], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __threadfence();
-    last = atomicAdd(a.ticket, 1) == a.S - 1;
+    last = atomicAdd(a.ticket, 1) == losses - 1;
     __threadfence();
   }
   __syncthreads();
   if (!last) return;
   float total = 0.0f, live = 0.0f;
-  for (int i = tid; i < a.S; i += kBalThreads) {
+  for (int i = tid; i < losses; i += kBalThreads)
     total += __hip_atomic_load(&a.seq_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    live += offset_of(a, i + 1) > offset_of(a, i) ? 1.0f : 0.0f;
-  }
+  for (int i = tid; i < a.S; i += kBalThreads) live += offset_of(a, i + 1) > offset_of(a, i) ? 1.0f : 0.0f;
   total = block_sum(total, lds);
   live = fmaxf(block_sum(live, lds), 1.0f);
   if (tid == 0) {
     *a.loss = a.alpha * total / live;
     a.coef[(size_t)a.S * a.E] = 1.0f / live;
   }
+}
+
+// Orders a wave's LDS accesses of different lanes (they are carried out in order; the compiler has to keep it).
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // The gradient of the logits. A group of G lanes takes the tokens of a run one after another.
@@ -326,6 +333,8 @@ template <int G, bool VEC, bool DW>
 __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs a, int per_group) {
   constexpr int TPW = 64 / G;
   constexpr int U = 2;  // tokens at a time; the next ones' logits are in flight meanwhile
+  __shared__ __align__(16) float rows[DW ? kGradWaves : 1][256];  // a wave's tokens by expert, four per lane
+  float* const mine = rows[DW ? threadIdx.x >> 6 : 0] + (threadIdx.x & 63) / G * (4 * G);
   const int lane = threadIdx.x & 63, l = lane & (G - 1);
   const long long wave = (long long)blockIdx.x * kGradWaves + (threadIdx.x >> 6), group = wave * TPW + lane / G;
   const int t0 = (int)min(group * per_group, (long long)a.T), t1 = min(t0 + per_group, a.T);
@@ -391,19 +400,20 @@ __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs 
 #pragma unroll
       for (int i = 0; i < 4; ++i) ds[i] = (g[i] - dot * inv) * inv;
       if constexpr (DW) {
-        // lane j of the group: slot j's score, from the lane that holds its expert
-        const int from = (lane & ~(G - 1)) + (id[u] < 0 ? 0 : id[u] >> 2), c = id[u] & 3;
-        const float a0 = __shfl(v[0].s, from), a1 = __shfl(v[1].s, from), a2 = __shfl(v[2].s, from),
-                    a3 = __shfl(v[3].s, from);
-        const float sj = id[u] < 0 ? 0.0f : c == 0 ? a0 : c == 1 ? a1 : c == 2 ? a2 : a3;
+        // lane j of the group: slot j's score, and its share of ds back to the expert's lane
+        auto own = [&]() -> f32x4_t& { return *reinterpret_cast<f32x4_t*>(mine + 4 * l); };
+        own() = (f32x4_t){v[0].s, v[1].s, v[2].s, v[3].s};
+        wave_lds_sync();
+        const float sj = id[u] < 0 ? 0.0f : mine[id[u]];
         const float ninv = inverse(group_sum<8>(sj)), wdot = group_sum<8>(id[u] < 0 ? 0.0f : dw[u] * sj);
-        const float dsj = a.scale * ninv * (dw[u] - wdot * ninv);
-        for (int j = 0; j < a.k; ++j) {  // in slot order
-          const int at = (lane & ~(G - 1)) + j, ej = __shfl(id[u], at);
-          const float dj = __shfl(dsj, at);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ds[i] += ej == 4 * l + i ? dj : 0.0f;
-        }
+        wave_lds_sync();
+        own() = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        wave_lds_sync();
+        // lanes of one instruction: an expert that stands in two slots takes both, in lane order
+        if (id[u] >= 0) atomicAdd(mine + id[u], a.scale * ninv * (dw[u] - wdot * ninv));
+        wave_lds_sync();
+        ds += own();
+        wave_lds_sync();
       }
       if (t >= t1) continue;
       f32x4_t o;
@@ -437,26 +447,32 @@ bool balance_args_ok(const BalanceArgs& a) {
 
 }  // namespace
 
-int balance_run(int T) {
-  const int run = (T + kBalRuns - 1) / kBalRuns;
-  return run < kBalRunMin ? kBalRunMin : run;
+// Tokens per run: the chip filled once or twice, and (a block takes its sequences one after another) no more of them than
+// a sequence has where sequences are short: 64 of one token 58 -> 14 us with runs of 4 in place of 32.
+int balance_run(int T, int S) {
+  const int fill = (T + kBalRuns - 1) / kBalRuns, mean = T / S;
+  const int small = mean < kBalRunMin ? kBalRunMin : mean < kBalRunSmall ? mean : kBalRunSmall;
+  return fill > small ? fill : small;
 }
 int balance_rows(int T, int S) {
-  const int run = balance_run(T);
+  const int run = balance_run(T, S);
   return (T > 0 ? (T + run - 1) / run : 1) + S;
 }
+// Experts per block of the fold: of few sequences each is folded by several blocks.
+static int fold_columns(int S) { return S <= 32 ? 64 : 256; }
+int balance_losses(int E, int S) { return S * ((E + fold_columns(S) - 1) / fold_columns(S)); }
 
-// Whether one block does the whole forward pass, in at most four steps of 64 tokens (of 256 experts; more of fewer): one
+// Whether one block does the whole forward pass, in at most two steps of 64 tokens (of 256 experts; more of fewer): one
 // launch for two.
 bool balance_one(int T, int E, int S) {
   const int lanes = E > 128 ? 64 : E > 64 ? 32 : E > 32 ? 16 : 8;
-  return (long long)T * lanes <= 16384 && S <= 8;
+  return (long long)T * lanes <= 8192 && S <= 8;
 }
 
 hipError_t launch_balance(BalanceArgs a, hipStream_t st) {
   if (!balance_args_ok(a)) return hipErrorInvalidValue;
   const bool one = balance_one(a.T, a.E, a.S);
-  a.run = one ? a.T : balance_run(a.T);
+  a.run = one ? a.T : balance_run(a.T, a.S);
   const unsigned runs = one ? 1u : (unsigned)(balance_rows(a.T, a.S) - a.S);
   const hipError_t e = by_group(a.E, [&](auto g) {
     if (a.E % 4 == 0) {
@@ -468,7 +484,8 @@ hipError_t launch_balance(BalanceArgs a, hipStream_t st) {
     }
   });
   if (e != hipSuccess || one) return e;
-  k_balance_fold<<<(unsigned)a.S, kBalThreads, 0, st>>>(a);
+  if (fold_columns(a.S) == 64) k_balance_fold<64><<<dim3((unsigned)a.S, (unsigned)((a.E + 63) / 64)), kBalThreads, 0, st>>>(a);
+  else k_balance_fold<256><<<(unsigned)a.S, kBalThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -507,7 +507,7 @@ struct BalanceArgs {
   int run;                 // tokens per block of the forward pass
   float* part_sum;         // [balance_rows][E] partial rows: of run r and sequence q at r + q
   int32_t* part_count;
-  float* seq_loss;         // [S]
+  float* seq_loss;         // [balance_losses]
   int32_t* ticket;
   const float* dloss;      // backward: the loss's gradient, or null for 1
   const float* dw;         // [T][k], or null
@@ -516,8 +516,9 @@ struct BalanceArgs {
   uint32_t* flags;
 };
 bool balance_one(int T, int E, int S);  // no workspace used
-int balance_run(int T);
+int balance_run(int T, int S);
 int balance_rows(int T, int S);
+int balance_losses(int E, int S);  // values of seq_loss
 hipError_t launch_balance(BalanceArgs a, hipStream_t st);
 hipError_t launch_route_backward(const BalanceArgs& a, hipStream_t st);
 
