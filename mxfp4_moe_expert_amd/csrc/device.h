@@ -170,6 +170,26 @@ __device__ __forceinline__ int int8_code(float v, const RowScale& s) {
   return (int)c;
 }
 
+// The codes of four values, value i in byte i. A sum with 1.5 2^23 is rounded to a whole number, its low byte the code; where
+// the remainder is below half a scale that code is the nearest, and only beside a border is it decided as above.
+__device__ __forceinline__ uint32_t int8_codes4(const f32x4_t& v, const RowScale& s) {
+  constexpr float kWhole = 12582912.0f;
+  float most = 0.0f;
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float t = __builtin_fmaf(v[i], s.inverse, kWhole);
+    most = fmaxf(most, __builtin_fabsf(__builtin_fmaf(kWhole - t, s.scale, v[i])));
+    b[i] = __float_as_uint(t);
+  }
+  if (2.0f * most < s.scale)
+    return __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u) | __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c |= ((uint32_t)int8_code(v[i], s) & 255u) << (8 * i);
+  return c;
+}
+
 __device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z))); }
 
 // silu(z) = z / (1 + e^-z) with the hardware base-2 exponential and

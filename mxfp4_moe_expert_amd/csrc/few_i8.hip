@@ -78,13 +78,14 @@ __global__ __launch_bounds__(NW * 64) void k_few_i8(FewI8Args a) {
       for (int i = 0; i < PER; ++i) {
         const int at = first + i * step;
         if (at >= P) continue;
-        uint2 c = make_uint2(0u, 0u);
+        f32x4_t lo, hi;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = (uint32_t)int8_code(__uint_as_float(p[i][j] << 16), s) & 255u;
-          const uint32_t hi = (uint32_t)int8_code(__uint_as_float(p[i][j] & 0xffff0000u), s) & 255u;
-          (j < 2 ? c.x : c.y) |= (lo | hi << 8) << (16 * (j & 1));
+          const uint32_t d = p[i][j];
+          (j < 2 ? lo : hi)[2 * (j & 1)] = __uint_as_float(d << 16);
+          (j < 2 ? lo : hi)[2 * (j & 1) + 1] = __uint_as_float(d & 0xffff0000u);
         }
+        const uint2 c = make_uint2(int8_codes4(lo, s), int8_codes4(hi, s));
         *reinterpret_cast<uint2*>(codes + row * a.K + at * 8) = c;
       }
       if (first == 0) scale_of[row] = s.scale;

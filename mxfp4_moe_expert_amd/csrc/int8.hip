@@ -46,11 +46,14 @@ __device__ __forceinline__ uint32_t piece_top(const u32x4_t& p, uint32_t m) {
 template <int DT>
 __device__ __forceinline__ uint2 piece_codes(const u32x4_t& p, const RowScale& s) {
   uint2 o = make_uint2(0u, 0u);
+  f32x4_t v;
 #pragma unroll
-  for (int i = 0; i < kPer<DT>; ++i) {
-    const uint32_t c = (uint32_t)int8_code(value_of<DT>(p, i), s) & 255u;
-    if (i < 4) o.x |= c << (8 * i);
-    else o.y |= c << (8 * (i - 4));
+  for (int i = 0; i < 4; ++i) v[i] = value_of<DT>(p, i);
+  o.x = int8_codes4(v, s);
+  if constexpr (kPer<DT> == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = value_of<DT>(p, 4 + i);
+    o.y = int8_codes4(v, s);
   }
   return o;
 }
