@@ -8,10 +8,16 @@
 // order of adding them changes a result.
 //   Activations that come as codes: a lane reads its tokens' codes as it reads
 //     the weights.
-//   Up to four tokens in bf16 (K short enough, see fits()): every block encodes
-//     them itself, while its first weights are under way, and keeps the codes in
-//     LDS. One token 4096 -> 1536 costs one launch then, not three.
-// Bound by the weight bytes; at one token by launch and load latency.
+//   Up to eight tokens in bf16 (few_i8_encodes): every block encodes them
+//     itself, while its first weights are under way, and keeps the codes in LDS:
+//     one launch. To about four tokens that is faster in itself (4096 -> 4096, 4
+//     tokens 7.8 us against 9.1 with a launch for the encoding), to eight it is
+//     within about 1 us (7 tokens 10.1 against 8.8) and saves the host the 3 us
+//     of a launch, which is what calls of this size wait for.
+// Bound by the weight bytes; at one token by launch and load latency. Measured
+// (captured, eight sets of weights in turn): 1 x 4096 -> 1536 5.6 us, 1 x 4096 ->
+// 4096 6.9 (2.4 TB/s of weights), 1 x 8192 -> 4096 9.3 (3.6); codes given, 4096 ->
+// 4096: 5.5 at one token, 6.9 at 16, 8.6 at 32.
 #include <type_traits>
 
 #include "dense.h"
@@ -20,9 +26,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kStep = 128;       // k values per wave and step
-constexpr int kEncodeMax = 16384;  // values that a block encodes (rows rounded up to a power of two)
-constexpr int kEncodeRows = 4;
+constexpr int kStep = 128;         // k values per wave and step
+constexpr int kEncodeMax = 32768;  // values that a block encodes (rows rounded up to a power of two)
+constexpr int kEncodeRows = 8;
+
+__host__ __device__ inline int encode_rows(int T) { return T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8; }
 
 // CT: blocks of 16 tokens. ENCODE: x is bf16, encoded here.
 template <bool ENCODE, int CT, int NW>
@@ -52,7 +60,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_i8(FewI8Args a) {
 
   if constexpr (ENCODE) {
     // the waves share the rows evenly: rp rows (a power of two), NW / rp waves on each
-    const int rp = a.T <= 1 ? 1 : a.T <= 2 ? 2 : 4, wpr = NW / rp;
+    const int rp = encode_rows(a.T), wpr = NW / rp;
     const int row = wave / wpr, first = (wave % wpr) * 64 + lane, step = wpr * 64, P = a.K / 8;
     constexpr int PER = kEncodeMax / 8 / (NW * 64);  // pieces per lane at most
     static_assert(PER >= 1, "");
@@ -134,22 +142,22 @@ __global__ __launch_bounds__(NW * 64) void k_few_i8(FewI8Args a) {
   }
 }
 
-// Waves per block: enough that the blocks of 16 rows give each of the 256 CUs about 16 waves.
+// Waves per block: enough that the blocks of 16 rows give each of the 256 CUs about 16 waves (to encode, one per row at
+// least).
 template <bool ENCODE, int CT>
 hipError_t go(const FewI8Args& a, hipStream_t st) {
   const int blocks = (a.N + 15) / 16;
   const size_t lds = ENCODE ? (size_t)a.T * a.K : 0;
   if (blocks <= 320) k_few_i8<ENCODE, CT, 16><<<blocks, 16 * 64, lds, st>>>(a);
-  else if (blocks <= 640) k_few_i8<ENCODE, CT, 8><<<blocks, 8 * 64, lds, st>>>(a);
-  else k_few_i8<ENCODE, CT, 4><<<blocks, 4 * 64, lds, st>>>(a);
+  else if (blocks <= 640 || ENCODE) k_few_i8<ENCODE, CT, 8><<<blocks, 8 * 64, lds, st>>>(a);
+  else if constexpr (!ENCODE) k_few_i8<ENCODE, CT, 4><<<blocks, 4 * 64, lds, st>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 bool few_i8_encodes(int T, int K) {
-  const int rows = T <= 1 ? 1 : T <= 2 ? 2 : 4;
-  return T <= kEncodeRows && rows * K <= kEncodeMax;
+  return T <= kEncodeRows && (long long)encode_rows(T) * K <= kEncodeMax;
 }
 
 hipError_t launch_few_i8(const FewI8Args& a, hipStream_t st) {

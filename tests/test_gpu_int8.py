@@ -149,7 +149,7 @@ def product(xq, xs, q, s, half):
 
 
 # rows: one, the sizes around those where kernel, tile or cut change, many; K and N: odd multiples of 16, any N
-LINEAR = [(1, 16, 1), (1, 4096, 1536), (2, 1040, 17), (7, 272, 100), (8, 4096, 256), (9, 8192, 48), (16, 2048, 1000),
+LINEAR = [(3, 8192, 12000), (5, 4096, 300), (6, 4112, 6000), (8, 1040, 12304), (1, 16, 1), (1, 4096, 1536), (2, 1040, 17), (7, 272, 100), (8, 4096, 256), (9, 8192, 48), (16, 2048, 1000),
           (17, 2064, 33), (31, 528, 4096), (32, 4096, 512), (33, 8192, 4096), (48, 144, 130), (64, 4096, 4096),
           (65, 65536, 64), (100, 4112, 127), (129, 1024, 257), (300, 4096, 768), (513, 1296, 2000), (1000, 4096, 4096),
           (4097, 512, 640)]
