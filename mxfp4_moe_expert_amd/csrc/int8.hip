@@ -99,13 +99,22 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_int8_quantize(long lo
   if (lane == 0) scales[row] = s.scale;
 }
 
+constexpr long long kMaxThreads = 1ll << 31;  // of a launch (the runtime takes fewer than 2^32); more rows, more launches
+
 template <int DT>
 hipError_t quantize(long long rows, int K, const char* x, long long ld, int8_t* codes, float* scales, hipStream_t st) {
   const int P = K / kPer<DT>;
   auto go = [&](auto tpr, auto per) {
     constexpr int threads = tpr > 256 ? tpr : 256, rpb = threads / tpr;
-    k_int8_quantize<DT, tpr, per><<<(unsigned)((rows + rpb - 1) / rpb), threads, 0, st>>>(rows, K, x, ld, codes, scales);
-    return hipGetLastError();
+    constexpr long long most = kMaxThreads / tpr;
+    for (long long r = 0; r < rows; r += most) {
+      const long long n = rows - r < most ? rows - r : most;
+      k_int8_quantize<DT, tpr, per><<<(unsigned)((n + rpb - 1) / rpb), threads, 0, st>>>(n, K, x + r * ld, ld, codes + r * K,
+                                                                                        scales + r);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   };
 #define ROW(tpr, per) go(std::integral_constant<int, tpr>{}, std::integral_constant<int, per>{})
   // Few rows: latency counts, and a row's pieces are spread over 1024 threads (33 x 8192 bf16 5.3 -> 3.4 us); rows past
@@ -201,13 +210,19 @@ hipError_t launch_int8_dequantize(long long rows, int K, const int8_t* codes, co
   const int P = K / (dtype == kDtF32 ? 4 : 8);
   const int rpb = P <= 128 ? 256 / P : 1;
   const int segs = rpb > 1 ? 1 : (P + 256 * kDeqAhead - 1) / (256 * kDeqAhead);
-  const long long nb = (rows + rpb - 1) / rpb * segs;
-  if (nb > 0x7fffffffll) return hipErrorInvalidValue;
-  if (dtype == kDtF32)
-    k_int8_dequantize<true><<<(unsigned)nb, 256, 0, st>>>(rows, K, rpb, segs, codes, scales, out);
-  else
-    k_int8_dequantize<false><<<(unsigned)nb, 256, 0, st>>>(rows, K, rpb, segs, codes, scales, out);
-  return hipGetLastError();
+  const long long most = kMaxThreads / 256 / segs * rpb;
+  for (long long r = 0; r < rows; r += most) {
+    const long long n = rows - r < most ? rows - r : most;
+    const unsigned nb = (unsigned)((n + rpb - 1) / rpb * segs);
+    if (dtype == kDtF32)
+      k_int8_dequantize<true><<<nb, 256, 0, st>>>(n, K, rpb, segs, codes + r * K, scales + r, static_cast<float*>(out) + r * K);
+    else
+      k_int8_dequantize<false><<<nb, 256, 0, st>>>(n, K, rpb, segs, codes + r * K, scales + r,
+                                                   static_cast<uint16_t*>(out) + r * K);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

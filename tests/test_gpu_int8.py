@@ -122,6 +122,22 @@ def test_quantize_tiny_rows():
     assert torch.equal(codes, q) and torch.equal(scales, s)
 
 
+def test_more_rows_than_one_launch_takes():
+    """2^29 + 40 rows of 16 values at eight threads each are more than 2^32 threads."""
+    rows, K = 2 ** 29 + 40, 16
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+    at = torch.tensor([0, 2 ** 28 - 1, 2 ** 28, 2 ** 28 + 1, 2 ** 29 - 1, 2 ** 29, rows - 1], device=DEV)
+    x[at] = _rand(17, at.numel(), K).bfloat16()
+    codes, scales = mx.quantize_int8(x)
+    want, ws = encode(x[at])
+    assert torch.equal(codes[at], want) and torch.equal(scales[at], ws)
+    assert int(torch.count_nonzero(codes)) == int(torch.count_nonzero(want))
+    assert int(torch.count_nonzero(scales != 1)) == at.numel()
+    mx.dequantize_int8(codes, scales, out=x)
+    assert torch.equal(x[at], (want.float() * ws[:, None]).bfloat16())
+    assert int(torch.count_nonzero(x)) == int(torch.count_nonzero(want))
+
+
 def test_quantize_strided_rows_shapes_and_outputs():
     whole = _rand(5, 40, 256).to(torch.bfloat16)
     part = whole[:, 64:160]
