@@ -295,8 +295,9 @@ int moe_linear_w8a16(int32_t T, int32_t K, int32_t N, int32_t groups, const uint
  *   loss   [1] f32 out; counts [E] i32 out (over all sequences)
  *   coef   [S E + 1] f32 out: what moe_route_backward takes
  * An expert with the logit -inf has the share 0 (and gets no gradient); a token
- * all of whose logits are has no shares. NaN logits give a NaN loss. Sums are
- * fp32 in an order that does not depend on timing.
+ * all of whose logits are, or whose scores sum to less than 2^-126 (logits of
+ * about -175 and below), has no shares and gets no gradient. NaN logits give a
+ * NaN loss. Sums are fp32 in an order that does not depend on timing.
  *   workspace: moe_balance_workspace_size(T, E, S) bytes, 256-byte aligned, any
  *   contents; calls sharing one must be ordered on one stream. A size of 256
  *   means that none is used (small batches: one launch; else two): workspace may

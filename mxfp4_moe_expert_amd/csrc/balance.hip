@@ -74,8 +74,9 @@ __device__ __forceinline__ float group_sum(float v) {
   }
   return v;
 }
-// 1 / v, 0 for 0 (a row whose scores are all 0 has no shares).
-__device__ __forceinline__ float inverse(float v) { return v != 0.0f ? __builtin_amdgcn_rcpf(v) : 0.0f; }
+// 1 / v, 0 below fp32's normal range, where it would be infinite (a token whose scores sum to less has no shares). NaN
+// stays NaN.
+__device__ __forceinline__ float inverse(float v) { return v < 0x1p-126f ? 0.0f : __builtin_amdgcn_rcpf(v); }
 
 // A token's four logits of lane l of its group; experts past E as -inf (score 0).
 template <bool VEC>

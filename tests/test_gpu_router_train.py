@@ -121,6 +121,20 @@ def test_logits_at_the_edges(E):
     check(got[ok], r["dz"][ok], r["edz"][ok], "dz")
 
 
+@pytest.mark.parametrize("T,E", [(6, 8), (700, 8), (700, 256)])
+def test_scores_below_the_normal_range_have_no_shares(T, E):
+    """exp(-100 / 2) is normal; 256 exp(-97) is not, and its inverse would be infinite."""
+    z, ids, dw = _batch(31, T, E, 6)
+    low, none = z.clone(), z.clone()
+    low[1], none[1] = -194.0, float("-inf")
+    low[3], none[3] = -100.0, -100.0
+    a, b = mx.balance_loss(low, ids, alpha=0.01), mx.balance_loss(none, ids, alpha=0.01)
+    assert bool(torch.isfinite(a[0])) and float(a[0]) == float(b[0])
+    d = mx.route_backward(low, ids, dw, a[2])
+    assert bool(torch.isfinite(d).all()) and bool((d[1] == 0).all())
+    assert torch.equal(d, mx.route_backward(none, ids, dw, b[2]))
+
+
 def test_nan_logits_stay_in_their_row():
     z, ids, dw = _batch(9, 70, 64, 4)
     _, _, saved = mx.balance_loss(z, ids)
