@@ -98,6 +98,16 @@ __device__ __forceinline__ f32x4_t four_logits(const float* row, int l, int E) {
 __device__ __forceinline__ int offset_of(const BalanceArgs& a, int q) {
   return a.offsets ? min(max(a.offsets[q], 0), a.T) : q > 0 ? a.T : 0;
 }
+// A sequence's first token and the one behind its last.
+__device__ __forceinline__ void borders_of(const BalanceArgs& a, int q, int& begin, int& end) {
+  begin = 0;
+  end = a.T;
+  if (a.offsets) {
+    const int b = a.offsets[q], e = a.offsets[q + 1];
+    begin = min(max(b, 0), a.T);
+    end = min(max(e, 0), a.T);
+  }
+}
 // The last sequence that starts at or before t (0 if none does), t the same in all lanes: a wave looks at 64 borders at a
 // time; of very many it searches by halves.
 __device__ __forceinline__ int sequence_of(const BalanceArgs& a, int t) {
@@ -186,7 +196,8 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_runs(BalanceArgs a) {
   float total = 0.0f, live = 0.0f;
   int loaded = t0 + group;         // z holds the logits of this token on
   for (int t = t0; (ONE || t < t1) && q < a.S; ++q) {
-    const int from = offset_of(a, q), to = offset_of(a, q + 1);
+    int from, to;
+    borders_of(a, q, from, to);
     const int first = max(t, from), end = min(t1, to);
     const bool some = first < end;
     if (!ONE && !some) continue;
@@ -261,7 +272,9 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fold(BalanceArgs a) {
   __shared__ float psum[SUB][COLS], lds[kBalWaves];
   __shared__ int pcount[SUB][COLS], last;
   const int tid = threadIdx.x, sub = tid / COLS, e = blockIdx.y * COLS + tid % COLS, q = blockIdx.x;
-  const int b = offset_of(a, q), end = offset_of(a, q + 1), n = end - b;
+  int b, end;
+  borders_of(a, q, b, end);
+  const int n = end - b;
   const bool bad = bad_borders(a, q);
   float sum = 0.0f;
   int count = 0;
@@ -348,8 +361,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs 
       const int t = min(t0 + b + u, a.T - 1);
       zn[u] = four_logits<VEC>(a.logits + (size_t)t * a.E, l, a.E);
       if constexpr (DW) {
-        idn[u] = l < a.k ? a.ids[(size_t)t * a.k + l] : -1;
-        dwn[u] = l < a.k ? a.dw[(size_t)t * a.k + l] : 0.0f;
+        idn[u] = a.ids[(size_t)t * a.k + min(l, a.k - 1)];
+        dwn[u] = a.dw[(size_t)t * a.k + min(l, a.k - 1)];
       }
     }
   };
@@ -359,11 +372,14 @@ __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs 
   int q = sequence_of(a, (int)min(wave * TPW * per_group, (long long)a.T)), begin, end;
   f32x4_t g;
   auto enter = [&]() {
-    begin = offset_of(a, q);
-    end = offset_of(a, q + 1);
+    borders_of(a, q, begin, end);
+    g = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    if (a.coef) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      g[i] = a.coef && 4 * l + i < a.E ? a.coef[(size_t)q * a.E + 4 * l + i] * lead : 0.0f;
+      for (int i = 0; i < 4; ++i) g[i] = a.coef[(size_t)q * a.E + min(4 * l + i, a.E - 1)];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = 4 * l + i < a.E ? g[i] * lead : 0.0f;
+    }
   };
   enter();
   // every group makes the same number of steps: the lanes of a wave exchange values
@@ -375,7 +391,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void k_route_backward(BalanceArgs 
     for (int u = 0; u < U; ++u) {
       z[u] = zn[u];
       if constexpr (DW) {
-        id[u] = idn[u];
+        id[u] = l < a.k ? idn[u] : -1;
         dw[u] = dwn[u];
         if ((unsigned)id[u] >= (unsigned)a.E) {
           if (l < a.k && a.flags) atomicOr(a.flags, kFlagExpertId);

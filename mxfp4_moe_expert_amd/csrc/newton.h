@@ -23,11 +23,18 @@ __device__ __forceinline__ f32x4_t unpack4_f16(const uint2& p) {
   return __builtin_convertvector(__builtin_bit_cast(f16x4_t, p), f32x4_t);
 }
 
+// Value i of G as stored, and as fp32 (exact). A lane outside the matrix reads a value inside it and takes 0 afterwards:
+// a load with its conversion behind a branch is waited for there, one after another (a stack of 3 x 1001 x 600 fp32 took
+// 13.6 us for its first X so).
 template <int DT>
-__device__ __forceinline__ double value_at(const void* p, size_t i) {
-  if constexpr (DT == kDtF32) return static_cast<const float*>(p)[i];
-  const uint32_t h = static_cast<const uint16_t*>(p)[i];
-  return DT == kDtBf16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
+__device__ __forceinline__ uint32_t stored_at(const void* p, size_t i) {
+  if constexpr (DT == kDtF32) return static_cast<const uint32_t*>(p)[i];
+  return static_cast<const uint16_t*>(p)[i];
+}
+template <int DT>
+__device__ __forceinline__ float stored_value(uint32_t v) {
+  if constexpr (DT == kDtF32) return __uint_as_float(v);
+  return DT == kDtBf16 ? __uint_as_float(v << 16) : f16_bits_to_f32(v);
 }
 
 // Sum over a block of WAVES waves in a fixed order; every thread has it.

@@ -27,11 +27,11 @@ namespace {
 struct NsArgs : DenseArgs {
   size_t x_batch, w_batch;        // bytes between the matrices of a stack
   size_t in_batch, out_batch;     // values: of hi / lo / mat, and of out
-  float ca, cb;                   // kNsGram: acc * ca; kNsPoly: mat * ca + acc * cb; kNsNext, kNsLast: x * ca + acc
   const uint16_t *hi, *lo;        // kNsPoly: hi is A
   uint16_t *hi_out, *lo_out;      // lo_out may be null
   int in_ld, out_ld;              // values per row of hi / lo, and of out
   int flip;                       // kNsLast: out is [N][M]
+  float ca, cb;                   // kNsGram: acc * ca; kNsPoly: mat * ca + acc * cb; kNsNext, kNsLast: x * ca + acc
 
   __device__ const void* x_base() const { return static_cast<const char*>(x) + blockIdx.z * x_batch; }
   __device__ const void* w_base() const { return static_cast<const char*>(w) + blockIdx.z * w_batch; }
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_norm(const void* g, siz
   if (blockIdx.x == 0) {
     const size_t ends = head + (n - tail);  // fewer than 16
     if (threadIdx.x < ends) {
-      const double v = value_at<DT>(p, threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head);
+      const double v = stored_value<DT>(stored_at<DT>(p, threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head));
       s += v * v;
     }
   }
@@ -297,17 +297,22 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_first(const void* g, in
   const long long n = (long long)Rp * (Cp / 8);
   for (long long i = (long long)blockIdx.x * kNormThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kNormThreads) {
     const int row = (int)(i / (Cp / 8)), col = (int)(i - (long long)row * (Cp / 8)) * 8;
+    const size_t first = (size_t)min(row, R - 1) * C;
     double v[8];
-    if (row < R && whole) {
-      eight_values<DT>(reinterpret_cast<const u32x4_t*>(p + ((size_t)row * C + col) * SIZE), v);
+    if (whole) {
+      eight_values<DT>(reinterpret_cast<const u32x4_t*>(p + (first + col) * SIZE), v);
     } else {
+      uint32_t raw[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = row < R && col + j < C ? value_at<DT>(p, (size_t)row * C + col + j) : 0.0;
+      for (int j = 0; j < 8; ++j) raw[j] = stored_at<DT>(p, first + min(col + j, C - 1));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = stored_value<DT>(raw[j]);
     }
     uint32_t h[4], l[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x = (float)(v[2 * j] * inv), y = (float)(v[2 * j + 1] * inv);
+      const float x = row < R && col + 2 * j < C ? (float)(v[2 * j] * inv) : 0.0f;
+      const float y = row < R && col + 2 * j + 1 < C ? (float)(v[2 * j + 1] * inv) : 0.0f;
       h[j] = f16x2_rne(x, y);
       const f16x2_t hv = __builtin_bit_cast(f16x2_t, h[j]);
       l[j] = f16x2_rne(x - (float)hv[0], y - (float)hv[1]);
@@ -330,20 +335,19 @@ __global__ __launch_bounds__(kNormThreads) void k_newton_first_tall(const void* 
   const int z = blockIdx.z;
   const char* p = static_cast<const char*>(g) + (size_t)z * R * C * SIZE;
   const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64, c = c0 + (int)(threadIdx.x & 63);
-  float g16[64 / (kNormThreads / 64)];  // under way while the norm is added up
+  constexpr int PER = 64 / (kNormThreads / 64);
+  const int i0 = threadIdx.x >> 6;
+  uint32_t raw[PER];  // under way while the norm is added up
 #pragma unroll
-  for (int k = 0; k < 64 / (kNormThreads / 64); ++k) {
-    const int r = r0 + (threadIdx.x >> 6) + k * (kNormThreads / 64);
-    g16[k] = r < R && c < C ? (float)value_at<DT>(p, (size_t)r * C + c) : 0.0f;
-  }
+  for (int k = 0; k < PER; ++k)
+    raw[k] = stored_at<DT>(p, (size_t)min(r0 + i0 + k * (kNormThreads / 64), R - 1) * C + min(c, C - 1));
   const double sum =
       block_sum<kNormThreads / 64>((int)threadIdx.x < parts ? part[(size_t)z * parts + threadIdx.x] : 0.0, lds);
   const double inv = (double)kXScale / (__builtin_sqrt(sum) + eps);
-  constexpr int PER = 64 / (kNormThreads / 64);
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    const int i = (threadIdx.x >> 6) + k * (kNormThreads / 64);
-    const float v = (float)(g16[k] * inv);
+    const int i = i0 + k * (kNormThreads / 64);
+    const float v = r0 + i < R && c < C ? (float)(stored_value<DT>(raw[k]) * inv) : 0.0f;
     const _Float16 h = (_Float16)v;
     th[c - c0][i] = __builtin_bit_cast(uint16_t, h);
     tl[c - c0][i] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)h));

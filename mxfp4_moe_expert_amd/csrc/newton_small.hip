@@ -197,20 +197,24 @@ struct Small {
   __device__ __forceinline__ int row_of(int t) const { return (row0 + t) * 16 + 4 * g; }
   __device__ __forceinline__ int col_of(int panel_at, int c) const { return panel_at * PC + (col0 + c) * 16 + r; }
 
-  // G's values (exact in fp32) at the wave's places of a panel, zeros past its edges
+  // G as stored at the wave's places of a panel (past its edges: other values of it), and its values as fp32 (exact; there
+  // zeros)
   template <int DT>
-  __device__ __forceinline__ void load_g(const void* gp, int at, f32x4_t (&v)[S::RT][S::CT]) const {
+  __device__ __forceinline__ void load_g(const void* gp, int at, u32x4_t (&v)[S::RT][S::CT]) const {
 #pragma unroll
     for (int t = 0; t < S::RT; ++t)
 #pragma unroll
       for (int c = 0; c < S::CT; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = row_of(t) + e, j = col_of(at, c);
-          const bool in = i < a.m && j < a.n;
-          const size_t o = a.tall ? (size_t)j * a.m + i : (size_t)i * a.n + j;
-          v[t][c][e] = in ? (float)value_at<DT>(gp, o) : 0.0f;
+          const int i = min(row_of(t) + e, a.m - 1), j = min(col_of(at, c), a.n - 1);
+          const uint32_t o = (uint32_t)(a.tall ? j * a.m + i : i * a.n + j) * (DT == kDtF32 ? 4u : 2u);  // m n <= 2^22
+          v[t][c][e] = stored_at<DT>(static_cast<const char*>(gp) + o, 0);
         }
+  }
+  template <int DT>
+  __device__ __forceinline__ float g_value(const u32x4_t (&v)[S::RT][S::CT], int at, int t, int c, int e) const {
+    return row_of(t) + e < a.m && col_of(at, c) < a.n ? stored_value<DT>(v[t][c][e]) : 0.0f;
   }
   __device__ __forceinline__ void store_out(uint16_t* out, int at, const f32x4_t (&y)[S::RT][S::CT]) const {
 #pragma unroll
@@ -246,24 +250,24 @@ __global__ __launch_bounds__(kThreads) void k_newton_panel(SmallArgs a) {
   u32x4_t* state = a.state + ((size_t)z * a.panels * S::RT * S::CT) * kThreads + threadIdx.x;
   double inv = 0.0;
   f32x4_t y[S::RT][S::CT];
+  u32x4_t x[S::RT][S::CT];
   const void* gp = static_cast<const char*>(a.g) + z * values * (DT == kDtF32 ? 4 : 2);
   if constexpr (MODE == kFirst) {
     __shared__ double lds[kWaves];
     const double* part = a.norm + z * a.norm_parts;
-    w.template load_g<DT>(gp, first, y);  // under way while the norm is added up
+    w.template load_g<DT>(gp, first, x);  // under way while the norm is added up
     inv = (double)kXScale / (__builtin_sqrt(block_sum<kWaves>((int)threadIdx.x < a.norm_parts ? part[threadIdx.x] : 0.0, lds)) + a.eps);
   } else {
     w.load_a(a.square + z * S::M * S::M);
   }
   w.clear_gram();
   for (int p = first; p < end; ++p) {
-    u32x4_t x[S::RT][S::CT];
     u32x4_t* at = state + (size_t)p * S::RT * S::CT * kThreads;
     if constexpr (MODE == kFirst) {
-      if (p > first) w.template load_g<DT>(gp, p, y);
+      if (p > first) w.template load_g<DT>(gp, p, x);
       w.each([&](int t, int c) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[t][c][e] = (float)((double)y[t][c][e] * inv);
+        for (int e = 0; e < 4; ++e) y[t][c][e] = (float)((double)w.template g_value<DT>(x, p, t, c, e) * inv);
       });
       w.next(x, y);
     } else {
@@ -342,12 +346,17 @@ __global__ __launch_bounds__(kThreads) void k_newton_one(SmallArgs a) {
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     if (p >= a.panels) continue;
-    w.template load_g<DT>(gp, p, y);
+    w.template load_g<DT>(gp, p, x[p]);
+  }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    if (p >= a.panels) continue;
     w.each([&](int t, int c) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        sum += (double)y[t][c][e] * y[t][c][e];
-        x[p][t][c][e] = __float_as_uint(y[t][c][e]);
+        const float v = w.template g_value<DT>(x[p], p, t, c, e);
+        sum += (double)v * v;
+        x[p][t][c][e] = __float_as_uint(v);
       }
     });
   }
