@@ -11,7 +11,10 @@ Entry points (same names as the C ABI): ``route``, ``hash_route``,
 Around the layer: ``quantize_mxfp4`` / ``dequantize_mxfp4`` (its weight
 format), ``linear_mxfp4`` / ``linear_mxfp4_dx`` (plain products with MXFP4
 weights) and ``gated_ffn`` / ``gated_ffn_backward`` (the expert's block with
-bf16 weights, and its gradients).
+bf16 weights, and its gradients). For training beside it: ``quantize_int8`` /
+``dequantize_int8`` / ``linear_w8a8`` (int8 tensors and the product of two of
+them), ``balance_loss`` / ``route_backward`` (the router's balance loss,
+per-expert counts and gradient) and ``orthogonalize`` (Newton-Schulz updates).
 """
 from __future__ import annotations
 
@@ -554,7 +557,7 @@ def linear_w8a16(x, q, scale, groups=1, out_fp32=False, out=None, ws=None):
     return out
 
 
-# ------------------------------------------------------------------ MXFP4 tensors and products, the gated block
+# ------------------------------------------------------------------ MXFP4 and int8 tensors and products, the gated block
 #
 # These calls take their scratch from torch's allocator per call (or from
 # ``ws``, a uint8 tensor of at least the size the C ABI names), so calls on

@@ -19,6 +19,13 @@
 // sequence). A second launch adds each sequence's partial rows in order and the
 // losses of the sequences in order: results do not depend on timing. Of small
 // batches one block does both. Backward: one pass over the logits.
+//
+// Bound, at many tokens, by the scores' vector instructions (forward) and by
+// memory (backward); at few by launch and load latency. Measured, 256 experts:
+// 65536 tokens in 16 sequences 22 + 6 us forward (3.1 TB/s of logits in the first
+// launch) and 30 backward (4.5 TB/s; a large copy: 5.0); 4097 tokens in 7
+// sequences 9.3 + 6.0 and, with the weights' gradient, 6.1; 64 tokens 5.6 (one
+// launch) and 4.8.
 #include <type_traits>
 
 #include "device.h"

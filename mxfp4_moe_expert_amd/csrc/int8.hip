@@ -12,9 +12,11 @@
 // the smaller one's last place), says on which side v lies.
 //
 // Memory-bound both ways: a row is read once and held in registers between its
-// maximum and its codes. Measured (a large copy: 5.1 TB/s): 16384 x 4096 fp32
-// 61 us to encode (5.5 TB/s, part of it from the last-level cache) and 61 to
-// decode, bf16 41 and 38; 33 x 8192 bf16 3.4 us.
+// maximum and its codes. Measured (a large copy: 5.0 to 5.1 TB/s): 16384 x 4096 fp32
+// 61 us to encode and 61 to decode again and again (part of it from the
+// last-level cache; on inputs in turn 82, 4.1 TB/s, and 54), bf16 37 and 38; 8192
+// x 4096 bf16 18 to 20; 33 x 8192 bf16 3.5, 64 x 4096 2.9 (launch and one round of
+// load latency).
 #include <type_traits>
 
 #include "device.h"
