@@ -202,6 +202,18 @@ def test_linear_largest_sums():
         assert bool((y[:, :12] == 2.0 ** 30).all()) and bool((y[:, 12:] == -128.0 * 127 * 65536).all())
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 65536, 65536), (70, 65536, 65536), (65536, 65536, 40)])
+def test_linear_operands_past_32_bits(T, K, N):
+    """Operands of 4 GB and more: rows at both ends, in the middle and on both sides of 2^31 and 2^32 bytes."""
+    x, q, s = _rand(T, T, K).to(torch.bfloat16), _codes(N, N, K), _rand(1, N).abs() + 1e-3
+    t = torch.tensor(sorted({0, T // 4, max(T // 2 - 1, 0), T // 2, T - 1}), device=DEV)
+    n = torch.tensor(sorted({0, N // 4, N // 2 - 1, N // 2, N - 2, N - 1}), device=DEV)
+    got = mx.linear_w8a8(x, q, s, out_fp32=True)[t][:, n]
+    xq, xs = encode(x[t])
+    y, b = product(xq, xs, q[n], s[n], 0.0)
+    check(got, y, b, "fp32")
+
+
 @pytest.mark.parametrize("T", [1, 6, 20, 90, 600])
 def test_linear_rows_do_not_depend_on_each_other(T):
     """A row's result is the same bits alone and among others; non-finite rows and channels stay by themselves."""

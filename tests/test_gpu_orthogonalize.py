@@ -118,6 +118,15 @@ def test_stack_in_parts(B, R, C):
         hold(got[i], G[i])
 
 
+def test_stack_past_32_bits():
+    """Nine matrices of 512 MB, each worked on by itself: the last starts 2^32 bytes in, and has the bits it has alone."""
+    g = torch.zeros(9, 16384, 16384, dtype=torch.bfloat16, device=DEV)
+    g[8] = torch.randn(16384, 16384, generator=_gen(3), device=DEV)
+    out = mx.orthogonalize(g, steps=1)
+    assert torch.equal(out[8], mx.orthogonalize(g[8], steps=1)) and bool(out[8].isfinite().all())
+    assert int(torch.count_nonzero(out[:8])) == 0 and int(torch.count_nonzero(out[8])) > 2 ** 27
+
+
 def test_scales_at_the_ends_of_the_range():
     G = gradient(7, 100, 60)
     base = mx.orthogonalize(G, eps=0.0)
