@@ -601,9 +601,10 @@ def _matrix(t, dtype, name):
     """Rows, columns and device index of a 2-D tensor whose own checks follow."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
         _need(t, dtype, None, name)
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name}: two dimensions expected")
-    return t.shape[0], t.shape[1], t.get_device()
+    return shape[0], shape[1], t.get_device()
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -665,6 +666,13 @@ def _result(out, shape, dtype, like, name="out"):
         return like.new_empty(shape, dtype=dtype)
     _arg(out, dtype, shape, like.get_device(), name)
     return out
+
+
+def _result_like(out, t, dtype, name="out"):
+    """``_result`` of the shape of a contiguous t (0.5 us less per tensor made)."""
+    if out is None:
+        return torch.empty_like(t, dtype=dtype)
+    return _result(out, t.shape, dtype, t, name)
 
 
 def _rows_to_encode(x, group):
@@ -779,7 +787,10 @@ def quantize_int8(x, out=None):
     column stride and 16-byte aligned rows."""
     K, ldx, dt, lead = _rows_to_encode(x, 16)
     c, s = out if out is not None else (None, None)
-    codes = _result(c, lead + (K,), torch.int8, x, "codes")
+    if ldx == K and x.is_contiguous():
+        codes = _result_like(c, x, torch.int8, "codes")
+    else:
+        codes = _result(c, lead + (K,), torch.int8, x, "codes")
     scales = _result(s, lead, torch.float32, x, "scales")
     _call(x.get_device(), "moe_int8_quantize", x.numel() // K, K, dt, x.data_ptr(), ldx, codes.data_ptr(),
           scales.data_ptr())
@@ -798,7 +809,7 @@ def dequantize_int8(codes, scales, dtype=torch.bfloat16, out=None):
         raise ValueError("codes: last dimension must be a positive multiple of 16")
     pc = _arg(codes, torch.int8, shape, index, "codes")
     ps = _arg(scales, torch.float32, tuple(shape[:-1]), index, "scales")
-    out = _result(out, tuple(shape), dtype, codes)
+    out = _result_like(out, codes, dtype)
     _call(index, "moe_int8_dequantize", codes.numel() // K, K, pc, ps, _DTYPES[dtype], out.data_ptr())
     return out
 
@@ -811,10 +822,12 @@ def linear_w8a8(x, q, scale, x_scale=None, out_fp32=False, out=None, ws=None):
     of 16. Autograd does not see it."""
     encoded = x_scale is not None
     T, K, index = _matrix(x, torch.int8 if encoded else torch.bfloat16, "x")
-    N, cols, _ = _matrix(q, torch.int8, "q")
+    N, cols, at = _matrix(q, torch.int8, "q")
     if cols != K or not x.is_contiguous():
         _need(x, None, (T, cols), "x")
-    pq = _arg(q, torch.int8, (N, K), index, "q")
+    pq = q.data_ptr()
+    if at != index or not q.is_contiguous():
+        _arg(q, torch.int8, (N, K), index, "q")
     ps = _arg(scale, torch.float32, (N,), index, "scale")
     pxs = _arg(x_scale, torch.float32, (T,), index, "x_scale") if encoded else None
     out = _result(out, (T, N), torch.float32 if out_fp32 else torch.bfloat16, x)
@@ -885,10 +898,13 @@ def _routed(logits, topk_ids, seq_offsets):
         _arg(topk_ids, torch.int32, (T, k), index, "topk_ids")
     S, po = 1, None
     if seq_offsets is not None:
-        if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+        if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
             raise ValueError("seq_offsets: int32 tensor of the sequences' borders [S + 1], S >= 1, expected")
-        S = seq_offsets.shape[0] - 1
-        po = _arg(seq_offsets, torch.int32, (S + 1,), index, "seq_offsets")
+        S = seq_offsets.numel() - 1
+        po = seq_offsets.data_ptr()
+        if (seq_offsets.dtype is not torch.int32 or seq_offsets.get_device() != index
+                or not seq_offsets.is_contiguous()):
+            _arg(seq_offsets, torch.int32, (S + 1,), index, "seq_offsets")
     return T, E, k, S, index, logits.data_ptr(), topk_ids.data_ptr(), po
 
 
@@ -932,14 +948,16 @@ def route_backward(logits, topk_ids, dw=None, saved=None, scale=1.5, dloss=None,
     if coef is not None:
         if n != S * E + 1 or coef.numel() < n:
             raise ValueError("saved: not that of these logits and offsets")
-        pc = _arg(coef, torch.float32, coef.shape, index, "coef")
+        pc = coef.data_ptr()
+        if coef.dtype is not torch.float32 or coef.get_device() != index or not coef.is_contiguous():
+            _arg(coef, torch.float32, coef.shape, index, "coef")
     pd = None
     if dloss is not None:
         if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
             raise ValueError("dloss: tensor of one element expected")
         pd = _arg(dloss, torch.float32, dloss.shape, index, "dloss")
     pw = None if dw is None else _arg(dw, torch.float32, (T, k), index, "dw")
-    out = _result(out, (T, E), torch.float32, logits)
+    out = _result_like(out, logits, torch.float32)
     _call(index, "moe_route_backward", T, E, k, S, pl, pi, po, pc, pd, pw, scale, out.data_ptr())
     return out
 
@@ -967,7 +985,7 @@ def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     B = 1
     for n in shape[:-2]:
         B *= n
-    out = _result(out, shape, torch.bfloat16, g)
+    out = _result_like(out, g, torch.bfloat16)
     need = lib().moe_orthogonalize_workspace_size(B, R, C)
     pw, nw = None, 0
     if need != 256 or ws is not None:
